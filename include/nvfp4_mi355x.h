@@ -356,6 +356,106 @@ int32_t nvfp4_mx_gemm(const uint8_t* a_tiled, const uint8_t* a_sf_tiled, const f
                       int64_t a_group_rows, const uint8_t* w_tiled, const uint8_t* w_sf_tiled,
                       const float* w_gscale, void* y, int64_t B, int64_t N, int64_t K, void* stream);
 
+/*
+ * Serving attention: a paged cache of keys and values, its bookkeeping and
+ * writer, and the attention of whole prompts and of new tokens over it.
+ *
+ * A cache is two arrays [num_pages, kv_heads, page_size, head_dim] (keys,
+ * values; bf16 or fp16), any page_size >= 1.  Position p of request i lies in
+ * page block_table[i, p / page_size] at place p % page_size; slot = page *
+ * page_size + place.
+ *
+ * nvfp4_page_maps -- one step's bookkeeping from the requests' lengths, on the
+ * device: request i has ctx_lens[i] cached tokens, in the pages its row of the
+ * block table starts with, and gets new_lens[i] more.
+ *   ctx_lens, new_lens : [seqs] int32 (negative lengths count as 0)
+ *   block_table : [seqs, max_pages] int32, extended in place: request after
+ *                 request, each new page takes the next entry of free_pages
+ *                 (-1 where the list is exhausted)
+ *   free_pages  : [num_free] int32
+ *   tokens      : entries of slot_map and positions; the new tokens are packed
+ *                 in request order, entries past the last one become -1, and
+ *                 tokens that do not fit are dropped (with the table entries of
+ *                 pages that none of the kept tokens opens)
+ *   cu_new      : [seqs + 1] int32 out, first new token of each request
+ *   kv_lens     : [seqs] int32 out, ctx_lens + new_lens
+ *   slot_map    : [tokens] int64 out; -1 for a token without a page (list
+ *                 exhausted, position past the table's width, negative entry
+ *                 in the table)
+ *   positions   : [tokens] int32 out
+ *   taken       : [1] int32 out, pages the step needs: above num_free, some
+ *                 tokens have no page; else the first `taken` entries are used
+ * Requires seqs <= 2^20, tokens < 2^31 - 2^16, sums of the lengths < 2^31.
+ */
+int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_t seqs,
+                        int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                        int32_t num_free, int32_t page_size, int64_t tokens, int32_t* cu_new,
+                        int32_t* kv_lens, int64_t* slot_map, int32_t* positions, int32_t* taken,
+                        void* stream);
+
+/*
+ * nvfp4_kv_write -- copies the rows of k and v [tokens, kv_heads, head_dim]
+ * (2-byte elements, given by their strides in elements: token, head) to their
+ * slots; a slot outside [0, num_pages * page_size) is skipped.  Two tokens
+ * with the same slot leave one of them (which one is not defined).
+ * Pointers 2-byte, slot_map 8-byte aligned; rows that are not 16-byte aligned
+ * take a 2-byte path.
+ */
+int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_heads, int32_t head_dim,
+                       int64_t k_stride, int64_t k_head_stride, int64_t v_stride, int64_t v_head_stride,
+                       const int64_t* slot_map, void* k_cache, void* v_cache, int32_t page_size,
+                       int64_t num_pages, void* stream);
+
+/*
+ * Attention.  Row i of a request's m new tokens over L keys is at position
+ * p = L - m + i and sees the keys j <= p, j < L and, with window > 0, only
+ * j > p - window.  With s_j = scale * q . k_j over the keys it sees:
+ *   out = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = log sum_j e^{s_j};
+ * a row that sees no key (or only keys with s_j = -inf): out = 0, lse = -inf.
+ * What a row does not see does not reach it, NaN and infinities included.
+ * Query head h reads key/value head h / (q_heads / kv_heads).  Scores, maxima,
+ * sums and accumulators are binary32; the weights e^{s_j - max} are rounded to
+ * the inputs' type for the product with the values.  Deterministic.
+ *
+ *   q        : [tokens, q_heads, head_dim], strides in elements (token, head),
+ *              multiples of 8; 16-byte aligned
+ *   out      : [tokens, q_heads, head_dim] dense, the inputs' type, 16-byte aligned
+ *   lse      : [tokens, q_heads] float, or NULL
+ *   scale    : > 0, finite
+ *   window   : >= 0, 0 = unlimited
+ * Requires q_heads % kv_heads == 0, head_dim % 8 == 0, 8 <= head_dim <= 128
+ * (EINVAL otherwise), tokens * q_heads / kv_heads <= 2^30, seqs <= 2^20.
+ *
+ * nvfp4_prompt_attn -- whole prompts, packed: request i's tokens are
+ * cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (m = L), cu_seqlens[0] = 0; rows past
+ * the last prompt get out = 0, lse = -inf.  k, v as q with kv_heads heads.
+ */
+int32_t nvfp4_prompt_attn(const void* q, const void* k, const void* v, int32_t dtype, const int32_t* cu_seqlens,
+                          int32_t seqs, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                          int64_t q_stride, int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride,
+                          int64_t v_stride, int64_t v_head_stride, float scale, int32_t window, void* out,
+                          float* lse, void* stream);
+
+/*
+ * nvfp4_paged_attn -- new tokens over the cache, which already holds them
+ * (nvfp4_kv_write): request i's tokens are cu_new[i] .. cu_new[i + 1] - 1, its
+ * keys the first kv_lens[i] positions of its pages (at most max_pages *
+ * page_size); one token per request is a decode step, more a chunk of a prompt
+ * or drafted tokens, in any mixture.  A page id outside [0, num_pages) reads as
+ * zero keys and values.  Rows past the last request get out = 0, lse = -inf.
+ *   k_cache, v_cache : 16-byte aligned
+ *   workspace        : nvfp4_paged_attn_workspace_size bytes, 256-byte aligned
+ * Requires max_pages * page_size <= 2^30, num_pages <= 2^31.
+ */
+int32_t nvfp4_paged_attn(const void* q, int32_t dtype, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens, int32_t seqs,
+                         int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                         int64_t num_pages, int32_t max_pages, int64_t q_stride, int64_t q_head_stride,
+                         float scale, int32_t window, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t nvfp4_paged_attn_workspace_size(int32_t seqs, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                       int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,8 @@ EXPORTS = [
     "nvfp4_register_weight", "nvfp4_unregister_weight", "nvfp4_gemm_external",
     "nvfp4_pretile_weight", "nvfp4_gemm_pretiled", "nvfp4_mx_quantize", "nvfp4_mx_tile",
     "nvfp4_mx_gemm", "nvfp4_moe_w4a16_noalloc", "nvfp4_moe_w4a16_pretiled",
+    "nvfp4_page_maps", "nvfp4_kv_write", "nvfp4_prompt_attn", "nvfp4_paged_attn",
+    "nvfp4_paged_attn_workspace_size",
 ]
 MX_ROWS, MX_TILED = 0, 1
 
@@ -81,6 +83,18 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_mx_tile.restype = i32
     L.nvfp4_mx_gemm.argtypes = [p, p, p, i64, p, p, p, p, i64, i64, i64, p]
     L.nvfp4_mx_gemm.restype = i32
+    L.nvfp4_page_maps.argtypes = [p, p, i32, p, i32, p, i32, i32, i64, p, p, p, p, p, p]
+    L.nvfp4_page_maps.restype = i32
+    L.nvfp4_kv_write.argtypes = [p, p, i64, i32, i32, i64, i64, i64, i64, p, p, p, i32, i64, p]
+    L.nvfp4_kv_write.restype = i32
+    L.nvfp4_prompt_attn.argtypes = [p, p, p, i32, p, i32, i64, i32, i32, i32, i64, i64, i64, i64, i64, i64,
+                                    f32, i32, p, p, p]
+    L.nvfp4_prompt_attn.restype = i32
+    L.nvfp4_paged_attn.argtypes = [p, i32, p, p, p, p, p, i32, i64, i32, i32, i32, i32, i64, i32, i64, i64,
+                                   f32, i32, p, p, p, sz, p]
+    L.nvfp4_paged_attn.restype = i32
+    L.nvfp4_paged_attn_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    L.nvfp4_paged_attn_workspace_size.restype = sz
     return L
 
 
@@ -518,3 +532,202 @@ def mx_gemm(a: dict, a_g: torch.Tensor, w: dict, w_g: torch.Tensor, a_group_rows
     if rc != NVFP4_OK:
         raise Nvfp4Error(rc, "nvfp4_mx_gemm")
     return y
+
+
+# ---------------------------------------------------------------- serving attention
+
+def _on_gpu(first: torch.Tensor, *ts):
+    """The device of `first`, which has to be the current one and that of all others."""
+    dev = first.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current GPU")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must be on one GPU")
+    return dev
+
+
+def _dense(t: torch.Tensor, name: str, dtype, shape):
+    _need(t, name, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _heads_3d(t, name: str):
+    """[tokens, heads, head_dim] with a dense last dimension; other strides are free."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError("%s must be a 3-D tensor [tokens, heads, head_dim]" % name)
+    if t.stride(2) != 1 and t.shape[2] > 1 and t.numel() > 0:
+        raise ValueError("%s must have a dense last dimension" % name)
+
+
+def _steps(t):
+    """Token and head stride in elements; a dimension of size 1 has none."""
+    a, b, _ = t.stride()
+    return (a if t.shape[0] > 1 else 0), (b if t.shape[1] > 1 else 0)
+
+
+def _fresh(stream, make):
+    """New buffers of a call: allocated on the stream that the call runs on, so that their
+    memory is not reused before the call's work on that stream is done."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+              free_pages: torch.Tensor, page_size: int, tokens: int, out: dict | None = None,
+              stream=None) -> dict:
+    """One step's bookkeeping on the GPU: extends block_table [seqs, max_pages] in place with pages
+    from free_pages for new_lens[i] tokens after the ctx_lens[i] cached ones, and returns
+    dict(cu_new [seqs + 1], kv_lens [seqs], slot_map [tokens] int64, positions [tokens],
+    taken [1]).  `tokens` is the size of the maps (entries past the last token are -1); `taken`
+    above len(free_pages) means that pages ran out."""
+    if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be a 1-D tensor")
+    n = ctx_lens.shape[0]
+    _dense(ctx_lens, "ctx_lens", torch.int32, (n,))
+    _dense(new_lens, "new_lens", torch.int32, (n,))
+    _need_2d(block_table, "block_table")
+    width = block_table.shape[1]
+    _dense(block_table, "block_table", torch.int32, (n, width))
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a 1-D tensor")
+    _dense(free_pages, "free_pages", torch.int32, free_pages.shape)
+    tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    if out is not None:
+        for key, dt, shape in (("cu_new", torch.int32, (n + 1,)), ("kv_lens", torch.int32, (n,)),
+                               ("slot_map", torch.int64, (tokens,)), ("positions", torch.int32, (tokens,)),
+                               ("taken", torch.int32, (1,))):
+            _dense(out.get(key), "out['%s']" % key, dt, shape)
+    dev = _on_gpu(ctx_lens, new_lens, block_table, free_pages, *(out.values() if out is not None else ()))
+    if out is None:
+        out = _fresh(stream, lambda: {
+            "cu_new": torch.empty(n + 1, dtype=torch.int32, device=dev),
+            "kv_lens": torch.empty(n, dtype=torch.int32, device=dev),
+            "slot_map": torch.empty(tokens, dtype=torch.int64, device=dev),
+            "positions": torch.empty(tokens, dtype=torch.int32, device=dev),
+            "taken": torch.empty(1, dtype=torch.int32, device=dev)})
+    st = _lib.nvfp4_page_maps(ctx_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), width,
+                              free_pages.data_ptr(), free_pages.shape[0], page_size, tokens,
+                              out["cu_new"].data_ptr(), out["kv_lens"].data_ptr(), out["slot_map"].data_ptr(),
+                              out["positions"].data_ptr(), out["taken"].data_ptr(), _stream(stream))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_page_maps")
+    return out
+
+
+def _caches(k_cache, v_cache, dtype):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a 4-D tensor [pages, kv_heads, page_size, head_dim]")
+    _dense(k_cache, "k_cache", dtype, k_cache.shape)
+    _dense(v_cache, "v_cache", dtype, k_cache.shape)
+    return k_cache.shape
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
+             v_cache: torch.Tensor, stream=None) -> None:
+    """Writes k, v [tokens, kv_heads, head_dim] to their slots of the caches
+    [pages, kv_heads, page_size, head_dim]; slots outside the cache (-1) are skipped."""
+    _heads_3d(k, "k")
+    _heads_3d(v, "v")
+    _dtype_code(k)
+    T, H, D = k.shape
+    _need(v, "v", k.dtype, (T, H, D))
+    pages, heads, page_size, dim = _caches(k_cache, v_cache, k.dtype)
+    if (heads, dim) != (H, D):
+        raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (heads, dim, H, D))
+    _dense(slot_map, "slot_map", torch.int64, (T,))
+    _on_gpu(k, v, slot_map, k_cache, v_cache)
+    ks, vs = _steps(k), _steps(v)
+    st = _lib.nvfp4_kv_write(k.data_ptr(), v.data_ptr(), T, H, D, ks[0], ks[1], vs[0], vs[1], slot_map.data_ptr(),
+                             k_cache.data_ptr(), v_cache.data_ptr(), page_size, pages, _stream(stream))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_kv_write")
+
+
+def _attn_out(q, out, lse, want_lse):
+    T, H, D = q.shape
+    if out is not None:
+        _dense(out, "out", q.dtype, (T, H, D))
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, (T, H))
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                scale: float | None = None, window: int = 0, want_lse: bool = False,
+                out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Causal attention of whole packed prompts: q [tokens, q_heads, head_dim], k and v
+    [tokens, kv_heads, head_dim] (any token and head strides that are multiples of 8), cu_seqlens
+    [seqs + 1] int32.  Returns out, or (out, lse) with want_lse or a given lse buffer.  scale
+    defaults to head_dim ** -0.5; window > 0 limits a row to the last `window` keys."""
+    _heads_3d(q, "q")
+    _heads_3d(k, "k")
+    _heads_3d(v, "v")
+    dtype = _dtype_code(q)
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    _need(k, "k", q.dtype, (T, Hk, D))
+    _need(v, "v", q.dtype, (T, Hk, D))
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a 1-D tensor of seqs + 1 entries")
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape)
+    _attn_out(q, out, lse, want_lse)
+    dev = _on_gpu(q, k, v, cu_seqlens, out, lse)
+    if out is None:
+        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=dev))
+    if lse is None and want_lse:
+        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
+    qs, ks, vs = _steps(q), _steps(k), _steps(v)
+    st = _lib.nvfp4_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, cu_seqlens.data_ptr(),
+                                cu_seqlens.shape[0] - 1, T, Hq, Hk, D, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+                                D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                None if lse is None else lse.data_ptr(), _stream(stream))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_prompt_attn")
+    return out if lse is None else (out, lse)
+
+
+def paged_attn_workspace_size(seqs: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib.nvfp4_paged_attn_workspace_size(seqs, tokens, q_heads, kv_heads, head_dim))
+
+
+def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+               cu_new: torch.Tensor, kv_lens: torch.Tensor, scale: float | None = None, window: int = 0,
+               want_lse: bool = False, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Causal attention of new tokens over the paged cache, which already holds them: q [tokens,
+    q_heads, head_dim] packed by cu_new [seqs + 1], caches [pages, kv_heads, page_size, head_dim],
+    block_table [seqs, max_pages], kv_lens [seqs] (all int32).  Decode steps, chunks of prompts and
+    mixtures.  Returns out, or (out, lse) with want_lse or a given lse buffer."""
+    _heads_3d(q, "q")
+    dtype = _dtype_code(q)
+    T, Hq, D = q.shape
+    pages, Hk, page_size, dim = _caches(k_cache, v_cache, q.dtype)
+    if dim != D:
+        raise ValueError("q has head_dim %d, the cache %d" % (D, dim))
+    _need_2d(block_table, "block_table")
+    n, width = block_table.shape
+    _dense(block_table, "block_table", torch.int32, (n, width))
+    _dense(cu_new, "cu_new", torch.int32, (n + 1,))
+    _dense(kv_lens, "kv_lens", torch.int32, (n,))
+    _attn_out(q, out, lse, want_lse)
+    dev = _on_gpu(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace)
+    if out is None:
+        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=dev))
+    if lse is None and want_lse:
+        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
+    ws, wsb = _fresh(stream, lambda: _workspace(
+        _lib.nvfp4_paged_attn_workspace_size(n, T, Hq, Hk, D), dev, workspace))
+    qs = _steps(q)
+    st = _lib.nvfp4_paged_attn(q.data_ptr(), dtype, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               cu_new.data_ptr(), kv_lens.data_ptr(), n, T, Hq, Hk, D, page_size, pages, width,
+                               qs[0], qs[1], D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), wsb,
+                               _stream(stream))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_paged_attn")
+    return out if lse is None else (out, lse)

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4_mi355x.so")
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "moe.hip", "mx_gemm.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "moe.hip", "mx_gemm.hip",
+           "kv_cache.hip", "attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -7,6 +7,7 @@
 #include <unordered_map>
 
 #include "../../include/nvfp4_mi355x.h"
+#include "attention.h"
 #include "internal.h"
 
 namespace {
@@ -397,6 +398,129 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
                    topk_group, norm_topk_prob ? 1 : 0, routed_scaling, scratch, scratch_bytes,
                    current_device()->num_cus, 0};
   return hip_status(nvfp4::launch_moe(m, (hipStream_t)stream));
+}
+
+int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_t seqs,
+                        int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                        int32_t num_free, int32_t page_size, int64_t tokens, int32_t* cu_new,
+                        int32_t* kv_lens, int64_t* slot_map, int32_t* positions, int32_t* taken,
+                        void* stream) {
+  if (seqs < 0 || max_pages < 0 || num_free < 0 || page_size < 1 || tokens < 0) return NVFP4_EINVAL;
+  if (!cu_new || !taken || !aligned4(cu_new) || !aligned4(taken)) return NVFP4_EINVAL;
+  if (seqs > 0 && (!ctx_lens || !new_lens || !kv_lens)) return NVFP4_EINVAL;
+  if (seqs > 0 && max_pages > 0 && !block_table) return NVFP4_EINVAL;
+  if (num_free > 0 && !free_pages) return NVFP4_EINVAL;
+  if (tokens > 0 && (!slot_map || !positions)) return NVFP4_EINVAL;
+  if (!aligned4(ctx_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+      !aligned4(kv_lens) || ((uintptr_t)slot_map % 8) != 0 || !aligned4(positions))
+    return NVFP4_EINVAL;
+  if (seqs > (1 << 20) || tokens > 0x7FFF0000LL) return NVFP4_EUNSUPPORTED;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::PageMapsArgs a{ctx_lens, new_lens, block_table, free_pages, seqs, max_pages, num_free, page_size,
+                        tokens, cu_new, kv_lens, slot_map, positions, taken};
+  return hip_status(nvfp4::launch_page_maps(a, (hipStream_t)stream));
+}
+
+int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_heads, int32_t head_dim,
+                       int64_t k_stride, int64_t k_head_stride, int64_t v_stride, int64_t v_head_stride,
+                       const int64_t* slot_map, void* k_cache, void* v_cache, int32_t page_size,
+                       int64_t num_pages, void* stream) {
+  if (tokens < 0 || kv_heads < 1 || head_dim < 1 || page_size < 1 || num_pages < 0) return NVFP4_EINVAL;
+  if (k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0) return NVFP4_EINVAL;
+  if (tokens == 0 || num_pages == 0) return NVFP4_OK;
+  if (!k || !v || !slot_map || !k_cache || !v_cache) return NVFP4_EINVAL;
+  if ((((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_cache | (uintptr_t)v_cache) % 2) != 0 ||
+      ((uintptr_t)slot_map % 8) != 0)
+    return NVFP4_EINVAL;
+  if (kv_heads > 65536 || head_dim > 65536 || tokens > (1LL << 40) || num_pages > (1LL << 32))
+    return NVFP4_EUNSUPPORTED;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::KvWriteArgs a{k, v, tokens, kv_heads, head_dim, k_stride, k_head_stride, v_stride, v_head_stride,
+                       slot_map, k_cache, v_cache, page_size, num_pages};
+  return hip_status(nvfp4::launch_kv_write(a, (hipStream_t)stream));
+}
+
+// Checks shared by both attention entry points.
+static int32_t attn_check(const void* q, int32_t dtype, int32_t seqs, int64_t tokens, int32_t q_heads,
+                          int32_t kv_heads, int32_t head_dim, int64_t q_stride, int64_t q_head_stride,
+                          float scale, int32_t window, const void* out, const float* lse) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_FP16) return NVFP4_EINVAL;
+  if (seqs < 0 || tokens < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return NVFP4_EINVAL;
+  if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0 || window < 0) return NVFP4_EINVAL;
+  if (!(scale > 0.0f && scale <= 3.402823466e+38f)) return NVFP4_EINVAL;
+  if (q_stride < 0 || q_head_stride < 0 || q_stride % 8 != 0 || q_head_stride % 8 != 0) return NVFP4_EINVAL;
+  if (tokens == 0) return NVFP4_OK;
+  if (!q || !out || ((uintptr_t)q % 16) != 0 || ((uintptr_t)out % 16) != 0 || !aligned4(lse)) return NVFP4_EINVAL;
+  if (q_heads > 65536 || seqs > (1 << 20) || tokens > (1LL << 30) ||
+      tokens * (q_heads / kv_heads) > (1LL << 30))
+    return NVFP4_EUNSUPPORTED;
+  return NVFP4_OK;
+}
+
+int32_t nvfp4_prompt_attn(const void* q, const void* k, const void* v, int32_t dtype, const int32_t* cu_seqlens,
+                          int32_t seqs, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                          int64_t q_stride, int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride,
+                          int64_t v_stride, int64_t v_head_stride, float scale, int32_t window, void* out,
+                          float* lse, void* stream) {
+  const int32_t st = attn_check(q, dtype, seqs, tokens, q_heads, kv_heads, head_dim, q_stride, q_head_stride,
+                                scale, window, out, lse);
+  if (st != NVFP4_OK) return st;
+  if (k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0 ||
+      ((k_stride | k_head_stride | v_stride | v_head_stride) % 8) != 0)
+    return NVFP4_EINVAL;
+  if (tokens == 0) return NVFP4_OK;
+  if (!k || !v || !cu_seqlens || !aligned4(cu_seqlens) || (((uintptr_t)k | (uintptr_t)v) % 16) != 0)
+    return NVFP4_EINVAL;
+  nvfp4::AttnArgs a{};
+  a.q = q; a.k = k; a.v = v; a.dtype = dtype; a.cu = cu_seqlens; a.seqs = seqs; a.tokens = (int)tokens;
+  a.q_heads = q_heads; a.kv_heads = kv_heads; a.head_dim = head_dim;
+  a.q_stride = q_stride; a.q_head_stride = q_head_stride; a.k_stride = k_stride;
+  a.k_head_stride = k_head_stride; a.v_stride = v_stride; a.v_head_stride = v_head_stride;
+  a.scale = scale; a.window = window; a.out = out; a.lse = lse;
+  if (!nvfp4::prompt_attn_fits(a)) return NVFP4_EUNSUPPORTED;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  return hip_status(nvfp4::launch_prompt_attn(a, (hipStream_t)stream));
+}
+
+size_t nvfp4_paged_attn_workspace_size(int32_t seqs, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                       int32_t head_dim) {
+  if (seqs < 0 || tokens <= 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 8 ||
+      head_dim > 128)
+    return 0;
+  return nvfp4::paged_attn_workspace_bytes(seqs, tokens, q_heads, kv_heads, head_dim);
+}
+
+int32_t nvfp4_paged_attn(const void* q, int32_t dtype, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens, int32_t seqs,
+                         int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                         int64_t num_pages, int32_t max_pages, int64_t q_stride, int64_t q_head_stride,
+                         float scale, int32_t window, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int32_t st = attn_check(q, dtype, seqs, tokens, q_heads, kv_heads, head_dim, q_stride, q_head_stride,
+                                scale, window, out, lse);
+  if (st != NVFP4_OK) return st;
+  if (page_size < 1 || num_pages < 0 || max_pages < 0) return NVFP4_EINVAL;
+  if ((int64_t)max_pages * page_size > (1LL << 30) || num_pages > (1LL << 31)) return NVFP4_EUNSUPPORTED;
+  if (tokens == 0) return NVFP4_OK;
+  if (!cu_new || !aligned4(cu_new)) return NVFP4_EINVAL;
+  if (seqs > 0 && (!kv_lens || !aligned4(kv_lens))) return NVFP4_EINVAL;
+  if (seqs > 0 && max_pages > 0 && (!block_table || !aligned4(block_table))) return NVFP4_EINVAL;
+  if (num_pages > 0 && (!k_cache || !v_cache)) return NVFP4_EINVAL;
+  if ((((uintptr_t)k_cache | (uintptr_t)v_cache) % 16) != 0) return NVFP4_EINVAL;
+  const size_t need = nvfp4::paged_attn_workspace_bytes(seqs, tokens, q_heads, kv_heads, head_dim);
+  if (!workspace || workspace_bytes < need || !aligned256(workspace)) return NVFP4_EWORKSPACE;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::AttnArgs a{};
+  a.q = q; a.k = k_cache; a.v = v_cache; a.dtype = dtype; a.cu = cu_new; a.kv_lens = kv_lens;
+  a.block_table = block_table; a.seqs = seqs; a.tokens = (int)tokens; a.q_heads = q_heads;
+  a.kv_heads = kv_heads; a.head_dim = head_dim; a.page_size = page_size; a.max_pages = max_pages;
+  a.num_pages = num_pages; a.q_stride = q_stride; a.q_head_stride = q_head_stride; a.scale = scale;
+  a.window = window; a.out = out; a.lse = lse; a.workspace = workspace;
+  return hip_status(nvfp4::launch_paged_attn(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

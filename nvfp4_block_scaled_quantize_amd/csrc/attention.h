@@ -1,0 +1,61 @@
+// attention.h -- launcher interfaces of the serving attention operators.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace nvfp4 {
+
+struct PageMapsArgs {
+  const int32_t* ctx_lens;
+  const int32_t* new_lens;
+  int32_t* block_table;        // [seqs, max_pages], extended in place
+  const int32_t* free_pages;   // [num_free]
+  int seqs, max_pages, num_free, page_size;
+  int64_t tokens;              // entries of slot_map and positions
+  int32_t* cu_new;             // [seqs + 1]
+  int32_t* kv_lens;            // [seqs]
+  int64_t* slot_map;
+  int32_t* positions;
+  int32_t* taken;              // [1]
+};
+hipError_t launch_page_maps(const PageMapsArgs& a, hipStream_t s);
+
+struct KvWriteArgs {
+  const void* k;
+  const void* v;
+  int64_t tokens;
+  int kv_heads, head_dim;
+  int64_t k_stride, k_head_stride, v_stride, v_head_stride;   // elements
+  const int64_t* slot_map;
+  void* k_cache;
+  void* v_cache;
+  int page_size;
+  int64_t num_pages;
+};
+hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t s);
+
+struct AttnArgs {
+  const void* q;               // [tokens, q_heads, head_dim] by strides
+  const void* k;               // prompt: [tokens, kv_heads, head_dim] by strides; paged: the cache
+  const void* v;
+  int dtype;
+  const int32_t* cu;           // [seqs + 1] first token of each request
+  const int32_t* kv_lens;      // paged: [seqs]
+  const int32_t* block_table;  // paged: [seqs, max_pages]
+  int seqs, tokens, q_heads, kv_heads, head_dim;
+  int page_size, max_pages;
+  int64_t num_pages;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;   // elements
+  float scale;
+  int window;                  // 0: no window
+  void* out;                   // [tokens, q_heads, head_dim]
+  float* lse;                  // [tokens, q_heads] or null
+  void* workspace;             // paged
+};
+bool prompt_attn_fits(const AttnArgs& a);   // the grid
+hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s);
+size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int kv_heads, int head_dim);
+hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s);
+
+}  // namespace nvfp4

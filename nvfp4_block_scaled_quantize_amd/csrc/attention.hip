@@ -1,0 +1,1029 @@
+// attention.hip -- attention over whole packed prompts and attention of new
+// tokens over a paged key/value cache, for gfx950.
+//
+// Row i of a request's m new tokens over L keys sits at position p = L - m + i
+// and sees the keys j <= p, j > p - window (window > 0), j < L:
+//   s_j = scale * q . k_j,   out = sum_j e^{s_j} v_j / sum_j e^{s_j},
+//   lse = log sum_j e^{s_j};   a row that sees nothing: out = 0, lse = -inf.
+//
+// The query heads that share a key/value head are rows of one problem: row r
+// of a request is (token r / G, query head h G + r % G), G = q_heads /
+// kv_heads, so keys and values are read once for the group.
+//
+// One pass over the keys with a running maximum: with t_j = s_j log2 e,
+//   m' = max(m, t), l = l 2^{m - m'} + sum 2^{t_j - m'}, O = O 2^{m - m'} + ...
+// in binary32 throughout; only the weights 2^{t - m} are rounded to the
+// inputs' type, because the matrix cores multiply them with the values (l sums
+// the unrounded ones).  The maximum is kept while the new one exceeds it by
+// less than 2^8: the weights then reach at most 2^8, which neither type nor
+// the binary32 sums notice, and the rescaling of O is skipped for most tiles.
+//
+// Matrix operands (v_mfma_f32_32x32x16, lane = 32 h + c): the score tile is
+// formed transposed, S^T = K Q^T, so that a lane holds 16 of the 32 keys of
+// ONE row c.  Row maxima and sums are then in-lane (plus one exchange between
+// the half-waves), and the lane's weights, rounded and packed, are already
+// the B operand of O^T += V^T P^T: the key order inside a product may be any
+// as long as both operands share it, and V^T is read from the row-major tile
+// by the transposing LDS read in just that order.  m, l and the rescaling are
+// one value per lane.
+#include "attention.h"
+#include "internal.h"
+#include "device_common.h"
+#include "lds_dma.h"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
+
+__device__ const uint4 kZeros[1] = {{0u, 0u, 0u, 0u}};   // rows that do not exist are copied from here
+
+template <int DT>
+__device__ __forceinline__ v16f mfma(v8s a, v8s b, v16f c) {
+  if constexpr (DT == kBf16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// Rounds to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (DT == kBf16) {
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){x, y}, v2b));
+  } else {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){x, y}, v2h));
+  }
+}
+
+// Value of the lane in the other half of the wave.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+
+// Wave-uniform values, kept in scalar registers.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uni64(int64_t v) {
+  return (int64_t)(((uint64_t)(uint32_t)uni((int)(v >> 32)) << 32) | (uint32_t)uni((int)v));
+}
+
+// ---------------------------------------------------------------- LDS tiles
+// A tile is rows of DP elements; 16-byte chunk p of row r holds chunk p ^
+// swz(r) of the row.  swz makes both reads conflict-free: eight consecutive
+// rows get eight different values (the b128 reads of K, one row per lane),
+// and rows 0..3 modulo 4 differ in the bits above the lowest (the transposing
+// reads of V, 32 bytes of each of four rows).
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
+
+template <int DP>
+__device__ __forceinline__ int chunk_at(int row, int chunk) {
+  return row * (DP * 2) + ((chunk ^ (swz(row) & (DP / 8 - 1))) * 16);
+}
+
+// Row `row` of V^T: four keys row..row+3 for the 16 values of d in
+// 16 dblk .. 16 dblk + 15, one d per lane of a 16-lane group.
+template <int DP>
+__device__ __forceinline__ uint32_t tr_at(int row, int dblk, int i) {
+  const int r = row + (i >> 2), chunk = dblk * 2 + ((i & 3) >> 1);
+  return (uint32_t)(chunk_at<DP>(r, chunk) + (i & 1) * 8);
+}
+
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+__device__ __forceinline__ v4s read_tr(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(uintptr_t)at);
+}
+__device__ __forceinline__ v8s read_b128(uint32_t at) {
+  return *(__attribute__((address_space(3))) v8s*)(uintptr_t)at;
+}
+
+// ---------------------------------------------------------------- sources
+// Where the keys and values of one (request, key/value head) are.
+struct Source {
+  const char* k;         // prompt: first row; paged: the cache at this head
+  const char* v;
+  int64_t k_step, v_step;   // prompt: bytes from key to key; paged: bytes from page to page (k_step)
+  const int32_t* table;  // paged: the request's row of the block table
+  int page_size;
+  uint32_t magic;        // paged: key / page_size as a multiply-high (see page_magic)
+  int shift;
+  int64_t num_pages;
+  int keys;              // keys that exist
+  int d_bytes;           // bytes of a row
+};
+
+// floor(j / d) = (j * magic) >> (32 + shift) for 0 <= j < 2^31, 2 <= d < 2^31:
+// magic = ceil(2^(32+shift) / d), shift = ceil(log2 d) - 1; d = 1 has magic 0.
+__device__ __forceinline__ int page_of(const Source& s, int j) {
+  return s.magic ? (int)(__umulhi((uint32_t)j, s.magic) >> s.shift) : j;
+}
+
+template <bool PAGED>
+__device__ __forceinline__ void row_at(const Source& s, int j, int page, int chunk_bytes, const char*& k, const char*& v) {
+  const char* zero = reinterpret_cast<const char*>(kZeros);
+  bool there = j < s.keys && chunk_bytes < s.d_bytes;
+  if constexpr (PAGED) {
+    there = there && (uint32_t)page < (uint64_t)s.num_pages;
+    const int64_t off = (int64_t)page * s.k_step + (int64_t)(j - page_of(s, j) * s.page_size) * s.d_bytes + chunk_bytes;
+    k = there ? s.k + off : zero;
+    v = there ? s.v + off : zero;
+  } else {
+    k = there ? s.k + (int64_t)j * s.k_step + chunk_bytes : zero;
+    v = there ? s.v + (int64_t)j * s.v_step + chunk_bytes : zero;
+  }
+}
+
+// ---------------------------------------------------------------- one tile
+// State of QT x 32 rows of one wave.
+template <int DP, int QT>
+struct Rows {
+  v8s q[QT][DP / 16];      // B operand: lane's row, d = 16 s + 8 h ..
+  v16f o[QT][DP / 32];     // O^T: d = 32 t + 8 (i / 4) + 4 h + i % 4
+  float m[QT], l[QT];      // l: this half-wave's keys only
+  int lo[QT], hi[QT];      // the row sees the keys lo <= j < hi
+};
+
+// NaN and infinities in a value that a row does not see must not reach it,
+// but 0 * inf would.  In tiles with a mask whose values are not all finite,
+// the products take the values with the non-finite ones replaced by 0, and
+// whether a row sees a non-finite value of a column (+inf, -inf or NaN) is
+// counted by three more products with the mask as weights.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite_bits() { return DT == kBf16 ? 0x7F80u : 0x7C00u; }
+
+template <int DT>
+__device__ __forceinline__ short one_bits() { return DT == kBf16 ? (short)0x3F80 : (short)0x3C00; }
+
+// kind 0: the value if finite, else 0; 1, 2, 3: 1 where it is +inf, -inf, NaN.
+template <int DT>
+__device__ __forceinline__ v8s classify(v8s v, int kind) {
+  v8s r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t x = (uint16_t)v[e], lim = not_finite_bits<DT>(), mag = x & 0x7FFFu;
+    const bool yes = kind == 1 ? x == lim : kind == 2 ? x == (lim | 0x8000u) : mag > lim;
+    r[e] = kind == 0 ? (mag >= lim ? (short)0 : v[e]) : (yes ? one_bits<DT>() : (short)0);
+  }
+  return r;
+}
+
+// Adds the keys kb .. kb + 32 KT - 1 of the tile at LDS addresses kt_lds,
+// vt_lds (rows of DP) to the rows' state.  MASK: some row does not see some
+// key of the tile.
+template <int DT, int DP, int QT, int KT, bool MASK>
+__device__ __forceinline__ void add_tile(Rows<DP, QT>& w, uint32_t kt_lds, uint32_t vt_lds, int kb, float c, int lane) {
+  const int h = lane >> 5, col = lane & 31;
+  v16f s[QT][KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[qt][kt][i] = 0.0f;
+#pragma unroll
+    for (int st = 0; st < DP / 16; ++st) {
+      const v8s kf = read_b128(kt_lds + chunk_at<DP>(col, 2 * st + h) + kt * 32 * DP * 2);
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) s[qt][kt] = mfma<DT>(kf, w.q[qt][st], s[qt][kt]);
+    }
+  }
+  v8s p[QT][KT][2];
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    if constexpr (MASK) {
+      const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = kt * 32 + 8 * (i / 4) + i % 4;
+          if (key < lo || key >= hi) s[qt][kt][i] = -__builtin_inff();
+        }
+    }
+    float top = s[qt][0][0];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[qt][kt][i]);
+    top = __builtin_fmaxf(top, other_half(top)) * c;
+    if (__any(top > w.m[qt] + kKeep)) {
+      const float m = __builtin_fmaxf(w.m[qt], top);
+      const float a = m == w.m[qt] ? 1.0f : __builtin_amdgcn_exp2f(w.m[qt] - m);
+      w.m[qt] = m;
+      w.l[qt] *= a;
+#pragma unroll
+      for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w.o[qt][t][i] *= a;
+    }
+    // nothing seen so far: every weight is 2^(-inf) = 0
+    const float m = w.m[qt] == -__builtin_inff() ? 0.0f : w.m[qt];
+    float l = 0.0f;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = half * 8 + e * 2;
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][kt][i], c, -m));
+          const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][kt][i + 1], c, -m));
+          l += x;
+          l += y;
+          d[e] = pack2<DT>(x, y);
+        }
+        p[qt][kt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
+      }
+    w.l[qt] += l;
+  }
+  // O^T += V^T P^T; element e of a value fragment: key 16 half + 4 h + e (e < 4),
+  // 16 half + 8 + 4 h + e - 4 -- the order of p
+  const int g = (lane >> 4) & 1, i16 = lane & 15;
+  auto value = [&](int kt, int half, int t) {
+    const v4s a = read_tr(vt_lds + tr_at<DP>(4 * h, 2 * t + g, i16) + (kt * 32 + half * 16) * DP * 2);
+    const v4s b = read_tr(vt_lds + tr_at<DP>(8 + 4 * h, 2 * t + g, i16) + (kt * 32 + half * 16) * DP * 2);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  if constexpr (MASK) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const v8s v = value(kt, half, t);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t mag = (uint16_t)v[e] & 0x7FFFu;
+            big = mag > big ? mag : big;
+          }
+        }
+    if (__any(big >= not_finite_bits<DT>())) {
+#pragma unroll 1
+      for (int kind = 0; kind < 4; ++kind) {
+#pragma unroll
+        for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+          for (int qt = 0; qt < QT; ++qt) {
+            v16f n;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) n[i] = kind == 0 ? w.o[qt][t][i] : 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const v8s v = classify<DT>(value(kt, half, t), kind);
+                const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
+                v8s weight = p[qt][kt][half];
+                if (kind != 0) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const int key = kt * 32 + 16 * half + 8 * (e / 4) + e % 4;
+                    weight[e] = key >= lo && key < hi ? one_bits<DT>() : (short)0;
+                  }
+                }
+                n = mfma<DT>(v, weight, n);
+              }
+            const float bad = kind == 1 ? __builtin_inff() : kind == 2 ? -__builtin_inff() : __builtin_nanf("");
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              w.o[qt][t][i] = kind == 0 ? n[i] : (n[i] > 0.0f ? w.o[qt][t][i] + bad : w.o[qt][t][i]);
+          }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const v8s v = value(kt, half, t);
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) w.o[qt][t] = mfma<DT>(v, p[qt][kt][half], w.o[qt][t]);
+      }
+}
+
+// ---------------------------------------------------------------- items
+// One (request, block of rows, key/value head).
+struct Item {
+  int start;      // request's first token
+  int news;       // its new tokens
+  int keys;       // its keys
+  int head;       // key/value head
+  int row0;       // first row of the block
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Loads the rows row0 .. of a wave; rows past the request's last take the last
+// one's limits and zero queries.
+template <int DP, int QT>
+__device__ __forceinline__ void load_rows(Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
+  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int h = lane >> 5, col = lane & 31;
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    const int r = row0 + qt * 32 + col;
+    const int tok = (r < rows ? r : rows - 1) / group, hd = it.head * group + r % group;
+    const char* q = (const char*)a.q + ((int64_t)(it.start + tok) * a.q_stride + (int64_t)hd * a.q_head_stride) * 2;
+#pragma unroll
+    for (int st = 0; st < DP / 16; ++st) {
+      const int ch = 2 * st + h;
+      v8s x = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (r < rows && ch * 8 < a.head_dim) x = *(const v8s*)(q + ch * 16);
+      w.q[qt][st] = x;
+    }
+    const int p = it.keys - it.news + tok;
+    w.hi[qt] = p + 1;
+    w.lo[qt] = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
+    w.m[qt] = -__builtin_inff();
+    w.l[qt] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w.o[qt][t][i] = 0.0f;
+  }
+}
+
+// Writes finished rows.
+template <int DT, int DP, int QT>
+__device__ __forceinline__ void store_rows(const Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
+  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int h = lane >> 5, col = lane & 31;
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    const float l = w.l[qt] + other_half(w.l[qt]);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int r = row0 + qt * 32 + col;
+    if (r >= rows) continue;
+    const int64_t at = (int64_t)(it.start + r / group) * a.q_heads + it.head * group + r % group;
+    uint32_t* out = (uint32_t*)a.out + at * (a.head_dim / 2);
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = t * 32 + 8 * i + 4 * h;
+        if (d < a.head_dim) {
+          const u32x2 x = {pack2<DT>(w.o[qt][t][4 * i] * inv, w.o[qt][t][4 * i + 1] * inv),
+                           pack2<DT>(w.o[qt][t][4 * i + 2] * inv, w.o[qt][t][4 * i + 3] * inv)};
+          *(u32x2*)(out + d / 2) = x;
+        }
+      }
+    if (a.lse && h == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (w.m[qt] + __builtin_log2f(l)) * kLn2;
+  }
+}
+
+// Parts of rows whose keys are split over workgroups: O (unnormalized), m, l.
+struct Part {
+  float* o;    // [slots][rows][DP]
+  float* ml;   // [slots][rows][2]
+};
+
+template <int DP, int QT>
+__device__ __forceinline__ void store_part(const Rows<DP, QT>& w, float* o, float* ml, int row0, int rows, int lane) {
+  const int h = lane >> 5, col = lane & 31;
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    const float l = w.l[qt] + other_half(w.l[qt]);
+    const int r = row0 + qt * 32 + col;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(v4f*)(o + (int64_t)r * DP + t * 32 + 8 * i + 4 * h) =
+            (v4f){w.o[qt][t][4 * i], w.o[qt][t][4 * i + 1], w.o[qt][t][4 * i + 2], w.o[qt][t][4 * i + 3]};
+    if (h == 0) *(v2f*)(ml + 2 * r) = (v2f){w.m[qt], l};
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+// A workgroup of NW waves, QT x 32 rows each; all waves share the tiles of 64
+// keys, copied global -> LDS one tile ahead (two buffers, one barrier a tile).
+constexpr int kTile = 64;
+
+template <int DP, int NW, bool PAGED>
+struct TileCopy {
+  static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
+  static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
+  static constexpr int kIters = kTile / (kRowsPer * NW);    // copies of each of K and V, per wave
+  static_assert(kIters >= 1, "tile too small for the waves");
+  int page[PAGED ? kIters : 1];
+
+  __device__ __forceinline__ static int row_of(int it, int wave, int lane) {
+    return (it * NW + wave) * kRowsPer + lane / kChunks;
+  }
+  // Page ids of the tile at key kb (waited for when the copies are issued).
+  __device__ __forceinline__ void pages(const Source& s, int kb, int wave, int lane) {
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int j = kb + row_of(it, wave, lane);
+        page[it] = j < s.keys ? s.table[page_of(s, j)] : -1;
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(const Source& s, int kb, uint32_t k_lds, uint32_t v_lds, int wave, int lane) {
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int r = row_of(it, wave, lane);
+      const int chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
+      const char *k, *v;
+      row_at<PAGED>(s, kb + r, PAGED ? page[it] : 0, chunk * 16, k, v);
+      const uint32_t at = (uint32_t)uni((it * NW + wave) * 1024);
+      dma16_at(k, k_lds + at);
+      dma16_at(v, v_lds + at);
+    }
+  }
+};
+
+template <int DP>
+constexpr int tile_bytes() { return kTile * DP * 2; }
+
+// Runs the keys of tiles [t0, t1) (tiles of 64 from key 0) through the block.
+template <int DT, int DP, int QT, int NW, bool PAGED>
+__device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, const Item& it, int t0, int t1,
+                                          Rows<DP, QT>& w, uint32_t lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int first = it.row0 + wave * QT * 32;
+  load_rows<DP, QT>(w, a, it, first, lane);
+  // limits of the wave's rows: positions of its first and last row
+  const bool active = first < rows;
+  const int end = first + QT * 32 < rows ? first + QT * 32 : rows;
+  const int p0 = it.keys - it.news + first / group, p1 = it.keys - it.news + (end - 1) / group;
+  const int hi_min = p0 + 1, hi_max = p1 + 1;
+  const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
+  const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
+  const float c = a.scale * kLog2e;
+  TileCopy<DP, NW, PAGED> cp;
+  constexpr int kBytes = tile_bytes<DP>();
+  if (t0 < t1) {
+    cp.pages(s, t0 * kTile, wave, lane);
+    cp.issue(s, t0 * kTile, lds, lds + kBytes, wave, lane);
+    if (t0 + 1 < t1) cp.pages(s, (t0 + 1) * kTile, wave, lane);
+  }
+  for (int t = t0; t < t1; ++t) {
+    const uint32_t buf = lds + ((t - t0) & 1) * (2 * kBytes);
+    wait_vmcnt_le<0>();
+    lds_barrier();
+    if (t + 1 < t1) {
+      const uint32_t nxt = lds + ((t + 1 - t0) & 1) * (2 * kBytes);
+      cp.issue(s, (t + 1) * kTile, nxt, nxt + kBytes, wave, lane);
+      if (t + 2 < t1) cp.pages(s, (t + 2) * kTile, wave, lane);
+    }
+    const int kb = t * kTile;
+    if (!active || kb >= hi_max || kb + kTile <= lo_min) continue;
+    if (kb + kTile > hi_min || kb < lo_max)
+      add_tile<DT, DP, QT, kTile / 32, true>(w, buf, buf + kBytes, kb, c, lane);
+    else
+      add_tile<DT, DP, QT, kTile / 32, false>(w, buf, buf + kBytes, kb, c, lane);
+  }
+  lds_barrier();   // the buffers may be filled again
+}
+
+// Tiles of `unit` keys that the rows row0 .. row0 + block - 1 see.
+__device__ __forceinline__ void tiles_of(const AttnArgs& a, const Item& it, int row0, int block, int unit, int& t0, int& t1) {
+  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int end = row0 + block < rows ? row0 + block : rows;
+  const int p0 = it.keys - it.news + row0 / group, p1 = it.keys - it.news + (end - 1) / group;
+  const int lo = (a.window > 0 && p0 + 1 > a.window) ? p0 + 1 - a.window : 0;
+  t0 = lo / unit;
+  t1 = p1 + 1 > 0 ? (p1 + unit) / unit : 0;
+  if (t1 < t0) t1 = t0;
+}
+
+extern __shared__ __align__(1024) unsigned char dyn_lds[];
+
+// Whole prompts.  Workgroup (b, h): b counts blocks of rows over all requests.
+// Request i owns the blocks f(i) .. f(i + 1) - 1 with f(i) = floor(cu_i G /
+// rows) + i, which are at least as many as it needs and are known without the
+// lengths on the host; the surplus workgroups end at once.  Request `seqs` is
+// what follows the last prompt, rows without keys, which are set to 0.  A
+// prompt's longest rows come first, and key/value heads are the fastest
+// index, so that workgroups on one XCD (dispatched round robin) share a head.
+template <int DT, int DP, int QT, int NW>
+__global__ void __launch_bounds__(64 * NW, QT == 2 ? 1 : 2) prompt_attn_kernel(AttnArgs a) {
+  __shared__ int found;
+  constexpr int kRows = 32 * QT * NW;
+  const int tid = threadIdx.x;
+  const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
+  const int group = a.q_heads / a.kv_heads;
+  if (tid == 0) found = 0;
+  __syncthreads();
+  int n = 0;
+  for (int i = tid; i <= a.seqs; i += 64 * NW)
+    n += (int64_t)clampi(a.cu[i], 0, a.tokens) * group / kRows + i <= b ? 1 : 0;
+  if (n) atomicAdd(&found, n);
+  __syncthreads();
+  const int req = uni(found) - 1;
+  if (req < 0) return;
+  const int start = clampi(uni(a.cu[req]), 0, a.tokens);
+  const int stop = req < a.seqs ? clampi(uni(a.cu[req + 1]), start, a.tokens) : a.tokens;
+  const int news = stop - start;
+  const int blocks = (int)(((int64_t)news * group + kRows - 1) / kRows);
+  const int rb = b - (int)((int64_t)start * group / kRows + req);
+  if (rb < 0 || rb >= blocks) return;
+  Item it{start, news, news, head, (blocks - 1 - rb) * kRows};
+  Source s{};
+  s.k = (const char*)a.k + ((int64_t)start * a.k_stride + (int64_t)head * a.k_head_stride) * 2;
+  s.v = (const char*)a.v + ((int64_t)start * a.v_stride + (int64_t)head * a.v_head_stride) * 2;
+  s.k_step = a.k_stride * 2;
+  s.v_step = a.v_stride * 2;
+  s.keys = news;
+  s.d_bytes = a.head_dim * 2;
+  int t0 = 0, t1 = 0;
+  if (req < a.seqs) tiles_of(a, it, it.row0, kRows, kTile, t0, t1);
+  Rows<DP, QT> w;
+  run_block<DT, DP, QT, NW, false>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
+  store_rows<DT, DP, QT>(w, a, it, it.row0 + uni(tid >> 6) * QT * 32, tid & 63);
+}
+
+// ---------------------------------------------------------------- paged: work split
+// The work of a call is the sequence of units (request, head, block of rows,
+// tile of keys), tiles innermost, and every workgroup takes an equal share of
+// consecutive units: long and short requests balance whatever their lengths,
+// which only the device knows.  A share that starts or ends inside an item
+// leaves a part (O, m, l) in the workspace, and combine_kernel joins the parts.
+// Each workgroup sums the units of all requests itself (one load and one scan
+// for up to 256 requests), which is cheaper than another launch.
+struct Split {
+  int block;      // rows of a block
+  int unit;       // keys of a unit
+  int min_rows;   // requests with min_rows <= rows <= max_rows take part
+  int max_rows;
+  int shares;     // workgroups
+};
+
+struct Req {
+  int start, news, keys, t0, tiles, blocks;
+  int64_t units;   // of one head
+};
+
+__device__ __forceinline__ Req request(const AttnArgs& a, const Split& sp, int i) {
+  Req r;
+  r.start = clampi(a.cu[i], 0, a.tokens);
+  const int stop = i < a.seqs ? clampi(a.cu[i + 1], r.start, a.tokens) : a.tokens;
+  r.news = stop - r.start;
+  r.keys = 0;
+  if (i < a.seqs) {
+    const int64_t most = (int64_t)a.max_pages * a.page_size;
+    r.keys = a.kv_lens[i];
+    if (r.keys < 0) r.keys = 0;
+    if (r.keys > most) r.keys = (int)most;
+  }
+  const int group = a.q_heads / a.kv_heads;
+  const int64_t rows = (int64_t)r.news * group;
+  r.units = 0;
+  r.t0 = r.tiles = r.blocks = 0;
+  if (rows >= sp.min_rows && rows <= sp.max_rows && rows > 0) {
+    const int p = r.keys - r.news;   // position of the first row
+    const int lo = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
+    r.t0 = lo / sp.unit;
+    const int t1 = (r.keys + sp.unit - 1) / sp.unit;
+    r.tiles = t1 > r.t0 ? t1 - r.t0 : 1;   // a request without keys still has its rows written
+    r.blocks = (int)((rows + sp.block - 1) / sp.block);
+    r.units = (int64_t)r.blocks * r.tiles;
+  }
+  return r;
+}
+
+struct Place {
+  int req;          // request, seqs + 1 if past the end
+  int64_t before;   // units before this request (all heads)
+  int64_t total;
+  int64_t share;    // units of a share
+};
+
+// Finds the request of unit `u` (or of the first unit of share `w`).
+template <int NT>
+__device__ __forceinline__ Place find_place(const AttnArgs& a, const Split& sp, int w, int64_t* lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = a.seqs + 1, per = (n + NT - 1) / NT;
+  const int i0 = tid * per, i1 = i0 + per < n ? i0 + per : n;
+  int64_t v = 0;
+  for (int i = i0; i < i1; ++i) v += request(a, sp, i).units;
+  v *= a.kv_heads;
+  int64_t x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63) lds[wave] = x;
+  if (tid == 0) lds[NT / 64] = -1;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 64; ++k) {
+    if (k < wave) before += lds[k];
+    total += lds[k];
+  }
+  before += x - v;
+  Place p;
+  p.total = total;
+  p.share = (total + sp.shares - 1) / sp.shares;
+  if (p.share < 1) p.share = 1;
+  const int64_t u = p.share * w;
+  if (u >= before && u < before + v) {
+    for (int i = i0; i < i1; ++i) {
+      const int64_t r = request(a, sp, i).units * a.kv_heads;
+      if (u < before + r) {
+        lds[NT / 64] = i;
+        lds[NT / 64 + 1] = before;
+        break;
+      }
+      before += r;
+    }
+  }
+  __syncthreads();
+  p.total = uni64(p.total);
+  p.share = uni64(p.share);
+  p.req = uni((int)lds[NT / 64]);
+  p.before = uni64(lds[NT / 64 + 1]);
+  if (p.req < 0) p.req = n;
+  return p;
+}
+
+// Segment of a share: the tiles [t0, t1) of one item.
+struct Segment {
+  Item it;
+  int req, t0, t1, tiles, tile_base;
+};
+
+template <int DP, int ROWS>
+__device__ __forceinline__ void part_of(float* ws, int shares, int slot, float*& o, float*& ml) {
+  ml = ws + (int64_t)slot * ROWS * 2;
+  o = ws + (int64_t)shares * 2 * ROWS * 2 + (int64_t)slot * ROWS * DP;
+}
+
+__device__ __forceinline__ void paged_source(const AttnArgs& a, const Item& it, int req, Source& s, uint32_t magic, int shift) {
+  const int64_t head = (int64_t)a.page_size * a.head_dim * 2;
+  s.k = (const char*)a.k + it.head * head;
+  s.v = (const char*)a.v + it.head * head;
+  s.k_step = s.v_step = head * a.kv_heads;
+  s.table = a.block_table + (int64_t)(req < a.seqs ? req : 0) * a.max_pages;
+  s.page_size = a.page_size;
+  s.magic = magic;
+  s.shift = shift;
+  s.num_pages = a.num_pages;
+  s.keys = it.keys;
+  s.d_bytes = a.head_dim * 2;
+}
+
+// Walks the segments of share w; f(segment, slot or -1).
+template <int NT, typename F>
+__device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp, int w, int64_t* lds, F f) {
+  const Place pl = find_place<NT>(a, sp, w, lds);
+  int64_t u = pl.share * w;
+  int64_t end = u + pl.share < pl.total ? u + pl.share : pl.total;
+  const int64_t begin = u;
+  int64_t before = pl.before;
+  for (int req = pl.req; req <= a.seqs && u < end; ++req) {
+    const Req r = request(a, sp, req);
+    const int64_t all = r.units * a.kv_heads;
+    while (u < end && u < before + all) {
+      const int64_t in = u - before;
+      const int head = (int)(in / r.units);
+      const int64_t rest = in - head * r.units;
+      const int rb = (int)(rest / r.tiles), tile = (int)(rest - (int64_t)rb * r.tiles);
+      const int64_t left = end - u;
+      const int count = left < r.tiles - tile ? (int)left : r.tiles - tile;
+      Segment g;
+      g.it = Item{r.start, r.news, r.keys, head, rb * sp.block};
+      g.req = req;
+      g.t0 = r.t0 + tile;
+      g.t1 = g.t0 + count;
+      // no key at all: the unit only writes the rows
+      if (r.keys == 0) g.t1 = g.t0;
+      const bool whole = tile == 0 && count == r.tiles;
+      f(g, whole ? -1 : 2 * w + (u > begin ? 1 : 0));
+      u += count;
+    }
+    before += all;
+  }
+}
+
+// ---------------------------------------------------------------- paged: many rows
+template <int DT, int DP, int QT, int NW>
+__global__ void __launch_bounds__(64 * NW, QT == 2 ? 1 : 2)
+paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
+  __shared__ int64_t lds[NW + 2];
+  constexpr int kRows = 32 * QT * NW;
+  const int per = sp.shares / 8;   // shares is a multiple of 8: an XCD takes consecutive shares
+  const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  for_segments<64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+    Source s;
+    paged_source(a, g.it, g.req, s, magic, shift);
+    int b0, b1;
+    tiles_of(a, g.it, g.it.row0, kRows, kTile, b0, b1);
+    const int t0 = uni(g.t0 > b0 ? g.t0 : b0), t1 = uni(g.t1 < b1 ? g.t1 : b1);
+    Rows<DP, QT> rows;
+    run_block<DT, DP, QT, NW, true>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
+    const int row = uni(threadIdx.x >> 6) * QT * 32, lane = threadIdx.x & 63;
+    if (slot < 0) {
+      store_rows<DT, DP, QT>(rows, a, g.it, g.it.row0 + row, lane);
+    } else {
+      float *o, *ml;
+      part_of<DP, kRows>((float*)a.workspace, sp.shares, slot, o, ml);
+      store_part<DP, QT>(rows, o, ml, row, kRows, lane);
+    }
+  });
+}
+
+// ---------------------------------------------------------------- paged: few rows
+// Up to 32 rows of an item (decode steps: the heads of a group, a few tokens).
+// Nothing is shared between waves but the queries: wave w takes the 32-key
+// tiles w, w + NW, ... and copies them itself, two tiles ahead, without a
+// barrier; the waves' states are joined at the end.  Page ids come from a
+// window of the block table in LDS, so that the copies in flight are not
+// waited for together with a page id.
+constexpr int kWindow = 256;   // page ids a wave keeps
+
+template <int DT, int DP, int NW>
+__global__ void __launch_bounds__(64 * NW, 1)
+paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
+  __shared__ int64_t lds[NW + 2];
+  __shared__ int win[NW][kWindow];
+  __shared__ float join_ml[NW][32][2];
+  constexpr int kChunks = DP / 8, kRowsPer = 64 / kChunks, kIters = 32 / kRowsPer;
+  constexpr int kStage = 2 * 32 * DP * 2;   // bytes of one tile of K and V
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const uint32_t mem = lds_addr(dyn_lds) + wave * 2 * kStage;
+  float* join_o = (float*)dyn_lds;          // [NW][32][DP] after the copies
+  const int per = sp.shares / 8;
+  const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  for_segments<64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+    Source s;
+    paged_source(a, g.it, g.req, s, magic, shift);
+    const int group = a.q_heads / a.kv_heads, rows = g.it.news * group;
+    const int last = (g.it.row0 + 32 < rows ? g.it.row0 + 32 : rows) - 1;
+    const int p0 = g.it.keys - g.it.news + g.it.row0 / group, p1 = g.it.keys - g.it.news + last / group;
+    const int hi_min = p0 + 1, hi_max = p1 + 1;
+    const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
+    const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
+    const float c = a.scale * kLog2e;
+    const int n = g.t1 - g.t0;
+    int win0 = 0, win1 = 0;   // pages held
+    auto issue = [&](int t) {
+      const int kb = ((g.t0 + t) * NW + wave) * 32;
+      if (kb >= s.keys) {   // nothing there: keep the count of copies
+        const uint32_t to = mem + (t & 1) * kStage;
+#pragma unroll
+        for (int it = 0; it < 2 * kIters; ++it) dma16_at(kZeros, to + it * 1024);
+        return;
+      }
+      const int first = page_of(s, kb), end = page_of(s, kb + 31 < s.keys ? kb + 31 : s.keys - 1) + 1;
+      if (first < win0 || end > win1) {
+        win0 = first;
+        win1 = first + kWindow;
+        for (int k = lane; k < kWindow; k += 64) win[wave][k] = first + k < a.max_pages ? s.table[first + k] : -1;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+      const uint32_t to = mem + (t & 1) * kStage;
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int r = it * kRowsPer + lane / kChunks, j = kb + r;
+        const int chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
+        const int pg = j < s.keys ? win[wave][page_of(s, j) - win0] : -1;
+        const char *k, *v;
+        row_at<true>(s, j, pg, chunk * 16, k, v);
+        dma16_at(k, to + it * 1024);
+        dma16_at(v, to + 32 * DP * 2 + it * 1024);
+      }
+    };
+    Rows<DP, 1> st;
+    load_rows<DP, 1>(st, a, g.it, g.it.row0, lane);
+    if (n > 0) issue(0);
+    if (n > 1) issue(1);
+    for (int t = 0; t < n; ++t) {
+      if (t + 1 < n) wait_vmcnt_le<2 * kIters>();
+      else wait_vmcnt_le<0>();
+      asm volatile("" ::: "memory");
+      const int kb = ((g.t0 + t) * NW + wave) * 32;
+      const uint32_t at = mem + (t & 1) * kStage;
+      if (kb < hi_max && kb + 32 > lo_min) {
+        if (kb + 32 > hi_min || kb < lo_max) add_tile<DT, DP, 1, 1, true>(st, at, at + 32 * DP * 2, kb, c, lane);
+        else add_tile<DT, DP, 1, 1, false>(st, at, at + 32 * DP * 2, kb, c, lane);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (t + 2 < n) issue(t + 2);
+    }
+    // join the waves: weights 2^(m_w - m)
+    const int h = lane >> 5, col = lane & 31;
+    const float l = st.l[0] + other_half(st.l[0]);
+    if (h == 0) { join_ml[wave][col][0] = st.m[0]; join_ml[wave][col][1] = l; }
+    __syncthreads();
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int k = 0; k < NW; ++k) m = __builtin_fmaxf(m, join_ml[k][col][0]);
+    const float mine = st.m[0] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.m[0] - m);
+    // a row stored from bank 4 col on: the 32 rows of a store take all banks in turn
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v4f x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mine == 0.0f ? 0.0f : st.o[0][t][4 * i + e] * mine;
+        const int q = t * 8 + 2 * i + h;
+        *(v4f*)(join_o + (wave * 32 + col) * DP + ((q ^ (col & (DP / 4 - 1))) * 4)) = x;
+      }
+    __syncthreads();
+    // thread: one row's four values of d at a time
+    float *po = nullptr, *pml = nullptr;
+    if (slot >= 0) part_of<DP, 32>((float*)a.workspace, sp.shares, slot, po, pml);
+    for (int k = tid; k < 32 * (DP / 4); k += 64 * NW) {
+      const int r = k / (DP / 4), q = k % (DP / 4), row = g.it.row0 + r;
+      if (row >= rows) continue;
+      float mm = -__builtin_inff();
+#pragma unroll
+      for (int x = 0; x < NW; ++x) mm = __builtin_fmaxf(mm, join_ml[x][r][0]);
+      float ll = 0.0f;
+      v4f o = {0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        const float mx = join_ml[x][r][0];
+        const float wx = mx == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
+        ll += wx == 0.0f ? 0.0f : join_ml[x][r][1] * wx;
+        const v4f y = *(const v4f*)(join_o + (x * 32 + r) * DP + ((q ^ (r & (DP / 4 - 1))) * 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += y[e];
+      }
+      if (slot < 0) {
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        const int64_t at = (int64_t)(g.it.start + row / group) * a.q_heads + g.it.head * group + row % group;
+        if (q * 4 < a.head_dim)
+          *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
+              (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+        if (a.lse && q == 0) a.lse[at] = ll == 0.0f ? -__builtin_inff() : (mm + __builtin_log2f(ll)) * kLn2;
+      } else {
+        *(v4f*)(po + (int64_t)r * DP + q * 4) = o;
+        if (q == 0) *(v2f*)(pml + 2 * r) = (v2f){mm, ll};
+      }
+    }
+    __syncthreads();   // join_o is the next segment's tile memory
+  });
+}
+
+// ---------------------------------------------------------------- paged: join the parts
+// Workgroup w: the item that share w's first unit lies inside of, if no
+// earlier share starts inside it too.  Its parts are the last segment of share
+// w - 1 and the first segments of the shares from w on.
+template <int DT, int DP, int ROWS>
+__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
+  __shared__ int64_t lds[6];
+  const int w = blockIdx.x + 1, tid = threadIdx.x;
+  const Place pl = find_place<256>(a, sp, w, lds);
+  if (pl.req > a.seqs) return;
+  const Req r = request(a, sp, pl.req);
+  const int64_t in = pl.share * w - pl.before;
+  const int64_t item = in / r.tiles;                         // (head, block) in this request
+  const int64_t s0 = pl.before + item * r.tiles, s1 = s0 + r.tiles;
+  if (s0 == pl.share * w || s0 < pl.share * (w - 1)) return;
+  const int last = (int)((s1 + pl.share - 1) / pl.share) - 1;
+  const int head = (int)(item / r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
+  const int group = a.q_heads / a.kv_heads, rows = r.news * group;
+  const int first_slot = 2 * (w - 1) + (s0 > pl.share * (w - 1) ? 1 : 0);
+  constexpr int kQ = DP / 4;
+  const int row = blockIdx.y * (256 / kQ) + tid / kQ, q = tid % kQ;
+  const int gr = rb * ROWS + row;
+  if (row >= ROWS || gr >= rows) return;
+  float m = -__builtin_inff(), l = 0.0f;
+  v4f o = {0, 0, 0, 0};
+  for (int j = w - 1; j <= last; ++j) {
+    float *po, *pml;
+    part_of<DP, ROWS>((float*)a.workspace, sp.shares, j == w - 1 ? first_slot : 2 * j, po, pml);
+    const v2f ml = *(const v2f*)(pml + 2 * row);
+    const v4f x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
+    if (ml[0] == -__builtin_inff()) continue;
+    const float nm = __builtin_fmaxf(m, ml[0]);
+    const float u = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(ml[0] - nm);
+    l = l * u + ml[1] * v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = o[e] * u + x[e] * v;
+    m = nm;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t at = (int64_t)(r.start + gr / group) * a.q_heads + head * group + gr % group;
+  if (q * 4 < a.head_dim)
+    *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
+        (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+  if (a.lse && q == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kShares = 256;        // one workgroup on each of the 256 CUs
+constexpr int kFewRows = 32;
+constexpr int kManyWaves = 8, kManyTiles = 1;
+constexpr int kManyRows = 32 * kManyTiles * kManyWaves;
+
+int padded_dim(int d) { return d <= 64 ? 64 : 128; }
+
+void page_magic(int page, uint32_t& magic, int& shift) {
+  magic = 0;
+  shift = 0;
+  if (page <= 1) return;
+  int up = 0;
+  while ((1ll << up) < page) ++up;
+  shift = up - 1;
+  magic = (uint32_t)(((1ull << (32 + shift)) + page - 1) / page);
+}
+
+// Which of the two kernels a call can need: a request of more than kFewRows
+// rows needs more than one token per request on average or a group of heads
+// above kFewRows; where one request makes the call, its size is known.
+bool needs_many(int64_t seqs, int64_t tokens, int group) {
+  if (tokens <= seqs) return false;
+  return tokens * group > kFewRows;
+}
+bool needs_few(int64_t seqs, int64_t tokens, int group) {
+  if (!needs_many(seqs, tokens, group)) return true;
+  return seqs > 1;
+}
+
+template <typename F>
+hipError_t launch_lds(F* f, dim3 grid, dim3 block, size_t lds, hipStream_t s, void** args) {
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  return hipLaunchKernel((const void*)f, grid, block, args, lds, s);
+}
+
+int64_t prompt_blocks(const AttnArgs& a) {
+  return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / kManyRows + a.seqs + 1;
+}
+
+template <int DT, int DP>
+hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
+  AttnArgs c = a;
+  void* args[] = {&c};
+  const int64_t blocks = prompt_blocks(a);
+  return launch_lds(prompt_attn_kernel<DT, DP, kManyTiles, kManyWaves>, dim3((unsigned)(blocks * a.kv_heads)),
+                    dim3(64 * kManyWaves), 4 * tile_bytes<DP>(), s, args);
+}
+
+template <int DT, int DP>
+hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
+  const int group = a.q_heads / a.kv_heads;
+  const bool many = needs_many(a.seqs, a.tokens, group), few = needs_few(a.seqs, a.tokens, group);
+  AttnArgs c = a;
+  uint32_t magic;
+  int shift;
+  page_magic(a.page_size, magic, shift);
+  hipError_t e = hipSuccess;
+  if (few) {
+    Split sp{32, 128, 1, many ? kFewRows : 0x7FFFFFFF, kShares};
+    void* args[] = {&c, &sp, &magic, &shift};
+    e = launch_lds(paged_few_kernel<DT, DP, 4>, dim3(kShares), dim3(256), 4 * 2 * 2 * 32 * DP * 2, s, args);
+    if (e != hipSuccess) return e;
+    void* cargs[] = {&c, &sp};
+    e = launch_lds(combine_kernel<DT, DP, 32>, dim3(kShares - 1, 32 / (256 / (DP / 4))), dim3(256), 0, s, cargs);
+    if (e != hipSuccess) return e;
+  }
+  if (many) {
+    Split sp{kManyRows, kTile, few ? kFewRows + 1 : 1, 0x7FFFFFFF, kShares};
+    void* args[] = {&c, &sp, &magic, &shift};
+    e = launch_lds(paged_rows_kernel<DT, DP, kManyTiles, kManyWaves>, dim3(kShares), dim3(64 * kManyWaves),
+                   4 * tile_bytes<DP>(), s, args);
+    if (e != hipSuccess) return e;
+    void* cargs[] = {&c, &sp};
+    e = launch_lds(combine_kernel<DT, DP, kManyRows>, dim3(kShares - 1, kManyRows / (256 / (DP / 4))), dim3(256), 0, s, cargs);
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
+  const int group = q_heads / kv_heads;
+  const size_t per_row = ((size_t)padded_dim(head_dim) + 2) * sizeof(float);
+  const size_t rows = needs_many(seqs, tokens, group) ? kManyRows : kFewRows;
+  return (size_t)kShares * 2 * rows * per_row;
+}
+
+bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }
+
+hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s) {
+  const bool wide = padded_dim(a.head_dim) == 128;
+  if (a.dtype == kBf16) return wide ? prompt_dp<kBf16, 128>(a, s) : prompt_dp<kBf16, 64>(a, s);
+  return wide ? prompt_dp<kFp16, 128>(a, s) : prompt_dp<kFp16, 64>(a, s);
+}
+
+hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {
+  const bool wide = padded_dim(a.head_dim) == 128;
+  if (a.dtype == kBf16) return wide ? paged_dp<kBf16, 128>(a, s) : paged_dp<kBf16, 64>(a, s);
+  return wide ? paged_dp<kFp16, 128>(a, s) : paged_dp<kFp16, 64>(a, s);
+}
+
+}  // namespace nvfp4
