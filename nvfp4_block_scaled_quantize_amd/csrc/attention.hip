@@ -43,7 +43,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
 
-__device__ const uint4 kZeros[1] = {{0u, 0u, 0u, 0u}};   // rows that do not exist are copied from here
+__device__ const uint4 kZeros[64] = {};   // rows that do not exist are copied from here
 
 template <int DT>
 __device__ __forceinline__ v16f mfma(v8s a, v8s b, v16f c) {
@@ -64,8 +64,15 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   }
 }
 
-// Value of the lane in the other half of the wave.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// Maximum and sum of a lane's value and that of the same lane of the other half-wave.
+__device__ __forceinline__ float both_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // Wave-uniform values, kept in scalar registers.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -148,71 +155,92 @@ struct Rows {
   int lo[QT], hi[QT];      // the row sees the keys lo <= j < hi
 };
 
-// NaN and infinities in a value that a row does not see must not reach it,
-// but 0 * inf would.  In tiles with a mask whose values are not all finite,
-// the products take the values with the non-finite ones replaced by 0, and
-// whether a row sees a non-finite value of a column (+inf, -inf or NaN) is
-// counted by three more products with the mask as weights.
 template <int DT>
 __device__ __forceinline__ uint32_t not_finite_bits() { return DT == kBf16 ? 0x7F80u : 0x7C00u; }
 
-template <int DT>
-__device__ __forceinline__ short one_bits() { return DT == kBf16 ? (short)0x3F80 : (short)0x3C00; }
-
-// kind 0: the value if finite, else 0; 1, 2, 3: 1 where it is +inf, -inf, NaN.
-template <int DT>
-__device__ __forceinline__ v8s classify(v8s v, int kind) {
-  v8s r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t x = (uint16_t)v[e], lim = not_finite_bits<DT>(), mag = x & 0x7FFFu;
-    const bool yes = kind == 1 ? x == lim : kind == 2 ? x == (lim | 0x8000u) : mag > lim;
-    r[e] = kind == 0 ? (mag >= lim ? (short)0 : v[e]) : (yes ? one_bits<DT>() : (short)0);
+// A lane's operand addresses relative to a tile (which starts at a multiple of
+// 256): chunk 2 st + h of K row `col` is at k ^ 32 st, and V^T's keys 4 h ..
+// for d = 32 t .. are at v ^ 64 t -- the swizzle and the chunk number are
+// joined by exclusive or.  Rows 8 further down have the swizzle ^ 8.
+template <int DP>
+struct Lanes {
+  uint32_t k, v;
+  __device__ __forceinline__ explicit Lanes(int lane) {
+    k = (uint32_t)chunk_at<DP>(lane & 31, lane >> 5);
+    v = tr_at<DP>(4 * (lane >> 5), (lane >> 4) & 1, lane & 15);
   }
-  return r;
+  static constexpr uint32_t kDown = DP == 64 ? 0 : 128;   // swizzle ^ 8, within the row
+};
+
+// S^T = K Q^T for KT x 32 keys.
+template <int DT, int DP, int QT, int KT>
+__device__ __forceinline__ void scores(v16f (&s)[QT][KT], const Rows<DP, QT>& w, const Lanes<DP>& ln, uint32_t k_lds) {
+  const uint32_t base = k_lds + ln.k;
+#pragma unroll
+  for (int st = 0; st < DP / 16; ++st)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const v8s kf = read_b128((base ^ (st * 32)) + kt * 32 * DP * 2);
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt) {
+        if (st == 0) {
+          v16f z;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+          s[qt][kt] = mfma<DT>(kf, w.q[qt][st], z);
+        } else {
+          s[qt][kt] = mfma<DT>(kf, w.q[qt][st], s[qt][kt]);
+        }
+      }
+    }
 }
 
-// Adds the keys kb .. kb + 32 KT - 1 of the tile at LDS addresses kt_lds,
-// vt_lds (rows of DP) to the rows' state.  MASK: some row does not see some
-// key of the tile.
-template <int DT, int DP, int QT, int KT, bool MASK>
-__device__ __forceinline__ void add_tile(Rows<DP, QT>& w, uint32_t kt_lds, uint32_t vt_lds, int kb, float c, int lane) {
-  const int h = lane >> 5, col = lane & 31;
-  v16f s[QT][KT];
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[qt][kt][i] = 0.0f;
-#pragma unroll
-    for (int st = 0; st < DP / 16; ++st) {
-      const v8s kf = read_b128(kt_lds + chunk_at<DP>(col, 2 * st + h) + kt * 32 * DP * 2);
-#pragma unroll
-      for (int qt = 0; qt < QT; ++qt) s[qt][kt] = mfma<DT>(kf, w.q[qt][st], s[qt][kt]);
-    }
-  }
-  v8s p[QT][KT][2];
+// -inf for the keys of the tile at kb that a lane's row does not see.
+template <int QT, int KT, typename R>
+__device__ __forceinline__ void mask_scores(v16f (&s)[QT][KT], const R& w, int kb, int h) {
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
-    if constexpr (MASK) {
-      const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = kt * 32 + 8 * (i / 4) + i % 4;
-          if (key < lo || key >= hi) s[qt][kt][i] = -__builtin_inff();
-        }
-    }
-    float top = s[qt][0][0];
+    const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[qt][kt][i]);
-    top = __builtin_fmaxf(top, other_half(top)) * c;
-    if (__any(top > w.m[qt] + kKeep)) {
-      const float m = __builtin_fmaxf(w.m[qt], top);
+      for (int i = 0; i < 16; ++i) {
+        const int key = kt * 32 + 8 * (i / 4) + i % 4;
+        if (key < lo || key >= hi) s[qt][kt][i] = -__builtin_inff();
+      }
+  }
+}
+
+template <int KT>
+__device__ __forceinline__ float largest(const v16f (&s)[KT]) {
+  float top = s[0][0];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kt][i]);
+  return top;
+}
+
+// 0 or 1, opaque to the compiler.  A rare step on the accumulators is written as a loop of at most
+// one turn: they are then updated where they are, while a branch gets a second set of registers for
+// them and copies between the two in the common path.
+__device__ __forceinline__ int turns_if(bool yes) {
+  int n = yes ? 1 : 0;
+  asm volatile("" : "+v"(n));
+  return uni(n);
+}
+
+// Raises the maximum to `top` (log2 units, of both half-waves) where it lags by more than kKeep.
+template <int DP, int QT>
+__device__ __forceinline__ void raise(Rows<DP, QT>& w, const float (&top)[QT]) {
+  bool far = false;
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) far |= top[qt] > w.m[qt] + kKeep;
+#pragma unroll 1
+  for (int turns = turns_if(__any(far)); turns > 0; --turns) {
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      const float m = __builtin_fmaxf(w.m[qt], top[qt]);
       const float a = m == w.m[qt] ? 1.0f : __builtin_amdgcn_exp2f(w.m[qt] - m);
       w.m[qt] = m;
       w.l[qt] *= a;
@@ -221,95 +249,188 @@ __device__ __forceinline__ void add_tile(Rows<DP, QT>& w, uint32_t kt_lds, uint3
 #pragma unroll
         for (int i = 0; i < 16; ++i) w.o[qt][t][i] *= a;
     }
-    // nothing seen so far: every weight is 2^(-inf) = 0
-    const float m = w.m[qt] == -__builtin_inff() ? 0.0f : w.m[qt];
-    float l = 0.0f;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = half * 8 + e * 2;
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][kt][i], c, -m));
-          const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][kt][i + 1], c, -m));
-          l += x;
-          l += y;
-          d[e] = pack2<DT>(x, y);
-        }
-        p[qt][kt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
-      }
-    w.l[qt] += l;
   }
-  // O^T += V^T P^T; element e of a value fragment: key 16 half + 4 h + e (e < 4),
-  // 16 half + 8 + 4 h + e - 4 -- the order of p
-  const int g = (lane >> 4) & 1, i16 = lane & 15;
-  auto value = [&](int kt, int half, int t) {
-    const v4s a = read_tr(vt_lds + tr_at<DP>(4 * h, 2 * t + g, i16) + (kt * 32 + half * 16) * DP * 2);
-    const v4s b = read_tr(vt_lds + tr_at<DP>(8 + 4 * h, 2 * t + g, i16) + (kt * 32 + half * 16) * DP * 2);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  if constexpr (MASK) {
-    uint32_t big = 0;
+}
+
+// Weights 2^(s c - m), summed into l and rounded into p (the B operand of the value product).
+template <int DT, int KT>
+__device__ __forceinline__ void weights(const v16f (&s)[KT], float c, float m, float& l, v8s (&p)[KT][2]) {
+  // nothing seen so far: every weight is 2^(-inf) = 0
+  const float mm = m == -__builtin_inff() ? 0.0f : m;
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
+  for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+    for (int half = 0; half < 2; ++half) {
+      uint32_t d[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const v8s v = value(kt, half, t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t mag = (uint16_t)v[e] & 0x7FFFu;
-            big = mag > big ? mag : big;
-          }
-        }
-    if (__any(big >= not_finite_bits<DT>())) {
-#pragma unroll 1
-      for (int kind = 0; kind < 4; ++kind) {
-#pragma unroll
-        for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-          for (int qt = 0; qt < QT; ++qt) {
-            v16f n;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) n[i] = kind == 0 ? w.o[qt][t][i] : 0.0f;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const v8s v = classify<DT>(value(kt, half, t), kind);
-                const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
-                v8s weight = p[qt][kt][half];
-                if (kind != 0) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const int key = kt * 32 + 16 * half + 8 * (e / 4) + e % 4;
-                    weight[e] = key >= lo && key < hi ? one_bits<DT>() : (short)0;
-                  }
-                }
-                n = mfma<DT>(v, weight, n);
-              }
-            const float bad = kind == 1 ? __builtin_inff() : kind == 2 ? -__builtin_inff() : __builtin_nanf("");
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w.o[qt][t][i] = kind == 0 ? n[i] : (n[i] > 0.0f ? w.o[qt][t][i] + bad : w.o[qt][t][i]);
-          }
+      for (int e = 0; e < 4; ++e) {
+        const int i = half * 8 + e * 2;
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c, -mm));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i + 1], c, -mm));
+        sum[0] += x;
+        sum[1] += y;
+        d[e] = pack2<DT>(x, y);
       }
-      return;
+      p[kt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
     }
-  }
+  l += sum[0] + sum[1];
+}
+
+// O^T += V^T P^T.  Element e of a value fragment: key 16 half + 4 h + e (e < 4), 16 half + 8 + 4 h
+// + e - 4 -- the order of p.
+template <int DT, int DP, int QT, int KT>
+__device__ __forceinline__ void values(Rows<DP, QT>& w, const v8s (&p)[QT][KT][2], const Lanes<DP>& ln, uint32_t v_lds) {
+  const uint32_t base = v_lds + ln.v;
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t)
+  for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const v8s v = value(kt, half, t);
+      for (int t = 0; t < DP / 32; ++t) {
+        constexpr uint32_t kRow = DP * 2;
+        const uint32_t step = (kt * 32 + half * 16) * kRow;
+        const v4s a = read_tr((base ^ (t * 64)) + step);
+        const v4s b = read_tr((base ^ (t * 64) ^ Lanes<DP>::kDown) + step + 8 * kRow);
+        const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) w.o[qt][t] = mfma<DT>(v, p[qt][kt][half], w.o[qt][t]);
       }
+}
+
+// Whether a tile's values are all finite (KT x 32 rows of DP).
+template <int DT, int DP, int KT>
+__device__ __forceinline__ bool all_finite(uint32_t v_lds, int lane) {
+  asm volatile("" : "+v"(lane));
+  uint32_t big = 0;
+#pragma unroll 4
+  for (int n = 0; n < KT * 32 * DP * 2 / 1024; ++n) {
+    const u32x4 x = __builtin_bit_cast(u32x4, read_b128(v_lds + n * 1024 + lane * 16));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t a = x[e] & 0x7FFFu, b = (x[e] >> 16) & 0x7FFFu;
+      big = a > big ? a : big;
+      big = b > big ? b : big;
+    }
+  }
+  return !__any(big >= not_finite_bits<DT>());
+}
+
+// Where some row does not see some key of a tile and a value there is not finite, 0 * inf in the
+// matrix cores would carry it to rows that do not see it.  Such a tile (32 keys) is multiplied from
+// a copy with 0 in place of those values (copy_finite, into the wave's own LDS), and they are added
+// one by one to the rows that see them (add_not_finite).
+template <int DT, int DP>
+__device__ __forceinline__ void copy_finite(uint32_t v_lds, uint32_t mine, int lane) {
+  asm volatile("" : "+v"(lane));
+#pragma unroll 1
+  for (int n = 0; n < 32 * DP * 2 / 1024; ++n) {
+    u32x4 x = __builtin_bit_cast(u32x4, read_b128(v_lds + n * 1024 + lane * 16));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((x[e] & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFF0000u;
+      if (((x[e] >> 16) & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFFu;
+    }
+    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(mine + n * 1024 + lane * 16) = x;
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+template <int DT, int DP>
+__device__ __forceinline__ void add_not_finite(v16f (&o)[DP / 32], const v16f& s, float c, float m, int lo, int hi,
+                                               uint32_t v_lds, uint32_t mine, int lane) {
+  asm volatile("" : "+v"(lane));
+  const int h = lane >> 5, col = lane & 31;
+  typedef __attribute__((address_space(3))) float* lds_f;
+  typedef __attribute__((address_space(3))) u32x2* lds_2;
+  const float mm = m == -__builtin_inff() ? 0.0f : m;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the copy has been read
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    *(lds_f)(uintptr_t)(mine + ((8 * (i / 4) + 4 * h + i % 4) * 32 + col) * 4) =
+        __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mm));
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+  for (int key = 0; key < 32; ++key) {
+    const float p = *(lds_f)(uintptr_t)(mine + (key * 32 + col) * 4);
+    const bool sees = key >= lo && key < hi;
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x2 x = *(lds_2)(uintptr_t)(v_lds + chunk_at<DP>(key, t * 4 + i) + 8 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = (x[e / 2] >> (16 * (e % 2))) & 0xFFFFu;
+          const bool add = sees && (y & 0x7FFFu) >= not_finite_bits<DT>();
+          o[t][4 * i + e] += add ? p * unpack1<DT>((uint16_t)y) : 0.0f;
+        }
+      }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+// Order of the instructions of a step (scores of the next 32 keys, weights and
+// value product of the current ones): the K operands are read ahead of the
+// first product, and every matrix instruction is followed by the share of the
+// vector work and of the V reads that fits beside it.
+template <int DP, int QT>
+__device__ __forceinline__ void interleave() {
+  constexpr int kRead = 0x100, kMatrix = 0x8, kVector = 0x2;
+  __builtin_amdgcn_sched_group_barrier(kRead, 4, 0);
+#pragma unroll
+  for (int i = 0; i < DP / 16 - 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, (128 / DP) * 7 * QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, (128 / DP) * 7 * QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 2 * QT, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+  }
+}
+
+// Adds 32 keys from key kb to the rows' state, whose scores are `cur` with the largest `top`, and
+// forms (NEXT) the next 32 keys' scores `nxt` and `top` from the K rows at k_next.  `all`: every row
+// sees every key of the current 32.  `mine`: 32 rows of DP of the wave's own LDS.
+template <int DT, int DP, int QT, bool NEXT>
+__device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f (&cur)[QT][1], v16f (&nxt)[QT][1],
+                                     float (&top)[QT], uint32_t k_next, uint32_t v_lds, int kb, float c, bool all,
+                                     uint32_t mine, int lane) {
+  int odd = 0;   // some value is not finite
+#pragma unroll 1
+  for (int turns = turns_if(!all); turns > 0; --turns) {
+    mask_scores(cur, w, kb, lane >> 5);
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(cur[qt])) * c;
+    odd = uni(all_finite<DT, DP, 1>(v_lds, lane) ? 0 : 1);
+    if (odd) copy_finite<DT, DP>(v_lds, mine, lane);
+  }
+  raise(w, top);
+  v8s p[QT][1][2];
+  const uint32_t v_at = odd ? mine : v_lds;
+  if constexpr (NEXT) scores<DT, DP, QT, 1>(nxt, w, ln, k_next);
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) weights<DT, 1>(cur[qt], c, w.m[qt], w.l[qt], p[qt]);
+  values<DT, DP, QT, 1>(w, p, ln, v_at);
+  if constexpr (NEXT) {
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(nxt[qt])) * c;
+    interleave<DP, QT>();
+  }
+#pragma unroll 1
+  for (int turns = turns_if(odd != 0); turns > 0; --turns)
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt)
+      add_not_finite<DT, DP>(w.o[qt], cur[qt][0], c, w.m[qt], w.lo[qt] - kb, w.hi[qt] - kb, v_lds, mine, lane);
 }
 
 // ---------------------------------------------------------------- items
@@ -361,7 +482,7 @@ __device__ __forceinline__ void store_rows(const Rows<DP, QT>& w, const AttnArgs
   const int h = lane >> 5, col = lane & 31;
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
-    const float l = w.l[qt] + other_half(w.l[qt]);
+    const float l = both_sum(w.l[qt]);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int r = row0 + qt * 32 + col;
     if (r >= rows) continue;
@@ -393,7 +514,7 @@ __device__ __forceinline__ void store_part(const Rows<DP, QT>& w, float* o, floa
   const int h = lane >> 5, col = lane & 31;
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
-    const float l = w.l[qt] + other_half(w.l[qt]);
+    const float l = both_sum(w.l[qt]);
     const int r = row0 + qt * 32 + col;
     if (r >= rows) continue;
 #pragma unroll
@@ -408,86 +529,165 @@ __device__ __forceinline__ void store_part(const Rows<DP, QT>& w, float* o, floa
 
 // ---------------------------------------------------------------- many rows
 // A workgroup of NW waves, QT x 32 rows each; all waves share the tiles of 64
-// keys, copied global -> LDS one tile ahead (two buffers, one barrier a tile).
+// keys, copied global -> LDS.
 constexpr int kTile = 64;
-
-template <int DP, int NW, bool PAGED>
-struct TileCopy {
-  static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
-  static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
-  static constexpr int kIters = kTile / (kRowsPer * NW);    // copies of each of K and V, per wave
-  static_assert(kIters >= 1, "tile too small for the waves");
-  int page[PAGED ? kIters : 1];
-
-  __device__ __forceinline__ static int row_of(int it, int wave, int lane) {
-    return (it * NW + wave) * kRowsPer + lane / kChunks;
-  }
-  // Page ids of the tile at key kb (waited for when the copies are issued).
-  __device__ __forceinline__ void pages(const Source& s, int kb, int wave, int lane) {
-    if constexpr (PAGED) {
-#pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int j = kb + row_of(it, wave, lane);
-        page[it] = j < s.keys ? s.table[page_of(s, j)] : -1;
-      }
-    }
-  }
-  __device__ __forceinline__ void issue(const Source& s, int kb, uint32_t k_lds, uint32_t v_lds, int wave, int lane) {
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int r = row_of(it, wave, lane);
-      const int chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
-      const char *k, *v;
-      row_at<PAGED>(s, kb + r, PAGED ? page[it] : 0, chunk * 16, k, v);
-      const uint32_t at = (uint32_t)uni((it * NW + wave) * 1024);
-      dma16_at(k, k_lds + at);
-      dma16_at(v, v_lds + at);
-    }
-  }
-};
 
 template <int DP>
 constexpr int tile_bytes() { return kTile * DP * 2; }
 
-// Runs the keys of tiles [t0, t1) (tiles of 64 from key 0) through the block.
+// Copies of one wave: kIters instructions for a tile of K or V, each of kRowsPer whole rows.
+template <int DP, int NW, bool PAGED>
+struct TileCopy {
+  static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
+  static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
+  static constexpr int kIters = kTile / (kRowsPer * NW);
+  static_assert(kIters >= 1 && (NW * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
+  const Source& s;
+  int wave, lane, chunk;    // chunk: the lane's 16 bytes of its row
+  uint32_t k_ofs, v_ofs;    // byte offset of the lane from an instruction's first row
+  bool whole;               // full rows, and the rows of an instruction lie in one page
+
+  __device__ __forceinline__ TileCopy(const Source& src, int wv, int ln) : s(src), wave(wv), lane(ln) {
+    const int r = wave * kRowsPer + lane / kChunks;
+    chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
+    const uint32_t k_row = PAGED ? s.d_bytes : (uint32_t)s.k_step, v_row = PAGED ? s.d_bytes : (uint32_t)s.v_step;
+    k_ofs = (lane / kChunks) * k_row + chunk * 16;
+    v_ofs = (lane / kChunks) * v_row + chunk * 16;
+    whole = s.d_bytes == DP * 2;
+    if constexpr (PAGED) whole = whole && s.page_size % kRowsPer == 0;
+    else whole = whole && s.k_step < (1 << 27) && s.v_step < (1 << 27);
+  }
+  // Page of each instruction's first row, in scalar registers.
+  struct Pages { int id[PAGED ? kIters : 1]; };
+  __device__ __forceinline__ Pages pages(int kb) const {
+    Pages p{};
+    if constexpr (PAGED) {
+      if (whole) {
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const int j = kb + (it * NW + wave) * kRowsPer;
+          const auto at = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(s.table + page_of(s, j < s.keys ? j : 0));
+          p.id[it] = *at;
+        }
+      }
+    }
+    return p;
+  }
+  template <bool V>
+  __device__ __forceinline__ void issue(int kb, const Pages& p, uint32_t lds) const {
+    if (whole && kb + kTile <= s.keys) {
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int j = kb + (it * NW + wave) * kRowsPer;
+        const char* base = V ? s.v : s.k;
+        if constexpr (PAGED) {
+          const int64_t off = (int64_t)p.id[it] * s.k_step + (int64_t)(j - page_of(s, j) * s.page_size) * s.d_bytes;
+          base = (uint32_t)p.id[it] < (uint64_t)s.num_pages ? base + off : reinterpret_cast<const char*>(kZeros);
+        } else {
+          base += (int64_t)j * (V ? s.v_step : s.k_step);
+        }
+        dma16(base, V ? v_ofs : k_ofs, lds + (it * NW + wave) * 1024);
+      }
+    } else {
+#pragma unroll 1
+      for (int it = 0; it < kIters; ++it) {
+        const int j = kb + (it * NW + wave) * kRowsPer + lane / kChunks;
+        int page = 0;
+        if constexpr (PAGED) page = j < s.keys ? s.table[page_of(s, j)] : -1;
+        const char *k, *v;
+        row_at<PAGED>(s, j, page, chunk * 16, k, v);
+        dma16_at(V ? v : k, (uint32_t)uni(lds + (it * NW + wave) * 1024));
+      }
+    }
+  }
+};
+
+// Runs the keys of tiles [t0, t1) (tiles of 64 from key 0) through the block,
+// 32 keys at a time.  The scores of the next 32 keys are formed while the
+// weights of the current 32 are, so that the matrix cores and the vector units
+// work side by side: iteration t uses K(t), K(t + 1) and V(t) while K(t + 2)
+// and V(t + 1) are on their way (three buffers of K, two of V, one barrier a
+// tile).
 template <int DT, int DP, int QT, int NW, bool PAGED>
 __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, const Item& it, int t0, int t1,
                                           Rows<DP, QT>& w, uint32_t lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int group = a.q_heads / a.kv_heads, rows = it.news * group;
   const int first = it.row0 + wave * QT * 32;
+  constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
+  const TileCopy<DP, NW, PAGED> cp(s, wave, lane);
+  typename TileCopy<DP, NW, PAGED>::Pages p1{}, p2{};
+  uint32_t k_now = lds, k_next = lds + kBytes, k_free = lds + 2 * kBytes;
+  uint32_t v_now = lds + 3 * kBytes, v_next = lds + 4 * kBytes;
+  if (t0 < t1) {
+    const auto p0 = cp.pages(t0 * kTile);
+    p1 = cp.pages((t0 + 1) * kTile);
+    p2 = cp.pages((t0 + 2) * kTile);
+    cp.template issue<false>(t0 * kTile, p0, k_now);
+    if (t0 + 1 < t1) cp.template issue<false>((t0 + 1) * kTile, p1, k_next);
+    cp.template issue<true>(t0 * kTile, p0, v_now);
+  }
   load_rows<DP, QT>(w, a, it, first, lane);
   // limits of the wave's rows: positions of its first and last row
   const bool active = first < rows;
   const int end = first + QT * 32 < rows ? first + QT * 32 : rows;
-  const int p0 = it.keys - it.news + first / group, p1 = it.keys - it.news + (end - 1) / group;
-  const int hi_min = p0 + 1, hi_max = p1 + 1;
-  const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
-  const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
+  const int pos0 = it.keys - it.news + first / group, pos1 = it.keys - it.news + (end - 1) / group;
+  const int hi_min = uni(pos0 + 1), hi_max = uni(active ? pos1 + 1 : 0);
+  const int lo_min = uni((a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0);
+  const int lo_max = uni((a.window > 0 && pos1 + 1 > a.window) ? pos1 + 1 - a.window : 0);
   const float c = a.scale * kLog2e;
-  TileCopy<DP, NW, PAGED> cp;
-  constexpr int kBytes = tile_bytes<DP>();
-  if (t0 < t1) {
-    cp.pages(s, t0 * kTile, wave, lane);
-    cp.issue(s, t0 * kTile, lds, lds + kBytes, wave, lane);
-    if (t0 + 1 < t1) cp.pages(s, (t0 + 1) * kTile, wave, lane);
-  }
-  for (int t = t0; t < t1; ++t) {
-    const uint32_t buf = lds + ((t - t0) & 1) * (2 * kBytes);
-    wait_vmcnt_le<0>();
-    lds_barrier();
-    if (t + 1 < t1) {
-      const uint32_t nxt = lds + ((t + 1 - t0) & 1) * (2 * kBytes);
-      cp.issue(s, (t + 1) * kTile, nxt, nxt + kBytes, wave, lane);
-      if (t + 2 < t1) cp.pages(s, (t + 2) * kTile, wave, lane);
+  const Lanes<DP> ln(lane);
+  const uint32_t mine = lds + 5 * kBytes + wave * kHalf;
+  // tiles that some row of the wave sees, and whether all rows see 32 keys
+  const int w0 = clampi(lo_min / kTile, t0, t1), w1 = clampi((hi_max + kTile - 1) / kTile, w0, t1);
+  auto all = [&](int kb) { return kb + 32 <= hi_min && kb >= lo_max; };
+  int t = t0;
+  auto begin = [&]() {
+    if (t > t0) {
+      wait_vmcnt_le<0>();
+      lds_barrier();
     }
-    const int kb = t * kTile;
-    if (!active || kb >= hi_max || kb + kTile <= lo_min) continue;
-    if (kb + kTile > hi_min || kb < lo_max)
-      add_tile<DT, DP, QT, kTile / 32, true>(w, buf, buf + kBytes, kb, c, lane);
-    else
-      add_tile<DT, DP, QT, kTile / 32, false>(w, buf, buf + kBytes, kb, c, lane);
+    if (t + 2 < t1) cp.template issue<false>((t + 2) * kTile, p2, k_free);
+    if (t + 1 < t1) cp.template issue<true>((t + 1) * kTile, p1, v_next);
+    p1 = p2;
+    p2 = cp.pages((t + 3) * kTile);
+  };
+  auto end_tile = [&]() {
+    const uint32_t k_old = k_now, v_old = v_now;
+    k_now = k_next;
+    k_next = k_free;
+    k_free = k_old;
+    v_now = v_next;
+    v_next = v_old;
+    ++t;
+  };
+  auto skip_to = [&](int stop) {
+#pragma unroll 1
+    while (t < stop) {
+      begin();
+      end_tile();
+    }
+  };
+  wait_vmcnt_le<0>();
+  lds_barrier();
+  skip_to(w0);
+  if (w0 < w1) {
+    v16f sa[QT][1], sb[QT][1];
+    float top[QT];
+    scores<DT, DP, QT, 1>(sa, w, ln, k_now);
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(sa[qt])) * c;
+    // past the last tile the next scores are formed from whatever the buffer holds, and not used
+#pragma unroll 1
+    do {
+      begin();
+      const int kb = t * kTile;
+      step<DT, DP, QT, true>(w, ln, sa, sb, top, k_now + kHalf, v_now, kb, c, all(kb), mine, lane);
+      step<DT, DP, QT, true>(w, ln, sb, sa, top, k_next, v_now + kHalf, kb + 32, c, all(kb + 32), mine, lane);
+      end_tile();
+    } while (t < w1);
   }
+  skip_to(t1);
   lds_barrier();   // the buffers may be filled again
 }
 
@@ -760,6 +960,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const uint32_t mem = lds_addr(dyn_lds) + wave * 2 * kStage;
   float* join_o = (float*)dyn_lds;          // [NW][32][DP] after the copies
+  const Lanes<DP> ln(lane);
   const int per = sp.shares / 8;
   const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   for_segments<64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
@@ -812,15 +1013,19 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       const int kb = ((g.t0 + t) * NW + wave) * 32;
       const uint32_t at = mem + (t & 1) * kStage;
       if (kb < hi_max && kb + 32 > lo_min) {
-        if (kb + 32 > hi_min || kb < lo_max) add_tile<DT, DP, 1, 1, true>(st, at, at + 32 * DP * 2, kb, c, lane);
-        else add_tile<DT, DP, 1, 1, false>(st, at, at + 32 * DP * 2, kb, c, lane);
+        v16f sc[1][1];
+        float top[1];
+        scores<DT, DP, 1, 1>(sc, st, ln, at);
+        top[0] = both_max(largest(sc[0])) * c;
+        // the K rows are not needed any more: their place is the wave's scratch
+        step<DT, DP, 1, false>(st, ln, sc, sc, top, 0, at + 32 * DP * 2, kb, c, kb + 32 <= hi_min && kb >= lo_max, at, lane);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (t + 2 < n) issue(t + 2);
     }
     // join the waves: weights 2^(m_w - m)
     const int h = lane >> 5, col = lane & 31;
-    const float l = st.l[0] + other_half(st.l[0]);
+    const float l = both_sum(st.l[0]);
     if (h == 0) { join_ml[wave][col][0] = st.m[0]; join_ml[wave][col][1] = l; }
     __syncthreads();
     float m = -__builtin_inff();
@@ -927,6 +1132,13 @@ constexpr int kFewRows = 32;
 constexpr int kManyWaves = 8, kManyTiles = 1;
 constexpr int kManyRows = 32 * kManyTiles * kManyWaves;
 
+// three tiles of K, two of V, and each wave's scratch for tiles with values that are not finite
+template <int DP>
+constexpr size_t many_lds_bytes() { return 5 * tile_bytes<DP>() + kManyWaves * 32 * DP * 2; }
+constexpr int kFewWaves = 4;
+template <int DP>
+constexpr size_t few_lds_bytes() { return kFewWaves * 2 * 2 * 32 * DP * 2; }
+
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 
 void page_magic(int page, uint32_t& magic, int& shift) {
@@ -970,7 +1182,7 @@ hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
   void* args[] = {&c};
   const int64_t blocks = prompt_blocks(a);
   return launch_lds(prompt_attn_kernel<DT, DP, kManyTiles, kManyWaves>, dim3((unsigned)(blocks * a.kv_heads)),
-                    dim3(64 * kManyWaves), 4 * tile_bytes<DP>(), s, args);
+                    dim3(64 * kManyWaves), many_lds_bytes<DP>(), s, args);
 }
 
 template <int DT, int DP>
@@ -983,9 +1195,9 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   page_magic(a.page_size, magic, shift);
   hipError_t e = hipSuccess;
   if (few) {
-    Split sp{32, 128, 1, many ? kFewRows : 0x7FFFFFFF, kShares};
+    Split sp{kFewRows, 32 * kFewWaves, 1, many ? kFewRows : 0x7FFFFFFF, kShares};
     void* args[] = {&c, &sp, &magic, &shift};
-    e = launch_lds(paged_few_kernel<DT, DP, 4>, dim3(kShares), dim3(256), 4 * 2 * 2 * 32 * DP * 2, s, args);
+    e = launch_lds(paged_few_kernel<DT, DP, kFewWaves>, dim3(kShares), dim3(64 * kFewWaves), few_lds_bytes<DP>(), s, args);
     if (e != hipSuccess) return e;
     void* cargs[] = {&c, &sp};
     e = launch_lds(combine_kernel<DT, DP, 32>, dim3(kShares - 1, 32 / (256 / (DP / 4))), dim3(256), 0, s, cargs);
@@ -995,7 +1207,7 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
     Split sp{kManyRows, kTile, few ? kFewRows + 1 : 1, 0x7FFFFFFF, kShares};
     void* args[] = {&c, &sp, &magic, &shift};
     e = launch_lds(paged_rows_kernel<DT, DP, kManyTiles, kManyWaves>, dim3(kShares), dim3(64 * kManyWaves),
-                   4 * tile_bytes<DP>(), s, args);
+                   many_lds_bytes<DP>(), s, args);
     if (e != hipSuccess) return e;
     void* cargs[] = {&c, &sp};
     e = launch_lds(combine_kernel<DT, DP, kManyRows>, dim3(kShares - 1, kManyRows / (256 / (DP / 4))), dim3(256), 0, s, cargs);
