@@ -370,32 +370,87 @@ __device__ __forceinline__ void add_not_finite(v16f (&o)[DP / 32], const v16f& s
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-// Order of the instructions of a step (scores of the next 32 keys, weights and
-// value product of the current ones): the K operands are read ahead of the
-// first product, and every matrix instruction is followed by the share of the
-// vector work and of the V reads that fits beside it.
-template <int DP, int QT>
-__device__ __forceinline__ void interleave() {
-  constexpr int kRead = 0x100, kMatrix = 0x8, kVector = 0x2;
-  __builtin_amdgcn_sched_group_barrier(kRead, 4, 0);
+// The common part of a step, in an order that keeps the matrix cores fed: the scores of the next 32
+// keys, the weights of the current ones beside them, then the value product.  Operands are read from
+// LDS four products ahead, and each matrix instruction is followed by the share of the vector work
+// that fits beside it; the scheduling barriers keep that order.
+template <int DT, int DP, int QT>
+__device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, const v16f (&cur)[QT][1],
+                                         v16f (&nxt)[QT][1], float (&top)[QT], uint32_t k_next, uint32_t v_lds, float c) {
+  constexpr int kSteps = DP / 16, kAhead = 4, kPer = 16 / kSteps, kTiles = DP / 32;
+  const uint32_t kb = k_next + ln.k, vb = v_lds + ln.v;
+  auto key = [&](int st) { return read_b128(kb ^ (st * 32)); };
+  auto value = [&](int n) {   // product n: half n / kTiles, d tile n % kTiles
+    constexpr uint32_t kRow = DP * 2;
+    const uint32_t t = n % kTiles, at = (n / kTiles) * 16 * kRow;
+    const v4s x = read_tr((vb ^ (t * 64)) + at), y = read_tr((vb ^ (t * 64) ^ Lanes<DP>::kDown) + at + 8 * kRow);
+    return (v8s)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  v8s f[kAhead], p[QT][2];
+  float m[QT], sum[QT][2], e[QT][16], best[QT];
 #pragma unroll
-  for (int i = 0; i < DP / 16 - 4; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kVector, (128 / DP) * 7 * QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+  for (int n = 0; n < kAhead; ++n) f[n] = key(n);
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) {
+    // nothing seen so far: every weight is 2^(-inf) = 0
+    m[qt] = w.m[qt] == -__builtin_inff() ? 0.0f : w.m[qt];
+    sum[qt][0] = w.l[qt];
+    sum[qt][1] = 0.0f;
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      if (st == 0) {
+        v16f z;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+        nxt[qt][0] = mfma<DT>(f[0], w.q[qt][0], z);
+      } else {
+        nxt[qt][0] = mfma<DT>(f[st % kAhead], w.q[qt][st], nxt[qt][0]);
+      }
+    }
+    f[st % kAhead] = st + kAhead < kSteps ? key(st + kAhead) : value(st + kAhead - kSteps);
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+      for (int i = st * kPer; i < (st + 1) * kPer; ++i) {
+        e[qt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[qt][0][i], c, -m[qt]));
+        sum[qt][i % 2] += e[qt][i];
+      }
+    __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kVector, (128 / DP) * 7 * QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+  for (int qt = 0; qt < QT; ++qt) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = pack2<DT>(e[qt][half * 8 + 2 * k], e[qt][half * 8 + 2 * k + 1]);
+      p[qt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
+    }
+    w.l[qt] = sum[qt][0] + sum[qt][1];
   }
 #pragma unroll
-  for (int i = 0; i < DP / 16; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMatrix, QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kVector, 2 * QT, 0);
-    __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+  for (int n = 0; n < 2 * kTiles; ++n) {
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt)
+      w.o[qt][n % kTiles] = mfma<DT>(f[(n + kSteps) % kAhead], p[qt][n / kTiles], w.o[qt][n % kTiles]);
+    if (n + kAhead < 2 * kTiles) f[(n + kSteps) % kAhead] = value(n + kAhead);
+    // the next scores are ready by the second product
+#pragma unroll
+    for (int qt = 0; qt < QT; ++qt) {
+      if (n == 1) best[qt] = nxt[qt][0][0];
+      constexpr int kShare = 16 / (2 * kTiles - 2) + 1;
+      if (n >= 1)
+#pragma unroll
+        for (int i = (n - 1) * kShare; i < n * kShare && i < 16; ++i) best[qt] = __builtin_fmaxf(best[qt], nxt[qt][0][i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
+#pragma unroll
+  for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(best[qt]) * c;
 }
 
 // Adds 32 keys from key kb to the rows' state, whose scores are `cur` with the largest `top`, and
@@ -415,16 +470,14 @@ __device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f 
     if (odd) copy_finite<DT, DP>(v_lds, mine, lane);
   }
   raise(w, top);
-  v8s p[QT][1][2];
   const uint32_t v_at = odd ? mine : v_lds;
-  if constexpr (NEXT) scores<DT, DP, QT, 1>(nxt, w, ln, k_next);
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) weights<DT, 1>(cur[qt], c, w.m[qt], w.l[qt], p[qt]);
-  values<DT, DP, QT, 1>(w, p, ln, v_at);
   if constexpr (NEXT) {
+    products<DT, DP, QT>(w, ln, cur, nxt, top, k_next, v_at, c);
+  } else {
+    v8s p[QT][1][2];
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(nxt[qt])) * c;
-    interleave<DP, QT>();
+    for (int qt = 0; qt < QT; ++qt) weights<DT, 1>(cur[qt], c, w.m[qt], w.l[qt], p[qt]);
+    values<DT, DP, QT, 1>(w, p, ln, v_at);
   }
 #pragma unroll 1
   for (int turns = turns_if(odd != 0); turns > 0; --turns)
