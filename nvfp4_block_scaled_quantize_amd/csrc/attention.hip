@@ -82,15 +82,20 @@ __device__ __forceinline__ int64_t uni64(int64_t v) {
 
 // ---------------------------------------------------------------- LDS tiles
 // A tile is rows of DP elements; 16-byte chunk p of row r holds chunk p ^
-// swz(r) of the row.  swz makes both reads conflict-free: eight consecutive
-// rows get eight different values (the b128 reads of K, one row per lane),
-// and rows 0..3 modulo 4 differ in the bits above the lowest (the transposing
-// reads of V, 32 bytes of each of four rows).
-__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
+// swz(r) of the row.  LDS serves 256 bytes (all 64 banks) a cycle: 16 lanes of
+// a b128 read, here 16 consecutive rows at one chunk, or 32 lanes of a
+// transposing read, 64 bytes of each of four consecutive rows.  Rows of 256
+// bytes start at the same bank, so swz puts the low row bits above the bits
+// that tell the chunks of 64 bytes apart and is different for 16 rows; rows of
+// 128 bytes differ in half the banks by themselves.
+template <int DP>
+__device__ __forceinline__ int swz(int r) {
+  return DP == 64 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+}
 
 template <int DP>
 __device__ __forceinline__ int chunk_at(int row, int chunk) {
-  return row * (DP * 2) + ((chunk ^ (swz(row) & (DP / 8 - 1))) * 16);
+  return row * (DP * 2) + ((chunk ^ swz<DP>(row)) * 16);
 }
 
 // Row `row` of V^T: four keys row..row+3 for the 16 values of d in
@@ -161,7 +166,7 @@ __device__ __forceinline__ uint32_t not_finite_bits() { return DT == kBf16 ? 0x7
 // A lane's operand addresses relative to a tile (which starts at a multiple of
 // 256): chunk 2 st + h of K row `col` is at k ^ 32 st, and V^T's keys 4 h ..
 // for d = 32 t .. are at v ^ 64 t -- the swizzle and the chunk number are
-// joined by exclusive or.  Rows 8 further down have the swizzle ^ 8.
+// joined by exclusive or.
 template <int DP>
 struct Lanes {
   uint32_t k, v;
@@ -169,7 +174,7 @@ struct Lanes {
     k = (uint32_t)chunk_at<DP>(lane & 31, lane >> 5);
     v = tr_at<DP>(4 * (lane >> 5), (lane >> 4) & 1, lane & 15);
   }
-  static constexpr uint32_t kDown = DP == 64 ? 0 : 128;   // swizzle ^ 8, within the row
+  static constexpr uint32_t kDown = 32;   // what 8 rows further down change in the swizzle
 };
 
 // S^T = K Q^T for KT x 32 keys.
@@ -221,13 +226,13 @@ __device__ __forceinline__ float largest(const v16f (&s)[KT]) {
   return top;
 }
 
-// 0 or 1, opaque to the compiler.  A rare step on the accumulators is written as a loop of at most
-// one turn: they are then updated where they are, while a branch gets a second set of registers for
-// them and copies between the two in the common path.
-__device__ __forceinline__ int turns_if(bool yes) {
-  int n = yes ? 1 : 0;
-  asm volatile("" : "+v"(n));
-  return uni(n);
+// A rare step on the accumulators is written as a loop of at most one turn, with a count that the
+// compiler does not know: they are then updated where they are, while a branch gets a second set of
+// registers for them and copies between the two in the common path.
+__device__ __forceinline__ int turns_if(int positive) {
+  int n = uni(positive < 1 ? positive : 1);
+  asm volatile("" : "+s"(n));
+  return n;
 }
 
 // Raises the maximum to `top` (log2 units, of both half-waves) where it lags by more than kKeep.
@@ -237,7 +242,7 @@ __device__ __forceinline__ void raise(Rows<DP, QT>& w, const float (&top)[QT]) {
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) far |= top[qt] > w.m[qt] + kKeep;
 #pragma unroll 1
-  for (int turns = turns_if(__any(far)); turns > 0; --turns) {
+  for (int turns = turns_if(__popcll(__ballot(far))); turns > 0; --turns) {
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
       const float m = __builtin_fmaxf(w.m[qt], top[qt]);
@@ -372,24 +377,31 @@ __device__ __forceinline__ void add_not_finite(v16f (&o)[DP / 32], const v16f& s
 
 // The common part of a step, in an order that keeps the matrix cores fed: the scores of the next 32
 // keys, the weights of the current ones beside them, then the value product.  Operands are read from
-// LDS four products ahead, and each matrix instruction is followed by the share of the vector work
+// LDS four products ahead (`f`: on entry the first K operands, on return those of the step after,
+// whose rows are at k_after), and each matrix instruction is followed by the share of the vector work
 // that fits beside it; the scheduling barriers keep that order.
+constexpr int kAhead = 4;
+
+template <int DP>
+__device__ __forceinline__ v8s key_operand(const Lanes<DP>& ln, uint32_t k_lds, int st) {
+  return read_b128((k_lds + ln.k) ^ (st * 32));
+}
+
 template <int DT, int DP, int QT>
 __device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, const v16f (&cur)[QT][1],
-                                         v16f (&nxt)[QT][1], float (&top)[QT], uint32_t k_next, uint32_t v_lds, float c) {
-  constexpr int kSteps = DP / 16, kAhead = 4, kPer = 16 / kSteps, kTiles = DP / 32;
-  const uint32_t kb = k_next + ln.k, vb = v_lds + ln.v;
-  auto key = [&](int st) { return read_b128(kb ^ (st * 32)); };
+                                         v16f (&nxt)[QT][1], float (&top)[QT], v8s (&f)[kAhead], uint32_t k_next,
+                                         uint32_t k_after, uint32_t v_lds, float c) {
+  constexpr int kSteps = DP / 16, kPer = 16 / kSteps, kTiles = DP / 32;
+  static_assert(kAhead <= kSteps && kAhead <= 2 * kTiles && kSteps % kAhead == 0 && 2 * kTiles % kAhead == 0, "operand ring");
+  const uint32_t vb = v_lds + ln.v;
   auto value = [&](int n) {   // product n: half n / kTiles, d tile n % kTiles
     constexpr uint32_t kRow = DP * 2;
     const uint32_t t = n % kTiles, at = (n / kTiles) * 16 * kRow;
     const v4s x = read_tr((vb ^ (t * 64)) + at), y = read_tr((vb ^ (t * 64) ^ Lanes<DP>::kDown) + at + 8 * kRow);
     return (v8s)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  v8s f[kAhead], p[QT][2];
+  v8s p[QT][2];
   float m[QT], sum[QT][2], e[QT][16], best[QT];
-#pragma unroll
-  for (int n = 0; n < kAhead; ++n) f[n] = key(n);
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
     // nothing seen so far: every weight is 2^(-inf) = 0
@@ -411,7 +423,7 @@ __device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, c
         nxt[qt][0] = mfma<DT>(f[st % kAhead], w.q[qt][st], nxt[qt][0]);
       }
     }
-    f[st % kAhead] = st + kAhead < kSteps ? key(st + kAhead) : value(st + kAhead - kSteps);
+    f[st % kAhead] = st + kAhead < kSteps ? key_operand(ln, k_next, st + kAhead) : value(st + kAhead - kSteps);
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
@@ -437,7 +449,7 @@ __device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, c
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt)
       w.o[qt][n % kTiles] = mfma<DT>(f[(n + kSteps) % kAhead], p[qt][n / kTiles], w.o[qt][n % kTiles]);
-    if (n + kAhead < 2 * kTiles) f[(n + kSteps) % kAhead] = value(n + kAhead);
+    f[(n + kSteps) % kAhead] = n + kAhead < 2 * kTiles ? value(n + kAhead) : key_operand(ln, k_after, n + kAhead - 2 * kTiles);
     // the next scores are ready by the second product
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
@@ -454,15 +466,16 @@ __device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, c
 }
 
 // Adds 32 keys from key kb to the rows' state, whose scores are `cur` with the largest `top`, and
-// forms (NEXT) the next 32 keys' scores `nxt` and `top` from the K rows at k_next.  `all`: every row
-// sees every key of the current 32.  `mine`: 32 rows of DP of the wave's own LDS.
+// forms (NEXT) the next 32 keys' scores `nxt` and `top` from the K rows at k_next (f, k_after: see
+// products).  `hidden` > 0: some row
+// does not see some key of the current 32.  `mine`: 32 rows of DP of the wave's own LDS.
 template <int DT, int DP, int QT, bool NEXT>
 __device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f (&cur)[QT][1], v16f (&nxt)[QT][1],
-                                     float (&top)[QT], uint32_t k_next, uint32_t v_lds, int kb, float c, bool all,
-                                     uint32_t mine, int lane) {
+                                     float (&top)[QT], v8s (&f)[kAhead], uint32_t k_next, uint32_t k_after,
+                                     uint32_t v_lds, int kb, float c, int hidden, uint32_t mine, int lane) {
   int odd = 0;   // some value is not finite
 #pragma unroll 1
-  for (int turns = turns_if(!all); turns > 0; --turns) {
+  for (int turns = turns_if(hidden); turns > 0; --turns) {
     mask_scores(cur, w, kb, lane >> 5);
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(cur[qt])) * c;
@@ -472,7 +485,7 @@ __device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f 
   raise(w, top);
   const uint32_t v_at = odd ? mine : v_lds;
   if constexpr (NEXT) {
-    products<DT, DP, QT>(w, ln, cur, nxt, top, k_next, v_at, c);
+    products<DT, DP, QT>(w, ln, cur, nxt, top, f, k_next, k_after, v_at, c);
   } else {
     v8s p[QT][1][2];
 #pragma unroll
@@ -480,7 +493,7 @@ __device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f 
     values<DT, DP, QT, 1>(w, p, ln, v_at);
   }
 #pragma unroll 1
-  for (int turns = turns_if(odd != 0); turns > 0; --turns)
+  for (int turns = turns_if(odd); turns > 0; --turns)
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt)
       add_not_finite<DT, DP>(w.o[qt], cur[qt][0], c, w.m[qt], w.lo[qt] - kb, w.hi[qt] - kb, v_lds, mine, lane);
@@ -588,13 +601,16 @@ constexpr int kTile = 64;
 template <int DP>
 constexpr int tile_bytes() { return kTile * DP * 2; }
 
-// Copies of one wave: kIters instructions for a tile of K or V, each of kRowsPer whole rows.
-template <int DP, int NW, bool PAGED>
+// Copies of one wave: kIters instructions for a tile of K or V, each of kRowsPer whole rows.  The
+// copy path of a CU takes 64 bytes a cycle, 512 cycles for a tile of K and V, and a wave waits while
+// it is busy.  So only the first NC waves copy: the waves of the other half, which share the SIMDs
+// with them, compute meanwhile, and the two are out of step from then on.
+template <int DP, int NC, bool PAGED>
 struct TileCopy {
   static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
   static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
-  static constexpr int kIters = kTile / (kRowsPer * NW);
-  static_assert(kIters >= 1 && (NW * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
+  static constexpr int kIters = kTile / (kRowsPer * NC);
+  static_assert(kIters >= 1 && (NC * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
   const Source& s;
   int wave, lane, chunk;    // chunk: the lane's 16 bytes of its row
   uint32_t k_ofs, v_ofs;    // byte offset of the lane from an instruction's first row
@@ -602,7 +618,7 @@ struct TileCopy {
 
   __device__ __forceinline__ TileCopy(const Source& src, int wv, int ln) : s(src), wave(wv), lane(ln) {
     const int r = wave * kRowsPer + lane / kChunks;
-    chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
+    chunk = (lane % kChunks) ^ swz<DP>(r);
     const uint32_t k_row = PAGED ? s.d_bytes : (uint32_t)s.k_step, v_row = PAGED ? s.d_bytes : (uint32_t)s.v_step;
     k_ofs = (lane / kChunks) * k_row + chunk * 16;
     v_ofs = (lane / kChunks) * v_row + chunk * 16;
@@ -615,10 +631,10 @@ struct TileCopy {
   __device__ __forceinline__ Pages pages(int kb) const {
     Pages p{};
     if constexpr (PAGED) {
-      if (whole) {
+      if (whole && wave < NC) {
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
-          const int j = kb + (it * NW + wave) * kRowsPer;
+          const int j = kb + (it * NC + wave) * kRowsPer;
           const auto at = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(s.table + page_of(s, j < s.keys ? j : 0));
           p.id[it] = *at;
         }
@@ -628,10 +644,11 @@ struct TileCopy {
   }
   template <bool V>
   __device__ __forceinline__ void issue(int kb, const Pages& p, uint32_t lds) const {
+    if (wave >= NC) return;
     if (whole && kb + kTile <= s.keys) {
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
-        const int j = kb + (it * NW + wave) * kRowsPer;
+        const int j = kb + (it * NC + wave) * kRowsPer;
         const char* base = V ? s.v : s.k;
         if constexpr (PAGED) {
           const int64_t off = (int64_t)p.id[it] * s.k_step + (int64_t)(j - page_of(s, j) * s.page_size) * s.d_bytes;
@@ -639,17 +656,17 @@ struct TileCopy {
         } else {
           base += (int64_t)j * (V ? s.v_step : s.k_step);
         }
-        dma16(base, V ? v_ofs : k_ofs, lds + (it * NW + wave) * 1024);
+        dma16(base, V ? v_ofs : k_ofs, lds + (it * NC + wave) * 1024);
       }
     } else {
 #pragma unroll 1
       for (int it = 0; it < kIters; ++it) {
-        const int j = kb + (it * NW + wave) * kRowsPer + lane / kChunks;
+        const int j = kb + (it * NC + wave) * kRowsPer + lane / kChunks;
         int page = 0;
         if constexpr (PAGED) page = j < s.keys ? s.table[page_of(s, j)] : -1;
         const char *k, *v;
         row_at<PAGED>(s, j, page, chunk * 16, k, v);
-        dma16_at(V ? v : k, (uint32_t)uni(lds + (it * NW + wave) * 1024));
+        dma16_at(V ? v : k, (uint32_t)uni(lds + (it * NC + wave) * 1024));
       }
     }
   }
@@ -668,8 +685,9 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   const int group = a.q_heads / a.kv_heads, rows = it.news * group;
   const int first = it.row0 + wave * QT * 32;
   constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
-  const TileCopy<DP, NW, PAGED> cp(s, wave, lane);
-  typename TileCopy<DP, NW, PAGED>::Pages p1{}, p2{};
+  using Copy = TileCopy<DP, NW / 2, PAGED>;
+  const Copy cp(s, wave, lane);
+  typename Copy::Pages p1{}, p2{};
   uint32_t k_now = lds, k_next = lds + kBytes, k_free = lds + 2 * kBytes;
   uint32_t v_now = lds + 3 * kBytes, v_next = lds + 4 * kBytes;
   if (t0 < t1) {
@@ -691,9 +709,9 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   const float c = a.scale * kLog2e;
   const Lanes<DP> ln(lane);
   const uint32_t mine = lds + 5 * kBytes + wave * kHalf;
-  // tiles that some row of the wave sees, and whether all rows see 32 keys
+  // tiles that some row of the wave sees, and (> 0) whether some row does not see some of 32 keys
   const int w0 = clampi(lo_min / kTile, t0, t1), w1 = clampi((hi_max + kTile - 1) / kTile, w0, t1);
-  auto all = [&](int kb) { return kb + 32 <= hi_min && kb >= lo_max; };
+  auto hidden = [&](int kb) { return kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb; };
   int t = t0;
   auto begin = [&]() {
     if (t > t0) {
@@ -730,13 +748,16 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
     scores<DT, DP, QT, 1>(sa, w, ln, k_now);
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(sa[qt])) * c;
+    v8s f[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) f[n] = key_operand(ln, k_now + kHalf, n);
     // past the last tile the next scores are formed from whatever the buffer holds, and not used
 #pragma unroll 1
     do {
       begin();
       const int kb = t * kTile;
-      step<DT, DP, QT, true>(w, ln, sa, sb, top, k_now + kHalf, v_now, kb, c, all(kb), mine, lane);
-      step<DT, DP, QT, true>(w, ln, sb, sa, top, k_next, v_now + kHalf, kb + 32, c, all(kb + 32), mine, lane);
+      step<DT, DP, QT, true>(w, ln, sa, sb, top, f, k_now + kHalf, k_next, v_now, kb, c, hidden(kb), mine, lane);
+      step<DT, DP, QT, true>(w, ln, sb, sa, top, f, k_next, k_next + kHalf, v_now + kHalf, kb + 32, c, hidden(kb + 32), mine, lane);
       end_tile();
     } while (t < w1);
   }
@@ -765,7 +786,7 @@ extern __shared__ __align__(1024) unsigned char dyn_lds[];
 // prompt's longest rows come first, and key/value heads are the fastest
 // index, so that workgroups on one XCD (dispatched round robin) share a head.
 template <int DT, int DP, int QT, int NW>
-__global__ void __launch_bounds__(64 * NW, QT == 2 ? 1 : 2) prompt_attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(AttnArgs a) {
   __shared__ int found;
   constexpr int kRows = 32 * QT * NW;
   const int tid = threadIdx.x;
@@ -968,7 +989,7 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 
 // ---------------------------------------------------------------- paged: many rows
 template <int DT, int DP, int QT, int NW>
-__global__ void __launch_bounds__(64 * NW, QT == 2 ? 1 : 2)
+__global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int64_t lds[NW + 2];
   constexpr int kRows = 32 * QT * NW;
@@ -1047,7 +1068,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 #pragma unroll
       for (int it = 0; it < kIters; ++it) {
         const int r = it * kRowsPer + lane / kChunks, j = kb + r;
-        const int chunk = (lane % kChunks) ^ (swz(r) & (kChunks - 1));
+        const int chunk = (lane % kChunks) ^ swz<DP>(r);
         const int pg = j < s.keys ? win[wave][page_of(s, j) - win0] : -1;
         const char *k, *v;
         row_at<true>(s, j, pg, chunk * 16, k, v);
@@ -1068,10 +1089,12 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       if (kb < hi_max && kb + 32 > lo_min) {
         v16f sc[1][1];
         float top[1];
+        v8s none[kAhead];
         scores<DT, DP, 1, 1>(sc, st, ln, at);
         top[0] = both_max(largest(sc[0])) * c;
         // the K rows are not needed any more: their place is the wave's scratch
-        step<DT, DP, 1, false>(st, ln, sc, sc, top, 0, at + 32 * DP * 2, kb, c, kb + 32 <= hi_min && kb >= lo_max, at, lane);
+        step<DT, DP, 1, false>(st, ln, sc, sc, top, none, 0, 0, at + 32 * DP * 2, kb, c,
+                                 uni(kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb), at, lane);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (t + 2 < n) issue(t + 2);
