@@ -6,6 +6,28 @@
 
 namespace nvfp4 {
 
+// ---------------------------------------------------------------- division by a run-time number
+// floor(j / d) = (j * magic) >> (32 + shift) for 0 <= j < 2^31, 2 <= d < 2^31: magic =
+// ceil(2^(32+shift) / d), shift = ceil(log2 d) - 1 (division_magic); d = 1 has magic 0.
+__device__ __forceinline__ int divide(int j, uint32_t magic, int shift) {
+  return magic ? (int)(__umulhi((uint32_t)j, magic) >> shift) : j;
+}
+inline void division_magic(int d, uint32_t& magic, int& shift) {
+  magic = 0;
+  shift = 0;
+  if (d <= 1) return;
+  int up = 0;
+  while ((1ll << up) < d) ++up;
+  shift = up - 1;
+  magic = (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
+}
+
+// a / b for 0 <= a, 0 < b; almost always both fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+
 struct PageMapsArgs {
   const int32_t* ctx_lens;
   const int32_t* new_lens;
@@ -18,6 +40,8 @@ struct PageMapsArgs {
   int64_t* slot_map;
   int32_t* positions;
   int32_t* taken;              // [1]
+  uint32_t magic;              // division by page_size, set by the launcher
+  int shift;
 };
 hipError_t launch_page_maps(const PageMapsArgs& a, hipStream_t s);
 
@@ -52,6 +76,9 @@ struct AttnArgs {
   void* out;                   // [tokens, q_heads, head_dim]
   float* lse;                  // [tokens, q_heads] or null
   void* workspace;             // paged
+  // set by the launchers: q_heads / kv_heads, and its division (see divide)
+  int group, group_shift;
+  uint32_t group_magic;
 };
 bool prompt_attn_fits(const AttnArgs& a);   // the grid
 hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s);

@@ -31,6 +31,8 @@
 #include "device_common.h"
 #include "lds_dma.h"
 
+#include <atomic>
+
 namespace nvfp4 {
 
 namespace {
@@ -80,6 +82,8 @@ __device__ __forceinline__ int64_t uni64(int64_t v) {
   return (int64_t)(((uint64_t)(uint32_t)uni((int)(v >> 32)) << 32) | (uint32_t)uni((int)v));
 }
 
+__device__ __forceinline__ int token_of(const AttnArgs& a, int row) { return divide(row, a.group_magic, a.group_shift); }
+
 // ---------------------------------------------------------------- LDS tiles
 // A tile is rows of DP elements; 16-byte chunk p of row r holds chunk p ^
 // swz(r) of the row.  LDS serves 256 bytes (all 64 banks) a cycle: 16 lanes of
@@ -122,18 +126,14 @@ struct Source {
   int64_t k_step, v_step;   // prompt: bytes from key to key; paged: bytes from page to page (k_step)
   const int32_t* table;  // paged: the request's row of the block table
   int page_size;
-  uint32_t magic;        // paged: key / page_size as a multiply-high (see page_magic)
+  uint32_t magic;        // paged: key / page_size as a multiply-high (see divide)
   int shift;
   int64_t num_pages;
   int keys;              // keys that exist
   int d_bytes;           // bytes of a row
 };
 
-// floor(j / d) = (j * magic) >> (32 + shift) for 0 <= j < 2^31, 2 <= d < 2^31:
-// magic = ceil(2^(32+shift) / d), shift = ceil(log2 d) - 1; d = 1 has magic 0.
-__device__ __forceinline__ int page_of(const Source& s, int j) {
-  return s.magic ? (int)(__umulhi((uint32_t)j, s.magic) >> s.shift) : j;
-}
+__device__ __forceinline__ int page_of(const Source& s, int j) { return divide(j, s.magic, s.shift); }
 
 template <bool PAGED>
 __device__ __forceinline__ void row_at(const Source& s, int j, int page, int chunk_bytes, const char*& k, const char*& v) {
@@ -515,12 +515,12 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // one's limits and zero queries.
 template <int DP, int QT>
 __device__ __forceinline__ void load_rows(Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
-  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int group = a.group, rows = it.news * group;
   const int h = lane >> 5, col = lane & 31;
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
-    const int r = row0 + qt * 32 + col;
-    const int tok = (r < rows ? r : rows - 1) / group, hd = it.head * group + r % group;
+    const int r = row0 + qt * 32 + col, at = r < rows ? r : rows - 1;
+    const int tok = token_of(a, at), hd = it.head * group + at - tok * group;
     const char* q = (const char*)a.q + ((int64_t)(it.start + tok) * a.q_stride + (int64_t)hd * a.q_head_stride) * 2;
 #pragma unroll
     for (int st = 0; st < DP / 16; ++st) {
@@ -544,7 +544,7 @@ __device__ __forceinline__ void load_rows(Rows<DP, QT>& w, const AttnArgs& a, co
 // Writes finished rows.
 template <int DT, int DP, int QT>
 __device__ __forceinline__ void store_rows(const Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
-  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int group = a.group, rows = it.news * group;
   const int h = lane >> 5, col = lane & 31;
 #pragma unroll
   for (int qt = 0; qt < QT; ++qt) {
@@ -552,7 +552,8 @@ __device__ __forceinline__ void store_rows(const Rows<DP, QT>& w, const AttnArgs
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int r = row0 + qt * 32 + col;
     if (r >= rows) continue;
-    const int64_t at = (int64_t)(it.start + r / group) * a.q_heads + it.head * group + r % group;
+    const int tok = token_of(a, r);
+    const int64_t at = (int64_t)(it.start + tok) * a.q_heads + it.head * group + r - tok * group;
     uint32_t* out = (uint32_t*)a.out + at * (a.head_dim / 2);
 #pragma unroll
     for (int t = 0; t < DP / 32; ++t)
@@ -597,6 +598,8 @@ __device__ __forceinline__ void store_part(const Rows<DP, QT>& w, float* o, floa
 // A workgroup of NW waves, QT x 32 rows each; all waves share the tiles of 64
 // keys, copied global -> LDS.
 constexpr int kTile = 64;
+constexpr int kManyWaves = 8, kManyTiles = 1, kManyRows = 32 * kManyTiles * kManyWaves;
+constexpr int kManyShares = 256;   // one workgroup on each of the 256 CUs
 
 template <int DP>
 constexpr int tile_bytes() { return kTile * DP * 2; }
@@ -682,7 +685,7 @@ template <int DT, int DP, int QT, int NW, bool PAGED>
 __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, const Item& it, int t0, int t1,
                                           Rows<DP, QT>& w, uint32_t lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
-  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int rows = it.news * a.group;
   const int first = it.row0 + wave * QT * 32;
   constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
   using Copy = TileCopy<DP, NW / 2, PAGED>;
@@ -702,7 +705,7 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   // limits of the wave's rows: positions of its first and last row
   const bool active = first < rows;
   const int end = first + QT * 32 < rows ? first + QT * 32 : rows;
-  const int pos0 = it.keys - it.news + first / group, pos1 = it.keys - it.news + (end - 1) / group;
+  const int pos0 = it.keys - it.news + token_of(a, first), pos1 = it.keys - it.news + (end > 0 ? token_of(a, end - 1) : 0);
   const int hi_min = uni(pos0 + 1), hi_max = uni(active ? pos1 + 1 : 0);
   const int lo_min = uni((a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0);
   const int lo_max = uni((a.window > 0 && pos1 + 1 > a.window) ? pos1 + 1 - a.window : 0);
@@ -767,9 +770,9 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
 
 // Tiles of `unit` keys that the rows row0 .. row0 + block - 1 see.
 __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Item& it, int row0, int block, int unit, int& t0, int& t1) {
-  const int group = a.q_heads / a.kv_heads, rows = it.news * group;
+  const int rows = it.news * a.group;
   const int end = row0 + block < rows ? row0 + block : rows;
-  const int p0 = it.keys - it.news + row0 / group, p1 = it.keys - it.news + (end - 1) / group;
+  const int p0 = it.keys - it.news + token_of(a, row0), p1 = it.keys - it.news + token_of(a, end - 1);
   const int lo = (a.window > 0 && p0 + 1 > a.window) ? p0 + 1 - a.window : 0;
   t0 = lo / unit;
   t1 = p1 + 1 > 0 ? (p1 + unit) / unit : 0;
@@ -791,21 +794,34 @@ __global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(
   constexpr int kRows = 32 * QT * NW;
   const int tid = threadIdx.x;
   const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
-  const int group = a.q_heads / a.kv_heads;
-  if (tid == 0) found = 0;
-  __syncthreads();
-  int n = 0;
-  for (int i = tid; i <= a.seqs; i += 64 * NW)
-    n += (int64_t)clampi(a.cu[i], 0, a.tokens) * group / kRows + i <= b ? 1 : 0;
-  if (n) atomicAdd(&found, n);
-  __syncthreads();
-  const int req = uni(found) - 1;
-  if (req < 0) return;
-  const int start = clampi(uni(a.cu[req]), 0, a.tokens);
-  const int stop = req < a.seqs ? clampi(uni(a.cu[req + 1]), start, a.tokens) : a.tokens;
+  const int group = a.group;
+  // tokens * group <= 2^30
+  auto first_block = [&](int start, int i) { return (int)((uint32_t)(start * group) / kRows) + i; };
+  int req, start, stop;
+  if (a.seqs < 64) {   // a request per lane
+    const int i = tid & 63;
+    const int at = i <= a.seqs ? clampi(a.cu[i], 0, a.tokens) : a.tokens;
+    req = __popcll(__ballot(i <= a.seqs && first_block(at, i) <= b)) - 1;
+    if (req < 0) return;
+    start = __builtin_amdgcn_readlane(at, req);
+    stop = __builtin_amdgcn_readlane(at, req < 63 ? req + 1 : 63);
+  } else {
+    if (tid == 0) found = 0;
+    __syncthreads();
+    int n = 0;
+    for (int i = tid; i <= a.seqs; i += 64 * NW) n += first_block(clampi(a.cu[i], 0, a.tokens), i) <= b ? 1 : 0;
+    if (n) atomicAdd(&found, n);
+    __syncthreads();
+    req = uni(found) - 1;
+    if (req < 0) return;
+    start = clampi(uni(a.cu[req]), 0, a.tokens);
+    stop = req < a.seqs ? uni(a.cu[req + 1]) : a.tokens;
+  }
+  if (req >= a.seqs) stop = a.tokens;
+  stop = clampi(stop, start, a.tokens);
   const int news = stop - start;
-  const int blocks = (int)(((int64_t)news * group + kRows - 1) / kRows);
-  const int rb = b - (int)((int64_t)start * group / kRows + req);
+  const int blocks = (int)((uint32_t)(news * group + kRows - 1) / kRows);
+  const int rb = b - first_block(start, req);
   if (rb < 0 || rb >= blocks) return;
   Item it{start, news, news, head, (blocks - 1 - rb) * kRows};
   Source s{};
@@ -831,113 +847,141 @@ __global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(
 // Each workgroup sums the units of all requests itself (one load and one scan
 // for up to 256 requests), which is cheaper than another launch.
 struct Split {
-  int block;      // rows of a block
-  int unit;       // keys of a unit
   int min_rows;   // requests with min_rows <= rows <= max_rows take part
   int max_rows;
-  int shares;     // workgroups
 };
 
 struct Req {
-  int start, news, keys, t0, tiles, blocks;
-  int64_t units;   // of one head
+  int start, news, keys;
+  int t0, tiles;    // tiles that some row sees
+  int blocks;
+  int64_t units;    // of all heads
 };
 
+// BLOCK rows, UNIT keys of a tile (powers of two).
+template <int BLOCK, int UNIT>
 __device__ __forceinline__ Req request(const AttnArgs& a, const Split& sp, int i) {
   Req r;
   r.start = clampi(a.cu[i], 0, a.tokens);
   const int stop = i < a.seqs ? clampi(a.cu[i + 1], r.start, a.tokens) : a.tokens;
   r.news = stop - r.start;
-  r.keys = 0;
-  if (i < a.seqs) {
-    const int64_t most = (int64_t)a.max_pages * a.page_size;
-    r.keys = a.kv_lens[i];
-    if (r.keys < 0) r.keys = 0;
-    if (r.keys > most) r.keys = (int)most;
-  }
-  const int group = a.q_heads / a.kv_heads;
-  const int64_t rows = (int64_t)r.news * group;
+  r.keys = i < a.seqs ? clampi(a.kv_lens[i], 0, a.max_pages * a.page_size) : 0;
+  const int rows = r.news * a.group;
   r.units = 0;
   r.t0 = r.tiles = r.blocks = 0;
   if (rows >= sp.min_rows && rows <= sp.max_rows && rows > 0) {
     const int p = r.keys - r.news;   // position of the first row
     const int lo = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
-    r.t0 = lo / sp.unit;
-    const int t1 = (r.keys + sp.unit - 1) / sp.unit;
+    r.t0 = lo / UNIT;
+    const int t1 = (int)((uint32_t)(r.keys + UNIT - 1) / UNIT);
     r.tiles = t1 > r.t0 ? t1 - r.t0 : 1;   // a request without keys still has its rows written
-    r.blocks = (int)((rows + sp.block - 1) / sp.block);
-    r.units = (int64_t)r.blocks * r.tiles;
+    r.blocks = (int)((uint32_t)(rows + BLOCK - 1) / BLOCK);
+    r.units = (int64_t)r.blocks * r.tiles * a.kv_heads;
   }
   return r;
 }
 
-struct Place {
-  int req;          // request, seqs + 1 if past the end
-  int64_t before;   // units before this request (all heads)
-  int64_t total;
-  int64_t share;    // units of a share
-};
+// The place of a share's first unit, and access to the requests from there on.  Up to 63 requests
+// (and the rows past the last) are held one per lane, by every wave for itself: one load, a scan over
+// the lanes and no barrier.  More are summed by the workgroup and loaded again when they are reached.
+template <int BLOCK, int UNIT, int SHARES, int NT>
+struct Plan {
+  const AttnArgs& a;
+  const Split& sp;
+  Req mine;         // of request `lane`
+  int req;          // request of the first unit, > seqs if past the end
+  int64_t before;   // units before this request
+  int64_t total, share;
 
-// Finds the request of unit `u` (or of the first unit of share `w`).
-template <int NT>
-__device__ __forceinline__ Place find_place(const AttnArgs& a, const Split& sp, int w, int64_t* lds) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = a.seqs + 1, per = (n + NT - 1) / NT;
-  const int i0 = tid * per, i1 = i0 + per < n ? i0 + per : n;
-  int64_t v = 0;
-  for (int i = i0; i < i1; ++i) v += request(a, sp, i).units;
-  v *= a.kv_heads;
-  int64_t x = v;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t y = __shfl_up(x, off, 64);
-    if (lane >= off) x += y;
-  }
-  if (lane == 63) lds[wave] = x;
-  if (tid == 0) lds[NT / 64] = -1;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int k = 0; k < NT / 64; ++k) {
-    if (k < wave) before += lds[k];
-    total += lds[k];
-  }
-  before += x - v;
-  Place p;
-  p.total = total;
-  p.share = (total + sp.shares - 1) / sp.shares;
-  if (p.share < 1) p.share = 1;
-  const int64_t u = p.share * w;
-  if (u >= before && u < before + v) {
-    for (int i = i0; i < i1; ++i) {
-      const int64_t r = request(a, sp, i).units * a.kv_heads;
-      if (u < before + r) {
-        lds[NT / 64] = i;
-        lds[NT / 64 + 1] = before;
-        break;
+  __device__ __forceinline__ Plan(const AttnArgs& args, const Split& split, int w, int64_t* lds) : a(args), sp(split) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (a.seqs < 64) {
+      mine = Req{};
+      if (lane <= a.seqs) mine = request<BLOCK, UNIT>(a, sp, lane);
+      int64_t x = mine.units;
+#pragma unroll 1
+      for (int off = 1; off <= a.seqs; off <<= 1) {
+        const int64_t y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
       }
-      before += r;
+      set_total(lane64(x, a.seqs));
+      const int64_t u = share * w;
+      // the requests whose units end at or before u come first
+      req = __popcll(__ballot(lane <= a.seqs && x <= u));
+      before = req > 0 ? lane64(x, req - 1) : 0;
+      return;
     }
+    const int n = a.seqs + 1, per = (n + NT - 1) / NT;
+    const int i0 = tid * per, i1 = i0 + per < n ? i0 + per : n;
+    int64_t v = 0;
+    for (int i = i0; i < i1; ++i) v += request<BLOCK, UNIT>(a, sp, i).units;
+    int64_t x = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t y = __shfl_up(x, off, 64);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) lds[wave] = x;
+    if (tid == 0) lds[NT / 64] = n;
+    __syncthreads();
+    int64_t start = x - v, all = 0;
+#pragma unroll
+    for (int k = 0; k < NT / 64; ++k) {
+      if (k < wave) start += lds[k];
+      all += lds[k];
+    }
+    set_total(uni64(all));
+    const int64_t u = share * w;
+    if (u >= start && u < start + v) {
+      for (int i = i0; i < i1; ++i) {
+        const int64_t r = request<BLOCK, UNIT>(a, sp, i).units;
+        if (u < start + r) {
+          lds[NT / 64] = i;
+          lds[NT / 64 + 1] = start;
+          break;
+        }
+        start += r;
+      }
+    }
+    __syncthreads();
+    req = uni((int)lds[NT / 64]);
+    before = req < n ? uni64(lds[NT / 64 + 1]) : 0;
   }
-  __syncthreads();
-  p.total = uni64(p.total);
-  p.share = uni64(p.share);
-  p.req = uni((int)lds[NT / 64]);
-  p.before = uni64(lds[NT / 64 + 1]);
-  if (p.req < 0) p.req = n;
-  return p;
-}
+  __device__ __forceinline__ static int64_t lane64(int64_t v, int l) {
+    return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32) |
+                     (uint32_t)__builtin_amdgcn_readlane((int)v, l));
+  }
+  __device__ __forceinline__ void set_total(int64_t all) {
+    total = all;
+    share = (all + SHARES - 1) / SHARES;
+    if (share < 1) share = 1;
+  }
+  __device__ __forceinline__ Req get(int i) const {
+    if (a.seqs < 64) {
+      Req r;
+      r.start = __builtin_amdgcn_readlane(mine.start, i);
+      r.news = __builtin_amdgcn_readlane(mine.news, i);
+      r.keys = __builtin_amdgcn_readlane(mine.keys, i);
+      r.t0 = __builtin_amdgcn_readlane(mine.t0, i);
+      r.tiles = __builtin_amdgcn_readlane(mine.tiles, i);
+      r.blocks = __builtin_amdgcn_readlane(mine.blocks, i);
+      r.units = lane64(mine.units, i);
+      return r;
+    }
+    return request<BLOCK, UNIT>(a, sp, i);
+  }
+};
 
 // Segment of a share: the tiles [t0, t1) of one item.
 struct Segment {
   Item it;
-  int req, t0, t1, tiles, tile_base;
+  int req, t0, t1;
 };
 
-template <int DP, int ROWS>
-__device__ __forceinline__ void part_of(float* ws, int shares, int slot, float*& o, float*& ml) {
+template <int DP, int ROWS, int SHARES>
+__device__ __forceinline__ void part_of(float* ws, int slot, float*& o, float*& ml) {
   ml = ws + (int64_t)slot * ROWS * 2;
-  o = ws + (int64_t)shares * 2 * ROWS * 2 + (int64_t)slot * ROWS * DP;
+  o = ws + (int64_t)SHARES * 2 * ROWS * 2 + (int64_t)slot * ROWS * DP;
 }
 
 __device__ __forceinline__ void paged_source(const AttnArgs& a, const Item& it, int req, Source& s, uint32_t magic, int shift) {
@@ -955,47 +999,45 @@ __device__ __forceinline__ void paged_source(const AttnArgs& a, const Item& it, 
 }
 
 // Walks the segments of share w; f(segment, slot or -1).
-template <int NT, typename F>
+template <int BLOCK, int UNIT, int SHARES, int NT, typename F>
 __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp, int w, int64_t* lds, F f) {
-  const Place pl = find_place<NT>(a, sp, w, lds);
+  const Plan<BLOCK, UNIT, SHARES, NT> pl(a, sp, w, lds);
   int64_t u = pl.share * w;
-  int64_t end = u + pl.share < pl.total ? u + pl.share : pl.total;
-  const int64_t begin = u;
+  const int64_t begin = u, end = u + pl.share < pl.total ? u + pl.share : pl.total;
   int64_t before = pl.before;
+#pragma unroll 1
   for (int req = pl.req; req <= a.seqs && u < end; ++req) {
-    const Req r = request(a, sp, req);
-    const int64_t all = r.units * a.kv_heads;
-    while (u < end && u < before + all) {
-      const int64_t in = u - before;
-      const int head = (int)(in / r.units);
-      const int64_t rest = in - head * r.units;
-      const int rb = (int)(rest / r.tiles), tile = (int)(rest - (int64_t)rb * r.tiles);
+    const Req r = pl.get(req);
+#pragma unroll 1
+    while (u < end && u < before + r.units) {
+      const int64_t item = quotient(u - before, r.tiles);   // (head, block)
+      const int tile = (int)(u - before - item * r.tiles);
+      const int head = (int)quotient(item, r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
       const int64_t left = end - u;
       const int count = left < r.tiles - tile ? (int)left : r.tiles - tile;
       Segment g;
-      g.it = Item{r.start, r.news, r.keys, head, rb * sp.block};
+      g.it = Item{uni(r.start), uni(r.news), uni(r.keys), uni(head), uni(rb * BLOCK)};
       g.req = req;
-      g.t0 = r.t0 + tile;
-      g.t1 = g.t0 + count;
+      g.t0 = uni(r.t0 + tile);
       // no key at all: the unit only writes the rows
-      if (r.keys == 0) g.t1 = g.t0;
+      g.t1 = uni(r.keys == 0 ? r.t0 + tile : r.t0 + tile + count);
       const bool whole = tile == 0 && count == r.tiles;
-      f(g, whole ? -1 : 2 * w + (u > begin ? 1 : 0));
+      f(g, uni(whole ? -1 : 2 * w + (u > begin ? 1 : 0)));
       u += count;
     }
-    before += all;
+    before += r.units;
   }
 }
 
 // ---------------------------------------------------------------- paged: many rows
 template <int DT, int DP, int QT, int NW>
-__global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2)
+__global__ void __launch_bounds__(64 * NW, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int64_t lds[NW + 2];
   constexpr int kRows = 32 * QT * NW;
-  const int per = sp.shares / 8;   // shares is a multiple of 8: an XCD takes consecutive shares
-  const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  for_segments<64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+  // an XCD takes consecutive shares, so that workgroups that read the same keys share its L2
+  const int w = (blockIdx.x & 7) * (kManyShares / 8) + (blockIdx.x >> 3);
+  for_segments<kRows, kTile, kManyShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
     paged_source(a, g.it, g.req, s, magic, shift);
     int b0, b1;
@@ -1008,7 +1050,7 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       store_rows<DT, DP, QT>(rows, a, g.it, g.it.row0 + row, lane);
     } else {
       float *o, *ml;
-      part_of<DP, kRows>((float*)a.workspace, sp.shares, slot, o, ml);
+      part_of<DP, kRows, kManyShares>((float*)a.workspace, slot, o, ml);
       store_part<DP, QT>(rows, o, ml, row, kRows, lane);
     }
   });
@@ -1021,6 +1063,8 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // barrier; the waves' states are joined at the end.  Page ids come from a
 // window of the block table in LDS, so that the copies in flight are not
 // waited for together with a page id.
+constexpr int kFewRows = 32, kFewWaves = 2;
+constexpr int kFewShares = 512;    // two workgroups on each CU
 constexpr int kWindow = 256;   // page ids a wave keeps
 
 template <int DT, int DP, int NW>
@@ -1035,14 +1079,13 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   const uint32_t mem = lds_addr(dyn_lds) + wave * 2 * kStage;
   float* join_o = (float*)dyn_lds;          // [NW][32][DP] after the copies
   const Lanes<DP> ln(lane);
-  const int per = sp.shares / 8;
-  const int w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  for_segments<64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+  const int w = (blockIdx.x & 7) * (kFewShares / 8) + (blockIdx.x >> 3);
+  for_segments<kFewRows, 32 * NW, kFewShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
     paged_source(a, g.it, g.req, s, magic, shift);
-    const int group = a.q_heads / a.kv_heads, rows = g.it.news * group;
+    const int group = a.group, rows = g.it.news * group;
     const int last = (g.it.row0 + 32 < rows ? g.it.row0 + 32 : rows) - 1;
-    const int p0 = g.it.keys - g.it.news + g.it.row0 / group, p1 = g.it.keys - g.it.news + last / group;
+    const int p0 = g.it.keys - g.it.news + token_of(a, g.it.row0), p1 = g.it.keys - g.it.news + token_of(a, last);
     const int hi_min = p0 + 1, hi_max = p1 + 1;
     const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
     const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
@@ -1122,7 +1165,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     __syncthreads();
     // thread: one row's four values of d at a time
     float *po = nullptr, *pml = nullptr;
-    if (slot >= 0) part_of<DP, 32>((float*)a.workspace, sp.shares, slot, po, pml);
+    if (slot >= 0) part_of<DP, kFewRows, kFewShares>((float*)a.workspace, slot, po, pml);
     for (int k = tid; k < 32 * (DP / 4); k += 64 * NW) {
       const int r = k / (DP / 4), q = k % (DP / 4), row = g.it.row0 + r;
       if (row >= rows) continue;
@@ -1142,7 +1185,8 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       }
       if (slot < 0) {
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        const int64_t at = (int64_t)(g.it.start + row / group) * a.q_heads + g.it.head * group + row % group;
+        const int tok = token_of(a, row);
+        const int64_t at = (int64_t)(g.it.start + tok) * a.q_heads + g.it.head * group + row - tok * group;
         if (q * 4 < a.head_dim)
           *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
               (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
@@ -1159,73 +1203,119 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // ---------------------------------------------------------------- paged: join the parts
 // Workgroup w: the item that share w's first unit lies inside of, if no
 // earlier share starts inside it too.  Its parts are the last segment of share
-// w - 1 and the first segments of the shares from w on.
-template <int DT, int DP, int ROWS>
+// w - 1 and the first segments of the shares from w on.  The parts come from
+// other XCDs' L2s, so a load takes most of a microsecond and what counts is
+// that few wait for one another: 8 groups of threads (DP = 128; a group holds a
+// row) either take 8 rows, each reading kBatch parts at a time (ROWS = 256: two
+// or three parts), or every 8th part of one row after another (ROWS = 32: a
+// long request alone has dozens of parts).
+constexpr int kBatch = 4;
+
+template <int DT, int DP, int ROWS, int UNIT, int SHARES>
 __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
+  constexpr int kQ = DP / 4, kGroups = 256 / kQ;
+  constexpr bool kByPart = ROWS <= 32;
   __shared__ int64_t lds[6];
+  __shared__ float part_m[kByPart ? kBatch : 1][kGroups], part_l[kByPart ? kBatch : 1][kGroups];
+  __shared__ v4f part_o[kByPart ? kBatch : 1][kGroups][kQ];
   const int w = blockIdx.x + 1, tid = threadIdx.x;
-  const Place pl = find_place<256>(a, sp, w, lds);
-  if (pl.req > a.seqs) return;
-  const Req r = request(a, sp, pl.req);
-  const int64_t in = pl.share * w - pl.before;
-  const int64_t item = in / r.tiles;                         // (head, block) in this request
+  const Plan<ROWS, UNIT, SHARES, 256> pl(a, sp, w, lds);
+  if (pl.req > a.seqs || pl.share * w >= pl.total) return;
+  const Req r = pl.get(pl.req);
+  const int64_t item = quotient(pl.share * w - pl.before, r.tiles);   // (head, block) in this request
   const int64_t s0 = pl.before + item * r.tiles, s1 = s0 + r.tiles;
   if (s0 == pl.share * w || s0 < pl.share * (w - 1)) return;
-  const int last = (int)((s1 + pl.share - 1) / pl.share) - 1;
-  const int head = (int)(item / r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
-  const int group = a.q_heads / a.kv_heads, rows = r.news * group;
+  const int last = (int)quotient(s1 + pl.share - 1, pl.share) - 1;
+  const int head = (int)quotient(item, r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
+  const int group = a.group, rows = r.news * group - rb * ROWS < ROWS ? r.news * group - rb * ROWS : ROWS;
   const int first_slot = 2 * (w - 1) + (s0 > pl.share * (w - 1) ? 1 : 0);
-  constexpr int kQ = DP / 4;
-  const int row = blockIdx.y * (256 / kQ) + tid / kQ, q = tid % kQ;
-  const int gr = rb * ROWS + row;
-  if (row >= ROWS || gr >= rows) return;
-  float m = -__builtin_inff(), l = 0.0f;
-  v4f o = {0, 0, 0, 0};
-  for (int j = w - 1; j <= last; ++j) {
+  const int q = tid % kQ, g = tid / kQ;
+  auto load = [&](int j, int row, v2f& ml, v4f& x) {   // part j
     float *po, *pml;
-    part_of<DP, ROWS>((float*)a.workspace, sp.shares, j == w - 1 ? first_slot : 2 * j, po, pml);
-    const v2f ml = *(const v2f*)(pml + 2 * row);
-    const v4f x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
-    if (ml[0] == -__builtin_inff()) continue;
-    const float nm = __builtin_fmaxf(m, ml[0]);
-    const float u = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(ml[0] - nm);
-    l = l * u + ml[1] * v;
+    part_of<DP, ROWS, SHARES>((float*)a.workspace, j == w - 1 ? first_slot : 2 * j, po, pml);
+    ml = *(const v2f*)(pml + 2 * row);
+    x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
+  };
+  auto join = [&](float& m, float& l, v4f& o, float pm, float pl2, v4f x) {
+    if (pm == -__builtin_inff()) return;   // saw nothing
+    const float nm = __builtin_fmaxf(m, pm);
+    const float u = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(pm - nm);
+    l = l * u + pl2 * v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = o[e] * u + x[e] * v;
     m = nm;
+  };
+  auto write = [&](int row, float m, float l, v4f o) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int gr = rb * ROWS + row, tok = token_of(a, gr);
+    const int64_t at = (int64_t)(r.start + tok) * a.q_heads + head * group + gr - tok * group;
+    if (q * 4 < a.head_dim)
+      *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
+          (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+    if (a.lse && q == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+  };
+  if constexpr (!kByPart) {
+    const int row = blockIdx.y * kGroups + g;
+    if (row >= rows) return;
+    float m = -__builtin_inff(), l = 0.0f;
+    v4f o = {0, 0, 0, 0};
+    for (int j = w - 1; j <= last; j += kBatch) {
+      v2f ml[kBatch];
+      v4f x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) load(j + k < last ? j + k : last, row, ml[k], x[k]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (j + k <= last) join(m, l, o, ml[k][0], ml[k][1], x[k]);
+    }
+    write(row, m, l, o);
+  } else {
+    for (int row0 = 0; row0 < rows; row0 += kBatch) {
+      float m[kBatch], l[kBatch];
+      v4f o[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        m[k] = -__builtin_inff();
+        l[k] = 0.0f;
+        o[k] = (v4f){0, 0, 0, 0};
+      }
+      for (int j = w - 1 + g; j <= last; j += kGroups) {
+        v2f ml[kBatch];
+        v4f x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) load(j, row0 + k < rows ? row0 + k : rows - 1, ml[k], x[k]);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) join(m[k], l[k], o[k], ml[k][0], ml[k][1], x[k]);
+      }
+      if (row0 > 0) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (q == 0) {
+          part_m[k][g] = m[k];
+          part_l[k][g] = l[k];
+        }
+        part_o[k][g][q] = o[k];
+      }
+      __syncthreads();
+      if (g < kBatch && row0 + g < rows) {
+        float jm = -__builtin_inff(), jl = 0.0f;
+        v4f jo = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) join(jm, jl, jo, part_m[g][k], part_l[g][k], part_o[g][k][q]);
+        write(row0 + g, jm, jl, jo);
+      }
+    }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (int64_t)(r.start + gr / group) * a.q_heads + head * group + gr % group;
-  if (q * 4 < a.head_dim)
-    *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
-        (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-  if (a.lse && q == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host
-constexpr int kShares = 256;        // one workgroup on each of the 256 CUs
-constexpr int kFewRows = 32;
-constexpr int kManyWaves = 8, kManyTiles = 1;
-constexpr int kManyRows = 32 * kManyTiles * kManyWaves;
-
 // three tiles of K, two of V, and each wave's scratch for tiles with values that are not finite
 template <int DP>
 constexpr size_t many_lds_bytes() { return 5 * tile_bytes<DP>() + kManyWaves * 32 * DP * 2; }
-constexpr int kFewWaves = 4;
 template <int DP>
 constexpr size_t few_lds_bytes() { return kFewWaves * 2 * 2 * 32 * DP * 2; }
 
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
-
-void page_magic(int page, uint32_t& magic, int& shift) {
-  magic = 0;
-  shift = 0;
-  if (page <= 1) return;
-  int up = 0;
-  while ((1ll << up) < page) ++up;
-  shift = up - 1;
-  magic = (uint32_t)(((1ull << (32 + shift)) + page - 1) / page);
-}
 
 // Which of the two kernels a call can need: a request of more than kFewRows
 // rows needs more than one token per request on average or a group of heads
@@ -1239,13 +1329,29 @@ bool needs_few(int64_t seqs, int64_t tokens, int group) {
   return seqs > 1;
 }
 
-template <typename F>
-hipError_t launch_lds(F* f, dim3 grid, dim3 block, size_t lds, hipStream_t s, void** args) {
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+AttnArgs with_group(const AttnArgs& a) {
+  AttnArgs c = a;
+  c.group = a.q_heads / a.kv_heads;
+  division_magic(c.group, c.group_magic, c.group_shift);
+  return c;
+}
+
+// Launch of kernel F with more dynamic LDS than the 64 KiB a kernel gets unasked; asked for once on
+// each device.
+template <auto F, typename... A>
+hipError_t launch_lds(unsigned grid, unsigned block, size_t lds, hipStream_t s, A... args) {
+  static std::atomic<uint64_t> asked{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(F), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
+    asked.fetch_or(bit, std::memory_order_relaxed);
   }
-  return hipLaunchKernel((const void*)f, grid, block, args, lds, s);
+  F<<<dim3(grid), dim3(block), lds, s>>>(args...);
+  return hipGetLastError();
 }
 
 int64_t prompt_blocks(const AttnArgs& a) {
@@ -1254,39 +1360,36 @@ int64_t prompt_blocks(const AttnArgs& a) {
 
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  AttnArgs c = a;
-  void* args[] = {&c};
-  const int64_t blocks = prompt_blocks(a);
-  return launch_lds(prompt_attn_kernel<DT, DP, kManyTiles, kManyWaves>, dim3((unsigned)(blocks * a.kv_heads)),
-                    dim3(64 * kManyWaves), many_lds_bytes<DP>(), s, args);
+  return launch_lds<prompt_attn_kernel<DT, DP, kManyTiles, kManyWaves>>(
+      (unsigned)(prompt_blocks(a) * a.kv_heads), 64 * kManyWaves, many_lds_bytes<DP>(), s, with_group(a));
 }
 
 template <int DT, int DP>
 hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
-  const int group = a.q_heads / a.kv_heads;
-  const bool many = needs_many(a.seqs, a.tokens, group), few = needs_few(a.seqs, a.tokens, group);
-  AttnArgs c = a;
+  const AttnArgs c = with_group(a);
+  const bool many = needs_many(a.seqs, a.tokens, c.group), few = needs_few(a.seqs, a.tokens, c.group);
   uint32_t magic;
   int shift;
-  page_magic(a.page_size, magic, shift);
+  division_magic(a.page_size, magic, shift);
   hipError_t e = hipSuccess;
+  constexpr int kRowsAtOnce = 256 / (DP / 4);   // of a combining workgroup
   if (few) {
-    Split sp{kFewRows, 32 * kFewWaves, 1, many ? kFewRows : 0x7FFFFFFF, kShares};
-    void* args[] = {&c, &sp, &magic, &shift};
-    e = launch_lds(paged_few_kernel<DT, DP, kFewWaves>, dim3(kShares), dim3(64 * kFewWaves), few_lds_bytes<DP>(), s, args);
+    const Split sp{1, many ? kFewRows : 0x7FFFFFFF};
+    e = launch_lds<paged_few_kernel<DT, DP, kFewWaves>>(kFewShares, 64 * kFewWaves, few_lds_bytes<DP>(), s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
-    void* cargs[] = {&c, &sp};
-    e = launch_lds(combine_kernel<DT, DP, 32>, dim3(kShares - 1, 32 / (256 / (DP / 4))), dim3(256), 0, s, cargs);
+    combine_kernel<DT, DP, kFewRows, 32 * kFewWaves, kFewShares>
+        <<<dim3(kFewShares - 1), dim3(256), 0, s>>>(c, sp);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (many) {
-    Split sp{kManyRows, kTile, few ? kFewRows + 1 : 1, 0x7FFFFFFF, kShares};
-    void* args[] = {&c, &sp, &magic, &shift};
-    e = launch_lds(paged_rows_kernel<DT, DP, kManyTiles, kManyWaves>, dim3(kShares), dim3(64 * kManyWaves),
-                   many_lds_bytes<DP>(), s, args);
+    const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
+    e = launch_lds<paged_rows_kernel<DT, DP, kManyTiles, kManyWaves>>(kManyShares, 64 * kManyWaves, many_lds_bytes<DP>(),
+                                                                     s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
-    void* cargs[] = {&c, &sp};
-    e = launch_lds(combine_kernel<DT, DP, kManyRows>, dim3(kShares - 1, kManyRows / (256 / (DP / 4))), dim3(256), 0, s, cargs);
+    combine_kernel<DT, DP, kManyRows, kTile, kManyShares>
+        <<<dim3(kManyShares - 1, kManyRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
+    e = hipGetLastError();
   }
   return e;
 }
@@ -1296,8 +1399,9 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
 size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
   const int group = q_heads / kv_heads;
   const size_t per_row = ((size_t)padded_dim(head_dim) + 2) * sizeof(float);
-  const size_t rows = needs_many(seqs, tokens, group) ? kManyRows : kFewRows;
-  return (size_t)kShares * 2 * rows * per_row;
+  const size_t few = needs_few(seqs, tokens, group) ? (size_t)kFewShares * 2 * kFewRows * per_row : 0;
+  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kManyShares * 2 * kManyRows * per_row : 0;
+  return few > many ? few : many;
 }
 
 bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }

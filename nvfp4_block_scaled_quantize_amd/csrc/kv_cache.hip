@@ -30,12 +30,16 @@ constexpr int kMapThreads = 256;
 constexpr int kMapTokens = 2048;                       // tokens per workgroup
 constexpr int kMapPer = kMapTokens / kMapThreads;
 
-__device__ __forceinline__ int64_t len_of(const int32_t* p, int i) {
-  const int32_t v = p[i];
-  return v > 0 ? v : 0;
-}
+constexpr int kMost = 0x7FFFFFFF;
 
-__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int len_of(const int32_t* p, int i) { return p[i] > 0 ? p[i] : 0; }
+__device__ __forceinline__ int clamp64(int64_t v) { return v < kMost ? (int)v : kMost; }
+
+// Pages of n tokens: ceil(n / page_size), at most the table's width.
+__device__ __forceinline__ int pages_of(const PageMapsArgs& a, int n) {
+  const int p = n > 0 ? divide(n - 1, a.magic, a.shift) + 1 : 0;
+  return p < a.max_pages ? p : a.max_pages;
+}
 
 // Exclusive prefix of v over the threads of the workgroup; total in `all`.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s, int64_t& all) {
@@ -67,23 +71,23 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
   __shared__ int wave_last[kMapThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kMapTokens;
-  const int64_t P = a.page_size, width = a.max_pages;
+  const int width = a.max_pages;
   for (int k = tid; k < kMapTokens; k += kMapThreads) start_req[k] = -1;
 
   const int per = (a.seqs + kMapThreads - 1) / kMapThreads;
   const int i0 = tid * per, i1 = (i0 + per < a.seqs) ? i0 + per : a.seqs;
   int64_t tok = 0, pag = 0;
   for (int i = i0; i < i1; ++i) {
-    const int64_t c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i);
+    const int c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i);
     tok += m;
-    pag += min64((c + m + P - 1) / P, width) - min64((c + P - 1) / P, width);
+    pag += pages_of(a, clamp64((int64_t)c + m)) - pages_of(a, c);
   }
   int64_t all_tok, all_pag;
   int64_t at = block_scan(tok, scan, all_tok);
   int64_t page = block_scan(pag, scan, all_pag);   // its first barrier orders the fill of start_req
   const bool mine = (tid % gridDim.x) == blockIdx.x;   // writes this share's cu_new and kv_lens
   for (int i = i0; i < i1; ++i) {
-    const int64_t c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i);
+    const int c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i), all = clamp64((int64_t)c + m);
     if (m > 0 && at < t0 + kMapTokens && at + m > t0) {
       const int k = (int)(at > t0 ? at - t0 : 0);
       start_req[k] = i;
@@ -91,15 +95,15 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
       start_page[k] = page;
     }
     if (mine) {
-      a.cu_new[i] = (int32_t)min64(at, 0x7FFFFFFF);
-      a.kv_lens[i] = (int32_t)min64(c + m, 0x7FFFFFFF);
+      a.cu_new[i] = clamp64(at);
+      a.kv_lens[i] = all;
     }
     at += m;
-    page += min64((c + m + P - 1) / P, width) - min64((c + P - 1) / P, width);
+    page += pages_of(a, all) - pages_of(a, c);
   }
   if (blockIdx.x == 0 && tid == 0) {
-    a.cu_new[a.seqs] = (int32_t)min64(all_tok, 0x7FFFFFFF);
-    a.taken[0] = (int32_t)min64(all_pag, 0x7FFFFFFF);
+    a.cu_new[a.seqs] = clamp64(all_tok);
+    a.taken[0] = clamp64(all_pag);
   }
   __syncthreads();
 
@@ -133,19 +137,19 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
     int32_t position = -1;
     if (st >= 0 && t < all_tok) {
       const int i = start_req[st];
-      const int64_t c = len_of(a.ctx_lens, i);
-      const int64_t pos = c + (t - start_cu[st]);
-      const int64_t col = pos / P, held = min64((c + P - 1) / P, width);
-      int64_t pg = -1;
-      position = (int32_t)min64(pos, 0x7FFFFFFF);
+      const int c = len_of(a.ctx_lens, i);
+      position = clamp64(c + (t - start_cu[st]));
+      const int col = divide(position, a.magic, a.shift), place = position - col * a.page_size;
+      const int held = pages_of(a, c);
+      int pg = -1;
       if (col < held) {
         pg = a.block_table[(int64_t)i * width + col];
       } else if (col < width) {
         const int64_t f = start_page[st] + (col - held);
         if (f < a.num_free) pg = a.free_pages[f];
-        if (pos == col * P) a.block_table[(int64_t)i * width + col] = (int32_t)pg;
+        if (place == 0) a.block_table[(int64_t)i * width + col] = pg;
       }
-      if (pg >= 0) slot = pg * P + (pos - col * P);
+      if (pg >= 0) slot = (int64_t)pg * a.page_size + place;
     }
     a.slot_map[t] = slot;
     a.positions[t] = position;
@@ -160,12 +164,12 @@ template <typename U>
 __global__ void __launch_bounds__(256) kv_write_kernel(KvWriteArgs a, int units_row, int64_t total) {
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += step) {
-    const int64_t row = u / units_row;           // (token, head)
-    const int64_t t = row / a.kv_heads;
+    const int64_t row = quotient(u, units_row);           // (token, head)
+    const int64_t t = quotient(row, a.kv_heads);
     const int h = (int)(row - t * a.kv_heads), c = (int)(u - row * units_row);
     const int64_t slot = a.slot_map[t];
     if (slot < 0 || slot >= a.num_pages * a.page_size) continue;
-    const int64_t page = slot / a.page_size, place = slot - page * a.page_size;
+    const int64_t page = quotient(slot, a.page_size), place = slot - page * a.page_size;
     const int64_t to = ((page * a.kv_heads + h) * a.page_size + place) * units_row + c;
     const char* k = (const char*)a.k + (t * a.k_stride + (int64_t)h * a.k_head_stride) * 2;
     const char* v = (const char*)a.v + (t * a.v_stride + (int64_t)h * a.v_head_stride) * 2;
@@ -179,7 +183,9 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvWriteArgs a, int units_
 
 hipError_t launch_page_maps(const PageMapsArgs& a, hipStream_t s) {
   const int64_t blocks = (a.tokens + kMapTokens - 1) / kMapTokens;
-  page_maps_kernel<<<dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kMapThreads), 0, s>>>(a);
+  PageMapsArgs c = a;
+  division_magic(c.page_size, c.magic, c.shift);
+  page_maps_kernel<<<dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kMapThreads), 0, s>>>(c);
   return hipGetLastError();
 }
 
