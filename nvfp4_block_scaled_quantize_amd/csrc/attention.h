@@ -22,11 +22,11 @@ inline void division_magic(int d, uint32_t& magic, int& shift) {
   magic = (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
 }
 
-// a / b for 0 <= a, 0 < b; almost always both fit 32 bits.
+// floor(a / b) for 0 <= a < 2^52, 0 < b < 2^52: the binary64 quotient is within one of it.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  const int64_t q = (int64_t)((double)a / (double)b), r = a - q * b;
+  return r < 0 ? q - 1 : r >= b ? q + 1 : q;
 }
-
 
 struct PageMapsArgs {
   const int32_t* ctx_lens;

@@ -842,7 +842,9 @@ __global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(
 // The work of a call is the sequence of units (request, head, block of rows,
 // tile of keys), tiles innermost, and every workgroup takes an equal share of
 // consecutive units: long and short requests balance whatever their lengths,
-// which only the device knows.  A share that starts or ends inside an item
+// which only the device knows.  What an item costs besides its tiles (finding
+// it, its queries, the first copies, its results) counts as kExtra units ahead
+// of its tiles; a share that ends among those has none of the item's work.  A share that starts or ends inside an item
 // leaves a part (O, m, l) in the workspace, and combine_kernel joins the parts.
 // Each workgroup sums the units of all requests itself (one load and one scan
 // for up to 256 requests), which is cheaper than another launch.
@@ -850,6 +852,10 @@ struct Split {
   int min_rows;   // requests with min_rows <= rows <= max_rows take part
   int max_rows;
 };
+
+// Measured with 64-key units (64 requests of 100 .. 8192 keys): 158 us without, 122 / 111 / 104 /
+// 102 / 101 / 103 / 106 us with 1 / 2 / 3 / 4 / 5 / 6 / 8.
+constexpr int kExtra = 4;
 
 struct Req {
   int start, news, keys;
@@ -876,7 +882,7 @@ __device__ __forceinline__ Req request(const AttnArgs& a, const Split& sp, int i
     const int t1 = (int)((uint32_t)(r.keys + UNIT - 1) / UNIT);
     r.tiles = t1 > r.t0 ? t1 - r.t0 : 1;   // a request without keys still has its rows written
     r.blocks = (int)((uint32_t)(rows + BLOCK - 1) / BLOCK);
-    r.units = (int64_t)r.blocks * r.tiles * a.kv_heads;
+    r.units = (int64_t)r.blocks * (r.tiles + kExtra) * a.kv_heads;
   }
   return r;
 }
@@ -1010,19 +1016,22 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
     const Req r = pl.get(req);
 #pragma unroll 1
     while (u < end && u < before + r.units) {
-      const int64_t item = quotient(u - before, r.tiles);   // (head, block)
-      const int tile = (int)(u - before - item * r.tiles);
+      const int cost = r.tiles + kExtra;
+      const int64_t item = quotient(u - before, cost);   // (head, block)
+      const int at = (int)(u - before - item * cost);
       const int head = (int)quotient(item, r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
       const int64_t left = end - u;
-      const int count = left < r.tiles - tile ? (int)left : r.tiles - tile;
-      Segment g;
-      g.it = Item{uni(r.start), uni(r.news), uni(r.keys), uni(head), uni(rb * BLOCK)};
-      g.req = req;
-      g.t0 = uni(r.t0 + tile);
-      // no key at all: the unit only writes the rows
-      g.t1 = uni(r.keys == 0 ? r.t0 + tile : r.t0 + tile + count);
-      const bool whole = tile == 0 && count == r.tiles;
-      f(g, uni(whole ? -1 : 2 * w + (u > begin ? 1 : 0)));
+      const int count = left < cost - at ? (int)left : cost - at;
+      const int first = at > kExtra ? at - kExtra : 0, last = at + count - kExtra;
+      if (last > first) {
+        Segment g;
+        g.it = Item{uni(r.start), uni(r.news), uni(r.keys), uni(head), uni(rb * BLOCK)};
+        g.req = req;
+        g.t0 = uni(r.t0 + first);
+        // no key at all: the unit only writes the rows
+        g.t1 = uni(r.t0 + (r.keys == 0 ? first : last));
+        f(g, uni(first == 0 && last == r.tiles ? -1 : 2 * w + (u > begin ? 1 : 0)));
+      }
       u += count;
     }
     before += r.units;
@@ -1061,11 +1070,12 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // Nothing is shared between waves but the queries: wave w takes the 32-key
 // tiles w, w + NW, ... and copies them itself, two tiles ahead, without a
 // barrier; the waves' states are joined at the end.  Page ids come from a
-// window of the block table in LDS, so that the copies in flight are not
-// waited for together with a page id.
+// window of the block table in LDS: a load of them from memory would be waited
+// for together with the copies in flight (vector loads) or with the operands
+// from LDS (scalar loads).
+constexpr int kWindow = 256;   // page ids a wave keeps
 constexpr int kFewRows = 32, kFewWaves = 2;
 constexpr int kFewShares = 512;    // two workgroups on each CU
-constexpr int kWindow = 256;   // page ids a wave keeps
 
 template <int DT, int DP, int NW>
 __global__ void __launch_bounds__(64 * NW, 1)
@@ -1074,11 +1084,14 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int win[NW][kWindow];
   __shared__ float join_ml[NW][32][2];
   constexpr int kChunks = DP / 8, kRowsPer = 64 / kChunks, kIters = 32 / kRowsPer;
-  constexpr int kStage = 2 * 32 * DP * 2;   // bytes of one tile of K and V
+  constexpr int kHalf = 32 * DP * 2, kStage = 2 * kHalf;   // bytes of a tile of K, of K and V
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const uint32_t mem = lds_addr(dyn_lds) + wave * 2 * kStage;
   float* join_o = (float*)dyn_lds;          // [NW][32][DP] after the copies
   const Lanes<DP> ln(lane);
+  // the lane's bytes in copy 0; in copy it its row is kRowsPer it further down, and the swizzle
+  // differs in bits 4 and 5
+  const uint32_t ofs = (lane / kChunks) * DP * 2 + ((lane % kChunks) ^ swz<DP>(lane / kChunks)) * 16;
   const int w = (blockIdx.x & 7) * (kFewShares / 8) + (blockIdx.x >> 3);
   for_segments<kFewRows, 32 * NW, kFewShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
@@ -1091,55 +1104,77 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
     const float c = a.scale * kLog2e;
     const int n = g.t1 - g.t0;
+    // eight keys lie in one page and no row has a rest
+    const bool whole = s.d_bytes == DP * 2 && s.page_size % 8 == 0;
+    const int64_t k_to_v = s.v - s.k;
     int win0 = 0, win1 = 0;   // pages held
+    auto hold = [&](int kb) {   // the pages of keys kb .. kb + 31
+      const int first = page_of(s, kb), end = page_of(s, kb + 31 < s.keys ? kb + 31 : s.keys - 1) + 1;
+      if (first >= win0 && end <= win1) return;
+      win0 = first;
+      win1 = first + kWindow;
+#pragma unroll
+      for (int k = 0; k < kWindow; k += 64)
+        win[wave][k + lane] = first + k + lane < a.max_pages ? s.table[first + k + lane] : -1;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
     auto issue = [&](int t) {
       const int kb = ((g.t0 + t) * NW + wave) * 32;
-      if (kb >= s.keys) {   // nothing there: keep the count of copies
-        const uint32_t to = mem + (t & 1) * kStage;
-#pragma unroll
-        for (int it = 0; it < 2 * kIters; ++it) dma16_at(kZeros, to + it * 1024);
-        return;
-      }
-      const int first = page_of(s, kb), end = page_of(s, kb + 31 < s.keys ? kb + 31 : s.keys - 1) + 1;
-      if (first < win0 || end > win1) {
-        win0 = first;
-        win1 = first + kWindow;
-        for (int k = lane; k < kWindow; k += 64) win[wave][k] = first + k < a.max_pages ? s.table[first + k] : -1;
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      }
       const uint32_t to = mem + (t & 1) * kStage;
+      if (kb < s.keys) hold(kb);
+      if (whole && kb + 32 <= s.keys) {
+        const int ids = win[wave][page_of(s, kb + (lane & 3) * 8) - win0];
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int r = it * kRowsPer + lane / kChunks, j = kb + r;
-        const int chunk = (lane % kChunks) ^ swz<DP>(r);
-        const int pg = j < s.keys ? win[wave][page_of(s, j) - win0] : -1;
-        const char *k, *v;
-        row_at<true>(s, j, pg, chunk * 16, k, v);
-        dma16_at(k, to + it * 1024);
-        dma16_at(v, to + 32 * DP * 2 + it * 1024);
+        for (int n8 = 0; n8 < 4; ++n8) {
+          const int id = __builtin_amdgcn_readlane(ids, n8), j = kb + n8 * 8;
+          const bool there = (uint32_t)id < (uint64_t)s.num_pages;
+          const int64_t off = (int64_t)id * s.k_step + (j - page_of(s, j) * s.page_size) * (DP * 2);
+          const char* k = there ? s.k + off : reinterpret_cast<const char*>(kZeros);
+          const char* v = there ? k + k_to_v : k;
+#pragma unroll
+          for (int m = 0; m < 8 / kRowsPer; ++m) {
+            const int it = n8 * (8 / kRowsPer) + m, skip = there ? m * 1024 : 0;
+            const uint32_t o = ofs ^ ((it * kRowsPer / 4 % 4) * 16);
+            dma16(k + skip, o, to + it * 1024);
+            dma16(v + skip, o, to + kHalf + it * 1024);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < kIters; ++it) {
+          const int r = it * kRowsPer + lane / kChunks, j = kb + r;
+          const int page = j < s.keys ? win[wave][page_of(s, j) - win0] : -1;
+          const char *kr, *vr;
+          row_at<true>(s, j, page, ((lane % kChunks) ^ swz<DP>(r)) * 16, kr, vr);
+          dma16_at(kr, (uint32_t)uni(to + it * 1024));
+          dma16_at(vr, (uint32_t)uni(to + kHalf + it * 1024));
+        }
       }
     };
     Rows<DP, 1> st;
     load_rows<DP, 1>(st, a, g.it, g.it.row0, lane);
-    if (n > 0) issue(0);
-    if (n > 1) issue(1);
-    for (int t = 0; t < n; ++t) {
-      if (t + 1 < n) wait_vmcnt_le<2 * kIters>();
-      else wait_vmcnt_le<0>();
-      asm volatile("" ::: "memory");
-      const int kb = ((g.t0 + t) * NW + wave) * 32;
-      const uint32_t at = mem + (t & 1) * kStage;
-      if (kb < hi_max && kb + 32 > lo_min) {
-        v16f sc[1][1];
-        float top[1];
-        v8s none[kAhead];
-        scores<DT, DP, 1, 1>(sc, st, ln, at);
-        top[0] = both_max(largest(sc[0])) * c;
-        // the K rows are not needed any more: their place is the wave's scratch
-        step<DT, DP, 1, false>(st, ln, sc, sc, top, none, 0, 0, at + 32 * DP * 2, kb, c,
-                                 uni(kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb), at, lane);
+    if (n > 0 && (g.t0 * NW + wave) * 32 < s.keys) hold((g.t0 * NW + wave) * 32);
+    wait_vmcnt_le<0>();   // the queries: from here on only copies are waited for
+#pragma unroll 1
+    for (int t = -2; t < n; ++t) {
+      if (t >= 0) {
+        const int kb = ((g.t0 + t) * NW + wave) * 32;
+        const uint32_t at = mem + (t & 1) * kStage;
+        const bool more = t + 1 < n, seen = kb < hi_max && kb + 32 > lo_min;
+        if (more) wait_vmcnt_le<2 * kIters>();
+        else wait_vmcnt_le<0>();
+        asm volatile("" ::: "memory");
+        if (seen) {
+          v16f sc[1][1];
+          scores<DT, DP, 1, 1>(sc, st, ln, at);
+          float top[1] = {both_max(largest(sc[0])) * c};
+          v8s none[kAhead];
+          // the K rows are not needed any more: their place is the wave's scratch
+          step<DT, DP, 1, false>(st, ln, sc, sc, top, none, 0, 0, at + kHalf, kb, c,
+                                 kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb, at, lane);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (t + 2 < n) issue(t + 2);
     }
     // join the waves: weights 2^(m_w - m)
@@ -1152,6 +1187,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     for (int k = 0; k < NW; ++k) m = __builtin_fmaxf(m, join_ml[k][col][0]);
     const float mine = st.m[0] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.m[0] - m);
     // a row stored from bank 4 col on: the 32 rows of a store take all banks in turn
+    if (g.it.row0 + col < rows)
 #pragma unroll
     for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
@@ -1222,9 +1258,11 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
   const Plan<ROWS, UNIT, SHARES, 256> pl(a, sp, w, lds);
   if (pl.req > a.seqs || pl.share * w >= pl.total) return;
   const Req r = pl.get(pl.req);
-  const int64_t item = quotient(pl.share * w - pl.before, r.tiles);   // (head, block) in this request
-  const int64_t s0 = pl.before + item * r.tiles, s1 = s0 + r.tiles;
-  if (s0 == pl.share * w || s0 < pl.share * (w - 1)) return;
+  const int cost = r.tiles + kExtra;
+  const int64_t item = quotient(pl.share * w - pl.before, cost);   // (head, block) in this request
+  const int64_t s0 = pl.before + item * cost, s1 = s0 + cost;
+  // the share starts inside the item's tiles, and it is the first that does
+  if (pl.share * w - s0 <= kExtra || pl.share * (w - 1) - s0 > kExtra) return;
   const int last = (int)quotient(s1 + pl.share - 1, pl.share) - 1;
   const int head = (int)quotient(item, r.blocks), rb = (int)(item - (int64_t)head * r.blocks);
   const int group = a.group, rows = r.news * group - rb * ROWS < ROWS ? r.news * group - rb * ROWS : ROWS;
