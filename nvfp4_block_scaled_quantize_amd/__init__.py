@@ -8,6 +8,7 @@ fails, and every call checks the library's status code.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -19,6 +20,7 @@ NVFP4_OK, NVFP4_EINVAL, NVFP4_EUNSUPPORTED, NVFP4_EWORKSPACE, NVFP4_EHIP, NVFP4_
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # NVFP4_NOALLOC_SCRATCH_BYTES
 NVFP4_BF16, NVFP4_FP16 = 0, 1
 ACT = {"none": 0, "swiglu": 1, "relu2": 2}
+_TYPE_CODE = {torch.bfloat16: NVFP4_BF16, torch.float16: NVFP4_FP16}
 
 EXPORTS = [
     "nvfp4_status_string", "nvfp4_quantize", "nvfp4_quantize_workspace_size", "nvfp4_act_quant",
@@ -537,16 +539,18 @@ def mx_gemm(a: dict, a_g: torch.Tensor, w: dict, w_g: torch.Tensor, a_group_rows
 
 
 # ---------------------------------------------------------------- serving attention
+#
+# A decode step's kernels take a few microseconds, about as long as checking their operands one by
+# one in Python.  Each call therefore first asks one plain question -- are the operands what they are
+# in an ordinary call -- and only where the answer is no runs the checks that name what is wrong.
 
-def _on_gpu(first: torch.Tensor, *ts):
-    """The device of `first`, which has to be the current one and that of all others."""
+def _need_gpu(first: torch.Tensor, *ts):
     dev = first.device
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         raise ValueError("tensors must be on the current GPU")
     for t in ts:
         if t is not None and t.device != dev:
             raise ValueError("tensors must be on one GPU")
-    return dev
 
 
 def _dense(t: torch.Tensor, name: str, dtype, shape):
@@ -555,7 +559,17 @@ def _dense(t: torch.Tensor, name: str, dtype, shape):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _heads_3d(t, name: str):
+def _gpu_of(t) -> int:
+    """Index of the tensor's GPU if that is the current one, else -1."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -1
+
+
+def _is(t, dtype, shape, dev) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _need_heads(t, name: str):
     """[tokens, heads, head_dim] with a dense last dimension; other strides are free."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError("%s must be a 3-D tensor [tokens, heads, head_dim]" % name)
@@ -578,6 +592,46 @@ def _fresh(stream, make):
         return make()
 
 
+def _handle(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out):
+    if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be a 1-D tensor")
+    n = ctx_lens.shape[0]
+    _dense(ctx_lens, "ctx_lens", torch.int32, (n,))
+    _dense(new_lens, "new_lens", torch.int32, (n,))
+    _need_2d(block_table, "block_table")
+    _dense(block_table, "block_table", torch.int32, (n, block_table.shape[1]))
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a 1-D tensor")
+    _dense(free_pages, "free_pages", torch.int32, free_pages.shape)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    if out is not None:
+        for key, dt, shape in (("cu_new", torch.int32, (n + 1,)), ("kv_lens", torch.int32, (n,)),
+                               ("slot_map", torch.int64, (tokens,)), ("positions", torch.int32, (tokens,)),
+                               ("taken", torch.int32, (1,))):
+            _dense(out.get(key), "out['%s']" % key, dt, shape)
+        out = [out[key] for key in ("cu_new", "kv_lens", "slot_map", "positions", "taken")]
+    _need_gpu(ctx_lens, new_lens, block_table, free_pages, *(out or ()))
+
+
+def _plain_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out, dev) -> bool:
+    try:
+        n, i32 = ctx_lens.shape[0], torch.int32
+        return (tokens >= 0 and _is(ctx_lens, i32, (n,), dev) and _is(new_lens, i32, (n,), dev) and
+                _is(block_table, i32, (n, block_table.shape[1]), dev) and
+                _is(free_pages, i32, (free_pages.shape[0],), dev) and
+                (out is None or
+                 (_is(out["cu_new"], i32, (n + 1,), dev) and _is(out["kv_lens"], i32, (n,), dev) and
+                  _is(out["slot_map"], torch.int64, (tokens,), dev) and _is(out["positions"], i32, (tokens,), dev) and
+                  _is(out["taken"], i32, (1,), dev))))
+    except (AttributeError, IndexError, KeyError, TypeError):
+        return False
+
+
 def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
               free_pages: torch.Tensor, page_size: int, tokens: int, out: dict | None = None,
               stream=None) -> dict:
@@ -586,77 +640,110 @@ def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     dict(cu_new [seqs + 1], kv_lens [seqs], slot_map [tokens] int64, positions [tokens],
     taken [1]).  `tokens` is the size of the maps (entries past the last token are -1); `taken`
     above len(free_pages) means that pages ran out."""
-    if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
-        raise ValueError("ctx_lens must be a 1-D tensor")
+    tokens, dev = int(tokens), _gpu_of(ctx_lens)
+    if dev < 0 or not _plain_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out, dev):
+        _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out)
     n = ctx_lens.shape[0]
-    _dense(ctx_lens, "ctx_lens", torch.int32, (n,))
-    _dense(new_lens, "new_lens", torch.int32, (n,))
-    _need_2d(block_table, "block_table")
-    width = block_table.shape[1]
-    _dense(block_table, "block_table", torch.int32, (n, width))
-    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
-        raise ValueError("free_pages must be a 1-D tensor")
-    _dense(free_pages, "free_pages", torch.int32, free_pages.shape)
-    tokens = int(tokens)
-    if tokens < 0:
-        raise ValueError("tokens must not be negative")
-    if out is not None:
-        for key, dt, shape in (("cu_new", torch.int32, (n + 1,)), ("kv_lens", torch.int32, (n,)),
-                               ("slot_map", torch.int64, (tokens,)), ("positions", torch.int32, (tokens,)),
-                               ("taken", torch.int32, (1,))):
-            _dense(out.get(key), "out['%s']" % key, dt, shape)
-    dev = _on_gpu(ctx_lens, new_lens, block_table, free_pages, *(out.values() if out is not None else ()))
     if out is None:
+        where = ctx_lens.device
         out = _fresh(stream, lambda: {
-            "cu_new": torch.empty(n + 1, dtype=torch.int32, device=dev),
-            "kv_lens": torch.empty(n, dtype=torch.int32, device=dev),
-            "slot_map": torch.empty(tokens, dtype=torch.int64, device=dev),
-            "positions": torch.empty(tokens, dtype=torch.int32, device=dev),
-            "taken": torch.empty(1, dtype=torch.int32, device=dev)})
-    st = _lib.nvfp4_page_maps(ctx_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(), width,
-                              free_pages.data_ptr(), free_pages.shape[0], page_size, tokens,
+            "cu_new": torch.empty(n + 1, dtype=torch.int32, device=where),
+            "kv_lens": torch.empty(n, dtype=torch.int32, device=where),
+            "slot_map": torch.empty(tokens, dtype=torch.int64, device=where),
+            "positions": torch.empty(tokens, dtype=torch.int32, device=where),
+            "taken": torch.empty(1, dtype=torch.int32, device=where)})
+    st = _lib.nvfp4_page_maps(ctx_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(),
+                              block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], page_size, tokens,
                               out["cu_new"].data_ptr(), out["kv_lens"].data_ptr(), out["slot_map"].data_ptr(),
-                              out["positions"].data_ptr(), out["taken"].data_ptr(), _stream(stream))
+                              out["positions"].data_ptr(), out["taken"].data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_page_maps")
     return out
 
 
-def _caches(k_cache, v_cache, dtype):
+def _check_caches(k_cache, v_cache, dtype):
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a 4-D tensor [pages, kv_heads, page_size, head_dim]")
     _dense(k_cache, "k_cache", dtype, k_cache.shape)
     _dense(v_cache, "v_cache", dtype, k_cache.shape)
-    return k_cache.shape
+
+
+def _check_kv_write(k, v, slot_map, k_cache, v_cache):
+    _need_heads(k, "k")
+    _need_heads(v, "v")
+    _dtype_code(k)
+    T, H, D = k.shape
+    _need(v, "v", k.dtype, (T, H, D))
+    _check_caches(k_cache, v_cache, k.dtype)
+    if (k_cache.shape[1], k_cache.shape[3]) != (H, D):
+        raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (k_cache.shape[1], k_cache.shape[3], H, D))
+    _dense(slot_map, "slot_map", torch.int64, (T,))
+    _need_gpu(k, v, slot_map, k_cache, v_cache)
+
+
+def _plain_kv_write(k, v, slot_map, k_cache, v_cache, dev) -> bool:
+    try:
+        dt, shape, cache = k.dtype, k.shape, k_cache.shape
+        T, H, D = shape
+        _, heads, _, dim = cache
+        return (dt in _TYPE_CODE and T > 0 and heads == H and dim == D and v.dtype is dt and v.shape == shape and
+                k.stride(2) == 1 and v.stride(2) == 1 and k.get_device() == dev and v.get_device() == dev and
+                _is(slot_map, torch.int64, (T,), dev) and _is(k_cache, dt, cache, dev) and _is(v_cache, dt, cache, dev))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
 
 
 def kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor,
              v_cache: torch.Tensor, stream=None) -> None:
     """Writes k, v [tokens, kv_heads, head_dim] to their slots of the caches
     [pages, kv_heads, page_size, head_dim]; slots outside the cache (-1) are skipped."""
-    _heads_3d(k, "k")
-    _heads_3d(v, "v")
-    _dtype_code(k)
+    dev = _gpu_of(k)
+    if dev < 0 or not _plain_kv_write(k, v, slot_map, k_cache, v_cache, dev):
+        _check_kv_write(k, v, slot_map, k_cache, v_cache)
     T, H, D = k.shape
-    _need(v, "v", k.dtype, (T, H, D))
-    pages, heads, page_size, dim = _caches(k_cache, v_cache, k.dtype)
-    if (heads, dim) != (H, D):
-        raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (heads, dim, H, D))
-    _dense(slot_map, "slot_map", torch.int64, (T,))
-    _on_gpu(k, v, slot_map, k_cache, v_cache)
-    ks, vs = _steps(k), _steps(v)
-    st = _lib.nvfp4_kv_write(k.data_ptr(), v.data_ptr(), T, H, D, ks[0], ks[1], vs[0], vs[1], slot_map.data_ptr(),
-                             k_cache.data_ptr(), v_cache.data_ptr(), page_size, pages, _stream(stream))
+    (kt, kh), (vt, vh) = _steps(k), _steps(v)
+    st = _lib.nvfp4_kv_write(k.data_ptr(), v.data_ptr(), T, H, D, kt, kh, vt, vh, slot_map.data_ptr(),
+                             k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[2], k_cache.shape[0],
+                             _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_kv_write")
 
 
-def _attn_out(q, out, lse, want_lse):
+def _check_attn_out(q, out, lse):
     T, H, D = q.shape
     if out is not None:
         _dense(out, "out", q.dtype, (T, H, D))
     if lse is not None:
         _dense(lse, "lse", torch.float32, (T, H))
+
+
+def _check_prompt_attn(q, k, v, cu_seqlens, out, lse):
+    _need_heads(q, "q")
+    _need_heads(k, "k")
+    _need_heads(v, "v")
+    _dtype_code(q)
+    T, _, D = q.shape
+    _need(k, "k", q.dtype, (T, k.shape[1], D))
+    _need(v, "v", q.dtype, k.shape)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a 1-D tensor of seqs + 1 entries")
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape)
+    _check_attn_out(q, out, lse)
+    _need_gpu(q, k, v, cu_seqlens, out, lse)
+
+
+def _plain_prompt_attn(q, k, v, cu_seqlens, out, lse, dev) -> bool:
+    try:
+        dt, shape = q.dtype, q.shape
+        T, H, D = shape
+        return (dt in _TYPE_CODE and T > 0 and k.dtype is dt and v.dtype is dt and
+                k.shape == (T, k.shape[1], D) and v.shape == k.shape and
+                q.stride(2) == 1 and k.stride(2) == 1 and v.stride(2) == 1 and
+                q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and
+                cu_seqlens.shape[0] > 0 and _is(cu_seqlens, torch.int32, (cu_seqlens.shape[0],), dev) and
+                (out is None or _is(out, dt, shape, dev)) and (lse is None or _is(lse, torch.float32, (T, H), dev)))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -666,35 +753,58 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     [tokens, kv_heads, head_dim] (any token and head strides that are multiples of 8), cu_seqlens
     [seqs + 1] int32.  Returns out, or (out, lse) with want_lse or a given lse buffer.  scale
     defaults to head_dim ** -0.5; window > 0 limits a row to the last `window` keys."""
-    _heads_3d(q, "q")
-    _heads_3d(k, "k")
-    _heads_3d(v, "v")
-    dtype = _dtype_code(q)
+    dev = _gpu_of(q)
+    if dev < 0 or not _plain_prompt_attn(q, k, v, cu_seqlens, out, lse, dev):
+        _check_prompt_attn(q, k, v, cu_seqlens, out, lse)
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    _need(k, "k", q.dtype, (T, Hk, D))
-    _need(v, "v", q.dtype, (T, Hk, D))
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be a 1-D tensor of seqs + 1 entries")
-    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape)
-    _attn_out(q, out, lse, want_lse)
-    dev = _on_gpu(q, k, v, cu_seqlens, out, lse)
     if out is None:
-        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=dev))
+        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
     if lse is None and want_lse:
-        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
-    qs, ks, vs = _steps(q), _steps(k), _steps(v)
-    st = _lib.nvfp4_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, cu_seqlens.data_ptr(),
-                                cu_seqlens.shape[0] - 1, T, Hq, Hk, D, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=q.device))
+    (qt, qh), (kt, kh), (vt, vh) = _steps(q), _steps(k), _steps(v)
+    st = _lib.nvfp4_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPE_CODE[q.dtype], cu_seqlens.data_ptr(),
+                                cu_seqlens.shape[0] - 1, T, Hq, k.shape[1], D, qt, qh, kt, kh, vt, vh,
                                 D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                                None if lse is None else lse.data_ptr(), _stream(stream))
+                                None if lse is None else lse.data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_prompt_attn")
     return out if lse is None else (out, lse)
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_attn_workspace_size(seqs: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(_lib.nvfp4_paged_attn_workspace_size(seqs, tokens, q_heads, kv_heads, head_dim))
+
+
+def _check_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace):
+    _need_heads(q, "q")
+    _dtype_code(q)
+    _check_caches(k_cache, v_cache, q.dtype)
+    if k_cache.shape[3] != q.shape[2]:
+        raise ValueError("q has head_dim %d, the cache %d" % (q.shape[2], k_cache.shape[3]))
+    _need_2d(block_table, "block_table")
+    n = block_table.shape[0]
+    _dense(block_table, "block_table", torch.int32, block_table.shape)
+    _dense(cu_new, "cu_new", torch.int32, (n + 1,))
+    _dense(kv_lens, "kv_lens", torch.int32, (n,))
+    _check_attn_out(q, out, lse)
+    _need_gpu(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace)
+
+
+def _plain_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace, dev) -> bool:
+    try:
+        dt, shape, cache, i32 = q.dtype, q.shape, k_cache.shape, torch.int32
+        T, H, D = shape
+        n, width = block_table.shape
+        _, _, _, dim = cache
+        return (dt in _TYPE_CODE and T > 0 and dim == D and q.stride(2) == 1 and q.get_device() == dev and
+                _is(k_cache, dt, cache, dev) and _is(v_cache, dt, cache, dev) and
+                _is(block_table, i32, (n, width), dev) and _is(cu_new, i32, (n + 1,), dev) and
+                _is(kv_lens, i32, (n,), dev) and (out is None or _is(out, dt, shape, dev)) and
+                (lse is None or _is(lse, torch.float32, (T, H), dev)) and
+                (workspace is None or workspace.get_device() == dev))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
 
 
 def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -705,31 +815,23 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     q_heads, head_dim] packed by cu_new [seqs + 1], caches [pages, kv_heads, page_size, head_dim],
     block_table [seqs, max_pages], kv_lens [seqs] (all int32).  Decode steps, chunks of prompts and
     mixtures.  Returns out, or (out, lse) with want_lse or a given lse buffer."""
-    _heads_3d(q, "q")
-    dtype = _dtype_code(q)
+    dev = _gpu_of(q)
+    if dev < 0 or not _plain_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace, dev):
+        _check_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace)
     T, Hq, D = q.shape
-    pages, Hk, page_size, dim = _caches(k_cache, v_cache, q.dtype)
-    if dim != D:
-        raise ValueError("q has head_dim %d, the cache %d" % (D, dim))
-    _need_2d(block_table, "block_table")
+    pages, Hk, page_size, _ = k_cache.shape
     n, width = block_table.shape
-    _dense(block_table, "block_table", torch.int32, (n, width))
-    _dense(cu_new, "cu_new", torch.int32, (n + 1,))
-    _dense(kv_lens, "kv_lens", torch.int32, (n,))
-    _attn_out(q, out, lse, want_lse)
-    dev = _on_gpu(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace)
     if out is None:
-        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=dev))
+        out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
     if lse is None and want_lse:
-        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
-    ws, wsb = _fresh(stream, lambda: _workspace(
-        _lib.nvfp4_paged_attn_workspace_size(n, T, Hq, Hk, D), dev, workspace))
-    qs = _steps(q)
-    st = _lib.nvfp4_paged_attn(q.data_ptr(), dtype, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                               cu_new.data_ptr(), kv_lens.data_ptr(), n, T, Hq, Hk, D, page_size, pages, width,
-                               qs[0], qs[1], D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), wsb,
-                               _stream(stream))
+        lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=q.device))
+    ws, wsb = _fresh(stream, lambda: _workspace(paged_attn_workspace_size(n, T, Hq, Hk, D), q.device, workspace))
+    qt, qh = _steps(q)
+    st = _lib.nvfp4_paged_attn(q.data_ptr(), _TYPE_CODE[q.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
+                               block_table.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), n, T, Hq, Hk, D,
+                               page_size, pages, width, qt, qh, D ** -0.5 if scale is None else scale, window,
+                               out.data_ptr(), None if lse is None else lse.data_ptr(),
+                               None if ws is None else ws.data_ptr(), wsb, _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_paged_attn")
     return out if lse is None else (out, lse)
