@@ -25,134 +25,143 @@ namespace {
 // costs more than forming them again: each workgroup sums all the requests
 // (contiguous shares per thread, one scan over the threads), keeps the starts
 // that fall into its own range of tokens in LDS, and finds each token's
-// request by a running maximum over those starts.
+// request by a running maximum over those starts.  Sums are 32 bits and stop at
+// 2^31 - 1 (min(a + b, 2^31 - 1) is associative), so lengths that break the
+// contract cannot index anything.
 constexpr int kMapThreads = 256;
-constexpr int kMapTokens = 2048;                       // tokens per workgroup
-constexpr int kMapPer = kMapTokens / kMapThreads;
+constexpr int kMapPer = 4;
+constexpr int kMapTokens = kMapThreads * kMapPer;      // tokens per workgroup
+constexpr uint32_t kMost = 0x7FFFFFFFu;
 
-constexpr int kMost = 0x7FFFFFFF;
-
-__device__ __forceinline__ int len_of(const int32_t* p, int i) { return p[i] > 0 ? p[i] : 0; }
-__device__ __forceinline__ int clamp64(int64_t v) { return v < kMost ? (int)v : kMost; }
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return a + b < kMost ? a + b : kMost; }
+__device__ __forceinline__ uint32_t len_of(const int32_t* p, int i) { return p[i] > 0 ? (uint32_t)p[i] : 0u; }
 
 // Pages of n tokens: ceil(n / page_size), at most the table's width.
-__device__ __forceinline__ int pages_of(const PageMapsArgs& a, int n) {
-  const int p = n > 0 ? divide(n - 1, a.magic, a.shift) + 1 : 0;
-  return p < a.max_pages ? p : a.max_pages;
-}
-
-// Exclusive prefix of v over the threads of the workgroup; total in `all`.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s, int64_t& all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t x = v;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t y = __shfl_up(x, off, 64);
-    if (lane >= off) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) s[wave] = x;
-  __syncthreads();
-  int64_t before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kMapThreads / 64; ++w) {
-    if (w < wave) before += s[w];
-    all += s[w];
-  }
-  return before + x - v;
+__device__ __forceinline__ uint32_t pages_of(const PageMapsArgs& a, uint32_t n) {
+  const int p = n > 0 ? divide((int)(n - 1), a.magic, a.shift) + 1 : 0;
+  return (uint32_t)(p < a.max_pages ? p : a.max_pages);
 }
 
 __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) {
-  __shared__ int64_t scan[kMapThreads / 64];
-  __shared__ int start_req[kMapTokens];        // request that starts at this token of the range, or -1
-  __shared__ int start_cu[kMapTokens];         // its first token
-  __shared__ int64_t start_page[kMapTokens];   // its first page in the free list
-  __shared__ int wave_last[kMapThreads / 64];
+  constexpr int kWaves = kMapThreads / 64;
+  __shared__ uint32_t sums[2][kWaves];
+  __shared__ int owner[kMapTokens];            // a request starts at this token (its place in the range), or -1
+  __shared__ int4 starts[kMapTokens];          // request, its cached length, first token, first free page
+  __shared__ int wave_last[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kMapTokens;
-  const int width = a.max_pages;
-  for (int k = tid; k < kMapTokens; k += kMapThreads) start_req[k] = -1;
+#pragma unroll
+  for (int k = 0; k < kMapPer; ++k) owner[k * kMapThreads + tid] = -1;
 
   const int per = (a.seqs + kMapThreads - 1) / kMapThreads;
   const int i0 = tid * per, i1 = (i0 + per < a.seqs) ? i0 + per : a.seqs;
-  int64_t tok = 0, pag = 0;
+  uint32_t tok = 0, pag = 0, c0 = 0, m0 = 0;
   for (int i = i0; i < i1; ++i) {
-    const int c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i);
-    tok += m;
-    pag += pages_of(a, clamp64((int64_t)c + m)) - pages_of(a, c);
+    const uint32_t c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i);
+    if (i == i0) { c0 = c; m0 = m; }
+    tok = add(tok, m);
+    pag = add(pag, pages_of(a, add(c, m)) - pages_of(a, c));
   }
-  int64_t all_tok, all_pag;
-  int64_t at = block_scan(tok, scan, all_tok);
-  int64_t page = block_scan(pag, scan, all_pag);   // its first barrier orders the fill of start_req
+  uint32_t x = tok, y = pag;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t u = __shfl_up(x, off, 64), v = __shfl_up(y, off, 64);
+    if (lane >= off) {
+      x = add(x, u);
+      y = add(y, v);
+    }
+  }
+  if (lane == 63) {
+    sums[0][wave] = x;
+    sums[1][wave] = y;
+  }
+  // exclusive: the inclusive value of the lane before
+  uint32_t at = __shfl_up(x, 1, 64), page = __shfl_up(y, 1, 64);
+  if (lane == 0) at = page = 0;
+  __syncthreads();   // also orders the fill of owner
+  uint32_t all_tok = 0, all_pag = 0, tb = 0, pb = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == wave) { tb = all_tok; pb = all_pag; }
+    all_tok = add(all_tok, sums[0][w]);
+    all_pag = add(all_pag, sums[1][w]);
+  }
+  at = add(at, tb);
+  page = add(page, pb);
   const bool mine = (tid % gridDim.x) == blockIdx.x;   // writes this share's cu_new and kv_lens
   for (int i = i0; i < i1; ++i) {
-    const int c = len_of(a.ctx_lens, i), m = len_of(a.new_lens, i), all = clamp64((int64_t)c + m);
-    if (m > 0 && at < t0 + kMapTokens && at + m > t0) {
-      const int k = (int)(at > t0 ? at - t0 : 0);
-      start_req[k] = i;
-      start_cu[k] = (int)at;
-      start_page[k] = page;
+    const uint32_t c = i == i0 ? c0 : len_of(a.ctx_lens, i), m = i == i0 ? m0 : len_of(a.new_lens, i);
+    const uint32_t all = add(c, m);
+    if (m > 0 && at < t0 + kMapTokens && (int64_t)at + m > t0) {
+      const int k = at > t0 ? (int)(at - t0) : 0;
+      owner[k] = k;
+      starts[k] = make_int4(i, (int)c, (int)at, (int)page);
     }
     if (mine) {
-      a.cu_new[i] = clamp64(at);
-      a.kv_lens[i] = all;
+      a.cu_new[i] = (int32_t)at;
+      a.kv_lens[i] = (int32_t)all;
     }
-    at += m;
-    page += pages_of(a, all) - pages_of(a, c);
+    at = add(at, m);
+    page = add(page, pages_of(a, all) - pages_of(a, c));
   }
   if (blockIdx.x == 0 && tid == 0) {
-    a.cu_new[a.seqs] = clamp64(all_tok);
-    a.taken[0] = clamp64(all_pag);
+    a.cu_new[a.seqs] = (int32_t)all_tok;
+    a.taken[0] = (int32_t)all_pag;
   }
   __syncthreads();
 
-  // last start at or before each token: thread tid looks at kMapPer tokens,
+  // last start at or before each token: kMapPer consecutive tokens per thread,
   // then a scan of maxima over the threads
-  int last[kMapPer];
-  int run = -1;
+  int last[kMapPer], run = -1;
 #pragma unroll
   for (int k = 0; k < kMapPer; ++k) {
-    const int idx = tid * kMapPer + k;
-    if (start_req[idx] >= 0) run = idx;
+    const int o = owner[tid * kMapPer + k];
+    run = o >= 0 ? o : run;
     last[k] = run;
   }
   int inc = run;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(inc, off, 64);
-    if (lane >= off && y > inc) inc = y;
+    const int u = __shfl_up(inc, off, 64);
+    if (lane >= off && u > inc) inc = u;
   }
   if (lane == 63) wave_last[wave] = inc;
-  __syncthreads();
   int before = __shfl_up(inc, 1, 64);
   if (lane == 0) before = -1;
-  for (int w = 0; w < wave; ++w) before = wave_last[w] > before ? wave_last[w] : before;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves - 1; ++w)
+    if (w < wave && wave_last[w] > before) before = wave_last[w];
+#pragma unroll
+  for (int k = 0; k < kMapPer; ++k) owner[tid * kMapPer + k] = last[k] > before ? last[k] : before;
+  __syncthreads();
+  // from here on neighbouring threads have neighbouring tokens
 #pragma unroll
   for (int k = 0; k < kMapPer; ++k) {
-    const int64_t t = t0 + tid * kMapPer + k;
-    if (t >= a.tokens) break;
-    const int st = last[k] > before ? last[k] : before;
+    const int idx = k * kMapThreads + tid;
+    const int64_t t = t0 + idx;
+    const int st = owner[idx];
     int64_t slot = -1;
     int32_t position = -1;
-    if (st >= 0 && t < all_tok) {
-      const int i = start_req[st];
-      const int c = len_of(a.ctx_lens, i);
-      position = clamp64(c + (t - start_cu[st]));
+    if (st >= 0 && t < (int64_t)all_tok && t < a.tokens) {
+      const int4 s = starts[st];
+      position = (int32_t)add((uint32_t)s.y, (uint32_t)(t - s.z));
       const int col = divide(position, a.magic, a.shift), place = position - col * a.page_size;
-      const int held = pages_of(a, c);
+      const int held = (int)pages_of(a, (uint32_t)s.y);
       int pg = -1;
       if (col < held) {
-        pg = a.block_table[(int64_t)i * width + col];
-      } else if (col < width) {
-        const int64_t f = start_page[st] + (col - held);
+        pg = a.block_table[(int64_t)s.x * a.max_pages + col];
+      } else if (col < a.max_pages) {
+        const int64_t f = (int64_t)s.w + (col - held);
         if (f < a.num_free) pg = a.free_pages[f];
-        if (place == 0) a.block_table[(int64_t)i * width + col] = pg;
+        if (place == 0) a.block_table[(int64_t)s.x * a.max_pages + col] = pg;
       }
       if (pg >= 0) slot = (int64_t)pg * a.page_size + place;
     }
-    a.slot_map[t] = slot;
-    a.positions[t] = position;
+    if (t < a.tokens) {
+      a.slot_map[t] = slot;
+      a.positions[t] = position;
+    }
   }
 }
 
