@@ -151,13 +151,23 @@ __device__ __forceinline__ void row_at(const Source& s, int j, int page, int chu
 }
 
 // ---------------------------------------------------------------- one tile
-// State of QT x 32 rows of one wave.
-template <int DP, int QT>
+// State of the 32 rows of a wave.
+template <int DP>
 struct Rows {
-  v8s q[QT][DP / 16];      // B operand: lane's row, d = 16 s + 8 h ..
-  v16f o[QT][DP / 32];     // O^T: d = 32 t + 8 (i / 4) + 4 h + i % 4
-  float m[QT], l[QT];      // l: this half-wave's keys only
-  int lo[QT], hi[QT];      // the row sees the keys lo <= j < hi
+  v8s q[DP / 16];      // B operand: lane's row, d = 16 st + 8 h ..
+  v16f o[DP / 32];     // O^T: d = 32 t + 8 (i / 4) + 4 h + i % 4
+  float m, l;          // log2 units; l: this half-wave's keys only
+  float far;           // m + kKeep as a score (before scaling)
+  int lo, hi;          // the row sees the keys lo <= j < hi
+};
+
+// A row starts at the lowest number instead of -inf: differences of maxima are
+// then never inf - inf, and every weight of a row that has seen nothing is
+// 2^(-inf) = 0.
+constexpr float kLowest = -3.40282346638528859812e+38f;
+
+struct Scaling {
+  float c, inv;   // scale log2 e and its inverse
 };
 
 template <int DT>
@@ -177,52 +187,41 @@ struct Lanes {
   static constexpr uint32_t kDown = 32;   // what 8 rows further down change in the swizzle
 };
 
+// K operand of score product n: 16 d of 32 keys; products of KT key groups alternate.
+template <int DP, int KT>
+__device__ __forceinline__ v8s key_operand(const Lanes<DP>& ln, uint32_t k_lds, int n) {
+  return read_b128(((k_lds + ln.k) ^ (n / KT * 32)) + n % KT * 32 * DP * 2);
+}
+
+// V^T operand of value product n: d tile n % (DP / 32), 16 keys n / (DP / 32).
+// Element e: key 4 h + e (e < 4), 8 + 4 h + e - 4 -- the order of the weights.
+template <int DP>
+__device__ __forceinline__ v8s value_operand(const Lanes<DP>& ln, uint32_t v_lds, int n) {
+  constexpr uint32_t kRow = DP * 2;
+  const uint32_t at = (v_lds + ln.v) ^ (n % (DP / 32) * 64), down = n / (DP / 32) * 16 * kRow;
+  const v4s x = read_tr(at + down), y = read_tr((at ^ Lanes<DP>::kDown) + down + 8 * kRow);
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ v16f zero16() {
+  v16f z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
 // S^T = K Q^T for KT x 32 keys.
-template <int DT, int DP, int QT, int KT>
-__device__ __forceinline__ void scores(v16f (&s)[QT][KT], const Rows<DP, QT>& w, const Lanes<DP>& ln, uint32_t k_lds) {
-  const uint32_t base = k_lds + ln.k;
+template <int DT, int DP, int KT>
+__device__ __forceinline__ void scores(v16f (&s)[KT], const Rows<DP>& w, const Lanes<DP>& ln, uint32_t k_lds) {
 #pragma unroll
-  for (int st = 0; st < DP / 16; ++st)
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const v8s kf = read_b128((base ^ (st * 32)) + kt * 32 * DP * 2);
-#pragma unroll
-      for (int qt = 0; qt < QT; ++qt) {
-        if (st == 0) {
-          v16f z;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-          s[qt][kt] = mfma<DT>(kf, w.q[qt][st], z);
-        } else {
-          s[qt][kt] = mfma<DT>(kf, w.q[qt][st], s[qt][kt]);
-        }
-      }
-    }
+  for (int n = 0; n < KT * DP / 16; ++n)
+    s[n % KT] = mfma<DT>(key_operand<DP, KT>(ln, k_lds, n), w.q[n / KT], n < KT ? zero16() : s[n % KT]);
 }
 
-// -inf for the keys of the tile at kb that a lane's row does not see.
-template <int QT, int KT, typename R>
-__device__ __forceinline__ void mask_scores(v16f (&s)[QT][KT], const R& w, int kb, int h) {
+__device__ __forceinline__ float largest(const v16f& s) {
+  float top = s[0];
 #pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    const int lo = w.lo[qt] - kb - 4 * h, hi = w.hi[qt] - kb - 4 * h;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = kt * 32 + 8 * (i / 4) + i % 4;
-        if (key < lo || key >= hi) s[qt][kt][i] = -__builtin_inff();
-      }
-  }
-}
-
-template <int KT>
-__device__ __forceinline__ float largest(const v16f (&s)[KT]) {
-  float top = s[0][0];
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[kt][i]);
+  for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, s[i]);
   return top;
 }
 
@@ -235,81 +234,32 @@ __device__ __forceinline__ int turns_if(int positive) {
   return n;
 }
 
-// Raises the maximum to `top` (log2 units, of both half-waves) where it lags by more than kKeep.
-template <int DP, int QT>
-__device__ __forceinline__ void raise(Rows<DP, QT>& w, const float (&top)[QT]) {
-  bool far = false;
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) far |= top[qt] > w.m[qt] + kKeep;
+// Raises the maximum to `top` (a score, of both half-waves) where it lags by more than kKeep.
+template <int DP>
+__device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc) {
+  const uint64_t far = __ballot(top > w.far);
+  int turns;   // see turns_if
+  asm volatile("s_cmp_lg_u64 %1, 0\n\ts_cselect_b32 %0, 1, 0" : "=s"(turns) : "s"(far) : "scc");
 #pragma unroll 1
-  for (int turns = turns_if(__popcll(__ballot(far))); turns > 0; --turns) {
+  for (; turns > 0; --turns) {
+    const float m = __builtin_fmaxf(w.m, top * sc.c), a = __builtin_amdgcn_exp2f(w.m - m);
+    w.m = m;
+    w.far = (m + kKeep) * sc.inv;
+    w.l *= a;
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      const float m = __builtin_fmaxf(w.m[qt], top[qt]);
-      const float a = m == w.m[qt] ? 1.0f : __builtin_amdgcn_exp2f(w.m[qt] - m);
-      w.m[qt] = m;
-      w.l[qt] *= a;
+    for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
-      for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w.o[qt][t][i] *= a;
-    }
+      for (int i = 0; i < 16; ++i) w.o[t][i] *= a;
   }
 }
 
-// Weights 2^(s c - m), summed into l and rounded into p (the B operand of the value product).
-template <int DT, int KT>
-__device__ __forceinline__ void weights(const v16f (&s)[KT], float c, float m, float& l, v8s (&p)[KT][2]) {
-  // nothing seen so far: every weight is 2^(-inf) = 0
-  const float mm = m == -__builtin_inff() ? 0.0f : m;
-  float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t d[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = half * 8 + e * 2;
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c, -mm));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i + 1], c, -mm));
-        sum[0] += x;
-        sum[1] += y;
-        d[e] = pack2<DT>(x, y);
-      }
-      p[kt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
-    }
-  l += sum[0] + sum[1];
-}
-
-// O^T += V^T P^T.  Element e of a value fragment: key 16 half + 4 h + e (e < 4), 16 half + 8 + 4 h
-// + e - 4 -- the order of p.
-template <int DT, int DP, int QT, int KT>
-__device__ __forceinline__ void values(Rows<DP, QT>& w, const v8s (&p)[QT][KT][2], const Lanes<DP>& ln, uint32_t v_lds) {
-  const uint32_t base = v_lds + ln.v;
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int t = 0; t < DP / 32; ++t) {
-        constexpr uint32_t kRow = DP * 2;
-        const uint32_t step = (kt * 32 + half * 16) * kRow;
-        const v4s a = read_tr((base ^ (t * 64)) + step);
-        const v4s b = read_tr((base ^ (t * 64) ^ Lanes<DP>::kDown) + step + 8 * kRow);
-        const v8s v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) w.o[qt][t] = mfma<DT>(v, p[qt][kt][half], w.o[qt][t]);
-      }
-}
-
-// Whether a tile's values are all finite (KT x 32 rows of DP).
-template <int DT, int DP, int KT>
+// Whether the values of 32 rows are all finite.
+template <int DT, int DP>
 __device__ __forceinline__ bool all_finite(uint32_t v_lds, int lane) {
   asm volatile("" : "+v"(lane));
   uint32_t big = 0;
 #pragma unroll 4
-  for (int n = 0; n < KT * 32 * DP * 2 / 1024; ++n) {
+  for (int n = 0; n < 32 * DP * 2 / 1024; ++n) {
     const u32x4 x = __builtin_bit_cast(u32x4, read_b128(v_lds + n * 1024 + lane * 16));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -342,23 +292,22 @@ __device__ __forceinline__ void copy_finite(uint32_t v_lds, uint32_t mine, int l
 }
 
 template <int DT, int DP>
-__device__ __forceinline__ void add_not_finite(v16f (&o)[DP / 32], const v16f& s, float c, float m, int lo, int hi,
-                                               uint32_t v_lds, uint32_t mine, int lane) {
+__device__ __forceinline__ void add_not_finite(Rows<DP>& w, const v16f& s, float c, int kb, uint32_t v_lds,
+                                               uint32_t mine, int lane) {
   asm volatile("" : "+v"(lane));
   const int h = lane >> 5, col = lane & 31;
   typedef __attribute__((address_space(3))) float* lds_f;
   typedef __attribute__((address_space(3))) u32x2* lds_2;
-  const float mm = m == -__builtin_inff() ? 0.0f : m;
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the copy has been read
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     *(lds_f)(uintptr_t)(mine + ((8 * (i / 4) + 4 * h + i % 4) * 32 + col) * 4) =
-        __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mm));
+        __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -w.m));
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
   for (int key = 0; key < 32; ++key) {
     const float p = *(lds_f)(uintptr_t)(mine + (key * 32 + col) * 4);
-    const bool sees = key >= lo && key < hi;
+    const bool sees = kb + key >= w.lo && kb + key < w.hi;
 #pragma unroll
     for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
@@ -368,135 +317,112 @@ __device__ __forceinline__ void add_not_finite(v16f (&o)[DP / 32], const v16f& s
         for (int e = 0; e < 4; ++e) {
           const uint32_t y = (x[e / 2] >> (16 * (e % 2))) & 0xFFFFu;
           const bool add = sees && (y & 0x7FFFu) >= not_finite_bits<DT>();
-          o[t][4 * i + e] += add ? p * unpack1<DT>((uint16_t)y) : 0.0f;
+          w.o[t][4 * i + e] += add ? p * unpack1<DT>((uint16_t)y) : 0.0f;
         }
       }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
-// The common part of a step, in an order that keeps the matrix cores fed: the scores of the next 32
-// keys, the weights of the current ones beside them, then the value product.  Operands are read from
-// LDS four products ahead (`f`: on entry the first K operands, on return those of the step after,
-// whose rows are at k_after), and each matrix instruction is followed by the share of the vector work
-// that fits beside it; the scheduling barriers keep that order.
-constexpr int kAhead = 4;
-
-template <int DP>
-__device__ __forceinline__ v8s key_operand(const Lanes<DP>& ln, uint32_t k_lds, int st) {
-  return read_b128((k_lds + ln.k) ^ (st * 32));
-}
-
-template <int DT, int DP, int QT>
-__device__ __forceinline__ void products(Rows<DP, QT>& w, const Lanes<DP>& ln, const v16f (&cur)[QT][1],
-                                         v16f (&nxt)[QT][1], float (&top)[QT], v8s (&f)[kAhead], uint32_t k_next,
-                                         uint32_t k_after, uint32_t v_lds, float c) {
-  constexpr int kSteps = DP / 16, kPer = 16 / kSteps, kTiles = DP / 32;
-  static_assert(kAhead <= kSteps && kAhead <= 2 * kTiles && kSteps % kAhead == 0 && 2 * kTiles % kAhead == 0, "operand ring");
-  const uint32_t vb = v_lds + ln.v;
-  auto value = [&](int n) {   // product n: half n / kTiles, d tile n % kTiles
-    constexpr uint32_t kRow = DP * 2;
-    const uint32_t t = n % kTiles, at = (n / kTiles) * 16 * kRow;
-    const v4s x = read_tr((vb ^ (t * 64)) + at), y = read_tr((vb ^ (t * 64) ^ Lanes<DP>::kDown) + at + 8 * kRow);
-    return (v8s)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  v8s p[QT][2];
-  float m[QT], sum[QT][2], e[QT][16], best[QT];
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    // nothing seen so far: every weight is 2^(-inf) = 0
-    m[qt] = w.m[qt] == -__builtin_inff() ? 0.0f : w.m[qt];
-    sum[qt][0] = w.l[qt];
-    sum[qt][1] = 0.0f;
-  }
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int st = 0; st < kSteps; ++st) {
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      if (st == 0) {
-        v16f z;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-        nxt[qt][0] = mfma<DT>(f[0], w.q[qt][0], z);
-      } else {
-        nxt[qt][0] = mfma<DT>(f[st % kAhead], w.q[qt][st], nxt[qt][0]);
-      }
-    }
-    f[st % kAhead] = st + kAhead < kSteps ? key_operand(ln, k_next, st + kAhead) : value(st + kAhead - kSteps);
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-      for (int i = st * kPer; i < (st + 1) * kPer; ++i) {
-        e[qt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[qt][0][i], c, -m[qt]));
-        sum[qt][i % 2] += e[qt][i];
-      }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t d[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) d[k] = pack2<DT>(e[qt][half * 8 + 2 * k], e[qt][half * 8 + 2 * k + 1]);
-      p[qt][half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
-    }
-    w.l[qt] = sum[qt][0] + sum[qt][1];
-  }
-#pragma unroll
-  for (int n = 0; n < 2 * kTiles; ++n) {
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-      w.o[qt][n % kTiles] = mfma<DT>(f[(n + kSteps) % kAhead], p[qt][n / kTiles], w.o[qt][n % kTiles]);
-    f[(n + kSteps) % kAhead] = n + kAhead < 2 * kTiles ? value(n + kAhead) : key_operand(ln, k_after, n + kAhead - 2 * kTiles);
-    // the next scores are ready by the second product
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-      if (n == 1) best[qt] = nxt[qt][0][0];
-      constexpr int kShare = 16 / (2 * kTiles - 2) + 1;
-      if (n >= 1)
-#pragma unroll
-        for (int i = (n - 1) * kShare; i < n * kShare && i < 16; ++i) best[qt] = __builtin_fmaxf(best[qt], nxt[qt][0][i]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-#pragma unroll
-  for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(best[qt]) * c;
-}
-
-// Adds 32 keys from key kb to the rows' state, whose scores are `cur` with the largest `top`, and
-// forms (NEXT) the next 32 keys' scores `nxt` and `top` from the K rows at k_next (f, k_after: see
-// products).  `hidden` > 0: some row
-// does not see some key of the current 32.  `mine`: 32 rows of DP of the wave's own LDS.
-template <int DT, int DP, int QT, bool NEXT>
-__device__ __forceinline__ void step(Rows<DP, QT>& w, const Lanes<DP>& ln, v16f (&cur)[QT][1], v16f (&nxt)[QT][1],
-                                     float (&top)[QT], v8s (&f)[kAhead], uint32_t k_next, uint32_t k_after,
-                                     uint32_t v_lds, int kb, float c, int hidden, uint32_t mine, int lane) {
+// Adds 32 keys from key kb, whose scores are `s` and whose values are at v_lds.  `hidden` > 0: some
+// row does not see some of them.  `mine`: 32 rows of DP of the wave's own LDS.
+template <int DT, int DP>
+__device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f& s, uint32_t v_lds, int kb,
+                                         const Scaling& sc, int hidden, uint32_t mine, int lane) {
   int odd = 0;   // some value is not finite
 #pragma unroll 1
   for (int turns = turns_if(hidden); turns > 0; --turns) {
-    mask_scores(cur, w, kb, lane >> 5);
+    const int h = lane >> 5, lo = w.lo - kb - 4 * h, hi = w.hi - kb - 4 * h;
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(cur[qt])) * c;
-    odd = uni(all_finite<DT, DP, 1>(v_lds, lane) ? 0 : 1);
+    for (int i = 0; i < 16; ++i) {
+      const int key = 8 * (i / 4) + i % 4;
+      if (key < lo || key >= hi) s[i] = -__builtin_inff();
+    }
+    odd = uni(all_finite<DT, DP>(v_lds, lane) ? 0 : 1);
     if (odd) copy_finite<DT, DP>(v_lds, mine, lane);
   }
-  raise(w, top);
-  const uint32_t v_at = odd ? mine : v_lds;
-  if constexpr (NEXT) {
-    products<DT, DP, QT>(w, ln, cur, nxt, top, f, k_next, k_after, v_at, c);
-  } else {
-    v8s p[QT][1][2];
+  raise(w, both_max(largest(s)), sc);
+  v8s p[2];
+  float sum[2] = {w.l, 0.0f};
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) weights<DT, 1>(cur[qt], c, w.m[qt], w.l[qt], p[qt]);
-    values<DT, DP, QT, 1>(w, p, ln, v_at);
+  for (int half = 0; half < 2; ++half) {
+    uint32_t d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = half * 8 + e * 2;
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], sc.c, -w.m));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], sc.c, -w.m));
+      sum[0] += x;
+      sum[1] += y;
+      d[e] = pack2<DT>(x, y);
+    }
+    p[half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
   }
-#pragma unroll 1
-  for (int turns = turns_if(odd); turns > 0; --turns)
+  w.l = sum[0] + sum[1];
+  const uint32_t v_at = odd ? mine : v_lds;
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-      add_not_finite<DT, DP>(w.o[qt], cur[qt][0], c, w.m[qt], w.lo[qt] - kb, w.hi[qt] - kb, v_lds, mine, lane);
+  for (int n = 0; n < 2 * (DP / 32); ++n)
+    w.o[n % (DP / 32)] = mfma<DT>(value_operand(ln, v_at, n), p[n / (DP / 32)], w.o[n % (DP / 32)]);
+#pragma unroll 1
+  for (int turns = turns_if(odd); turns > 0; --turns) add_not_finite<DT, DP>(w, s, sc.c, kb, v_lds, mine, lane);
+}
+
+// Adds 64 keys that every row sees, whose scores are `cur` with the largest `top`, and forms the next
+// 64 keys' scores `nxt` and `top`, in an order that keeps the matrix cores fed: the weights of the
+// current keys beside the score products of the next, then the value products.  Operands are read
+// from LDS kAhead products ahead (`f`: on entry the first K operands, on return those of the step
+// after, whose rows are at k_after), and each matrix instruction is followed by the share of the
+// vector work that fits beside it; the scheduling barriers keep that order.
+//
+// Two waves share a SIMD, and each issues an instruction every 4 cycles at best: a step has to stay
+// well under its matrix time of 1024 cycles (DP = 128) in instructions.  With 32 keys a step the
+// votes, the branches and the addresses cost as much as the weights do.
+constexpr int kAhead = 4, kGroups = 2;
+
+template <int DT, int DP>
+__device__ __forceinline__ void add_tile(Rows<DP>& w, const Lanes<DP>& ln, const v16f (&cur)[kGroups],
+                                         v16f (&nxt)[kGroups], float& top, v8s (&f)[kAhead], uint32_t k_next,
+                                         uint32_t k_after, uint32_t v_lds, const Scaling& sc) {
+  constexpr int kTiles = DP / 32, kScores = kGroups * DP / 16, kValues = kGroups * 2 * kTiles;
+  constexpr int kPer = 16 * kGroups / kScores;              // weights per score product
+  constexpr int kShare = 16 * kGroups / (kValues - 2) + 1;  // maxima per value product
+  static_assert(kScores % kAhead == 0 && kValues % kAhead == 0 && kPer % 2 == 0, "operand ring");
+  raise(w, top, sc);
+  uint32_t d[kGroups * 8];
+  float sum[2] = {w.l, 0.0f};
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int n = 0; n < kScores; ++n) {
+    nxt[n % kGroups] = mfma<DT>(f[n % kAhead], w.q[n / kGroups], n < kGroups ? zero16() : nxt[n % kGroups]);
+    f[n % kAhead] = n + kAhead < kScores ? key_operand<DP, kGroups>(ln, k_next, n + kAhead)
+                                         : value_operand(ln, v_lds, n + kAhead - kScores);
+#pragma unroll
+    for (int i = n * kPer; i < (n + 1) * kPer; i += 2) {
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[i / 16][i % 16], sc.c, -w.m));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[i / 16][i % 16 + 1], sc.c, -w.m));
+      sum[0] += x;
+      sum[1] += y;
+      d[i / 2] = pack2<DT>(x, y);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  w.l = sum[0] + sum[1];
+  float best = 0.0f;
+#pragma unroll
+  for (int n = 0; n < kValues; ++n) {
+    const int k = n / kTiles * 4;
+    const v8s p = __builtin_bit_cast(v8s, (u32x4){d[k], d[k + 1], d[k + 2], d[k + 3]});
+    w.o[n % kTiles] = mfma<DT>(f[n % kAhead], p, w.o[n % kTiles]);
+    f[n % kAhead] = n + kAhead < kValues ? value_operand(ln, v_lds, n + kAhead)
+                                         : key_operand<DP, kGroups>(ln, k_after, n + kAhead - kValues);
+    // the next scores are ready by the second product
+    if (n == 1) best = nxt[0][0];
+    if (n >= 1)
+#pragma unroll
+      for (int i = (n - 1) * kShare; i < n * kShare && i < 16 * kGroups; ++i) best = __builtin_fmaxf(best, nxt[i / 16][i % 16]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  top = both_max(best);
 }
 
 // ---------------------------------------------------------------- items
@@ -513,92 +439,73 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 
 // Loads the rows row0 .. of a wave; rows past the request's last take the last
 // one's limits and zero queries.
-template <int DP, int QT>
-__device__ __forceinline__ void load_rows(Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
-  const int group = a.group, rows = it.news * group;
-  const int h = lane >> 5, col = lane & 31;
+template <int DP>
+__device__ __forceinline__ void load_rows(Rows<DP>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
+  const int rows = it.news * a.group, h = lane >> 5;
+  const int r = row0 + (lane & 31), at = r < rows ? r : rows - 1;
+  const int tok = token_of(a, at), hd = it.head * a.group + at - tok * a.group;
+  const char* q = (const char*)a.q + ((int64_t)(it.start + tok) * a.q_stride + (int64_t)hd * a.q_head_stride) * 2;
 #pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    const int r = row0 + qt * 32 + col, at = r < rows ? r : rows - 1;
-    const int tok = token_of(a, at), hd = it.head * group + at - tok * group;
-    const char* q = (const char*)a.q + ((int64_t)(it.start + tok) * a.q_stride + (int64_t)hd * a.q_head_stride) * 2;
-#pragma unroll
-    for (int st = 0; st < DP / 16; ++st) {
-      const int ch = 2 * st + h;
-      v8s x = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (r < rows && ch * 8 < a.head_dim) x = *(const v8s*)(q + ch * 16);
-      w.q[qt][st] = x;
-    }
-    const int p = it.keys - it.news + tok;
-    w.hi[qt] = p + 1;
-    w.lo[qt] = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
-    w.m[qt] = -__builtin_inff();
-    w.l[qt] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w.o[qt][t][i] = 0.0f;
+  for (int st = 0; st < DP / 16; ++st) {
+    const int ch = 2 * st + h;
+    v8s x = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r < rows && ch * 8 < a.head_dim) x = *(const v8s*)(q + ch * 16);
+    w.q[st] = x;
   }
+  const int p = it.keys - it.news + tok;
+  w.hi = p + 1;
+  w.lo = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
+  w.m = kLowest;
+  w.far = -__builtin_inff();
+  w.l = 0.0f;
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t) w.o[t] = zero16();
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
 // Writes finished rows.
-template <int DT, int DP, int QT>
-__device__ __forceinline__ void store_rows(const Rows<DP, QT>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
-  const int group = a.group, rows = it.news * group;
-  const int h = lane >> 5, col = lane & 31;
+template <int DT, int DP>
+__device__ __forceinline__ void store_rows(const Rows<DP>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
+  const int rows = it.news * a.group, h = lane >> 5, r = row0 + (lane & 31);
+  const float l = both_sum(w.l), inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (r >= rows) return;
+  const int tok = token_of(a, r);
+  const int64_t at = (int64_t)(it.start + tok) * a.q_heads + it.head * a.group + r - tok * a.group;
+  uint32_t* out = (uint32_t*)a.out + at * (a.head_dim / 2);
 #pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    const float l = both_sum(w.l[qt]);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int r = row0 + qt * 32 + col;
-    if (r >= rows) continue;
-    const int tok = token_of(a, r);
-    const int64_t at = (int64_t)(it.start + tok) * a.q_heads + it.head * group + r - tok * group;
-    uint32_t* out = (uint32_t*)a.out + at * (a.head_dim / 2);
+  for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = t * 32 + 8 * i + 4 * h;
-        if (d < a.head_dim) {
-          const u32x2 x = {pack2<DT>(w.o[qt][t][4 * i] * inv, w.o[qt][t][4 * i + 1] * inv),
-                           pack2<DT>(w.o[qt][t][4 * i + 2] * inv, w.o[qt][t][4 * i + 3] * inv)};
-          *(u32x2*)(out + d / 2) = x;
-        }
-      }
-    if (a.lse && h == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (w.m[qt] + __builtin_log2f(l)) * kLn2;
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int d = t * 32 + 8 * i + 4 * h;
+      if (d < a.head_dim)
+        *(u32x2*)(out + d / 2) = (u32x2){pack2<DT>(w.o[t][4 * i] * inv, w.o[t][4 * i + 1] * inv),
+                                         pack2<DT>(w.o[t][4 * i + 2] * inv, w.o[t][4 * i + 3] * inv)};
+    }
+  if (a.lse && h == 0) a.lse[at] = lse_of(w.m, l);
 }
 
-// Parts of rows whose keys are split over workgroups: O (unnormalized), m, l.
-struct Part {
-  float* o;    // [slots][rows][DP]
-  float* ml;   // [slots][rows][2]
-};
-
-template <int DP, int QT>
-__device__ __forceinline__ void store_part(const Rows<DP, QT>& w, float* o, float* ml, int row0, int rows, int lane) {
-  const int h = lane >> 5, col = lane & 31;
+// Part of rows whose keys are split over workgroups: O (unnormalized) [rows][DP], (m, l) [rows].
+template <int DP>
+__device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* ml, int r, int lane) {
+  const int h = lane >> 5;
+  const float l = both_sum(w.l);
 #pragma unroll
-  for (int qt = 0; qt < QT; ++qt) {
-    const float l = both_sum(w.l[qt]);
-    const int r = row0 + qt * 32 + col;
-    if (r >= rows) continue;
+  for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(v4f*)(o + (int64_t)r * DP + t * 32 + 8 * i + 4 * h) =
-            (v4f){w.o[qt][t][4 * i], w.o[qt][t][4 * i + 1], w.o[qt][t][4 * i + 2], w.o[qt][t][4 * i + 3]};
-    if (h == 0) *(v2f*)(ml + 2 * r) = (v2f){w.m[qt], l};
-  }
+    for (int i = 0; i < 4; ++i)
+      *(v4f*)(o + (int64_t)r * DP + t * 32 + 8 * i + 4 * h) =
+          (v4f){w.o[t][4 * i], w.o[t][4 * i + 1], w.o[t][4 * i + 2], w.o[t][4 * i + 3]};
+  if (h == 0) *(v2f*)(ml + 2 * r) = (v2f){w.m, l};
 }
 
 // ---------------------------------------------------------------- many rows
-// A workgroup of NW waves, QT x 32 rows each; all waves share the tiles of 64
+// A workgroup of NW waves, 32 rows each; all waves share the tiles of 64
 // keys, copied global -> LDS.
 constexpr int kTile = 64;
-constexpr int kManyWaves = 8, kManyTiles = 1, kManyRows = 32 * kManyTiles * kManyWaves;
+constexpr int kManyWaves = 8, kManyRows = 32 * kManyWaves;
 constexpr int kManyShares = 256;   // one workgroup on each of the 256 CUs
 
 template <int DP>
@@ -675,65 +582,65 @@ struct TileCopy {
   }
 };
 
-// Runs the keys of tiles [t0, t1) (tiles of 64 from key 0) through the block,
-// 32 keys at a time.  The scores of the next 32 keys are formed while the
-// weights of the current 32 are, so that the matrix cores and the vector units
-// work side by side: iteration t uses K(t), K(t + 1) and V(t) while K(t + 2)
-// and V(t + 1) are on their way (three buffers of K, two of V, one barrier a
-// tile).
-template <int DT, int DP, int QT, int NW, bool PAGED>
+// Runs the keys of tiles [t0, t1) (tiles of 64 from key 0) through the block.
+// The scores of the next tile are formed while the weights of the current one
+// are, and the first operands of the tile after that are read ahead: iteration
+// t uses K(t + 1), K(t + 2) and V(t) while K(t + 3) and V(t + 1) are on their
+// way (three buffers of K, two of V, one barrier a tile).
+template <int DT, int DP, int NW, bool PAGED>
 __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, const Item& it, int t0, int t1,
-                                          Rows<DP, QT>& w, uint32_t lds) {
+                                          Rows<DP>& w, uint32_t lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rows = it.news * a.group;
-  const int first = it.row0 + wave * QT * 32;
+  const int first = it.row0 + wave * 32;
   constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
   using Copy = TileCopy<DP, NW / 2, PAGED>;
   const Copy cp(s, wave, lane);
-  typename Copy::Pages p1{}, p2{};
-  uint32_t k_now = lds, k_next = lds + kBytes, k_free = lds + 2 * kBytes;
+  typename Copy::Pages p1{}, p2{}, p3{};   // of the tiles t + 1 .. t + 3
+  uint32_t k_now = lds, k_next = lds + kBytes, k_after = lds + 2 * kBytes;
   uint32_t v_now = lds + 3 * kBytes, v_next = lds + 4 * kBytes;
   if (t0 < t1) {
     const auto p0 = cp.pages(t0 * kTile);
     p1 = cp.pages((t0 + 1) * kTile);
     p2 = cp.pages((t0 + 2) * kTile);
+    p3 = cp.pages((t0 + 3) * kTile);
     cp.template issue<false>(t0 * kTile, p0, k_now);
-    if (t0 + 1 < t1) cp.template issue<false>((t0 + 1) * kTile, p1, k_next);
     cp.template issue<true>(t0 * kTile, p0, v_now);
+    if (t0 + 1 < t1) cp.template issue<false>((t0 + 1) * kTile, p1, k_next);
+    if (t0 + 2 < t1) cp.template issue<false>((t0 + 2) * kTile, p2, k_after);
   }
-  load_rows<DP, QT>(w, a, it, first, lane);
+  load_rows<DP>(w, a, it, first, lane);
   // limits of the wave's rows: positions of its first and last row
   const bool active = first < rows;
-  const int end = first + QT * 32 < rows ? first + QT * 32 : rows;
+  const int end = first + 32 < rows ? first + 32 : rows;
   const int pos0 = it.keys - it.news + token_of(a, first), pos1 = it.keys - it.news + (end > 0 ? token_of(a, end - 1) : 0);
   const int hi_min = uni(pos0 + 1), hi_max = uni(active ? pos1 + 1 : 0);
   const int lo_min = uni((a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0);
   const int lo_max = uni((a.window > 0 && pos1 + 1 > a.window) ? pos1 + 1 - a.window : 0);
-  const float c = a.scale * kLog2e;
+  const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
   const Lanes<DP> ln(lane);
   const uint32_t mine = lds + 5 * kBytes + wave * kHalf;
-  // tiles that some row of the wave sees, and (> 0) whether some row does not see some of 32 keys
+  // tiles that some row of the wave sees; those that every row sees
   const int w0 = clampi(lo_min / kTile, t0, t1), w1 = clampi((hi_max + kTile - 1) / kTile, w0, t1);
-  auto hidden = [&](int kb) { return kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb; };
+  const int full0 = (lo_max + kTile - 1) / kTile, full1 = hi_min < 0 ? 0 : hi_min / kTile < w1 ? hi_min / kTile : w1;
   int t = t0;
   auto begin = [&]() {
-    if (t > t0) {
-      wait_vmcnt_le<0>();
-      lds_barrier();
-    }
-    if (t + 2 < t1) cp.template issue<false>((t + 2) * kTile, p2, k_free);
+    wait_vmcnt_le<0>();
+    lds_barrier();   // the copies have arrived, and K(t) and V(t - 1) have been read by all waves
+    if (t + 3 < t1) cp.template issue<false>((t + 3) * kTile, p3, k_now);
     if (t + 1 < t1) cp.template issue<true>((t + 1) * kTile, p1, v_next);
-    p1 = p2;
-    p2 = cp.pages((t + 3) * kTile);
   };
   auto end_tile = [&]() {
     const uint32_t k_old = k_now, v_old = v_now;
     k_now = k_next;
-    k_next = k_free;
-    k_free = k_old;
+    k_next = k_after;
+    k_after = k_old;
     v_now = v_next;
     v_next = v_old;
     ++t;
+    p1 = p2;
+    p2 = p3;
+    p3 = cp.pages((t + 3) * kTile);
   };
   auto skip_to = [&](int stop) {
 #pragma unroll 1
@@ -745,24 +652,40 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   wait_vmcnt_le<0>();
   lds_barrier();
   skip_to(w0);
-  if (w0 < w1) {
-    v16f sa[QT][1], sb[QT][1];
-    float top[QT];
-    scores<DT, DP, QT, 1>(sa, w, ln, k_now);
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) top[qt] = both_max(largest(sa[qt])) * c;
-    v8s f[kAhead];
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) f[n] = key_operand(ln, k_now + kHalf, n);
-    // past the last tile the next scores are formed from whatever the buffer holds, and not used
+  v16f sa[kGroups];
+  if (t < w1) scores<DT, DP, kGroups>(sa, w, ln, k_now);
 #pragma unroll 1
-    do {
+  while (t < w1) {
+    if (t >= full0 && t + 1 < full1) {
+      v16f sb[kGroups];
+      v8s f[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) f[n] = key_operand<DP, kGroups>(ln, k_next, n);
+      float top = both_max(__builtin_fmaxf(largest(sa[0]), largest(sa[1])));
+      // two tiles a turn, so that the scores change places; past the last tile the next scores are
+      // formed from whatever the buffer holds, and not used
+#pragma unroll 1
+      do {
+        begin();
+        add_tile<DT, DP>(w, ln, sa, sb, top, f, k_next, k_after, v_now, sc);
+        end_tile();
+        begin();
+        add_tile<DT, DP>(w, ln, sb, sa, top, f, k_next, k_after, v_now, sc);
+        end_tile();
+      } while (t + 1 < full1);
+    } else {
       begin();
-      const int kb = t * kTile;
-      step<DT, DP, QT, true>(w, ln, sa, sb, top, f, k_now + kHalf, k_next, v_now, kb, c, hidden(kb), mine, lane);
-      step<DT, DP, QT, true>(w, ln, sb, sa, top, f, k_next, k_next + kHalf, v_now + kHalf, kb + 32, c, hidden(kb + 32), mine, lane);
+      v16f x = sa[0];
+#pragma unroll 1
+      for (int g = 0; g < kGroups; ++g) {
+        const int kb = t * kTile + g * 32;
+        const int hidden = kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb;
+        if (kb < hi_max && kb + 32 > lo_min) add_keys<DT, DP>(w, ln, x, v_now + g * kHalf, kb, sc, hidden, mine, lane);
+        x = sa[1];
+      }
+      if (t + 1 < w1) scores<DT, DP, kGroups>(sa, w, ln, k_next);
       end_tile();
-    } while (t < w1);
+    }
   }
   skip_to(t1);
   lds_barrier();   // the buffers may be filled again
@@ -788,10 +711,10 @@ extern __shared__ __align__(1024) unsigned char dyn_lds[];
 // what follows the last prompt, rows without keys, which are set to 0.  A
 // prompt's longest rows come first, and key/value heads are the fastest
 // index, so that workgroups on one XCD (dispatched round robin) share a head.
-template <int DT, int DP, int QT, int NW>
-__global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(AttnArgs a) {
+template <int DT, int DP, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
   __shared__ int found;
-  constexpr int kRows = 32 * QT * NW;
+  constexpr int kRows = 32 * NW;
   const int tid = threadIdx.x;
   const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
   const int group = a.group;
@@ -833,9 +756,9 @@ __global__ void __launch_bounds__(64 * NW, DP == 64 ? 4 : 2) prompt_attn_kernel(
   s.d_bytes = a.head_dim * 2;
   int t0 = 0, t1 = 0;
   if (req < a.seqs) tiles_of(a, it, it.row0, kRows, kTile, t0, t1);
-  Rows<DP, QT> w;
-  run_block<DT, DP, QT, NW, false>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
-  store_rows<DT, DP, QT>(w, a, it, it.row0 + uni(tid >> 6) * QT * 32, tid & 63);
+  Rows<DP> w;
+  run_block<DT, DP, NW, false>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
+  store_rows<DT, DP>(w, a, it, it.row0 + uni(tid >> 6) * 32, tid & 63);
 }
 
 // ---------------------------------------------------------------- paged: work split
@@ -1039,11 +962,11 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 }
 
 // ---------------------------------------------------------------- paged: many rows
-template <int DT, int DP, int QT, int NW>
+template <int DT, int DP, int NW>
 __global__ void __launch_bounds__(64 * NW, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int64_t lds[NW + 2];
-  constexpr int kRows = 32 * QT * NW;
+  constexpr int kRows = 32 * NW;
   // an XCD takes consecutive shares, so that workgroups that read the same keys share its L2
   const int w = (blockIdx.x & 7) * (kManyShares / 8) + (blockIdx.x >> 3);
   for_segments<kRows, kTile, kManyShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
@@ -1052,15 +975,15 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     int b0, b1;
     tiles_of(a, g.it, g.it.row0, kRows, kTile, b0, b1);
     const int t0 = uni(g.t0 > b0 ? g.t0 : b0), t1 = uni(g.t1 < b1 ? g.t1 : b1);
-    Rows<DP, QT> rows;
-    run_block<DT, DP, QT, NW, true>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
-    const int row = uni(threadIdx.x >> 6) * QT * 32, lane = threadIdx.x & 63;
+    Rows<DP> rows;
+    run_block<DT, DP, NW, true>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
+    const int row = uni(threadIdx.x >> 6) * 32, lane = threadIdx.x & 63;
     if (slot < 0) {
-      store_rows<DT, DP, QT>(rows, a, g.it, g.it.row0 + row, lane);
+      store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane);
     } else {
       float *o, *ml;
       part_of<DP, kRows, kManyShares>((float*)a.workspace, slot, o, ml);
-      store_part<DP, QT>(rows, o, ml, row, kRows, lane);
+      store_part<DP>(rows, o, ml, row + (lane & 31), lane);
     }
   });
 }
@@ -1102,7 +1025,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     const int hi_min = p0 + 1, hi_max = p1 + 1;
     const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
     const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
-    const float c = a.scale * kLog2e;
+    const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
     const int n = g.t1 - g.t0;
     // eight keys lie in one page and no row has a rest
     const bool whole = s.d_bytes == DP * 2 && s.page_size % 8 == 0;
@@ -1151,8 +1074,8 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         }
       }
     };
-    Rows<DP, 1> st;
-    load_rows<DP, 1>(st, a, g.it, g.it.row0, lane);
+    Rows<DP> st;
+    load_rows<DP>(st, a, g.it, g.it.row0, lane);
     if (n > 0 && (g.t0 * NW + wave) * 32 < s.keys) hold((g.t0 * NW + wave) * 32);
     wait_vmcnt_le<0>();   // the queries: from here on only copies are waited for
 #pragma unroll 1
@@ -1165,13 +1088,11 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         else wait_vmcnt_le<0>();
         asm volatile("" ::: "memory");
         if (seen) {
-          v16f sc[1][1];
-          scores<DT, DP, 1, 1>(sc, st, ln, at);
-          float top[1] = {both_max(largest(sc[0])) * c};
-          v8s none[kAhead];
+          v16f x[1];
+          scores<DT, DP, 1>(x, st, ln, at);
           // the K rows are not needed any more: their place is the wave's scratch
-          step<DT, DP, 1, false>(st, ln, sc, sc, top, none, 0, 0, at + kHalf, kb, c,
-                                 kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb, at, lane);
+          add_keys<DT, DP>(st, ln, x[0], at + kHalf, kb, sc,
+                           kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb, at, lane);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
@@ -1179,13 +1100,13 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     }
     // join the waves: weights 2^(m_w - m)
     const int h = lane >> 5, col = lane & 31;
-    const float l = both_sum(st.l[0]);
-    if (h == 0) { join_ml[wave][col][0] = st.m[0]; join_ml[wave][col][1] = l; }
+    const float l = both_sum(st.l);
+    if (h == 0) { join_ml[wave][col][0] = st.m; join_ml[wave][col][1] = l; }
     __syncthreads();
-    float m = -__builtin_inff();
+    float m = kLowest;
 #pragma unroll
     for (int k = 0; k < NW; ++k) m = __builtin_fmaxf(m, join_ml[k][col][0]);
-    const float mine = st.m[0] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(st.m[0] - m);
+    const float mine = __builtin_amdgcn_exp2f(st.m - m);
     // a row stored from bank 4 col on: the 32 rows of a store take all banks in turn
     if (g.it.row0 + col < rows)
 #pragma unroll
@@ -1194,7 +1115,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       for (int i = 0; i < 4; ++i) {
         v4f x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mine == 0.0f ? 0.0f : st.o[0][t][4 * i + e] * mine;
+        for (int e = 0; e < 4; ++e) x[e] = st.o[t][4 * i + e] * mine;
         const int q = t * 8 + 2 * i + h;
         *(v4f*)(join_o + (wave * 32 + col) * DP + ((q ^ (col & (DP / 4 - 1))) * 4)) = x;
       }
@@ -1205,16 +1126,14 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     for (int k = tid; k < 32 * (DP / 4); k += 64 * NW) {
       const int r = k / (DP / 4), q = k % (DP / 4), row = g.it.row0 + r;
       if (row >= rows) continue;
-      float mm = -__builtin_inff();
+      float mm = kLowest;
 #pragma unroll
       for (int x = 0; x < NW; ++x) mm = __builtin_fmaxf(mm, join_ml[x][r][0]);
       float ll = 0.0f;
       v4f o = {0, 0, 0, 0};
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
-        const float mx = join_ml[x][r][0];
-        const float wx = mx == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mx - mm);
-        ll += wx == 0.0f ? 0.0f : join_ml[x][r][1] * wx;
+        ll += join_ml[x][r][1] * __builtin_amdgcn_exp2f(join_ml[x][r][0] - mm);
         const v4f y = *(const v4f*)(join_o + (x * 32 + r) * DP + ((q ^ (r & (DP / 4 - 1))) * 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] += y[e];
@@ -1226,7 +1145,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         if (q * 4 < a.head_dim)
           *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
               (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-        if (a.lse && q == 0) a.lse[at] = ll == 0.0f ? -__builtin_inff() : (mm + __builtin_log2f(ll)) * kLn2;
+        if (a.lse && q == 0) a.lse[at] = lse_of(mm, ll);
       } else {
         *(v4f*)(po + (int64_t)r * DP + q * 4) = o;
         if (q == 0) *(v2f*)(pml + 2 * r) = (v2f){mm, ll};
@@ -1241,7 +1160,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // earlier share starts inside it too.  Its parts are the last segment of share
 // w - 1 and the first segments of the shares from w on.  The parts come from
 // other XCDs' L2s, so a load takes most of a microsecond and what counts is
-// that few wait for one another: 8 groups of threads (DP = 128; a group holds a
+// that few wait for one another: 8 teams of threads (DP = 128; a team holds a
 // row) either take 8 rows, each reading kBatch parts at a time (ROWS = 256: two
 // or three parts), or every 8th part of one row after another (ROWS = 32: a
 // long request alone has dozens of parts).
@@ -1249,11 +1168,11 @@ constexpr int kBatch = 4;
 
 template <int DT, int DP, int ROWS, int UNIT, int SHARES>
 __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
-  constexpr int kQ = DP / 4, kGroups = 256 / kQ;
+  constexpr int kQ = DP / 4, kTeams = 256 / kQ;
   constexpr bool kByPart = ROWS <= 32;
   __shared__ int64_t lds[6];
-  __shared__ float part_m[kByPart ? kBatch : 1][kGroups], part_l[kByPart ? kBatch : 1][kGroups];
-  __shared__ v4f part_o[kByPart ? kBatch : 1][kGroups][kQ];
+  __shared__ float part_m[kByPart ? kBatch : 1][kTeams], part_l[kByPart ? kBatch : 1][kTeams];
+  __shared__ v4f part_o[kByPart ? kBatch : 1][kTeams][kQ];
   const int w = blockIdx.x + 1, tid = threadIdx.x;
   const Plan<ROWS, UNIT, SHARES, 256> pl(a, sp, w, lds);
   if (pl.req > a.seqs || pl.share * w >= pl.total) return;
@@ -1275,9 +1194,8 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
     x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
   };
   auto join = [&](float& m, float& l, v4f& o, float pm, float pl2, v4f x) {
-    if (pm == -__builtin_inff()) return;   // saw nothing
     const float nm = __builtin_fmaxf(m, pm);
-    const float u = m == nm ? 1.0f : __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(pm - nm);
+    const float u = __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(pm - nm);
     l = l * u + pl2 * v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = o[e] * u + x[e] * v;
@@ -1290,12 +1208,12 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
     if (q * 4 < a.head_dim)
       *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
           (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-    if (a.lse && q == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+    if (a.lse && q == 0) a.lse[at] = lse_of(m, l);
   };
   if constexpr (!kByPart) {
-    const int row = blockIdx.y * kGroups + g;
+    const int row = blockIdx.y * kTeams + g;
     if (row >= rows) return;
-    float m = -__builtin_inff(), l = 0.0f;
+    float m = kLowest, l = 0.0f;
     v4f o = {0, 0, 0, 0};
     for (int j = w - 1; j <= last; j += kBatch) {
       v2f ml[kBatch];
@@ -1313,11 +1231,11 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
       v4f o[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        m[k] = -__builtin_inff();
+        m[k] = kLowest;
         l[k] = 0.0f;
         o[k] = (v4f){0, 0, 0, 0};
       }
-      for (int j = w - 1 + g; j <= last; j += kGroups) {
+      for (int j = w - 1 + g; j <= last; j += kTeams) {
         v2f ml[kBatch];
         v4f x[kBatch];
 #pragma unroll
@@ -1336,10 +1254,10 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
       }
       __syncthreads();
       if (g < kBatch && row0 + g < rows) {
-        float jm = -__builtin_inff(), jl = 0.0f;
+        float jm = kLowest, jl = 0.0f;
         v4f jo = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) join(jm, jl, jo, part_m[g][k], part_l[g][k], part_o[g][k][q]);
+        for (int k = 0; k < kTeams; ++k) join(jm, jl, jo, part_m[g][k], part_l[g][k], part_o[g][k][q]);
         write(row0 + g, jm, jl, jo);
       }
     }
@@ -1398,7 +1316,7 @@ int64_t prompt_blocks(const AttnArgs& a) {
 
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  return launch_lds<prompt_attn_kernel<DT, DP, kManyTiles, kManyWaves>>(
+  return launch_lds<prompt_attn_kernel<DT, DP, kManyWaves>>(
       (unsigned)(prompt_blocks(a) * a.kv_heads), 64 * kManyWaves, many_lds_bytes<DP>(), s, with_group(a));
 }
 
@@ -1422,7 +1340,7 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   }
   if (many) {
     const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
-    e = launch_lds<paged_rows_kernel<DT, DP, kManyTiles, kManyWaves>>(kManyShares, 64 * kManyWaves, many_lds_bytes<DP>(),
+    e = launch_lds<paged_rows_kernel<DT, DP, kManyWaves>>(kManyShares, 64 * kManyWaves, many_lds_bytes<DP>(),
                                                                      s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
     combine_kernel<DT, DP, kManyRows, kTile, kManyShares>
