@@ -272,63 +272,56 @@ __device__ __forceinline__ bool all_finite(uint32_t v_lds, int lane) {
 }
 
 // Where some row does not see some key of a tile and a value there is not finite, 0 * inf in the
-// matrix cores would carry it to rows that do not see it.  Such a tile (32 keys) is multiplied from
-// a copy with 0 in place of those values (copy_finite, into the wave's own LDS), and they are added
-// one by one to the rows that see them (add_not_finite).
-template <int DT, int DP>
-__device__ __forceinline__ void copy_finite(uint32_t v_lds, uint32_t mine, int lane) {
-  asm volatile("" : "+v"(lane));
-#pragma unroll 1
-  for (int n = 0; n < 32 * DP * 2 / 1024; ++n) {
-    u32x4 x = __builtin_bit_cast(u32x4, read_b128(v_lds + n * 1024 + lane * 16));
+// matrix cores would carry it to rows that do not see it.  The products of such a tile are formed with
+// 0 in place of those values, and they are added one by one to the rows that see them.  Rare: short
+// rather than fast.
+template <int DT>
+__device__ __forceinline__ v8s finite_only(v8s v) {
+  u32x4 x = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if ((x[e] & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFF0000u;
-      if (((x[e] >> 16) & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFFu;
-    }
-    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(mine + n * 1024 + lane * 16) = x;
+  for (int e = 0; e < 4; ++e) {
+    if ((x[e] & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFF0000u;
+    if (((x[e] >> 16) & 0x7FFFu) >= not_finite_bits<DT>()) x[e] &= 0xFFFFu;
   }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  return __builtin_bit_cast(v8s, x);
 }
 
 template <int DT, int DP>
-__device__ __forceinline__ void add_not_finite(Rows<DP>& w, const v16f& s, float c, int kb, uint32_t v_lds,
-                                               uint32_t mine, int lane) {
+__device__ __forceinline__ void add_not_finite(Rows<DP>& w, const v16f& s, float c, int kb, uint32_t v_lds, int lane) {
   asm volatile("" : "+v"(lane));
-  const int h = lane >> 5, col = lane & 31;
-  typedef __attribute__((address_space(3))) float* lds_f;
+  const int h = lane >> 5;
   typedef __attribute__((address_space(3))) u32x2* lds_2;
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the copy has been read
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    *(lds_f)(uintptr_t)(mine + ((8 * (i / 4) + 4 * h + i % 4) * 32 + col) * 4) =
-        __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -w.m));
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
   for (int key = 0; key < 32; ++key) {
-    const float p = *(lds_f)(uintptr_t)(mine + (key * 32 + col) * 4);
+    // the row's score of this key: register 4 (key / 8) + key % 4 of half-wave key / 4 % 2
+    float x = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) x = i == key / 8 * 4 + key % 4 ? s[i] : x;
+    const float mine = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, -w.m));
+    const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(mine), __float_as_uint(mine), false, false);
+    const float p = __uint_as_float((key & 4) ? both[1] : both[0]);
     const bool sees = kb + key >= w.lo && kb + key < w.hi;
 #pragma unroll
     for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const u32x2 x = *(lds_2)(uintptr_t)(v_lds + chunk_at<DP>(key, t * 4 + i) + 8 * h);
+        const u32x2 y2 = *(lds_2)(uintptr_t)(v_lds + chunk_at<DP>(key, t * 4 + i) + 8 * h);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t y = (x[e / 2] >> (16 * (e % 2))) & 0xFFFFu;
+          const uint32_t y = (y2[e / 2] >> (16 * (e % 2))) & 0xFFFFu;
           const bool add = sees && (y & 0x7FFFu) >= not_finite_bits<DT>();
           w.o[t][4 * i + e] += add ? p * unpack1<DT>((uint16_t)y) : 0.0f;
         }
       }
   }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
 // Adds 32 keys from key kb, whose scores are `s` and whose values are at v_lds.  `hidden` > 0: some
-// row does not see some of them.  `mine`: 32 rows of DP of the wave's own LDS.
+// row does not see some of them.
 template <int DT, int DP>
 __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f& s, uint32_t v_lds, int kb,
-                                         const Scaling& sc, int hidden, uint32_t mine, int lane) {
+                                         const Scaling& sc, int hidden, int lane) {
+  constexpr int kTiles = DP / 32;
   int odd = 0;   // some value is not finite
 #pragma unroll 1
   for (int turns = turns_if(hidden); turns > 0; --turns) {
@@ -339,7 +332,6 @@ __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f&
       if (key < lo || key >= hi) s[i] = -__builtin_inff();
     }
     odd = uni(all_finite<DT, DP>(v_lds, lane) ? 0 : 1);
-    if (odd) copy_finite<DT, DP>(v_lds, mine, lane);
   }
   raise(w, both_max(largest(s)), sc);
   v8s p[2];
@@ -359,12 +351,21 @@ __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f&
     p[half] = __builtin_bit_cast(v8s, (u32x4){d[0], d[1], d[2], d[3]});
   }
   w.l = sum[0] + sum[1];
-  const uint32_t v_at = odd ? mine : v_lds;
-#pragma unroll
-  for (int n = 0; n < 2 * (DP / 32); ++n)
-    w.o[n % (DP / 32)] = mfma<DT>(value_operand(ln, v_at, n), p[n / (DP / 32)], w.o[n % (DP / 32)]);
 #pragma unroll 1
-  for (int turns = turns_if(odd); turns > 0; --turns) add_not_finite<DT, DP>(w, s, sc.c, kb, v_lds, mine, lane);
+  for (int turns = turns_if(1 - odd); turns > 0; --turns) {
+    asm volatile("" : "+s"(v_lds));   // the reads belong into the loop
+#pragma unroll
+    for (int n = 0; n < 2 * kTiles; ++n)
+      w.o[n % kTiles] = mfma<DT>(value_operand(ln, v_lds, n), p[n / kTiles], w.o[n % kTiles]);
+  }
+#pragma unroll 1
+  for (int turns = turns_if(odd); turns > 0; --turns) {
+    asm volatile("" : "+s"(v_lds));
+#pragma unroll
+    for (int n = 0; n < 2 * kTiles; ++n)
+      w.o[n % kTiles] = mfma<DT>(finite_only<DT>(value_operand(ln, v_lds, n)), p[n / kTiles], w.o[n % kTiles]);
+    add_not_finite<DT, DP>(w, s, sc.c, kb, v_lds, lane);
+  }
 }
 
 // Adds 64 keys that every row sees, whose scores are `cur` with the largest `top`, and forms the next
@@ -391,6 +392,9 @@ __device__ __forceinline__ void add_tile(Rows<DP>& w, const Lanes<DP>& ln, const
   uint32_t d[kGroups * 8];
   float sum[2] = {w.l, 0.0f};
   __builtin_amdgcn_sched_barrier(0);
+  // the wave at its score products, which have vector work beside them, goes before one at its value
+  // products (1 % of a long prompt; the other way round is slower)
+  __builtin_amdgcn_s_setprio(1);
 #pragma unroll
   for (int n = 0; n < kScores; ++n) {
     nxt[n % kGroups] = mfma<DT>(f[n % kAhead], w.q[n / kGroups], n < kGroups ? zero16() : nxt[n % kGroups]);
@@ -407,6 +411,7 @@ __device__ __forceinline__ void add_tile(Rows<DP>& w, const Lanes<DP>& ln, const
     __builtin_amdgcn_sched_barrier(0);
   }
   w.l = sum[0] + sum[1];
+  __builtin_amdgcn_s_setprio(0);
   float best = 0.0f;
 #pragma unroll
   for (int n = 0; n < kValues; ++n) {
@@ -502,33 +507,46 @@ __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* m
 }
 
 // ---------------------------------------------------------------- many rows
-// A workgroup of NW waves, 32 rows each; all waves share the tiles of 64
-// keys, copied global -> LDS.
+// A workgroup of NW = 4 or 8 waves, 32 rows each; all waves share the tiles of
+// 64 keys, copied global -> LDS.  A wave takes up to half the registers of two
+// waves' SIMD, so a CU holds two workgroups of four waves or one of eight.  Two
+// meet no common barrier, the start and end of one lie beside the work of the
+// other, and blocks of 128 rows waste less above the diagonal; but every tile
+// is copied twice as often.  Measured, 4 / 8 waves: head dimension 64 (9001
+// tokens, window 1024) 58.8 / 81.7 us; head dimension 128, 210 tokens 12.1 /
+// 14.3, ragged 8192 tokens 97.6 / 96.4, one prompt of 8192 560 / 524, 1700 new
+// tokens over 16k keys 1006 / 557 us, where the copies are what costs.  So four
+// waves for head dimensions up to 64, and above that for prompts that do not
+// give every CU a block of 256 rows.
+template <int NW>
+constexpr int kShares = NW == 4 ? 512 : 256;   // of paged work: workgroups that the 256 CUs hold
+template <int DP>
+constexpr int kPagedWaves = DP == 64 ? 4 : 8;
+constexpr int kCopyWaves = 4;
 constexpr int kTile = 64;
-constexpr int kManyWaves = 8, kManyRows = 32 * kManyWaves;
-constexpr int kManyShares = 256;   // one workgroup on each of the 256 CUs
 
 template <int DP>
 constexpr int tile_bytes() { return kTile * DP * 2; }
 
 // Copies of one wave: kIters instructions for a tile of K or V, each of kRowsPer whole rows.  The
-// copy path of a CU takes 64 bytes a cycle, 512 cycles for a tile of K and V, and a wave waits while
-// it is busy.  So only the first NC waves copy: the waves of the other half, which share the SIMDs
-// with them, compute meanwhile, and the two are out of step from then on.
-template <int DP, int NC, bool PAGED>
+// copy path of a CU takes 64 bytes a cycle, 512 cycles for a tile of K and V (DP = 128), and a wave
+// waits while it is busy.  Of eight waves only the first four copy: the others, which share the SIMDs
+// with them, compute meanwhile, and the two are out of step from then on (530 us with all eight
+// copying, 523 us).
+template <int DP, bool PAGED>
 struct TileCopy {
   static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
   static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
-  static constexpr int kIters = kTile / (kRowsPer * NC);
-  static_assert(kIters >= 1 && (NC * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
+  static constexpr int kIters = kTile / (kRowsPer * kCopyWaves);
+  static_assert(kIters >= 1 && (kCopyWaves * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
   const Source& s;
-  int wave, lane, chunk;    // chunk: the lane's 16 bytes of its row
+  int wave, lane;
   uint32_t k_ofs, v_ofs;    // byte offset of the lane from an instruction's first row
   bool whole;               // full rows, and the rows of an instruction lie in one page
 
   __device__ __forceinline__ TileCopy(const Source& src, int wv, int ln) : s(src), wave(wv), lane(ln) {
     const int r = wave * kRowsPer + lane / kChunks;
-    chunk = (lane % kChunks) ^ swz<DP>(r);
+    const int chunk = (lane % kChunks) ^ swz<DP>(r);   // the lane's 16 bytes of its row
     const uint32_t k_row = PAGED ? s.d_bytes : (uint32_t)s.k_step, v_row = PAGED ? s.d_bytes : (uint32_t)s.v_step;
     k_ofs = (lane / kChunks) * k_row + chunk * 16;
     v_ofs = (lane / kChunks) * v_row + chunk * 16;
@@ -541,10 +559,10 @@ struct TileCopy {
   __device__ __forceinline__ Pages pages(int kb) const {
     Pages p{};
     if constexpr (PAGED) {
-      if (whole && wave < NC) {
+      if (whole && wave < kCopyWaves) {
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
-          const int j = kb + (it * NC + wave) * kRowsPer;
+          const int j = kb + (it * kCopyWaves + wave) * kRowsPer;
           const auto at = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)(s.table + page_of(s, j < s.keys ? j : 0));
           p.id[it] = *at;
         }
@@ -554,29 +572,38 @@ struct TileCopy {
   }
   template <bool V>
   __device__ __forceinline__ void issue(int kb, const Pages& p, uint32_t lds) const {
-    if (wave >= NC) return;
+    if (wave >= kCopyWaves) return;
     if (whole && kb + kTile <= s.keys) {
+      const int j0 = kb + wave * kRowsPer;
+      const char* base = V ? s.v : s.k;
+      if constexpr (PAGED) {
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int j = kb + (it * NC + wave) * kRowsPer;
-        const char* base = V ? s.v : s.k;
-        if constexpr (PAGED) {
-          const int64_t off = (int64_t)p.id[it] * s.k_step + (int64_t)(j - page_of(s, j) * s.page_size) * s.d_bytes;
-          base = (uint32_t)p.id[it] < (uint64_t)s.num_pages ? base + off : reinterpret_cast<const char*>(kZeros);
-        } else {
-          base += (int64_t)j * (V ? s.v_step : s.k_step);
+        for (int it = 0; it < kIters; ++it) {
+          const int j = j0 + it * kCopyWaves * kRowsPer;
+          const int64_t off = (int64_t)p.id[it] * s.k_step + (j - page_of(s, j) * s.page_size) * s.d_bytes;
+          const bool there = (uint32_t)p.id[it] < (uint64_t)s.num_pages;
+          dma16(there ? base + off : reinterpret_cast<const char*>(kZeros), k_ofs, lds + (it * kCopyWaves + wave) * 1024);
         }
-        dma16(base, V ? v_ofs : k_ofs, lds + (it * NC + wave) * 1024);
+      } else {
+        const int64_t step = V ? s.v_step : s.k_step;
+        base += j0 * step;
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          dma16(base, V ? v_ofs : k_ofs, lds + (it * kCopyWaves + wave) * 1024);
+          base += step * (kCopyWaves * kRowsPer);
+        }
       }
     } else {
+      int l = lane;
+      asm volatile("" : "+v"(l));   // nothing of this path is kept in registers beside the common one
 #pragma unroll 1
       for (int it = 0; it < kIters; ++it) {
-        const int j = kb + (it * NC + wave) * kRowsPer + lane / kChunks;
+        const int r = (it * kCopyWaves + wave) * kRowsPer + l / kChunks, j = kb + r;
         int page = 0;
         if constexpr (PAGED) page = j < s.keys ? s.table[page_of(s, j)] : -1;
         const char *k, *v;
-        row_at<PAGED>(s, j, page, chunk * 16, k, v);
-        dma16_at(V ? v : k, (uint32_t)uni(lds + (it * NC + wave) * 1024));
+        row_at<PAGED>(s, j, page, ((l % kChunks) ^ swz<DP>(r)) * 16, k, v);
+        dma16_at(V ? v : k, (uint32_t)uni(lds + (it * kCopyWaves + wave) * 1024));
       }
     }
   }
@@ -594,7 +621,7 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   const int rows = it.news * a.group;
   const int first = it.row0 + wave * 32;
   constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
-  using Copy = TileCopy<DP, NW / 2, PAGED>;
+  using Copy = TileCopy<DP, PAGED>;
   const Copy cp(s, wave, lane);
   typename Copy::Pages p1{}, p2{}, p3{};   // of the tiles t + 1 .. t + 3
   uint32_t k_now = lds, k_next = lds + kBytes, k_after = lds + 2 * kBytes;
@@ -619,7 +646,6 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   const int lo_max = uni((a.window > 0 && pos1 + 1 > a.window) ? pos1 + 1 - a.window : 0);
   const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
   const Lanes<DP> ln(lane);
-  const uint32_t mine = lds + 5 * kBytes + wave * kHalf;
   // tiles that some row of the wave sees; those that every row sees
   const int w0 = clampi(lo_min / kTile, t0, t1), w1 = clampi((hi_max + kTile - 1) / kTile, w0, t1);
   const int full0 = (lo_max + kTile - 1) / kTile, full1 = hi_min < 0 ? 0 : hi_min / kTile < w1 ? hi_min / kTile : w1;
@@ -673,6 +699,13 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
         add_tile<DT, DP>(w, ln, sb, sa, top, f, k_next, k_after, v_now, sc);
         end_tile();
       } while (t + 1 < full1);
+      if (t < full1) {
+        begin();
+        add_tile<DT, DP>(w, ln, sa, sb, top, f, k_next, k_after, v_now, sc);
+        end_tile();
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) sa[g] = sb[g];
+      }
     } else {
       begin();
       v16f x = sa[0];
@@ -680,7 +713,7 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
       for (int g = 0; g < kGroups; ++g) {
         const int kb = t * kTile + g * 32;
         const int hidden = kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb;
-        if (kb < hi_max && kb + 32 > lo_min) add_keys<DT, DP>(w, ln, x, v_now + g * kHalf, kb, sc, hidden, mine, lane);
+        if (kb < hi_max && kb + 32 > lo_min) add_keys<DT, DP>(w, ln, x, v_now + g * kHalf, kb, sc, hidden, lane);
         x = sa[1];
       }
       if (t + 1 < w1) scores<DT, DP, kGroups>(sa, w, ln, k_next);
@@ -713,7 +746,7 @@ extern __shared__ __align__(1024) unsigned char dyn_lds[];
 // index, so that workgroups on one XCD (dispatched round robin) share a head.
 template <int DT, int DP, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
-  __shared__ int found;
+  int& found = *reinterpret_cast<int*>(dyn_lds);
   constexpr int kRows = 32 * NW;
   const int tid = threadIdx.x;
   const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
@@ -736,6 +769,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
     if (n) atomicAdd(&found, n);
     __syncthreads();
     req = uni(found) - 1;
+    __syncthreads();   // the tiles take its place
     if (req < 0) return;
     start = clampi(uni(a.cu[req]), 0, a.tokens);
     stop = req < a.seqs ? uni(a.cu[req + 1]) : a.tokens;
@@ -812,8 +846,9 @@ __device__ __forceinline__ Req request(const AttnArgs& a, const Split& sp, int i
 
 // The place of a share's first unit, and access to the requests from there on.  Up to 63 requests
 // (and the rows past the last) are held one per lane, by every wave for itself: one load, a scan over
-// the lanes and no barrier.  More are summed by the workgroup and loaded again when they are reached.
-template <int BLOCK, int UNIT, int SHARES, int NT>
+// the lanes and no barrier.  More are summed by the workgroup and loaded again when they are reached;
+// so are they, without KEEP, where the registers to hold them are missing.
+template <int BLOCK, int UNIT, int SHARES, int NT, bool KEEP = true>
 struct Plan {
   const AttnArgs& a;
   const Split& sp;
@@ -875,6 +910,7 @@ struct Plan {
     __syncthreads();
     req = uni((int)lds[NT / 64]);
     before = req < n ? uni64(lds[NT / 64 + 1]) : 0;
+    __syncthreads();   // the LDS may be used for something else
   }
   __device__ __forceinline__ static int64_t lane64(int64_t v, int l) {
     return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32) |
@@ -886,7 +922,7 @@ struct Plan {
     if (share < 1) share = 1;
   }
   __device__ __forceinline__ Req get(int i) const {
-    if (a.seqs < 64) {
+    if (KEEP && a.seqs < 64) {
       Req r;
       r.start = __builtin_amdgcn_readlane(mine.start, i);
       r.news = __builtin_amdgcn_readlane(mine.news, i);
@@ -928,9 +964,9 @@ __device__ __forceinline__ void paged_source(const AttnArgs& a, const Item& it, 
 }
 
 // Walks the segments of share w; f(segment, slot or -1).
-template <int BLOCK, int UNIT, int SHARES, int NT, typename F>
+template <int BLOCK, int UNIT, int SHARES, int NT, bool KEEP, typename F>
 __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp, int w, int64_t* lds, F f) {
-  const Plan<BLOCK, UNIT, SHARES, NT> pl(a, sp, w, lds);
+  const Plan<BLOCK, UNIT, SHARES, NT, KEEP> pl(a, sp, w, lds);
   int64_t u = pl.share * w;
   const int64_t begin = u, end = u + pl.share < pl.total ? u + pl.share : pl.total;
   int64_t before = pl.before;
@@ -965,11 +1001,11 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 template <int DT, int DP, int NW>
 __global__ void __launch_bounds__(64 * NW, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
-  __shared__ int64_t lds[NW + 2];
+  int64_t* lds = reinterpret_cast<int64_t*>(dyn_lds);   // before the tiles
   constexpr int kRows = 32 * NW;
   // an XCD takes consecutive shares, so that workgroups that read the same keys share its L2
-  const int w = (blockIdx.x & 7) * (kManyShares / 8) + (blockIdx.x >> 3);
-  for_segments<kRows, kTile, kManyShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+  const int w = (blockIdx.x & 7) * (kShares<NW> / 8) + (blockIdx.x >> 3);
+  for_segments<kRows, kTile, kShares<NW>, 64 * NW, false>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
     paged_source(a, g.it, g.req, s, magic, shift);
     int b0, b1;
@@ -982,7 +1018,7 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane);
     } else {
       float *o, *ml;
-      part_of<DP, kRows, kManyShares>((float*)a.workspace, slot, o, ml);
+      part_of<DP, kRows, kShares<NW>>((float*)a.workspace, slot, o, ml);
       store_part<DP>(rows, o, ml, row + (lane & 31), lane);
     }
   });
@@ -1016,7 +1052,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   // differs in bits 4 and 5
   const uint32_t ofs = (lane / kChunks) * DP * 2 + ((lane % kChunks) ^ swz<DP>(lane / kChunks)) * 16;
   const int w = (blockIdx.x & 7) * (kFewShares / 8) + (blockIdx.x >> 3);
-  for_segments<kFewRows, 32 * NW, kFewShares, 64 * NW>(a, sp, w, lds, [&](const Segment& g, int slot) {
+  for_segments<kFewRows, 32 * NW, kFewShares, 64 * NW, true>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
     paged_source(a, g.it, g.req, s, magic, shift);
     const int group = a.group, rows = g.it.news * group;
@@ -1090,9 +1126,8 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         if (seen) {
           v16f x[1];
           scores<DT, DP, 1>(x, st, ln, at);
-          // the K rows are not needed any more: their place is the wave's scratch
           add_keys<DT, DP>(st, ln, x[0], at + kHalf, kb, sc,
-                           kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb, at, lane);
+                           kb + 32 - hi_min > lo_max - kb ? kb + 32 - hi_min : lo_max - kb, lane);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
@@ -1265,9 +1300,10 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
 }
 
 // ---------------------------------------------------------------- host
-// three tiles of K, two of V, and each wave's scratch for tiles with values that are not finite
+// three tiles of K and two of V
 template <int DP>
-constexpr size_t many_lds_bytes() { return 5 * tile_bytes<DP>() + kManyWaves * 32 * DP * 2; }
+constexpr size_t many_lds_bytes() { return 5 * tile_bytes<DP>(); }
+constexpr int kRowsMost = 32 * 8;
 template <int DP>
 constexpr size_t few_lds_bytes() { return kFewWaves * 2 * 2 * 32 * DP * 2; }
 
@@ -1310,14 +1346,21 @@ hipError_t launch_lds(unsigned grid, unsigned block, size_t lds, hipStream_t s, 
   return hipGetLastError();
 }
 
-int64_t prompt_blocks(const AttnArgs& a) {
-  return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / kManyRows + a.seqs + 1;
+int64_t prompt_blocks(const AttnArgs& a, int rows) {
+  return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / rows + a.seqs + 1;
+}
+
+template <int DT, int DP, int NW>
+hipError_t prompt_waves(const AttnArgs& a, hipStream_t s) {
+  return launch_lds<prompt_attn_kernel<DT, DP, NW>>((unsigned)(prompt_blocks(a, 32 * NW) * a.kv_heads), 64 * NW,
+                                                    many_lds_bytes<DP>(), s, with_group(a));
 }
 
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  return launch_lds<prompt_attn_kernel<DT, DP, kManyWaves>>(
-      (unsigned)(prompt_blocks(a) * a.kv_heads), 64 * kManyWaves, many_lds_bytes<DP>(), s, with_group(a));
+  if constexpr (DP == 64) return prompt_waves<DT, DP, 4>(a, s);
+  else if ((int64_t)a.tokens * a.q_heads <= (int64_t)kRowsMost * a.num_cus) return prompt_waves<DT, DP, 4>(a, s);
+  else return prompt_waves<DT, DP, 8>(a, s);
 }
 
 template <int DT, int DP>
@@ -1340,11 +1383,10 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   }
   if (many) {
     const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
-    e = launch_lds<paged_rows_kernel<DT, DP, kManyWaves>>(kManyShares, 64 * kManyWaves, many_lds_bytes<DP>(),
-                                                                     s, c, sp, magic, shift);
+    constexpr int kWaves = kPagedWaves<DP>, kRows = 32 * kWaves, kMany = kShares<kWaves>;
+    e = launch_lds<paged_rows_kernel<DT, DP, kWaves>>(kMany, 64 * kWaves, many_lds_bytes<DP>(), s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
-    combine_kernel<DT, DP, kManyRows, kTile, kManyShares>
-        <<<dim3(kManyShares - 1, kManyRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
+    combine_kernel<DT, DP, kRows, kTile, kMany><<<dim3(kMany - 1, kRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
     e = hipGetLastError();
   }
   return e;
@@ -1356,11 +1398,11 @@ size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int
   const int group = q_heads / kv_heads;
   const size_t per_row = ((size_t)padded_dim(head_dim) + 2) * sizeof(float);
   const size_t few = needs_few(seqs, tokens, group) ? (size_t)kFewShares * 2 * kFewRows * per_row : 0;
-  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kManyShares * 2 * kManyRows * per_row : 0;
+  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kShares<8> * 2 * kRowsMost * per_row : 0;
   return few > many ? few : many;
 }
 
-bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }
+bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a, 128) * a.kv_heads <= 0x7FFFFFFFLL; }
 
 hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s) {
   const bool wide = padded_dim(a.head_dim) == 128;
