@@ -118,6 +118,10 @@ __device__ __forceinline__ v8s read_b128(uint32_t at) {
   return *(__attribute__((address_space(3))) v8s*)(uintptr_t)at;
 }
 
+__device__ __forceinline__ void zero_lds(uint32_t at) {
+  *(__attribute__((address_space(3))) u32x4*)(uintptr_t)at = (u32x4){0, 0, 0, 0};
+}
+
 // ---------------------------------------------------------------- sources
 // Where the keys and values of one (request, key/value head) are.
 struct Source {
@@ -515,13 +519,12 @@ __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* m
 // is copied twice as often.  Measured, 4 / 8 waves: head dimension 64 (9001
 // tokens, window 1024) 58.8 / 81.7 us; head dimension 128, 210 tokens 12.1 /
 // 14.3, ragged 8192 tokens 97.6 / 96.4, one prompt of 8192 560 / 524, 1700 new
-// tokens over 16k keys 1006 / 557 us, where the copies are what costs.  So four
-// waves for head dimensions up to 64, and above that for prompts that do not
-// give every CU a block of 256 rows.
+// tokens over 16k keys 1006 / 557 (head dimension 64: 360 / 328) us, where the
+// copies are what costs.  So paged work has eight waves; prompts have four for
+// head dimensions up to 64 and where they do not give every CU a block of 256
+// rows, else eight.
 template <int NW>
 constexpr int kShares = NW == 4 ? 512 : 256;   // of paged work: workgroups that the 256 CUs hold
-template <int DP>
-constexpr int kPagedWaves = DP == 64 ? 4 : 8;
 constexpr int kCopyWaves = 4;
 constexpr int kTile = 64;
 
@@ -533,7 +536,7 @@ constexpr int tile_bytes() { return kTile * DP * 2; }
 // waits while it is busy.  Of eight waves only the first four copy: the others, which share the SIMDs
 // with them, compute meanwhile, and the two are out of step from then on (530 us with all eight
 // copying, 523 us).
-template <int DP, bool PAGED>
+template <int DP, bool PAGED, bool FULL>
 struct TileCopy {
   static constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
   static constexpr int kRowsPer = 64 / kChunks;             // rows of one copy instruction
@@ -542,7 +545,8 @@ struct TileCopy {
   const Source& s;
   int wave, lane;
   uint32_t k_ofs, v_ofs;    // byte offset of the lane from an instruction's first row
-  bool whole;               // full rows, and the rows of an instruction lie in one page
+  bool mine;                // the lane's bytes exist (not FULL: rows shorter than DP, whose rest is zeroed once)
+  bool whole;               // the rows of an instruction lie in one page
 
   __device__ __forceinline__ TileCopy(const Source& src, int wv, int ln) : s(src), wave(wv), lane(ln) {
     const int r = wave * kRowsPer + lane / kChunks;
@@ -550,9 +554,9 @@ struct TileCopy {
     const uint32_t k_row = PAGED ? s.d_bytes : (uint32_t)s.k_step, v_row = PAGED ? s.d_bytes : (uint32_t)s.v_step;
     k_ofs = (lane / kChunks) * k_row + chunk * 16;
     v_ofs = (lane / kChunks) * v_row + chunk * 16;
-    whole = s.d_bytes == DP * 2;
-    if constexpr (PAGED) whole = whole && s.page_size % kRowsPer == 0;
-    else whole = whole && s.k_step < (1 << 27) && s.v_step < (1 << 27);
+    mine = chunk * 16 < s.d_bytes;
+    if constexpr (PAGED) whole = s.page_size % kRowsPer == 0;
+    else whole = s.k_step < (1 << 27) && s.v_step < (1 << 27);
   }
   // Page of each instruction's first row, in scalar registers.
   struct Pages { int id[PAGED ? kIters : 1]; };
@@ -574,6 +578,7 @@ struct TileCopy {
   __device__ __forceinline__ void issue(int kb, const Pages& p, uint32_t lds) const {
     if (wave >= kCopyWaves) return;
     if (whole && kb + kTile <= s.keys) {
+      if (!FULL && !mine) return;
       const int j0 = kb + wave * kRowsPer;
       const char* base = V ? s.v : s.k;
       if constexpr (PAGED) {
@@ -614,18 +619,22 @@ struct TileCopy {
 // are, and the first operands of the tile after that are read ahead: iteration
 // t uses K(t + 1), K(t + 2) and V(t) while K(t + 3) and V(t + 1) are on their
 // way (three buffers of K, two of V, one barrier a tile).
-template <int DT, int DP, int NW, bool PAGED>
+template <int DT, int DP, int NW, bool PAGED, bool FULL>
 __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, const Item& it, int t0, int t1,
                                           Rows<DP>& w, uint32_t lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int rows = it.news * a.group;
   const int first = it.row0 + wave * 32;
   constexpr int kBytes = tile_bytes<DP>(), kHalf = kBytes / 2;
-  using Copy = TileCopy<DP, PAGED>;
+  using Copy = TileCopy<DP, PAGED, FULL>;
   const Copy cp(s, wave, lane);
   typename Copy::Pages p1{}, p2{}, p3{};   // of the tiles t + 1 .. t + 3
   uint32_t k_now = lds, k_next = lds + kBytes, k_after = lds + 2 * kBytes;
   uint32_t v_now = lds + 3 * kBytes, v_next = lds + 4 * kBytes;
+  if constexpr (!FULL) {
+    for (int n = tid; n < 5 * kBytes / 16; n += 64 * NW) zero_lds(lds + n * 16);
+    lds_barrier();
+  }
   if (t0 < t1) {
     const auto p0 = cp.pages(t0 * kTile);
     p1 = cp.pages((t0 + 1) * kTile);
@@ -744,7 +753,7 @@ extern __shared__ __align__(1024) unsigned char dyn_lds[];
 // what follows the last prompt, rows without keys, which are set to 0.  A
 // prompt's longest rows come first, and key/value heads are the fastest
 // index, so that workgroups on one XCD (dispatched round robin) share a head.
-template <int DT, int DP, int NW>
+template <int DT, int DP, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
   int& found = *reinterpret_cast<int*>(dyn_lds);
   constexpr int kRows = 32 * NW;
@@ -791,7 +800,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
   int t0 = 0, t1 = 0;
   if (req < a.seqs) tiles_of(a, it, it.row0, kRows, kTile, t0, t1);
   Rows<DP> w;
-  run_block<DT, DP, NW, false>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
+  run_block<DT, DP, NW, false, FULL>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
   store_rows<DT, DP>(w, a, it, it.row0 + uni(tid >> 6) * 32, tid & 63);
 }
 
@@ -998,7 +1007,7 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 }
 
 // ---------------------------------------------------------------- paged: many rows
-template <int DT, int DP, int NW>
+template <int DT, int DP, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   int64_t* lds = reinterpret_cast<int64_t*>(dyn_lds);   // before the tiles
@@ -1012,7 +1021,7 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     tiles_of(a, g.it, g.it.row0, kRows, kTile, b0, b1);
     const int t0 = uni(g.t0 > b0 ? g.t0 : b0), t1 = uni(g.t1 < b1 ? g.t1 : b1);
     Rows<DP> rows;
-    run_block<DT, DP, NW, true>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
+    run_block<DT, DP, NW, true, FULL>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
     const int row = uni(threadIdx.x >> 6) * 32, lane = threadIdx.x & 63;
     if (slot < 0) {
       store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane);
@@ -1036,7 +1045,7 @@ constexpr int kWindow = 256;   // page ids a wave keeps
 constexpr int kFewRows = 32, kFewWaves = 2;
 constexpr int kFewShares = 512;    // two workgroups on each CU
 
-template <int DT, int DP, int NW>
+template <int DT, int DP, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, 1)
 paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int64_t lds[NW + 2];
@@ -1048,9 +1057,10 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   const uint32_t mem = lds_addr(dyn_lds) + wave * 2 * kStage;
   float* join_o = (float*)dyn_lds;          // [NW][32][DP] after the copies
   const Lanes<DP> ln(lane);
-  // the lane's bytes in copy 0; in copy it its row is kRowsPer it further down, and the swizzle
-  // differs in bits 4 and 5
-  const uint32_t ofs = (lane / kChunks) * DP * 2 + ((lane % kChunks) ^ swz<DP>(lane / kChunks)) * 16;
+  // the lane's row and chunk in copy 0; in copy it the row is kRowsPer it further down and the
+  // swizzle differs in its two lowest bits
+  const uint32_t row_ofs = (lane / kChunks) * (FULL ? DP : a.head_dim) * 2;
+  const int chunk0 = (lane % kChunks) ^ swz<DP>(lane / kChunks);
   const int w = (blockIdx.x & 7) * (kFewShares / 8) + (blockIdx.x >> 3);
   for_segments<kFewRows, 32 * NW, kFewShares, 64 * NW, true>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
@@ -1063,8 +1073,11 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
     const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
     const int n = g.t1 - g.t0;
-    // eight keys lie in one page and no row has a rest
-    const bool whole = s.d_bytes == DP * 2 && s.page_size % 8 == 0;
+    const bool whole = s.page_size % 8 == 0;   // eight keys lie in one page
+    if constexpr (!FULL) {   // what the copies leave out of the rows
+      for (int m = lane; m < 2 * kStage / 16; m += 64) zero_lds(mem + m * 16);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
     const int64_t k_to_v = s.v - s.k;
     int win0 = 0, win1 = 0;   // pages held
     auto hold = [&](int kb) {   // the pages of keys kb .. kb + 31
@@ -1087,15 +1100,17 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         for (int n8 = 0; n8 < 4; ++n8) {
           const int id = __builtin_amdgcn_readlane(ids, n8), j = kb + n8 * 8;
           const bool there = (uint32_t)id < (uint64_t)s.num_pages;
-          const int64_t off = (int64_t)id * s.k_step + (j - page_of(s, j) * s.page_size) * (DP * 2);
+          const int64_t off = (int64_t)id * s.k_step + (j - page_of(s, j) * s.page_size) * (FULL ? DP * 2 : s.d_bytes);
           const char* k = there ? s.k + off : reinterpret_cast<const char*>(kZeros);
           const char* v = there ? k + k_to_v : k;
 #pragma unroll
           for (int m = 0; m < 8 / kRowsPer; ++m) {
-            const int it = n8 * (8 / kRowsPer) + m, skip = there ? m * 1024 : 0;
-            const uint32_t o = ofs ^ ((it * kRowsPer / 4 % 4) * 16);
-            dma16(k + skip, o, to + it * 1024);
-            dma16(v + skip, o, to + kHalf + it * 1024);
+            const int it = n8 * (8 / kRowsPer) + m, skip = there ? m * kRowsPer * (FULL ? DP * 2 : s.d_bytes) : 0;
+            const uint32_t chunk = (uint32_t)(chunk0 ^ (it * kRowsPer / 4 % 4)) * 16;
+            if (FULL || chunk < (uint32_t)s.d_bytes) {
+              dma16(k + skip, row_ofs + chunk, to + it * 1024);
+              dma16(v + skip, row_ofs + chunk, to + kHalf + it * 1024);
+            }
           }
         }
       } else {
@@ -1350,20 +1365,21 @@ int64_t prompt_blocks(const AttnArgs& a, int rows) {
   return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / rows + a.seqs + 1;
 }
 
-template <int DT, int DP, int NW>
+template <int DT, int DP, int NW, bool FULL>
 hipError_t prompt_waves(const AttnArgs& a, hipStream_t s) {
-  return launch_lds<prompt_attn_kernel<DT, DP, NW>>((unsigned)(prompt_blocks(a, 32 * NW) * a.kv_heads), 64 * NW,
-                                                    many_lds_bytes<DP>(), s, with_group(a));
+  return launch_lds<prompt_attn_kernel<DT, DP, NW, FULL>>((unsigned)(prompt_blocks(a, 32 * NW) * a.kv_heads), 64 * NW,
+                                                          many_lds_bytes<DP>(), s, with_group(a));
 }
 
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  if constexpr (DP == 64) return prompt_waves<DT, DP, 4>(a, s);
-  else if ((int64_t)a.tokens * a.q_heads <= (int64_t)kRowsMost * a.num_cus) return prompt_waves<DT, DP, 4>(a, s);
-  else return prompt_waves<DT, DP, 8>(a, s);
+  const bool full = a.head_dim == DP, small = (int64_t)a.tokens * a.q_heads <= (int64_t)kRowsMost * a.num_cus;
+  if constexpr (DP == 64) return full ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 4, false>(a, s);
+  if (!full) return prompt_waves<DT, DP, 8, false>(a, s);
+  return small ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 8, true>(a, s);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool FULL>
 hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   const AttnArgs c = with_group(a);
   const bool many = needs_many(a.seqs, a.tokens, c.group), few = needs_few(a.seqs, a.tokens, c.group);
@@ -1374,7 +1390,7 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   constexpr int kRowsAtOnce = 256 / (DP / 4);   // of a combining workgroup
   if (few) {
     const Split sp{1, many ? kFewRows : 0x7FFFFFFF};
-    e = launch_lds<paged_few_kernel<DT, DP, kFewWaves>>(kFewShares, 64 * kFewWaves, few_lds_bytes<DP>(), s, c, sp, magic, shift);
+    e = launch_lds<paged_few_kernel<DT, DP, kFewWaves, FULL>>(kFewShares, 64 * kFewWaves, few_lds_bytes<DP>(), s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
     combine_kernel<DT, DP, kFewRows, 32 * kFewWaves, kFewShares>
         <<<dim3(kFewShares - 1), dim3(256), 0, s>>>(c, sp);
@@ -1383,8 +1399,8 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   }
   if (many) {
     const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
-    constexpr int kWaves = kPagedWaves<DP>, kRows = 32 * kWaves, kMany = kShares<kWaves>;
-    e = launch_lds<paged_rows_kernel<DT, DP, kWaves>>(kMany, 64 * kWaves, many_lds_bytes<DP>(), s, c, sp, magic, shift);
+    constexpr int kWaves = 8, kRows = 32 * kWaves, kMany = kShares<kWaves>;
+    e = launch_lds<paged_rows_kernel<DT, DP, kWaves, FULL>>(kMany, 64 * kWaves, many_lds_bytes<DP>(), s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
     combine_kernel<DT, DP, kRows, kTile, kMany><<<dim3(kMany - 1, kRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
     e = hipGetLastError();
@@ -1410,10 +1426,15 @@ hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s) {
   return wide ? prompt_dp<kFp16, 128>(a, s) : prompt_dp<kFp16, 64>(a, s);
 }
 
+template <int DT>
+static hipError_t paged_type(const AttnArgs& a, hipStream_t s) {
+  if (a.head_dim == 128) return paged_dp<DT, 128, true>(a, s);
+  if (a.head_dim > 64) return paged_dp<DT, 128, false>(a, s);
+  return a.head_dim == 64 ? paged_dp<DT, 64, true>(a, s) : paged_dp<DT, 64, false>(a, s);
+}
+
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t s) {
-  const bool wide = padded_dim(a.head_dim) == 128;
-  if (a.dtype == kBf16) return wide ? paged_dp<kBf16, 128>(a, s) : paged_dp<kBf16, 64>(a, s);
-  return wide ? paged_dp<kFp16, 128>(a, s) : paged_dp<kFp16, 64>(a, s);
+  return a.dtype == kBf16 ? paged_type<kBf16>(a, s) : paged_type<kFp16>(a, s);
 }
 
 }  // namespace nvfp4
