@@ -396,10 +396,11 @@ int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_
 /*
  * nvfp4_kv_write -- copies the rows of k and v [tokens, kv_heads, head_dim]
  * (2-byte elements, given by their strides in elements: token, head) to their
- * slots; a slot outside [0, num_pages * page_size) is skipped.  Two tokens
- * with the same slot leave one of them (which one is not defined).
+ * slots; a slot outside [0, num_pages * page_size) is skipped.  Where two
+ * tokens have the same slot, which of their bytes stay there is not defined.
  * Pointers 2-byte, slot_map 8-byte aligned; rows that are not 16-byte aligned
- * take a 2-byte path.
+ * take a 2-byte path.  Requires kv_heads, head_dim <= 2^16 and fewer than 2^50
+ * elements and slots (EUNSUPPORTED otherwise).
  */
 int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_heads, int32_t head_dim,
                        int64_t k_stride, int64_t k_head_stride, int64_t v_stride, int64_t v_head_stride,
@@ -421,7 +422,7 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
  *              multiples of 8; 16-byte aligned
  *   out      : [tokens, q_heads, head_dim] dense, the inputs' type, 16-byte aligned
  *   lse      : [tokens, q_heads] float, or NULL
- *   scale    : > 0, finite
+ *   scale    : 2^-96 .. 2^96
  *   window   : >= 0, 0 = unlimited
  * Requires q_heads % kv_heads == 0, head_dim % 8 == 0, 8 <= head_dim <= 128
  * (EINVAL otherwise), tokens * q_heads / kv_heads <= 2^30, seqs <= 2^20.

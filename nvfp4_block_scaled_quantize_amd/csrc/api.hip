@@ -433,7 +433,9 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
   if ((((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_cache | (uintptr_t)v_cache) % 2) != 0 ||
       ((uintptr_t)slot_map % 8) != 0)
     return NVFP4_EINVAL;
-  if (kv_heads > 65536 || head_dim > 65536 || tokens > (1LL << 40) || num_pages > (1LL << 32))
+  // the kernel divides element and slot numbers below 2^51
+  if (kv_heads > 65536 || head_dim > 65536 || tokens > (1LL << 50) / ((int64_t)kv_heads * head_dim) ||
+      num_pages > (1LL << 50) / page_size)
     return NVFP4_EUNSUPPORTED;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
@@ -449,7 +451,8 @@ static int32_t attn_check(const void* q, int32_t dtype, int32_t seqs, int64_t to
   if (dtype != NVFP4_BF16 && dtype != NVFP4_FP16) return NVFP4_EINVAL;
   if (seqs < 0 || tokens < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return NVFP4_EINVAL;
   if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0 || window < 0) return NVFP4_EINVAL;
-  if (!(scale > 0.0f && scale <= 3.402823466e+38f)) return NVFP4_EINVAL;
+  // scale log2 e and its inverse are normal numbers
+  if (!(scale >= 0x1p-96f && scale <= 0x1p96f)) return NVFP4_EINVAL;
   if (q_stride < 0 || q_head_stride < 0 || q_stride % 8 != 0 || q_head_stride % 8 != 0) return NVFP4_EINVAL;
   if (tokens == 0) return NVFP4_OK;
   if (!q || !out || ((uintptr_t)q % 16) != 0 || ((uintptr_t)out % 16) != 0 || !aligned4(lse)) return NVFP4_EINVAL;

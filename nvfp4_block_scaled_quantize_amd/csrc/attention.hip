@@ -523,8 +523,8 @@ __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* m
 // copies are what costs.  So paged work has eight waves; prompts have four for
 // head dimensions up to 64 and where they do not give every CU a block of 256
 // rows, else eight.
-template <int NW>
-constexpr int kShares = NW == 4 ? 512 : 256;   // of paged work: workgroups that the 256 CUs hold
+constexpr int kShares = 256;   // of paged work: the workgroups of eight waves that 256 CUs hold
+constexpr int kMostRows = 32 * 8;
 constexpr int kCopyWaves = 4;
 constexpr int kTile = 64;
 
@@ -1007,14 +1007,14 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 }
 
 // ---------------------------------------------------------------- paged: many rows
-template <int DT, int DP, int NW, bool FULL>
-__global__ void __launch_bounds__(64 * NW, 2)
+template <int DT, int DP, bool FULL>
+__global__ void __launch_bounds__(512, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   int64_t* lds = reinterpret_cast<int64_t*>(dyn_lds);   // before the tiles
-  constexpr int kRows = 32 * NW;
+  constexpr int NW = 8, kRows = kMostRows;
   // an XCD takes consecutive shares, so that workgroups that read the same keys share its L2
-  const int w = (blockIdx.x & 7) * (kShares<NW> / 8) + (blockIdx.x >> 3);
-  for_segments<kRows, kTile, kShares<NW>, 64 * NW, false>(a, sp, w, lds, [&](const Segment& g, int slot) {
+  const int w = (blockIdx.x & 7) * (kShares / 8) + (blockIdx.x >> 3);
+  for_segments<kRows, kTile, kShares, 64 * NW, false>(a, sp, w, lds, [&](const Segment& g, int slot) {
     Source s;
     paged_source(a, g.it, g.req, s, magic, shift);
     int b0, b1;
@@ -1027,7 +1027,7 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane);
     } else {
       float *o, *ml;
-      part_of<DP, kRows, kShares<NW>>((float*)a.workspace, slot, o, ml);
+      part_of<DP, kRows, kShares>((float*)a.workspace, slot, o, ml);
       store_part<DP>(rows, o, ml, row + (lane & 31), lane);
     }
   });
@@ -1318,7 +1318,6 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
 // three tiles of K and two of V
 template <int DP>
 constexpr size_t many_lds_bytes() { return 5 * tile_bytes<DP>(); }
-constexpr int kRowsMost = 32 * 8;
 template <int DP>
 constexpr size_t few_lds_bytes() { return kFewWaves * 2 * 2 * 32 * DP * 2; }
 
@@ -1371,12 +1370,17 @@ hipError_t prompt_waves(const AttnArgs& a, hipStream_t s) {
                                                           many_lds_bytes<DP>(), s, with_group(a));
 }
 
+// Padded head dimensions have one size of workgroup per DP (fewer kernels; 8 waves measured: head
+// dimension 96, ragged 8000 tokens, 169 us).
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  const bool full = a.head_dim == DP, small = (int64_t)a.tokens * a.q_heads <= (int64_t)kRowsMost * a.num_cus;
-  if constexpr (DP == 64) return full ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 4, false>(a, s);
-  if (!full) return prompt_waves<DT, DP, 8, false>(a, s);
-  return small ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 8, true>(a, s);
+  const bool full = a.head_dim == DP, small = (int64_t)a.tokens * a.q_heads <= (int64_t)kMostRows * a.num_cus;
+  if constexpr (DP == 64) {
+    return full ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 4, false>(a, s);
+  } else {
+    if (!full) return prompt_waves<DT, DP, 8, false>(a, s);
+    return small ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 8, true>(a, s);
+  }
 }
 
 template <int DT, int DP, bool FULL>
@@ -1399,10 +1403,10 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   }
   if (many) {
     const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
-    constexpr int kWaves = 8, kRows = 32 * kWaves, kMany = kShares<kWaves>;
-    e = launch_lds<paged_rows_kernel<DT, DP, kWaves, FULL>>(kMany, 64 * kWaves, many_lds_bytes<DP>(), s, c, sp, magic, shift);
+    e = launch_lds<paged_rows_kernel<DT, DP, FULL>>(kShares, 512, many_lds_bytes<DP>(), s, c, sp, magic, shift);
     if (e != hipSuccess) return e;
-    combine_kernel<DT, DP, kRows, kTile, kMany><<<dim3(kMany - 1, kRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
+    combine_kernel<DT, DP, kMostRows, kTile, kShares>
+        <<<dim3(kShares - 1, kMostRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
     e = hipGetLastError();
   }
   return e;
@@ -1414,7 +1418,7 @@ size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int
   const int group = q_heads / kv_heads;
   const size_t per_row = ((size_t)padded_dim(head_dim) + 2) * sizeof(float);
   const size_t few = needs_few(seqs, tokens, group) ? (size_t)kFewShares * 2 * kFewRows * per_row : 0;
-  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kShares<8> * 2 * kRowsMost * per_row : 0;
+  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kShares * 2 * kMostRows * per_row : 0;
   return few > many ? few : many;
 }
 
