@@ -261,17 +261,15 @@ __device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc)
 template <int DT, int DP>
 __device__ __forceinline__ bool all_finite(uint32_t v_lds, int lane) {
   asm volatile("" : "+v"(lane));
-  uint32_t big = 0;
+  typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+  v2u most = {0, 0};
 #pragma unroll 4
   for (int n = 0; n < 32 * DP * 2 / 1024; ++n) {
     const u32x4 x = __builtin_bit_cast(u32x4, read_b128(v_lds + n * 1024 + lane * 16));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t a = x[e] & 0x7FFFu, b = (x[e] >> 16) & 0x7FFFu;
-      big = a > big ? a : big;
-      big = b > big ? b : big;
-    }
+    for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(v2u, x[e] & 0x7FFF7FFFu));
   }
+  const uint32_t big = most[0] > most[1] ? most[0] : most[1];
   return !__any(big >= not_finite_bits<DT>());
 }
 
@@ -475,25 +473,36 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
-// Writes finished rows.
+// Writes a wave's finished rows, through its part `lds` of the tiles (32 rows of DP elements): a lane
+// holds every second 8 bytes of one row, and memory is written 16 bytes a lane, whole rows at a time
+// (8192 ragged tokens 89.5 -> 85.0 us, 32 prompts of 256 tokens 84 -> 65 us).  16-byte chunk p of row r is at chunk p ^ (r mod the chunks of a row).
 template <int DT, int DP>
-__device__ __forceinline__ void store_rows(const Rows<DP>& w, const AttnArgs& a, const Item& it, int row0, int lane) {
-  const int rows = it.news * a.group, h = lane >> 5, r = row0 + (lane & 31);
+__device__ __forceinline__ void store_rows(const Rows<DP>& w, const AttnArgs& a, const Item& it, int row0, int lane,
+                                           uint32_t lds) {
+  typedef __attribute__((address_space(3))) u32x2* lds_2;
+  constexpr int kChunks = DP / 8, kRowsPer = 64 / kChunks;
+  const int rows = it.news * a.group, h = lane >> 5, c = lane & 31;
   const float l = both_sum(w.l), inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (r >= rows) return;
-  const int tok = token_of(a, r);
-  const int64_t at = (int64_t)(it.start + tok) * a.q_heads + it.head * a.group + r - tok * a.group;
-  uint32_t* out = (uint32_t*)a.out + at * (a.head_dim / 2);
 #pragma unroll
   for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = t * 32 + 8 * i + 4 * h;
-      if (d < a.head_dim)
-        *(u32x2*)(out + d / 2) = (u32x2){pack2<DT>(w.o[t][4 * i] * inv, w.o[t][4 * i + 1] * inv),
-                                         pack2<DT>(w.o[t][4 * i + 2] * inv, w.o[t][4 * i + 3] * inv)};
-    }
-  if (a.lse && h == 0) a.lse[at] = lse_of(w.m, l);
+    for (int i = 0; i < 4; ++i)
+      *(lds_2)(uintptr_t)(lds + c * DP * 2 + ((t * 4 + i) ^ (c & (kChunks - 1))) * 16 + h * 8) =
+          (u32x2){pack2<DT>(w.o[t][4 * i] * inv, w.o[t][4 * i + 1] * inv),
+                  pack2<DT>(w.o[t][4 * i + 2] * inv, w.o[t][4 * i + 3] * inv)};
+  auto place = [&](int r) {   // (token, head) of row r
+    const int tok = token_of(a, r);
+    return (int64_t)(it.start + tok) * a.q_heads + it.head * a.group + r - tok * a.group;
+  };
+  const int chunk = lane % kChunks;
+#pragma unroll
+  for (int n = 0; n < 32 / kRowsPer; ++n) {
+    const int r = n * kRowsPer + lane / kChunks;
+    const v8s x = read_b128(lds + r * DP * 2 + (chunk ^ (r & (kChunks - 1))) * 16);
+    if (row0 + r < rows && chunk * 8 < a.head_dim)
+      *(v8s*)((uint16_t*)a.out + place(row0 + r) * a.head_dim + chunk * 8) = x;
+  }
+  if (a.lse && h == 0 && row0 + c < rows) a.lse[place(row0 + c)] = lse_of(w.m, l);
 }
 
 // Part of rows whose keys are split over workgroups: O (unnormalized) [rows][DP], (m, l) [rows].
@@ -514,17 +523,17 @@ __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* m
 // A workgroup of NW = 4 or 8 waves, 32 rows each; all waves share the tiles of
 // 64 keys, copied global -> LDS.  A wave takes up to half the registers of two
 // waves' SIMD, so a CU holds two workgroups of four waves or one of eight.  Two
-// meet no common barrier, the start and end of one lie beside the work of the
-// other, and blocks of 128 rows waste less above the diagonal; but every tile
-// is copied twice as often.  Measured, 4 / 8 waves: head dimension 64 (9001
-// tokens, window 1024) 58.8 / 81.7 us; head dimension 128, 210 tokens 12.1 /
-// 14.3, ragged 8192 tokens 97.6 / 96.4, one prompt of 8192 560 / 524, 1700 new
-// tokens over 16k keys 1006 / 557 (head dimension 64: 360 / 328) us, where the
-// copies are what costs.  So paged work has eight waves; prompts have four for
-// head dimensions up to 64 and where they do not give every CU a block of 256
-// rows, else eight.
+// meet no common barrier, the start and end of one (10 us of loads, stores and
+// dispatch) lie beside the work of the other, and blocks of 128 rows waste less
+// above the diagonal; but every tile is copied twice as often.  So prompts have
+// four waves and paged work, whose workgroups start and end once, has eight.
+// Measured, 4 / 8 waves: 8192 ragged tokens 89.3 / 95.4 us, 9001 tokens of head
+// dimension 64, window 1024 58.8 / 81.7, 210 tokens 12.1 / 14.3, one prompt of
+// 8192 541 / 536; 1700 new tokens over 16k keys 1006 / 557 (head dimension 64:
+// 360 / 328), where the copies from pages are what costs.
 constexpr int kShares = 256;   // of paged work: the workgroups of eight waves that 256 CUs hold
 constexpr int kMostRows = 32 * 8;
+constexpr int kPromptWaves = 4;
 constexpr int kCopyWaves = 4;
 constexpr int kTile = 64;
 
@@ -746,50 +755,142 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, const Item& it, int 
 
 extern __shared__ __align__(1024) unsigned char dyn_lds[];
 
-// Whole prompts.  Workgroup (b, h): b counts blocks of rows over all requests.
-// Request i owns the blocks f(i) .. f(i + 1) - 1 with f(i) = floor(cu_i G /
-// rows) + i, which are at least as many as it needs and are known without the
-// lengths on the host; the surplus workgroups end at once.  Request `seqs` is
-// what follows the last prompt, rows without keys, which are set to 0.  A
-// prompt's longest rows come first, and key/value heads are the fastest
-// index, so that workgroups on one XCD (dispatched round robin) share a head.
-template <int DT, int DP, int NW, bool FULL>
-__global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
-  int& found = *reinterpret_cast<int*>(dyn_lds);
-  constexpr int kRows = 32 * NW;
-  const int tid = threadIdx.x;
+// Sum and maximum of a wave's non-negative values.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp0(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
+__device__ __forceinline__ int wave_sum(int v) {
+  v += dpp0<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v += dpp0<0x112, 0xF>(v);
+  v += dpp0<0x114, 0xF>(v);
+  v += dpp0<0x118, 0xF>(v);
+  v += dpp0<0x142, 0xA>(v);   // row_bcast 15, 31
+  v += dpp0<0x143, 0xC>(v);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ int wave_or(int v) {
+  v |= dpp0<0x111, 0xF>(v);
+  v |= dpp0<0x112, 0xF>(v);
+  v |= dpp0<0x114, 0xF>(v);
+  v |= dpp0<0x118, 0xF>(v);
+  v |= dpp0<0x142, 0xA>(v);
+  v |= dpp0<0x143, 0xC>(v);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// Whole prompts.  Workgroup (b, h): b counts blocks of rows over all requests,
+// of which the host only knows a bound; the surplus, at the end, has nothing to
+// do.  Request `seqs` is what follows the last prompt, rows without keys, which
+// are set to 0.
+//
+// Workgroups go to the shader engines in turn, whatever these have left to do,
+// so neighbours should have the same length: the blocks come by their number
+// in the request, longest first (level L: block L of every request that has
+// one).  Up to 4 x 64 requests are held by each wave, 4 per lane; of more, the
+// blocks come in the requests' order.  Measured against the requests' order with
+// the surplus between the requests: 128 prompts of 64 tokens 106 -> 73 us, 8192
+// ragged tokens 97.6 -> 89.3 us.
+//
+// Key/value heads are the fastest index, so that workgroups on one XCD
+// (dispatched round robin) share a head.
+template <int DT, int DP, bool FULL>
+__global__ void __launch_bounds__(64 * kPromptWaves, 2) prompt_attn_kernel(AttnArgs a) {
+  constexpr int NW = kPromptWaves, kRows = 32 * NW, kThreads = 64 * NW, kHold = 4;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int head = blockIdx.x % a.kv_heads, b = blockIdx.x / a.kv_heads;
-  const int group = a.group;
-  // tokens * group <= 2^30
-  auto first_block = [&](int start, int i) { return (int)((uint32_t)(start * group) / kRows) + i; };
-  int req, start, stop;
-  if (a.seqs < 64) {   // a request per lane
-    const int i = tid & 63;
-    const int at = i <= a.seqs ? clampi(a.cu[i], 0, a.tokens) : a.tokens;
-    req = __popcll(__ballot(i <= a.seqs && first_block(at, i) <= b)) - 1;
-    if (req < 0) return;
-    start = __builtin_amdgcn_readlane(at, req);
-    stop = __builtin_amdgcn_readlane(at, req < 63 ? req + 1 : 63);
+  auto limits = [&](int i, int& start, int& stop) {   // returns the blocks of request i
+    start = clampi(a.cu[i], 0, a.tokens);
+    stop = i < a.seqs ? clampi(a.cu[i + 1], start, a.tokens) : a.tokens;
+    return (int)((uint32_t)((stop - start) * a.group + kRows - 1) / kRows);   // tokens * group <= 2^30
+  };
+  int req = -1, start = 0, stop = 0, block = 0;
+  if (a.seqs <= 64 * kHold) {
+    int n[kHold], first[kHold], end[kHold], all = 0, bits = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const int i = k * 64 + lane;
+      n[k] = first[k] = end[k] = 0;
+      if (i < a.seqs) n[k] = limits(i, first[k], end[k]);
+      all += n[k];
+      bits |= n[k];
+    }
+    all = wave_sum(all);
+    if (b >= all) {
+      req = a.seqs;
+      block = b - all;
+      if (block >= uni(limits(req, start, stop))) return;   // surplus
+    } else {
+      // the largest L with more than b blocks at the levels from L on
+      bits = wave_or(bits);
+      int level = 0, above = 0;
+      for (int bit = 31 - __builtin_clz(bits); bit >= 0; --bit) {
+        const int l = level | (1 << bit);
+        int x = 0;
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) x += n[k] > l ? n[k] - l : 0;
+        x = wave_sum(x);
+        if (x > b) level = l;
+        else above = x;   // ends as the blocks above the level
+      }
+      block = level;
+      int left = b - above;   // which of the requests that have this block
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const uint64_t has = __ballot(n[k] > level);
+        const int here = __popcll(has);
+        if (req < 0 && left < here) {
+          const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(has >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)has, 0));
+          const int l = __builtin_ctzll(__ballot(n[k] > level && before == left));
+          req = k * 64 + l;
+          start = __builtin_amdgcn_readlane(first[k], l);
+          stop = __builtin_amdgcn_readlane(end[k], l);
+        }
+        left -= here;
+      }
+      if (req < 0) return;   // not reached
+    }
   } else {
-    if (tid == 0) found = 0;
+    int* lds = reinterpret_cast<int*>(dyn_lds);   // before the tiles
+    const int n = a.seqs + 1, per = (n + kThreads - 1) / kThreads;
+    const int i0 = tid * per, i1 = i0 + per < n ? i0 + per : n;
+    int v = 0;
+    for (int i = i0; i < i1; ++i) v += limits(i, start, stop);
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off, 64);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) lds[tid >> 6] = x;
+    if (tid == 0) lds[NW] = -1;
     __syncthreads();
-    int n = 0;
-    for (int i = tid; i <= a.seqs; i += 64 * NW) n += first_block(clampi(a.cu[i], 0, a.tokens), i) <= b ? 1 : 0;
-    if (n) atomicAdd(&found, n);
+    int before = x - v;
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+      if (k < tid >> 6) before += lds[k];
+    if (b >= before && b < before + v) {
+      for (int i = i0; i < i1; ++i) {
+        const int m = limits(i, start, stop);
+        if (b < before + m) {
+          lds[NW] = i;
+          lds[NW + 1] = m - 1 - (b - before);   // a request's longest rows first
+          break;
+        }
+        before += m;
+      }
+    }
     __syncthreads();
-    req = uni(found) - 1;
-    __syncthreads();   // the tiles take its place
-    if (req < 0) return;
-    start = clampi(uni(a.cu[req]), 0, a.tokens);
-    stop = req < a.seqs ? uni(a.cu[req + 1]) : a.tokens;
+    req = uni(lds[NW]);
+    block = uni(lds[NW + 1]);
+    __syncthreads();   // the tiles take their place
+    // starts that do not rise can make a block that does not exist
+    if (req < 0 || block < 0 || block >= uni(limits(req, start, stop))) return;
   }
-  if (req >= a.seqs) stop = a.tokens;
-  stop = clampi(stop, start, a.tokens);
+  start = uni(start);
+  stop = uni(stop);
+  req = uni(req);
+  block = uni(block);
   const int news = stop - start;
-  const int blocks = (int)((uint32_t)(news * group + kRows - 1) / kRows);
-  const int rb = b - first_block(start, req);
-  if (rb < 0 || rb >= blocks) return;
-  Item it{start, news, news, head, (blocks - 1 - rb) * kRows};
+  Item it{start, news, news, head, block * kRows};
   Source s{};
   s.k = (const char*)a.k + ((int64_t)start * a.k_stride + (int64_t)head * a.k_head_stride) * 2;
   s.v = (const char*)a.v + ((int64_t)start * a.v_stride + (int64_t)head * a.v_head_stride) * 2;
@@ -801,7 +902,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attn_kernel(AttnArgs a) {
   if (req < a.seqs) tiles_of(a, it, it.row0, kRows, kTile, t0, t1);
   Rows<DP> w;
   run_block<DT, DP, NW, false, FULL>(a, s, it, t0, t1, w, lds_addr(dyn_lds));
-  store_rows<DT, DP>(w, a, it, it.row0 + uni(tid >> 6) * 32, tid & 63);
+  const int wave = uni(tid >> 6);
+  store_rows<DT, DP>(w, a, it, it.row0 + wave * 32, lane, lds_addr(dyn_lds) + wave * 32 * DP * 2);
 }
 
 // ---------------------------------------------------------------- paged: work split
@@ -1024,7 +1126,8 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     run_block<DT, DP, NW, true, FULL>(a, s, g.it, t0, t1, rows, lds_addr(dyn_lds));
     const int row = uni(threadIdx.x >> 6) * 32, lane = threadIdx.x & 63;
     if (slot < 0) {
-      store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane);
+      store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane, lds_addr(dyn_lds) + row * DP * 2);
+      lds_barrier();   // the tiles may be filled again
     } else {
       float *o, *ml;
       part_of<DP, kRows, kShares>((float*)a.workspace, slot, o, ml);
@@ -1360,27 +1463,20 @@ hipError_t launch_lds(unsigned grid, unsigned block, size_t lds, hipStream_t s, 
   return hipGetLastError();
 }
 
-int64_t prompt_blocks(const AttnArgs& a, int rows) {
-  return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / rows + a.seqs + 1;
+// At least the blocks of rows of all requests.
+int64_t prompt_blocks(const AttnArgs& a) {
+  return (int64_t)a.tokens * (a.q_heads / a.kv_heads) / (32 * kPromptWaves) + a.seqs + 1;
 }
 
-template <int DT, int DP, int NW, bool FULL>
-hipError_t prompt_waves(const AttnArgs& a, hipStream_t s) {
-  return launch_lds<prompt_attn_kernel<DT, DP, NW, FULL>>((unsigned)(prompt_blocks(a, 32 * NW) * a.kv_heads), 64 * NW,
-                                                          many_lds_bytes<DP>(), s, with_group(a));
+template <int DT, int DP, bool FULL>
+hipError_t prompt_full(const AttnArgs& a, hipStream_t s) {
+  return launch_lds<prompt_attn_kernel<DT, DP, FULL>>((unsigned)(prompt_blocks(a) * a.kv_heads), 64 * kPromptWaves,
+                                                      many_lds_bytes<DP>(), s, with_group(a));
 }
 
-// Padded head dimensions have one size of workgroup per DP (fewer kernels; 8 waves measured: head
-// dimension 96, ragged 8000 tokens, 169 us).
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
-  const bool full = a.head_dim == DP, small = (int64_t)a.tokens * a.q_heads <= (int64_t)kMostRows * a.num_cus;
-  if constexpr (DP == 64) {
-    return full ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 4, false>(a, s);
-  } else {
-    if (!full) return prompt_waves<DT, DP, 8, false>(a, s);
-    return small ? prompt_waves<DT, DP, 4, true>(a, s) : prompt_waves<DT, DP, 8, true>(a, s);
-  }
+  return a.head_dim == DP ? prompt_full<DT, DP, true>(a, s) : prompt_full<DT, DP, false>(a, s);
 }
 
 template <int DT, int DP, bool FULL>
@@ -1422,7 +1518,7 @@ size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int
   return few > many ? few : many;
 }
 
-bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a, 128) * a.kv_heads <= 0x7FFFFFFFLL; }
+bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }
 
 hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s) {
   const bool wide = padded_dim(a.head_dim) == 128;
