@@ -327,12 +327,10 @@ __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f&
   int odd = 0;   // some value is not finite
 #pragma unroll 1
   for (int turns = turns_if(hidden); turns > 0; --turns) {
-    const int h = lane >> 5, lo = w.lo - kb - 4 * h, hi = w.hi - kb - 4 * h;
+    const int lo = w.lo - kb - 4 * (lane >> 5);
+    const uint32_t count = w.hi > w.lo ? w.hi - w.lo : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int key = 8 * (i / 4) + i % 4;
-      if (key < lo || key >= hi) s[i] = -__builtin_inff();
-    }
+    for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(8 * (i / 4) + i % 4 - lo) < count ? s[i] : -__builtin_inff();
     odd = uni(all_finite<DT, DP>(v_lds, lane) ? 0 : 1);
   }
   raise(w, both_max(largest(s)), sc);
@@ -553,17 +551,18 @@ struct TileCopy {
   static_assert(kIters >= 1 && (kCopyWaves * kRowsPer) % 16 == 0, "a lane's swizzle is the same in all its copies");
   const Source& s;
   int wave, lane;
-  uint32_t k_ofs, v_ofs;    // byte offset of the lane from an instruction's first row
+  // The lane's place in an instruction, as a byte offset (paged) or as the byte of its row and, in the
+  // upper half, the row: with an offset each for K and V the 128-wide prompt kernel spills them, and
+  // reloading one waits for the copies in flight.
+  uint32_t at;
   bool mine;                // the lane's bytes exist (not FULL: rows shorter than DP, whose rest is zeroed once)
   bool whole;               // the rows of an instruction lie in one page
 
   __device__ __forceinline__ TileCopy(const Source& src, int wv, int ln) : s(src), wave(wv), lane(ln) {
-    const int r = wave * kRowsPer + lane / kChunks;
-    const int chunk = (lane % kChunks) ^ swz<DP>(r);   // the lane's 16 bytes of its row
-    const uint32_t k_row = PAGED ? s.d_bytes : (uint32_t)s.k_step, v_row = PAGED ? s.d_bytes : (uint32_t)s.v_step;
-    k_ofs = (lane / kChunks) * k_row + chunk * 16;
-    v_ofs = (lane / kChunks) * v_row + chunk * 16;
-    mine = chunk * 16 < s.d_bytes;
+    const int row = lane / kChunks;
+    at = (uint32_t)(((lane % kChunks) ^ swz<DP>(wave * kRowsPer + row)) * 16);
+    mine = at < (uint32_t)s.d_bytes;
+    at += PAGED ? (uint32_t)(row * s.d_bytes) : (uint32_t)row << 16;
     if constexpr (PAGED) whole = s.page_size % kRowsPer == 0;
     else whole = s.k_step < (1 << 27) && s.v_step < (1 << 27);
   }
@@ -588,6 +587,11 @@ struct TileCopy {
     if (wave >= kCopyWaves) return;
     if (whole && kb + kTile <= s.keys) {
       if (!FULL && !mine) return;
+      uint32_t ofs = at;
+      if constexpr (!PAGED) {
+        asm volatile("" : "+v"(ofs));   // formed here each time
+        ofs = (ofs >> 16) * (uint32_t)(V ? s.v_step : s.k_step) + (ofs & 0xFFFFu);
+      }
       const int j0 = kb + wave * kRowsPer;
       const char* base = V ? s.v : s.k;
       if constexpr (PAGED) {
@@ -596,14 +600,14 @@ struct TileCopy {
           const int j = j0 + it * kCopyWaves * kRowsPer;
           const int64_t off = (int64_t)p.id[it] * s.k_step + (j - page_of(s, j) * s.page_size) * s.d_bytes;
           const bool there = (uint32_t)p.id[it] < (uint64_t)s.num_pages;
-          dma16(there ? base + off : reinterpret_cast<const char*>(kZeros), k_ofs, lds + (it * kCopyWaves + wave) * 1024);
+          dma16(there ? base + off : reinterpret_cast<const char*>(kZeros), ofs, lds + (it * kCopyWaves + wave) * 1024);
         }
       } else {
         const int64_t step = V ? s.v_step : s.k_step;
         base += j0 * step;
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
-          dma16(base, V ? v_ofs : k_ofs, lds + (it * kCopyWaves + wave) * 1024);
+          dma16(base, ofs, lds + (it * kCopyWaves + wave) * 1024);
           base += step * (kCopyWaves * kRowsPer);
         }
       }
@@ -700,7 +704,9 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   if (t < w1) scores<DT, DP, kGroups>(sa, w, ln, k_now);
 #pragma unroll 1
   while (t < w1) {
-    if (t >= full0 && t + 1 < full1) {
+    // A single tile that every row sees goes this way in prompts only (210 tokens 11.2 -> 10.0 us; in the
+    // paged kernel of padded rows it costs registers: 161 -> 179 us for a chunk of head dimension 80).
+    if (t >= full0 && t + (PAGED ? 1 : 0) < full1) {
       v16f sb[kGroups];
       v8s f[kAhead];
 #pragma unroll
@@ -709,14 +715,14 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
       // two tiles a turn, so that the scores change places; past the last tile the next scores are
       // formed from whatever the buffer holds, and not used
 #pragma unroll 1
-      do {
+      while (t + 1 < full1) {
         begin();
         add_tile<DT, DP>(w, ln, sa, sb, top, f, k_next, k_after, v_now, sc);
         end_tile();
         begin();
         add_tile<DT, DP>(w, ln, sb, sa, top, f, k_next, k_after, v_now, sc);
         end_tile();
-      } while (t + 1 < full1);
+      }
       if (t < full1) {
         begin();
         add_tile<DT, DP>(w, ln, sa, sb, top, f, k_next, k_after, v_now, sc);
