@@ -1341,14 +1341,15 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // long request alone has dozens of parts).
 constexpr int kBatch = 4;
 
+// Block (bx, by) of the items of one kind, whose parts are at ws.
 template <int DT, int DP, int ROWS, int UNIT, int SHARES>
-__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
+__device__ __forceinline__ void combine(const AttnArgs& a, const Split& sp, float* ws, int bx, int by) {
   constexpr int kQ = DP / 4, kTeams = 256 / kQ;
   constexpr bool kByPart = ROWS <= 32;
   __shared__ int64_t lds[6];
   __shared__ float part_m[kByPart ? kBatch : 1][kTeams], part_l[kByPart ? kBatch : 1][kTeams];
   __shared__ v4f part_o[kByPart ? kBatch : 1][kTeams][kQ];
-  const int w = blockIdx.x + 1, tid = threadIdx.x;
+  const int w = bx + 1, tid = threadIdx.x;
   const Plan<ROWS, UNIT, SHARES, 256> pl(a, sp, w, lds);
   if (pl.req > a.seqs || pl.share * w >= pl.total) return;
   const Req r = pl.get(pl.req);
@@ -1364,7 +1365,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
   const int q = tid % kQ, g = tid / kQ;
   auto load = [&](int j, int row, v2f& ml, v4f& x) {   // part j
     float *po, *pml;
-    part_of<DP, ROWS, SHARES>((float*)a.workspace, j == w - 1 ? first_slot : 2 * j, po, pml);
+    part_of<DP, ROWS, SHARES>(ws, j == w - 1 ? first_slot : 2 * j, po, pml);
     ml = *(const v2f*)(pml + 2 * row);
     x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
   };
@@ -1386,7 +1387,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
     if (a.lse && q == 0) a.lse[at] = lse_of(m, l);
   };
   if constexpr (!kByPart) {
-    const int row = blockIdx.y * kTeams + g;
+    const int row = by * kTeams + g;
     if (row >= rows) return;
     float m = kLowest, l = 0.0f;
     v4f o = {0, 0, 0, 0};
@@ -1437,6 +1438,18 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split sp) {
       }
     }
   }
+}
+
+// Joins the parts of both kinds in one launch: one for each takes 3 to 5 us even if nothing was split
+// (100 new tokens for each of 4 requests over 3000 keys 68.9 -> 63.4 us).  The few-row items'
+// workgroups come first; a kind that the call does not run has no rows.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Split few, Split many, float* many_ws) {
+  const int few_blocks = few.max_rows > 0 ? kFewShares - 1 : 0, b = (int)blockIdx.x - few_blocks;
+  if (b < 0)
+    combine<DT, DP, kFewRows, 32 * kFewWaves, kFewShares>(a, few, (float*)a.workspace, blockIdx.x, 0);
+  else
+    combine<DT, DP, kMostRows, kTile, kShares>(a, many, many_ws, b % (kShares - 1), b / (kShares - 1));
 }
 
 // ---------------------------------------------------------------- host
@@ -1496,6 +1509,10 @@ hipError_t prompt_full(const AttnArgs& a, hipStream_t s) {
                                                       many_lds_bytes<DP>(), s, with_group(a));
 }
 
+// Bytes of the parts of few-row and of many-row items.
+size_t few_bytes(int padded) { return (size_t)kFewShares * 2 * kFewRows * (padded + 2) * sizeof(float); }
+size_t many_bytes(int padded) { return (size_t)kShares * 2 * kMostRows * (padded + 2) * sizeof(float); }
+
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {
   return a.head_dim == DP ? prompt_full<DT, DP, true>(a, s) : prompt_full<DT, DP, false>(a, s);
@@ -1509,35 +1526,30 @@ hipError_t paged_dp(const AttnArgs& a, hipStream_t s) {
   int shift;
   division_magic(a.page_size, magic, shift);
   hipError_t e = hipSuccess;
-  constexpr int kRowsAtOnce = 256 / (DP / 4);   // of a combining workgroup
+  constexpr int kTeams = 256 / (DP / 4);   // rows of a combining workgroup
+  const Split none{1, 0}, sf = few ? Split{1, many ? kFewRows : 0x7FFFFFFF} : none;
+  const Split sm = many ? Split{few ? kFewRows + 1 : 1, 0x7FFFFFFF} : none;
+  AttnArgs cm = c;
+  if (few) cm.workspace = (char*)c.workspace + few_bytes(DP);
   if (few) {
-    const Split sp{1, many ? kFewRows : 0x7FFFFFFF};
-    e = launch_lds<paged_few_kernel<DT, DP, kFewWaves, FULL>>(kFewShares, 64 * kFewWaves, few_lds_bytes<DP>(), s, c, sp, magic, shift);
-    if (e != hipSuccess) return e;
-    combine_kernel<DT, DP, kFewRows, 32 * kFewWaves, kFewShares>
-        <<<dim3(kFewShares - 1), dim3(256), 0, s>>>(c, sp);
-    e = hipGetLastError();
+    e = launch_lds<paged_few_kernel<DT, DP, kFewWaves, FULL>>(kFewShares, 64 * kFewWaves, few_lds_bytes<DP>(), s, c, sf, magic, shift);
     if (e != hipSuccess) return e;
   }
   if (many) {
-    const Split sp{few ? kFewRows + 1 : 1, 0x7FFFFFFF};
-    e = launch_lds<paged_rows_kernel<DT, DP, FULL>>(kShares, 512, many_lds_bytes<DP>(), s, c, sp, magic, shift);
+    e = launch_lds<paged_rows_kernel<DT, DP, FULL>>(kShares, 512, many_lds_bytes<DP>(), s, cm, sm, magic, shift);
     if (e != hipSuccess) return e;
-    combine_kernel<DT, DP, kMostRows, kTile, kShares>
-        <<<dim3(kShares - 1, kMostRows / kRowsAtOnce), dim3(256), 0, s>>>(c, sp);
-    e = hipGetLastError();
   }
-  return e;
+  const int blocks = (few ? kFewShares - 1 : 0) + (many ? (kShares - 1) * (kMostRows / kTeams) : 0);
+  combine_kernel<DT, DP><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(c, sf, sm, (float*)cm.workspace);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
   const int group = q_heads / kv_heads;
-  const size_t per_row = ((size_t)padded_dim(head_dim) + 2) * sizeof(float);
-  const size_t few = needs_few(seqs, tokens, group) ? (size_t)kFewShares * 2 * kFewRows * per_row : 0;
-  const size_t many = needs_many(seqs, tokens, group) ? (size_t)kShares * 2 * kMostRows * per_row : 0;
-  return few > many ? few : many;
+  const int dim = padded_dim(head_dim);
+  return (needs_few(seqs, tokens, group) ? few_bytes(dim) : 0) + (needs_many(seqs, tokens, group) ? many_bytes(dim) : 0);
 }
 
 bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }
