@@ -28,6 +28,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return r < 0 ? q - 1 : r >= b ? q + 1 : q;
 }
 
+// Bytes from a page's first row to the row at `place`: a page has up to 2^30 places of up to 256 bytes.
+__host__ __device__ __forceinline__ int64_t place_bytes(int place, int row_bytes) { return (int64_t)place * row_bytes; }
+
 struct PageMapsArgs {
   const int32_t* ctx_lens;
   const int32_t* new_lens;

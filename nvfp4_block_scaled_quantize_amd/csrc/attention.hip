@@ -145,7 +145,7 @@ __device__ __forceinline__ void row_at(const Source& s, int j, int page, int chu
   bool there = j < s.keys && chunk_bytes < s.d_bytes;
   if constexpr (PAGED) {
     there = there && (uint32_t)page < (uint64_t)s.num_pages;
-    const int64_t off = (int64_t)page * s.k_step + (int64_t)(j - page_of(s, j) * s.page_size) * s.d_bytes + chunk_bytes;
+    const int64_t off = (int64_t)page * s.k_step + place_bytes(j - page_of(s, j) * s.page_size, s.d_bytes) + chunk_bytes;
     k = there ? s.k + off : zero;
     v = there ? s.v + off : zero;
   } else {
@@ -599,7 +599,7 @@ struct TileCopy {
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
           const int j = j0 + it * kCopyWaves * kRowsPer;
-          const int64_t off = (int64_t)p.id[it] * s.k_step + (j - page_of(s, j) * s.page_size) * s.d_bytes;
+          const int64_t off = (int64_t)p.id[it] * s.k_step + place_bytes(j - page_of(s, j) * s.page_size, FULL ? DP * 2 : s.d_bytes);
           const bool there = (uint32_t)p.id[it] < (uint64_t)s.num_pages;
           dma16(there ? base + off : reinterpret_cast<const char*>(kZeros), ofs, lds + (it * kCopyWaves + wave) * 1024);
         }
@@ -1225,7 +1225,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         for (int n8 = 0; n8 < 4; ++n8) {
           const int id = __builtin_amdgcn_readlane(ids, n8), j = kb + n8 * 8;
           const bool there = (uint32_t)id < (uint64_t)s.num_pages;
-          const int64_t off = (int64_t)id * s.k_step + (j - page_of(s, j) * s.page_size) * (FULL ? DP * 2 : s.d_bytes);
+          const int64_t off = (int64_t)id * s.k_step + place_bytes(j - page_of(s, j) * s.page_size, FULL ? DP * 2 : s.d_bytes);
           const char* k = there ? s.k + off : reinterpret_cast<const char*>(kZeros);
           const char* v = there ? k + k_to_v : k;
 #pragma unroll
