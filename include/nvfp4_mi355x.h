@@ -378,13 +378,15 @@ int32_t nvfp4_mx_gemm(const uint8_t* a_tiled, const uint8_t* a_sf_tiled, const f
  *                 tokens that do not fit are dropped (with the table entries of
  *                 pages that none of the kept tokens opens)
  *   cu_new      : [seqs + 1] int32 out, first new token of each request
- *   kv_lens     : [seqs] int32 out, ctx_lens + new_lens
+ *   kv_lens     : [seqs] int32 out, ctx_lens + new_lens; may be ctx_lens itself
+ *                 (lengths updated in place)
  *   slot_map    : [tokens] int64 out; -1 for a token without a page (list
  *                 exhausted, position past the table's width, negative entry
  *                 in the table)
  *   positions   : [tokens] int32 out
  *   taken       : [1] int32 out, pages the step needs: above num_free, some
  *                 tokens have no page; else the first `taken` entries are used
+ * What is written overlaps nothing else that is passed (EINVAL otherwise).
  * Requires seqs <= 2^20, tokens < 2^31 - 2^16, sums of the lengths < 2^31.
  */
 int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_t seqs,

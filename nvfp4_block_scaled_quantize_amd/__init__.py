@@ -596,6 +596,12 @@ def _handle(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _overlap(a, b) -> bool:
+    """Whether two dense tensors share memory."""
+    x, y, n, m = a.data_ptr(), b.data_ptr(), a.numel() * a.element_size(), b.numel() * b.element_size()
+    return n > 0 and m > 0 and x < y + m and y < x + n
+
+
 def _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out):
     if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be a 1-D tensor")
@@ -614,8 +620,16 @@ def _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out):
                                ("slot_map", torch.int64, (tokens,)), ("positions", torch.int32, (tokens,)),
                                ("taken", torch.int32, (1,))):
             _dense(out.get(key), "out['%s']" % key, dt, shape)
-        out = [out[key] for key in ("cu_new", "kv_lens", "slot_map", "positions", "taken")]
-    _need_gpu(ctx_lens, new_lens, block_table, free_pages, *(out or ()))
+    written = [("block_table", block_table)]
+    if out is not None:
+        written += [("out['%s']" % key, out[key]) for key in ("cu_new", "kv_lens", "slot_map", "positions", "taken")]
+    everything = written + [("ctx_lens", ctx_lens), ("new_lens", new_lens), ("free_pages", free_pages)]
+    for i, (name, t) in enumerate(written):
+        for other, u in everything[i + 1:]:
+            in_place = name == "out['kv_lens']" and other == "ctx_lens" and t.data_ptr() == u.data_ptr()
+            if _overlap(t, u) and not in_place:
+                raise ValueError("%s must not overlap %s" % (name, other))
+    _need_gpu(ctx_lens, new_lens, block_table, free_pages, *(t for _, t in written))
 
 
 def _plain_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out, dev) -> bool:
@@ -639,7 +653,8 @@ def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     from free_pages for new_lens[i] tokens after the ctx_lens[i] cached ones, and returns
     dict(cu_new [seqs + 1], kv_lens [seqs], slot_map [tokens] int64, positions [tokens],
     taken [1]).  `tokens` is the size of the maps (entries past the last token are -1); `taken`
-    above len(free_pages) means that pages ran out."""
+    above len(free_pages) means that pages ran out.  out["kv_lens"] may be ctx_lens itself, which then
+    holds the new lengths; other buffers must not overlap."""
     tokens, dev = int(tokens), _gpu_of(ctx_lens)
     if dev < 0 or not _plain_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out, dev):
         _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out)
@@ -657,6 +672,8 @@ def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
                               out["cu_new"].data_ptr(), out["kv_lens"].data_ptr(), out["slot_map"].data_ptr(),
                               out["positions"].data_ptr(), out["taken"].data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
+        if st == NVFP4_EINVAL:   # buffers that overlap: only the library looks for them in a plain call
+            _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out)
         raise Nvfp4Error(st, "nvfp4_page_maps")
     return out
 

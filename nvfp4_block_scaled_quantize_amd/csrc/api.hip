@@ -44,6 +44,15 @@ int32_t device_status() {
 int32_t hip_status(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_EHIP; }
 
 bool aligned4(const void* p) { return ((uintptr_t)p % 4) == 0; }
+
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
 bool aligned256(const void* p) { return ((uintptr_t)p % 256) == 0; }
 
 // External weights of "Fused Nvfp4 GEMM All Reduce Plugin" (external-weight
@@ -415,6 +424,18 @@ int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_
       !aligned4(kv_lens) || ((uintptr_t)slot_map % 8) != 0 || !aligned4(positions))
     return NVFP4_EINVAL;
   if (seqs > (1 << 20) || tokens > 0x7FFF0000LL) return NVFP4_EUNSUPPORTED;
+  // every workgroup reads the inputs while others already write: what is written overlaps nothing else,
+  // but for lengths updated in place (see launch_page_maps)
+  const size_t n = (size_t)seqs, t = (size_t)tokens;
+  const Bytes all[] = {{block_table, n * max_pages * 4}, {cu_new, (n + 1) * 4}, {kv_lens, n * 4}, {slot_map, t * 8},
+                       {positions, t * 4}, {taken, 4}, {ctx_lens, n * 4}, {new_lens, n * 4},
+                       {free_pages, (size_t)num_free * 4}};
+  constexpr int kWritten = 6, kAll = 9, kKvLens = 2, kCtxLens = 6;
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kAll; ++j) {
+      const bool in_place = i == kKvLens && j == kCtxLens && kv_lens == ctx_lens;
+      if (overlap(all[i], all[j]) && !in_place) return NVFP4_EINVAL;
+    }
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
   nvfp4::PageMapsArgs a{ctx_lens, new_lens, block_table, free_pages, seqs, max_pages, num_free, page_size,

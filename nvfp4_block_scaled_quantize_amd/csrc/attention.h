@@ -39,7 +39,7 @@ struct PageMapsArgs {
   int seqs, max_pages, num_free, page_size;
   int64_t tokens;              // entries of slot_map and positions
   int32_t* cu_new;             // [seqs + 1]
-  int32_t* kv_lens;            // [seqs]
+  int32_t* kv_lens;            // [seqs], may be ctx_lens
   int64_t* slot_map;
   int32_t* positions;
   int32_t* taken;              // [1]

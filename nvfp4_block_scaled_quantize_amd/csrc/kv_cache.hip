@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
     }
     if (mine) {
       a.cu_new[i] = (int32_t)at;
-      a.kv_lens[i] = (int32_t)all;
+      if (a.kv_lens) a.kv_lens[i] = (int32_t)all;
     }
     at = add(at, m);
     page = add(page, pages_of(a, all) - pages_of(a, c));
@@ -170,6 +170,12 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(PageMapsArgs a) 
   }
 }
 
+// kv_lens alone, where they replace ctx_lens.
+__global__ void __launch_bounds__(kMapThreads) grow_kernel(int32_t* lens, const int32_t* new_lens, int seqs) {
+  const int i = blockIdx.x * kMapThreads + threadIdx.x;
+  if (i < seqs) lens[i] = (int32_t)add(len_of(lens, i), len_of(new_lens, i));
+}
+
 // ---------------------------------------------------------------- writer
 // A copy: token t's row of each head goes to its slot.  One thread moves U
 // bytes; a token's rows are consecutive units, so the reads of a wave are
@@ -203,7 +209,14 @@ hipError_t launch_page_maps(const PageMapsArgs& a, hipStream_t s) {
   const int64_t blocks = (a.tokens + kMapTokens - 1) / kMapTokens;
   PageMapsArgs c = a;
   division_magic(c.page_size, c.magic, c.shift);
+  // Lengths updated in place: one workgroup reads and writes each of them in the same thread, but of
+  // several each reads all of them, so they are written after the last has read.
+  const bool later = a.kv_lens == a.ctx_lens && blocks > 1;
+  if (later) c.kv_lens = nullptr;
   page_maps_kernel<<<dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(kMapThreads), 0, s>>>(c);
+  if (later && a.seqs > 0)
+    grow_kernel<<<dim3((unsigned)((a.seqs + kMapThreads - 1) / kMapThreads)), dim3(kMapThreads), 0, s>>>(
+        a.kv_lens, a.new_lens, a.seqs);
   return hipGetLastError();
 }
 
