@@ -18,6 +18,14 @@
 // less than 2^8: the weights then reach at most 2^8, which neither type nor
 // the binary32 sums notice, and the rescaling of O is skipped for most tiles.
 //
+// t_j - m is one fma(s_j, scale log2 e, -m): what m's own rounding leaves is the
+// same factor for all keys of a row and cancels in O / l, but it must not leave
+// the exponent's range, and from |m| = 2^28 on half a unit in m's last place
+// does.  A wave that met such a row (|m| >= kBig; no trained model has one)
+// computes its rows again, from a reference r, the largest raw score so far:
+// scores become s_j - r as they come, m stays at 0 and the maximum never lags
+// (see again).
+//
 // Matrix operands (v_mfma_f32_32x32x16, lane = 32 h + c): the score tile is
 // formed transposed, S^T = K Q^T, so that a lane holds 16 of the 32 keys of
 // ONE row c.  Row maxima and sums are then in-lane (plus one exchange between
@@ -44,6 +52,7 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
+constexpr float kBig = 4194304.0f;   // 2^22: a maximum's last place is still half a unit of log2
 
 __device__ const uint4 kZeros[64] = {};   // rows that do not exist are copied from here
 
@@ -161,8 +170,10 @@ struct Rows {
   v8s q[DP / 16];      // B operand: lane's row, d = 16 st + 8 h ..
   v16f o[DP / 32];     // O^T: d = 32 t + 8 (i / 4) + 4 h + i % 4
   float m, l;          // log2 units; l: this half-wave's keys only
-  float far;           // m + kKeep as a score (before scaling)
+  float far;           // m + kKeep as a score (before scaling); of a big row its reference
   int lo, hi;          // the row sees the keys lo <= j < hi
+  uint64_t late;       // lanes whose row needs a reference
+  uint64_t big;        // lanes whose row counts from one
 };
 
 // A row starts at the lowest number instead of -inf: differences of maxima are
@@ -171,7 +182,9 @@ struct Rows {
 constexpr float kLowest = -3.40282346638528859812e+38f;
 
 struct Scaling {
-  float c, inv;   // scale log2 e and its inverse
+  float c, inv;   // scale log2 e and its inverse, in scalar registers
+  __device__ __forceinline__ explicit Scaling(float scale)
+      : c(__uint_as_float(uni(__float_as_uint(scale * kLog2e)))), inv(__uint_as_float(uni(__float_as_uint(1.0f / c)))) {}
 };
 
 template <int DT>
@@ -238,22 +251,63 @@ __device__ __forceinline__ int turns_if(int positive) {
   return n;
 }
 
-// Raises the maximum to `top` (a score, of both half-waves) where it lags by more than kKeep.
+// A row's reference.
+template <int DP>
+__device__ __forceinline__ float reference(const Rows<DP>& w) {
+  return __builtin_amdgcn_inverse_ballot_w64(w.big) ? w.far : 0.0f;
+}
+
+// log2 of how far the maximum (m, ref) lies above (m2, ref2): the references are scores, and their
+// difference is exact where it matters.
+__device__ __forceinline__ float above(float m, float ref, float m2, float ref2, float c) {
+  return __builtin_fmaf(ref - ref2, c, m) - m2;
+}
+
+template <int DP>
+__device__ __forceinline__ void rescale(Rows<DP>& w, float a) {
+  w.l *= a;
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w.o[t][i] *= a;
+}
+
+__device__ __forceinline__ int turns_any(uint64_t lanes) {   // see turns_if
+  int turns;
+  asm volatile("s_cmp_lg_u64 %1, 0\n\ts_cselect_b32 %0, 1, 0" : "=s"(turns) : "s"(lanes) : "scc");
+  return turns;
+}
+
+// Raises the maximum to `top` (a score, of both half-waves) where it lags by more than kKeep, and notes
+// the rows that this is not enough for.
 template <int DP>
 __device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc) {
-  const uint64_t far = __ballot(top > w.far);
-  int turns;   // see turns_if
-  asm volatile("s_cmp_lg_u64 %1, 0\n\ts_cselect_b32 %0, 1, 0" : "=s"(turns) : "s"(far) : "scc");
 #pragma unroll 1
-  for (; turns > 0; --turns) {
-    const float m = __builtin_fmaxf(w.m, top * sc.c), a = __builtin_amdgcn_exp2f(w.m - m);
+  for (int turns = turns_any(__ballot(top > w.far)); turns > 0; --turns) {
+    const float t = top * sc.c, m = __builtin_fmaxf(w.m, t), a = __builtin_amdgcn_exp2f(w.m - m);
+    w.late |= __ballot(t > w.m && __builtin_fabsf(t) >= kBig);
     w.m = m;
     w.far = (m + kKeep) * sc.inv;
-    w.l *= a;
+    rescale(w, a);
+  }
+}
+
+// The same with references, which are taken off the scores `s`.
+template <int DP>
+__device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc, v16f& s) {
+#pragma unroll 1
+  for (int turns = turns_any(__ballot(top > w.far) | w.big); turns > 0; --turns) {
+    const float old = reference(w), t = top * sc.c;
+    const bool was = __builtin_amdgcn_inverse_ballot_w64(w.big), is = was || (t > w.m && __builtin_fabsf(t) >= kBig);
+    const float ref = was ? __builtin_fmaxf(old, top) : is ? top : 0.0f;
+    const float m = is ? 0.0f : __builtin_fmaxf(w.m, t);
+    const float a = __builtin_amdgcn_exp2f(above(w.m, old, m, ref, sc.c));
+    w.m = m;
+    w.far = is ? ref : (m + kKeep) * sc.inv;
+    w.big = __ballot(is);
 #pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w.o[t][i] *= a;
+    for (int i = 0; i < 16; ++i) s[i] -= ref;
+    rescale(w, a);
   }
 }
 
@@ -319,8 +373,8 @@ __device__ __forceinline__ void add_not_finite(Rows<DP>& w, const v16f& s, float
 }
 
 // Adds 32 keys from key kb, whose scores are `s` and whose values are at v_lds.  `hidden` > 0: some
-// row does not see some of them.
-template <int DT, int DP>
+// row does not see some of them.  REF: rows may have references.
+template <int DT, int DP, bool REF = false>
 __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f& s, uint32_t v_lds, int kb,
                                          const Scaling& sc, int hidden, int lane) {
   constexpr int kTiles = DP / 32;
@@ -333,7 +387,8 @@ __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f&
     for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(8 * (i / 4) + i % 4 - lo) < count ? s[i] : -__builtin_inff();
     odd = uni(all_finite<DT, DP>(v_lds, lane) ? 0 : 1);
   }
-  raise(w, both_max(largest(s)), sc);
+  if constexpr (REF) raise(w, both_max(largest(s)), sc, s);
+  else raise(w, both_max(largest(s)), sc);
   v8s p[2];
   float sum[2] = {w.l, 0.0f};
 #pragma unroll
@@ -462,13 +517,50 @@ __device__ __forceinline__ void load_rows(Rows<DP>& w, const AttnArgs& a, const 
   w.lo = (a.window > 0 && p + 1 > a.window) ? p + 1 - a.window : 0;
   w.m = kLowest;
   w.far = -__builtin_inff();
+  w.late = w.big = 0;
   w.l = 0.0f;
 #pragma unroll
   for (int t = 0; t < DP / 32; ++t) w.o[t] = zero16();
 }
 
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+// The rows of a wave again, with references: 32 keys at a time, from first_key on every `step`-th such
+// group before end_key.  `lds`: 32 rows of DP elements of the wave's own, for the keys and then the values
+// of a group.  Rare: short rather than fast.
+template <int DT, int DP, bool PAGED>
+__device__ __forceinline__ void again(Rows<DP>& w, const AttnArgs& a, const Source& s, const Item& it, int row0,
+                                      int first_key, int end_key, int step, const Scaling& sc, uint32_t lds) {
+  constexpr int kChunks = DP / 8, kRowsPer = 64 / kChunks;
+  uint32_t ones = ~0u;
+  asm volatile("" : "+s"(ones));   // nothing here is shared with the common path and kept in registers for it
+  const int lane = __builtin_amdgcn_mbcnt_hi(ones, __builtin_amdgcn_mbcnt_lo(ones, 0));
+  load_rows<DP>(w, a, it, row0, lane);
+  const Lanes<DP> ln(lane);
+#pragma unroll 1
+  for (int kb = uni(first_key); kb < end_key; kb += step) {
+    v16f x[1];
+#pragma unroll 1
+    for (int values = 0; values < 2; ++values) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what is there has been read
+#pragma unroll 1
+      for (int n = 0; n < 32 / kRowsPer; ++n) {
+        const int r = n * kRowsPer + lane / kChunks, j = kb + r;
+        int page = 0;
+        if constexpr (PAGED) page = j < s.keys ? s.table[page_of(s, j)] : -1;
+        const char *k, *v;
+        row_at<PAGED>(s, j, page, ((lane % kChunks) ^ swz<DP>(r)) * 16, k, v);
+        dma16_at(values ? v : k, (uint32_t)uni(lds + n * 1024));
+      }
+      wait_vmcnt_le<0>();
+      asm volatile("" ::: "memory");
+      if (!values) scores<DT, DP, 1>(x, w, ln, lds);
+    }
+    add_keys<DT, DP, true>(w, ln, x[0], lds, kb, sc, 1, lane);
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+__device__ __forceinline__ float lse_of(float m, float ref, float l, float c) {
+  return l == 0.0f ? -__builtin_inff() : (__builtin_fmaf(ref, c, m) + __builtin_log2f(l)) * kLn2;
 }
 
 // Writes a wave's finished rows, through its part `lds` of the tiles (32 rows of DP elements): a lane
@@ -501,10 +593,10 @@ __device__ __forceinline__ void store_rows(const Rows<DP>& w, const AttnArgs& a,
     if (row0 + r < rows && chunk * 8 < a.head_dim)
       *(v8s*)((uint16_t*)a.out + place(row0 + r) * a.head_dim + chunk * 8) = x;
   }
-  if (a.lse && h == 0 && row0 + c < rows) a.lse[place(row0 + c)] = lse_of(w.m, l);
+  if (a.lse && h == 0 && row0 + c < rows) a.lse[place(row0 + c)] = lse_of(w.m, reference(w), l, a.scale * kLog2e);
 }
 
-// Part of rows whose keys are split over workgroups: O (unnormalized) [rows][DP], (m, l) [rows].
+// Part of rows whose keys are split over workgroups: O (unnormalized) [rows][DP], (m, l, reference, 0) [rows].
 template <int DP>
 __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* ml, int r, int lane) {
   const int h = lane >> 5;
@@ -515,7 +607,8 @@ __device__ __forceinline__ void store_part(const Rows<DP>& w, float* o, float* m
     for (int i = 0; i < 4; ++i)
       *(v4f*)(o + (int64_t)r * DP + t * 32 + 8 * i + 4 * h) =
           (v4f){w.o[t][4 * i], w.o[t][4 * i + 1], w.o[t][4 * i + 2], w.o[t][4 * i + 3]};
-  if (h == 0) *(v2f*)(ml + 2 * r) = (v2f){w.m, l};
+  const float ref = reference(w);
+  if (h == 0) *(v4f*)(ml + 4 * r) = (v4f){w.m, l, ref, 0.0f};
 }
 
 // ---------------------------------------------------------------- many rows
@@ -667,7 +760,7 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   const int hi_min = uni(pos0 + 1), hi_max = uni(active ? pos1 + 1 : 0);
   const int lo_min = uni((a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0);
   const int lo_max = uni((a.window > 0 && pos1 + 1 > a.window) ? pos1 + 1 - a.window : 0);
-  const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
+  const Scaling sc(a.scale);
   const Lanes<DP> ln(lane);
   // tiles that some row of the wave sees; those that every row sees
   const int w0 = clampi(lo_min / kTile, t0, t1), w1 = clampi((hi_max + kTile - 1) / kTile, w0, t1);
@@ -747,6 +840,9 @@ __device__ __forceinline__ void run_block(const AttnArgs& a, const Source& s, co
   }
   skip_to(t1);
   lds_barrier();   // the buffers may be filled again
+#pragma unroll 1
+  for (int turns = turns_any(w.late); turns > 0; --turns)
+    again<DT, DP, PAGED>(w, a, s, it, first, t0 * kTile, t1 * kTile, 32, sc, lds + wave * 32 * DP * 2);
 }
 
 // Tiles of `unit` keys that the rows row0 .. row0 + block - 1 see.
@@ -1069,8 +1165,8 @@ struct Segment {
 
 template <int DP, int ROWS, int SHARES>
 __device__ __forceinline__ void part_of(float* ws, int slot, float*& o, float*& ml) {
-  ml = ws + (int64_t)slot * ROWS * 2;
-  o = ws + (int64_t)SHARES * 2 * ROWS * 2 + (int64_t)slot * ROWS * DP;
+  ml = ws + (int64_t)slot * ROWS * 4;
+  o = ws + (int64_t)SHARES * 2 * ROWS * 4 + (int64_t)slot * ROWS * DP;
 }
 
 __device__ __forceinline__ void paged_source(const AttnArgs& a, const Item& it, int req, Source& s, uint32_t magic, int shift) {
@@ -1143,12 +1239,12 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     const int row = uni(threadIdx.x >> 6) * 32, lane = threadIdx.x & 63;
     if (slot < 0) {
       store_rows<DT, DP>(rows, a, g.it, g.it.row0 + row, lane, lds_addr(dyn_lds) + row * DP * 2);
-      lds_barrier();   // the tiles may be filled again
     } else {
       float *o, *ml;
       part_of<DP, kRows, kShares>((float*)a.workspace, slot, o, ml);
       store_part<DP>(rows, o, ml, row + (lane & 31), lane);
     }
+    lds_barrier();   // the tiles may be filled again
   });
 }
 
@@ -1175,7 +1271,7 @@ __global__ void __launch_bounds__(64 * NW, 1)
 paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
   __shared__ int64_t lds[NW + 2];
   __shared__ int win[NW][kWindow];
-  __shared__ float join_ml[NW][32][2];
+  __shared__ float join_ml[NW][32][3];   // maximum, sum, reference
   constexpr int kChunks = DP / 8, kRowsPer = 64 / kChunks, kIters = 32 / kRowsPer;
   constexpr int kHalf = 32 * DP * 2, kStage = 2 * kHalf;   // bytes of a tile of K, of K and V
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
@@ -1196,7 +1292,7 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     const int hi_min = p0 + 1, hi_max = p1 + 1;
     const int lo_min = (a.window > 0 && hi_min > a.window) ? hi_min - a.window : 0;
     const int lo_max = (a.window > 0 && hi_max > a.window) ? hi_max - a.window : 0;
-    const Scaling sc{a.scale * kLog2e, 1.0f / (a.scale * kLog2e)};
+    const Scaling sc(a.scale);
     const int n = g.t1 - g.t0;
     const bool whole = s.page_size % 8 == 0;   // eight keys lie in one page
     if constexpr (!FULL) {   // what the copies leave out of the rows
@@ -1273,15 +1369,32 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
       }
       if (t + 2 < n) issue(t + 2);
     }
+#pragma unroll 1
+    for (int turns = turns_any(st.late); turns > 0; --turns)
+      again<DT, DP, true>(st, a, s, g.it, g.it.row0, (g.t0 * NW + wave) * 32, g.t1 * NW * 32, NW * 32, sc, mem);
     // join the waves: weights 2^(m_w - m)
     const int h = lane >> 5, col = lane & 31;
-    const float l = both_sum(st.l);
-    if (h == 0) { join_ml[wave][col][0] = st.m; join_ml[wave][col][1] = l; }
+    const float l = both_sum(st.l), own = reference(st);
+    if (h == 0) {
+      join_ml[wave][col][0] = st.m;
+      join_ml[wave][col][1] = l;
+      join_ml[wave][col][2] = own;
+    }
     __syncthreads();
-    float m = kLowest;
+    // the largest maximum of row r, and its reference
+    auto largest_of = [&](int r, float& m, float& ref) {
+      m = join_ml[0][r][0];
+      ref = join_ml[0][r][2];
 #pragma unroll
-    for (int k = 0; k < NW; ++k) m = __builtin_fmaxf(m, join_ml[k][col][0]);
-    const float mine = __builtin_amdgcn_exp2f(st.m - m);
+      for (int k = 1; k < NW; ++k)
+        if (above(join_ml[k][r][0], join_ml[k][r][2], m, ref, sc.c) > 0.0f) {
+          m = join_ml[k][r][0];
+          ref = join_ml[k][r][2];
+        }
+    };
+    float m, ref;
+    largest_of(col, m, ref);
+    const float mine = __builtin_amdgcn_exp2f(above(st.m, own, m, ref, sc.c));
     // a row stored from bank 4 col on: the 32 rows of a store take all banks in turn
     if (g.it.row0 + col < rows)
 #pragma unroll
@@ -1301,14 +1414,13 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
     for (int k = tid; k < 32 * (DP / 4); k += 64 * NW) {
       const int r = k / (DP / 4), q = k % (DP / 4), row = g.it.row0 + r;
       if (row >= rows) continue;
-      float mm = kLowest;
-#pragma unroll
-      for (int x = 0; x < NW; ++x) mm = __builtin_fmaxf(mm, join_ml[x][r][0]);
+      float mm, rr;
+      largest_of(r, mm, rr);
       float ll = 0.0f;
       v4f o = {0, 0, 0, 0};
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
-        ll += join_ml[x][r][1] * __builtin_amdgcn_exp2f(join_ml[x][r][0] - mm);
+        ll += join_ml[x][r][1] * __builtin_amdgcn_exp2f(above(join_ml[x][r][0], join_ml[x][r][2], mm, rr, sc.c));
         const v4f y = *(const v4f*)(join_o + (x * 32 + r) * DP + ((q ^ (r & (DP / 4 - 1))) * 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] += y[e];
@@ -1320,10 +1432,10 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
         if (q * 4 < a.head_dim)
           *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
               (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-        if (a.lse && q == 0) a.lse[at] = lse_of(mm, ll);
+        if (a.lse && q == 0) a.lse[at] = lse_of(mm, rr, ll, sc.c);
       } else {
         *(v4f*)(po + (int64_t)r * DP + q * 4) = o;
-        if (q == 0) *(v2f*)(pml + 2 * r) = (v2f){mm, ll};
+        if (q == 0) *(v4f*)(pml + 4 * r) = (v4f){mm, ll, rr, 0.0f};
       }
     }
     __syncthreads();   // join_o is the next segment's tile memory
@@ -1347,7 +1459,7 @@ __device__ __forceinline__ void combine(const AttnArgs& a, const Split& sp, floa
   constexpr int kQ = DP / 4, kTeams = 256 / kQ;
   constexpr bool kByPart = ROWS <= 32;
   __shared__ int64_t lds[6];
-  __shared__ float part_m[kByPart ? kBatch : 1][kTeams], part_l[kByPart ? kBatch : 1][kTeams];
+  __shared__ v4f part_ml[kByPart ? kBatch : 1][kTeams];
   __shared__ v4f part_o[kByPart ? kBatch : 1][kTeams][kQ];
   const int w = bx + 1, tid = threadIdx.x;
   const Plan<ROWS, UNIT, SHARES, 256> pl(a, sp, w, lds);
@@ -1363,78 +1475,72 @@ __device__ __forceinline__ void combine(const AttnArgs& a, const Split& sp, floa
   const int group = a.group, rows = r.news * group - rb * ROWS < ROWS ? r.news * group - rb * ROWS : ROWS;
   const int first_slot = 2 * (w - 1) + (s0 > pl.share * (w - 1) ? 1 : 0);
   const int q = tid % kQ, g = tid / kQ;
-  auto load = [&](int j, int row, v2f& ml, v4f& x) {   // part j
+  const float c = a.scale * kLog2e;
+  auto load = [&](int j, int row, v4f& ml, v4f& x) {   // part j
     float *po, *pml;
     part_of<DP, ROWS, SHARES>(ws, j == w - 1 ? first_slot : 2 * j, po, pml);
-    ml = *(const v2f*)(pml + 2 * row);
+    ml = *(const v4f*)(pml + 4 * row);
     x = *(const v4f*)(po + (int64_t)row * DP + q * 4);
   };
-  auto join = [&](float& m, float& l, v4f& o, float pm, float pl2, v4f x) {
-    const float nm = __builtin_fmaxf(m, pm);
-    const float u = __builtin_amdgcn_exp2f(m - nm), v = __builtin_amdgcn_exp2f(pm - nm);
-    l = l * u + pl2 * v;
+  const v4f none = {kLowest, 0.0f, 0.0f, 0.0f};   // maximum, sum, reference
+  auto join = [&](v4f& ml, v4f& o, v4f pml, v4f x) {
+    const float d = above(pml[0], pml[2], ml[0], ml[2], c);
+    const float u = __builtin_amdgcn_exp2f(__builtin_fminf(-d, 0.0f)), v = __builtin_amdgcn_exp2f(__builtin_fminf(d, 0.0f));
+    ml[1] = ml[1] * u + pml[1] * v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = o[e] * u + x[e] * v;
-    m = nm;
+    ml[0] = d > 0.0f ? pml[0] : ml[0];
+    ml[2] = d > 0.0f ? pml[2] : ml[2];
   };
-  auto write = [&](int row, float m, float l, v4f o) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  auto write = [&](int row, v4f ml, v4f o) {
+    const float l = ml[1], inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int gr = rb * ROWS + row, tok = token_of(a, gr);
     const int64_t at = (int64_t)(r.start + tok) * a.q_heads + head * group + gr - tok * group;
     if (q * 4 < a.head_dim)
       *(u32x2*)((uint32_t*)a.out + at * (a.head_dim / 2) + q * 2) =
           (u32x2){pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-    if (a.lse && q == 0) a.lse[at] = lse_of(m, l);
+    if (a.lse && q == 0) a.lse[at] = lse_of(ml[0], ml[2], l, c);
   };
   if constexpr (!kByPart) {
     const int row = by * kTeams + g;
     if (row >= rows) return;
-    float m = kLowest, l = 0.0f;
-    v4f o = {0, 0, 0, 0};
+    v4f ml = none, o = {0, 0, 0, 0};
     for (int j = w - 1; j <= last; j += kBatch) {
-      v2f ml[kBatch];
-      v4f x[kBatch];
+      v4f p[kBatch], x[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) load(j + k < last ? j + k : last, row, ml[k], x[k]);
+      for (int k = 0; k < kBatch; ++k) load(j + k < last ? j + k : last, row, p[k], x[k]);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (j + k <= last) join(m, l, o, ml[k][0], ml[k][1], x[k]);
+        if (j + k <= last) join(ml, o, p[k], x[k]);
     }
-    write(row, m, l, o);
+    write(row, ml, o);
   } else {
     for (int row0 = 0; row0 < rows; row0 += kBatch) {
-      float m[kBatch], l[kBatch];
-      v4f o[kBatch];
+      v4f ml[kBatch], o[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        m[k] = kLowest;
-        l[k] = 0.0f;
+        ml[k] = none;
         o[k] = (v4f){0, 0, 0, 0};
       }
       for (int j = w - 1 + g; j <= last; j += kTeams) {
-        v2f ml[kBatch];
-        v4f x[kBatch];
+        v4f p[kBatch], x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) load(j, row0 + k < rows ? row0 + k : rows - 1, ml[k], x[k]);
+        for (int k = 0; k < kBatch; ++k) load(j, row0 + k < rows ? row0 + k : rows - 1, p[k], x[k]);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) join(m[k], l[k], o[k], ml[k][0], ml[k][1], x[k]);
+        for (int k = 0; k < kBatch; ++k) join(ml[k], o[k], p[k], x[k]);
       }
       if (row0 > 0) __syncthreads();
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (q == 0) {
-          part_m[k][g] = m[k];
-          part_l[k][g] = l[k];
-        }
+        if (q == 0) part_ml[k][g] = ml[k];
         part_o[k][g][q] = o[k];
       }
       __syncthreads();
       if (g < kBatch && row0 + g < rows) {
-        float jm = kLowest, jl = 0.0f;
-        v4f jo = {0, 0, 0, 0};
+        v4f jml = none, jo = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < kTeams; ++k) join(jm, jl, jo, part_m[g][k], part_l[g][k], part_o[g][k][q]);
-        write(row0 + g, jm, jl, jo);
+        for (int k = 0; k < kTeams; ++k) join(jml, jo, part_ml[g][k], part_o[g][k][q]);
+        write(row0 + g, jml, jo);
       }
     }
   }
@@ -1510,8 +1616,8 @@ hipError_t prompt_full(const AttnArgs& a, hipStream_t s) {
 }
 
 // Bytes of the parts of few-row and of many-row items.
-size_t few_bytes(int padded) { return (size_t)kFewShares * 2 * kFewRows * (padded + 2) * sizeof(float); }
-size_t many_bytes(int padded) { return (size_t)kShares * 2 * kMostRows * (padded + 2) * sizeof(float); }
+size_t few_bytes(int padded) { return (size_t)kFewShares * 2 * kFewRows * (padded + 4) * sizeof(float); }
+size_t many_bytes(int padded) { return (size_t)kShares * 2 * kMostRows * (padded + 4) * sizeof(float); }
 
 template <int DT, int DP>
 hipError_t prompt_dp(const AttnArgs& a, hipStream_t s) {

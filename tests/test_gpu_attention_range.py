@@ -1,10 +1,10 @@
-"""Attention at the ends of what it accepts: pages of several GiB."""
+"""Attention at the ends of what it accepts: pages of several GiB, scores of any size."""
 import numpy as np
 import pytest
 import torch
 
 import attention_checks as ac
-from test_gpu_attention import f64, normal
+from test_gpu_attention import f64, normal, paged_refs, prompt_refs
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.float16, torch.bfloat16]
@@ -35,3 +35,101 @@ def test_places_past_32_bit_offsets_in_a_page(nv, dim, news):
                              torch.tensor([keys], dtype=torch.int32).cuda(), window=window, want_lse=True)
     refs = [ac.attend(f64(q), f64(k), f64(v), dim ** -0.5, window)]
     ac.check(out.cpu(), lse.cpu(), refs, dtype, window, 8.0)
+
+
+# ---------------------------------------------------------------- large scores
+#
+# Scores are whole numbers below 2^24 here (two channels of q and k are whole numbers, the others 0), so
+# binary32 forms them exactly whatever the order, and what is left is the exponent's argument: (s_j - top)
+# scale log2 e with a relative error of at most 3 x 2^-24.  Keys further than 2^21 below the top in weight do
+# not count; for the others that is at most 21 x 3 x 2^-24 < 2^-18 of the weight.
+ARGUMENT = 2.0 ** -18
+
+# the large part of key j's score, in units of 2048
+PATTERNS = {
+    "level": lambda j: 2000 + 0 * j,
+    "negative": lambda j: -2000 + 0 * j,
+    "rising": lambda j: 8 * (j % 250),
+    "falling": lambda j: 8 * (249 - j % 250),
+    "rises late": lambda j: np.where(j % 256 == 150, 2000, 0),
+    "from far below": lambda j: np.where(j < 70, -2000, np.where(j < 140, 0, 3)),
+    "signs": lambda j: np.where(j % 3 == 0, 2000, -2000),
+}
+SCALES = [0, 2, 6, 10, 30, 60, 90]   # log2
+
+
+def whole_numbers(rng, rows, hq, keys, hk, dim, dtype, pattern):
+    q, k = np.zeros((rows, hq, dim)), np.zeros((keys, hk, dim))
+    # large scores of both signs in one wave, and rows without them
+    q[..., 3], q[..., dim - 1] = rng.choice([2048, 2048, 2048, -2048, 0], (rows, hq)), rng.choice([-1, 1, 2], (rows, hq))
+    k[..., 3] = PATTERNS[pattern](np.arange(keys))[:, None]
+    k[..., dim - 1] = rng.integers(-8, 9, (keys, hk))
+    return torch.from_numpy(q).to(dtype), torch.from_numpy(k).to(dtype), normal(rng, (keys, hk, dim), dtype)
+
+
+def exact_scores(refs):
+    return [(o, lse, big, np.where(np.isfinite(lse), ARGUMENT, 0.0)) for o, lse, big, _ in refs]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pattern", PATTERNS)
+def test_prompt_with_large_scores(nv, pattern, dtype):
+    n = 330
+    for dim in (64, 128):
+        rng = np.random.default_rng([42, dim])
+        q, k, v = whole_numbers(rng, n, 4, n, 2, dim, dtype, pattern)
+        for e in SCALES:
+            out, lse = nv.prompt_attn(q.cuda(), k.cuda(), v.cuda(), ac.starts([n]).cuda(), scale=2.0 ** e, want_lse=True)
+            ac.check(out.cpu(), lse.cpu(), exact_scores(prompt_refs(q, k, v, [n], 2.0 ** e)), dtype, n, 8.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pattern", PATTERNS)
+@pytest.mark.parametrize("news,lens", [([1, 5], [2000, 333]), ([1, 70], [300, 900])])
+def test_paged_with_large_scores(nv, news, lens, pattern, dtype):
+    # split over workgroups, whose parts have references of their own
+    dim, page = 64, 16
+    rng = np.random.default_rng([43, sum(news)])
+    parts = [whole_numbers(rng, m, 4, n, 2, dim, dtype, pattern) for m, n in zip(news, lens)]
+    q, ks, vs = torch.cat([x[0] for x in parts]), [x[1] for x in parts], [x[2] for x in parts]
+    table, total = ac.pages_of(lens, page, 3, rng)
+    kc, vc = (ac.fill_cache(x, table, page, total, float("nan")).cuda() for x in (ks, vs))
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    for e in SCALES:
+        out, lse = nv.paged_attn(q.cuda(), kc, vc, table.cuda(), ac.starts(news).cuda(), ln, scale=2.0 ** e, want_lse=True)
+        ac.check(out.cpu(), lse.cpu(), exact_scores(paged_refs(q, ks, vs, news, 2.0 ** e)), dtype, max(lens), 8.0)
+
+
+def winners(q, k, scale):
+    """The key of each row's largest score, that score, and whether no rounding of binary32 can change who
+    wins: the next one is further below than both scores' bounds (see attention_checks) and 2^60 in weight."""
+    n, hq, dim = q.shape
+    best, top, sure, bound = (np.zeros((n, hq), t) for t in (int, float, bool, float))
+    for i in range(n):
+        for h in range(hq):
+            kk = k[:i + 1, h * k.shape[1] // hq]
+            s = scale * (kk @ q[i, h])
+            d = 2.0 ** -24 * (dim + 4) * scale * (np.abs(kk) @ np.abs(q[i, h])).max()
+            best[i, h], top[i, h], bound[i, h] = s.argmax(), s.max(), d
+            sure[i, h] = i == 0 or s.max() - np.partition(s, -2)[-2] > 4 * d + 42
+    return best, top, sure, bound
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size,scale", [(1.0, 2.0 ** 24), (1.0, 2.0 ** 30), (1.0, 2.0 ** 90), (2e4, 128 ** -0.5)])
+def test_one_key_takes_all(nv, size, scale, dtype):
+    # ordinary numbers with a large scale, and large finite numbers with an ordinary one
+    n, dim = 200, 128
+    rng = np.random.default_rng(44)
+    q, k = (torch.from_numpy(np.clip(rng.standard_normal((n, h, dim)) * size, -6e4, 6e4)).to(dtype) for h in (4, 2))
+    v = normal(rng, (n, 2, dim), dtype)
+    out, lse = nv.prompt_attn(q.cuda(), k.cuda(), v.cuda(), ac.starts([n]).cuda(), scale=scale, want_lse=True)
+    best, top, sure, bound = winners(f64(q), f64(k), scale)
+    assert sure.mean() > 0.9
+    want = f64(v)[best, np.arange(4)[None] // 2]
+    u = ac.UNIT[dtype]
+    g, x = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    assert np.isfinite(g).all() and np.isfinite(x).all()
+    # one rounding of the weight and one of the result
+    assert np.all(np.abs(g - want)[sure] <= (2 * u * 1.01 * np.abs(want) + 2.0 ** -24)[sure])
+    assert np.all(np.abs(x - top) <= bound + 2.0 ** -22 * np.abs(top) + np.log(n))
