@@ -14,16 +14,17 @@
 //   m' = max(m, t), l = l 2^{m - m'} + sum 2^{t_j - m'}, O = O 2^{m - m'} + ...
 // in binary32 throughout; only the weights 2^{t - m} are rounded to the
 // inputs' type, because the matrix cores multiply them with the values (l sums
-// the unrounded ones).  The maximum is kept while the new one exceeds it by
-// less than 2^8: the weights then reach at most 2^8, which neither type nor
-// the binary32 sums notice, and the rescaling of O is skipped for most tiles.
+// the unrounded ones).  The maximum is kept while the new one exceeds it by less
+// than 2^8, and the rescaling of O is skipped for most tiles.  m stands kShift
+// above the maximum that it was set to, so that the weights end where their
+// type has room (see kShift).
 //
 // t_j - m is one fma(s_j, scale log2 e, -m): what m's own rounding leaves is the
 // same factor for all keys of a row and cancels in O / l, but it must not leave
 // the exponent's range, and from |m| = 2^28 on half a unit in m's last place
 // does.  A wave that met such a row (|m| >= kBig; no trained model has one)
 // computes its rows again, from a reference r, the largest raw score so far:
-// scores become s_j - r as they come, m stays at 0 and the maximum never lags
+// scores become s_j - r as they come, m stays at kShift and the maximum never lags
 // (see again).
 //
 // Matrix operands (v_mfma_f32_32x32x16, lane = 32 h + c): the score tile is
@@ -52,6 +53,10 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
+// bf16: no weight exceeds 1, so that values near the type's largest do not leave binary32 where the
+// weighted mean does not.
+template <int DT>
+constexpr float kShift = DT == kBf16 ? kKeep : 0.0f;
 constexpr float kBig = 4194304.0f;   // 2^22: a maximum's last place is still half a unit of log2
 
 __device__ const uint4 kZeros[64] = {};   // rows that do not exist are copied from here
@@ -170,7 +175,7 @@ struct Rows {
   v8s q[DP / 16];      // B operand: lane's row, d = 16 st + 8 h ..
   v16f o[DP / 32];     // O^T: d = 32 t + 8 (i / 4) + 4 h + i % 4
   float m, l;          // log2 units; l: this half-wave's keys only
-  float far;           // m + kKeep as a score (before scaling); of a big row its reference
+  float far;           // the score (before scaling) that m is raised at; of a big row its reference
   int lo, hi;          // the row sees the keys lo <= j < hi
   uint64_t late;       // lanes whose row needs a reference
   uint64_t big;        // lanes whose row counts from one
@@ -280,30 +285,30 @@ __device__ __forceinline__ int turns_any(uint64_t lanes) {   // see turns_if
 
 // Raises the maximum to `top` (a score, of both half-waves) where it lags by more than kKeep, and notes
 // the rows that this is not enough for.
-template <int DP>
+template <int DT, int DP>
 __device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc) {
 #pragma unroll 1
   for (int turns = turns_any(__ballot(top > w.far)); turns > 0; --turns) {
-    const float t = top * sc.c, m = __builtin_fmaxf(w.m, t), a = __builtin_amdgcn_exp2f(w.m - m);
+    const float t = __builtin_fmaf(top, sc.c, kShift<DT>), m = __builtin_fmaxf(w.m, t), a = __builtin_amdgcn_exp2f(w.m - m);
     w.late |= __ballot(t > w.m && __builtin_fabsf(t) >= kBig);
     w.m = m;
-    w.far = (m + kKeep) * sc.inv;
+    w.far = (m + (kKeep - kShift<DT>)) * sc.inv;
     rescale(w, a);
   }
 }
 
 // The same with references, which are taken off the scores `s`.
-template <int DP>
+template <int DT, int DP>
 __device__ __forceinline__ void raise(Rows<DP>& w, float top, const Scaling& sc, v16f& s) {
 #pragma unroll 1
   for (int turns = turns_any(__ballot(top > w.far) | w.big); turns > 0; --turns) {
-    const float old = reference(w), t = top * sc.c;
+    const float old = reference(w), t = __builtin_fmaf(top, sc.c, kShift<DT>);
     const bool was = __builtin_amdgcn_inverse_ballot_w64(w.big), is = was || (t > w.m && __builtin_fabsf(t) >= kBig);
     const float ref = was ? __builtin_fmaxf(old, top) : is ? top : 0.0f;
-    const float m = is ? 0.0f : __builtin_fmaxf(w.m, t);
+    const float m = is ? kShift<DT> : __builtin_fmaxf(w.m, t);
     const float a = __builtin_amdgcn_exp2f(above(w.m, old, m, ref, sc.c));
     w.m = m;
-    w.far = is ? ref : (m + kKeep) * sc.inv;
+    w.far = is ? ref : (m + (kKeep - kShift<DT>)) * sc.inv;
     w.big = __ballot(is);
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] -= ref;
@@ -387,8 +392,8 @@ __device__ __forceinline__ void add_keys(Rows<DP>& w, const Lanes<DP>& ln, v16f&
     for (int i = 0; i < 16; ++i) s[i] = (uint32_t)(8 * (i / 4) + i % 4 - lo) < count ? s[i] : -__builtin_inff();
     odd = uni(all_finite<DT, DP>(v_lds, lane) ? 0 : 1);
   }
-  if constexpr (REF) raise(w, both_max(largest(s)), sc, s);
-  else raise(w, both_max(largest(s)), sc);
+  if constexpr (REF) raise<DT>(w, both_max(largest(s)), sc, s);
+  else raise<DT>(w, both_max(largest(s)), sc);
   v8s p[2];
   float sum[2] = {w.l, 0.0f};
 #pragma unroll
@@ -443,7 +448,7 @@ __device__ __forceinline__ void add_tile(Rows<DP>& w, const Lanes<DP>& ln, const
   constexpr int kPer = 16 * kGroups / kScores;              // weights per score product
   constexpr int kShare = 16 * kGroups / (kValues - 2) + 1;  // maxima per value product
   static_assert(kScores % kAhead == 0 && kValues % kAhead == 0 && kPer % 2 == 0, "operand ring");
-  raise(w, top, sc);
+  raise<DT>(w, top, sc);
   uint32_t d[kGroups * 8];
   float sum[2] = {w.l, 0.0f};
   __builtin_amdgcn_sched_barrier(0);

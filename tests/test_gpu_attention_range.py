@@ -1,4 +1,5 @@
-"""Attention at the ends of what it accepts: pages of several GiB, scores of any size."""
+"""Attention at the ends of what it accepts: pages of several GiB, scores of any size, values at the ends of
+their type."""
 import numpy as np
 import pytest
 import torch
@@ -133,3 +134,39 @@ def test_one_key_takes_all(nv, size, scale, dtype):
     # one rounding of the weight and one of the result
     assert np.all(np.abs(g - want)[sure] <= (2 * u * 1.01 * np.abs(want) + 2.0 ** -24)[sure])
     assert np.all(np.abs(x - top) <= bound + 2.0 ** -22 * np.abs(top) + np.log(n))
+
+
+# ---------------------------------------------------------------- values and weights at the ends of their types
+
+def both_ways(nv, q, k, v, scale):
+    """The last row of a prompt (with all its keys) and the same row as a decode step, and the rows before
+    them as one chunk over the cache."""
+    n, hk, dim = k.shape
+    page = 16
+    table, total = ac.pages_of([n], page, 1, np.random.default_rng(45))
+    kc, vc = (ac.fill_cache([x], table, page, total, 0.0).cuda() for x in (k, v))
+    yield n, nv.prompt_attn(q.cuda(), k.cuda(), v.cuda(), ac.starts([n]).cuda(), scale=scale, want_lse=True)
+    for m in (1, 100):
+        yield m, nv.paged_attn(q[-m:].cuda(), kc, vc, table.cuda(), ac.starts([m]).cuda(),
+                               torch.tensor([n], dtype=torch.int32).cuda(), scale=scale, want_lse=True)
+
+
+@pytest.mark.parametrize("size", [3e38, 2.0 ** -118])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_bf16_values_at_the_ends_of_the_range(nv, dim, size):
+    # one value per channel near the largest of the type, and a later key that outweighs all before it by a
+    # factor of 220: less than makes the running maximum follow.  The weighted sum stays below the largest
+    # binary32 as long as no weight exceeds 1.
+    dtype, n = torch.bfloat16, 300
+    rng = np.random.default_rng([46, dim])
+    q, k = torch.zeros((n, 4, dim), dtype=dtype), torch.zeros((n, 2, dim), dtype=dtype)
+    q[:, :, 5] = 1.0
+    k[160, :, 5] = 5.375
+    if size > 1:
+        v = normal(rng, (n, 2, dim), dtype, 1e30)
+        v[160] = torch.from_numpy(rng.choice([-3e38, 3e38], (2, dim))).to(dtype)
+    else:
+        v = normal(rng, (n, 2, dim), dtype, size)
+    for m, (out, lse) in both_ways(nv, q, k, v, 1.0):
+        refs = [ac.attend(f64(q)[-m:], f64(k), f64(v), 1.0)]
+        ac.check(out.cpu(), lse.cpu(), refs, dtype, n, 0.0)
