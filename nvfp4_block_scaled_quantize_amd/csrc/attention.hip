@@ -54,9 +54,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
 // bf16: no weight exceeds 1, so that values near the type's largest do not leave binary32 where the
-// weighted mean does not.
+// weighted mean does not.  fp16: weights reach 2^14 (of 65504), so that those of many keys far below the
+// largest are not lost: the type rounds to 0 what is below 2^-25, here 2^-31 of the largest.
 template <int DT>
-constexpr float kShift = DT == kBf16 ? kKeep : 0.0f;
+constexpr float kShift = DT == kBf16 ? kKeep : -6.0f;
 constexpr float kBig = 4194304.0f;   // 2^22: a maximum's last place is still half a unit of log2
 
 __device__ const uint4 kZeros[64] = {};   // rows that do not exist are copied from here

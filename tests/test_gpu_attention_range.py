@@ -1,5 +1,5 @@
 """Attention at the ends of what it accepts: pages of several GiB, scores of any size, values at the ends of
-their type."""
+their type and weights far below the largest."""
 import numpy as np
 import pytest
 import torch
@@ -170,3 +170,27 @@ def test_bf16_values_at_the_ends_of_the_range(nv, dim, size):
     for m, (out, lse) in both_ways(nv, q, k, v, 1.0):
         refs = [ac.attend(f64(q)[-m:], f64(k), f64(v), 1.0)]
         ac.check(out.cpu(), lse.cpu(), refs, dtype, n, 0.0)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("first", [True, False])
+def test_fp16_weights_far_below_the_largest(nv, first, dim):
+    # 4000 keys whose weight is 2^-25.6 of the largest, which is on a value of 0: together they are the
+    # result.  The rounding of a weight to the type is at most 2^-31 of the largest each.
+    dtype, n = torch.float16, 4000
+    rng = np.random.default_rng([47, dim])
+    q, k = torch.zeros((n, 4, dim), dtype=dtype), torch.zeros((n, 2, dim), dtype=dtype)
+    q[:, :, 7] = 1.0
+    k[:, :, 7] = -25.6
+    top = 0 if first else n - 200
+    k[top, :, 7] = 0.0
+    v = torch.from_numpy(rng.uniform(0.5, 1.0, (n, 2, dim))).to(dtype)
+    v[top] = 0.0
+    u, scale = ac.UNIT[dtype], float(np.log(2.0))
+    for m, (out, lse) in both_ways(nv, q, k, v, scale):
+        rows = min(m, 50)     # the last ones
+        want, want_lse, big, d = ac.attend(f64(q)[-rows:], f64(k), f64(v), scale)
+        tol = 1.05 * (u * np.abs(want) + (u + 2 * d[..., None] + 2.0 ** -21 + 2 * n * 2.0 ** -24) * big) + n * 2.0 ** -31 + \
+            2.0 ** -25
+        assert np.all(np.abs(out[-rows:].cpu().double().numpy() - want) <= tol)
+        assert np.all(np.abs(lse[-rows:].cpu().double().numpy() - want_lse) <= 2 * d + 2.0 ** -20 + n * 2.0 ** -24)
