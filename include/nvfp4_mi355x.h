@@ -432,6 +432,8 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
  * nvfp4_prompt_attn -- whole prompts, packed: request i's tokens are
  * cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (m = L), cu_seqlens[0] = 0; rows past
  * the last prompt get out = 0, lse = -inf.  k, v as q with kv_heads heads.
+ * Requires (tokens * q_heads / kv_heads / 128 + seqs + 1) * kv_heads < 2^24
+ * (EUNSUPPORTED otherwise: the workgroups of one launch).
  */
 int32_t nvfp4_prompt_attn(const void* q, const void* k, const void* v, int32_t dtype, const int32_t* cu_seqlens,
                           int32_t seqs, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,

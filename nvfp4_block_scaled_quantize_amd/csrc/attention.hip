@@ -1664,7 +1664,8 @@ size_t paged_attn_workspace_bytes(int64_t seqs, int64_t tokens, int q_heads, int
   return (needs_few(seqs, tokens, group) ? few_bytes(dim) : 0) + (needs_many(seqs, tokens, group) ? many_bytes(dim) : 0);
 }
 
-bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads <= 0x7FFFFFFFLL; }
+// HIP takes fewer than 2^32 threads in a dimension of the grid.
+bool prompt_attn_fits(const AttnArgs& a) { return prompt_blocks(a) * a.kv_heads * (64 * kPromptWaves) < (1LL << 32); }
 
 hipError_t launch_prompt_attn(const AttnArgs& a, hipStream_t s) {
   const bool wide = padded_dim(a.head_dim) == 128;
