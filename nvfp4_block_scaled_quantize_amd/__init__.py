@@ -596,6 +596,13 @@ def _handle(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _need_32_bits(**numbers):
+    """The C entry points take these as 32-bit integers, and ctypes would cut them without a word."""
+    for name, v in numbers.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError("%s must fit 32 bits, got %d" % (name, v))
+
+
 def _overlap(a, b) -> bool:
     """Whether two dense tensors share memory."""
     x, y, n, m = a.data_ptr(), b.data_ptr(), a.numel() * a.element_size(), b.numel() * b.element_size()
@@ -655,10 +662,14 @@ def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     taken [1]).  `tokens` is the size of the maps (entries past the last token are -1); `taken`
     above len(free_pages) means that pages ran out.  out["kv_lens"] may be ctx_lens itself, which then
     holds the new lengths; other buffers must not overlap."""
+    if page_size >> 31:
+        _need_32_bits(page_size=page_size)
     tokens, dev = int(tokens), _gpu_of(ctx_lens)
     if dev < 0 or not _plain_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out, dev):
         _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out)
-    n = ctx_lens.shape[0]
+    (n, width), (num_free,) = block_table.shape, free_pages.shape
+    if (n | width | num_free) >> 31:
+        _need_32_bits(seqs=n, max_pages=width, num_free=num_free)
     if out is None:
         where = ctx_lens.device
         out = _fresh(stream, lambda: {
@@ -668,7 +679,7 @@ def page_maps(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
             "positions": torch.empty(tokens, dtype=torch.int32, device=where),
             "taken": torch.empty(1, dtype=torch.int32, device=where)})
     st = _lib.nvfp4_page_maps(ctx_lens.data_ptr(), new_lens.data_ptr(), n, block_table.data_ptr(),
-                              block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], page_size, tokens,
+                              width, free_pages.data_ptr(), num_free, page_size, tokens,
                               out["cu_new"].data_ptr(), out["kv_lens"].data_ptr(), out["slot_map"].data_ptr(),
                               out["positions"].data_ptr(), out["taken"].data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
@@ -717,10 +728,13 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: 
     dev = _gpu_of(k)
     if dev < 0 or not _plain_kv_write(k, v, slot_map, k_cache, v_cache, dev):
         _check_kv_write(k, v, slot_map, k_cache, v_cache)
-    T, H, D = k.shape
+    T = k.shape[0]
+    pages, H, page_size, D = k_cache.shape
+    if (H | page_size | D) >> 31:
+        _need_32_bits(kv_heads=H, page_size=page_size, head_dim=D)
     (kt, kh), (vt, vh) = _steps(k), _steps(v)
     st = _lib.nvfp4_kv_write(k.data_ptr(), v.data_ptr(), T, H, D, kt, kh, vt, vh, slot_map.data_ptr(),
-                             k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[2], k_cache.shape[0],
+                             k_cache.data_ptr(), v_cache.data_ptr(), page_size, pages,
                              _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_kv_write")
@@ -770,17 +784,22 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     [tokens, kv_heads, head_dim] (any token and head strides that are multiples of 8), cu_seqlens
     [seqs + 1] int32.  Returns out, or (out, lse) with want_lse or a given lse buffer.  scale
     defaults to head_dim ** -0.5; window > 0 limits a row to the last `window` keys."""
+    if window >> 31:
+        _need_32_bits(window=window)
     dev = _gpu_of(q)
     if dev < 0 or not _plain_prompt_attn(q, k, v, cu_seqlens, out, lse, dev):
         _check_prompt_attn(q, k, v, cu_seqlens, out, lse)
     T, Hq, D = q.shape
+    Hk, starts = k.shape[1], cu_seqlens.shape[0]
+    if (Hq | Hk | starts) >> 31:
+        _need_32_bits(q_heads=Hq, kv_heads=Hk, seqs=starts)
     if out is None:
         out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
     if lse is None and want_lse:
         lse = _fresh(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=q.device))
     (qt, qh), (kt, kh), (vt, vh) = _steps(q), _steps(k), _steps(v)
     st = _lib.nvfp4_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPE_CODE[q.dtype], cu_seqlens.data_ptr(),
-                                cu_seqlens.shape[0] - 1, T, Hq, k.shape[1], D, qt, qh, kt, kh, vt, vh,
+                                starts - 1, T, Hq, Hk, D, qt, qh, kt, kh, vt, vh,
                                 D ** -0.5 if scale is None else scale, window, out.data_ptr(),
                                 None if lse is None else lse.data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
@@ -832,12 +851,16 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     q_heads, head_dim] packed by cu_new [seqs + 1], caches [pages, kv_heads, page_size, head_dim],
     block_table [seqs, max_pages], kv_lens [seqs] (all int32).  Decode steps, chunks of prompts and
     mixtures.  Returns out, or (out, lse) with want_lse or a given lse buffer."""
+    if window >> 31:
+        _need_32_bits(window=window)
     dev = _gpu_of(q)
     if dev < 0 or not _plain_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace, dev):
         _check_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, out, lse, workspace)
     T, Hq, D = q.shape
     pages, Hk, page_size, _ = k_cache.shape
     n, width = block_table.shape
+    if (Hq | Hk | page_size | n | width) >> 31:
+        _need_32_bits(q_heads=Hq, kv_heads=Hk, page_size=page_size, seqs=n, max_pages=width)
     if out is None:
         out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
     if lse is None and want_lse:
