@@ -800,7 +800,7 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     (qt, qh), (kt, kh), (vt, vh) = _steps(q), _steps(k), _steps(v)
     st = _lib.nvfp4_prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPE_CODE[q.dtype], cu_seqlens.data_ptr(),
                                 starts - 1, T, Hq, Hk, D, qt, qh, kt, kh, vt, vh,
-                                D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                (D or 1) ** -0.5 if scale is None else scale, window, out.data_ptr(),
                                 None if lse is None else lse.data_ptr(), _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_prompt_attn")
@@ -869,7 +869,7 @@ def paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     qt, qh = _steps(q)
     st = _lib.nvfp4_paged_attn(q.data_ptr(), _TYPE_CODE[q.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
                                block_table.data_ptr(), cu_new.data_ptr(), kv_lens.data_ptr(), n, T, Hq, Hk, D,
-                               page_size, pages, width, qt, qh, D ** -0.5 if scale is None else scale, window,
+                               page_size, pages, width, qt, qh, (D or 1) ** -0.5 if scale is None else scale, window,
                                out.data_ptr(), None if lse is None else lse.data_ptr(),
                                None if ws is None else ws.data_ptr(), wsb, _handle(stream, dev))
     if st != NVFP4_OK:

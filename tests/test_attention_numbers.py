@@ -41,3 +41,12 @@ def test_wide_shapes_are_refused(nv):
     finally:
         del cache
         torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+def test_head_dimension_of_zero_is_refused(nv):
+    q, cache = torch.zeros((2, 1, 0), dtype=BF16, device="cuda"), torch.zeros((1, 1, 4, 0), dtype=BF16, device="cuda")
+    with pytest.raises(nv.Nvfp4Error):
+        nv.prompt_attn(q, q, q, i32(2).cuda())
+    with pytest.raises(nv.Nvfp4Error):
+        nv.paged_attn(q, cache, cache, i32(2, 1).cuda(), i32(3).cuda(), i32(2).cuda())
