@@ -506,7 +506,6 @@ int32_t nvfp4_prompt_attn(const void* q, const void* k, const void* v, int32_t d
   if (!nvfp4::prompt_attn_fits(a)) return NVFP4_EUNSUPPORTED;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
-  a.num_cus = current_device()->num_cus;
   return hip_status(nvfp4::launch_prompt_attn(a, (hipStream_t)stream));
 }
 

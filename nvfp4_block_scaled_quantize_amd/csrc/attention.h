@@ -79,7 +79,6 @@ struct AttnArgs {
   void* out;                   // [tokens, q_heads, head_dim]
   float* lse;                  // [tokens, q_heads] or null
   void* workspace;             // paged
-  int num_cus;                 // compute units of the current device
   // set by the launchers: q_heads / kv_heads, and its division (see divide)
   int group, group_shift;
   uint32_t group_magic;

@@ -961,7 +961,6 @@ __global__ void __launch_bounds__(64 * kPromptWaves, 2) prompt_attn_kernel(AttnA
         }
         left -= here;
       }
-      if (req < 0) return;   // not reached
     }
   } else {
     int* lds = reinterpret_cast<int*>(dyn_lds);   // before the tiles
