@@ -138,3 +138,32 @@ def test_large_scores(nv, dim, scale, dtype):
     (few, _), (many, _) = shares(news, lens, 0)
     assert few >= 8 and many >= 16
     run(nv, news, lens, dim, 16, 0, dtype, scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_chunk_among_idle_requests(nv, dim, dtype):
+    # no more tokens than requests: the chunk's 240 rows go through the kernel of few rows, in blocks
+    news, lens = [0] * 60 + [60] + [1, 0] * 10, [9] * 60 + [5000] + [900, 33] * 10
+    assert sum(news) <= len(news) and max(news) * HQ // HK > 32 * 7
+    run(nv, news, lens, dim, 16, 0, dtype)
+    run(nv, news, lens, dim, 16, 700, dtype)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("news", [1, 40])
+def test_a_query_that_is_not_finite_stays_in_its_row(nv, news, bad):
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    kc, vc = (torch.empty((40, HK, 16, 64), dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    q = torch.empty((news, HQ, 64), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    table, cu = torch.arange(40, dtype=torch.int32, device="cuda")[None], ac.starts([news]).cuda()
+    n = torch.tensor([633], dtype=torch.int32).cuda()
+    want, want_lse = nv.paged_attn(q, kc, vc, table, cu, n, want_lse=True)
+    q[news // 2, 5, 7] = bad
+    out, lse = nv.paged_attn(q, kc, vc, table, cu, n, want_lse=True)
+    row = torch.zeros((news, HQ), dtype=torch.bool, device="cuda")
+    row[news // 2, 5] = True
+    assert torch.isnan(out[row]).all() and torch.isnan(lse[row]).all()
+    # the others may have had their maximum raised at other keys: equal up to the roundings
+    close = (out.float() - want.float()).abs() <= 2.0 ** -7 * (want.float().abs() + vc.float().abs().max())
+    assert close[~row].all() and ((lse - want_lse).abs() <= 1e-4)[~row].all()
