@@ -418,7 +418,11 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
  * What a row does not see does not reach it, NaN and infinities included.
  * Query head h reads key/value head h / (q_heads / kv_heads).  Scores, maxima,
  * sums and accumulators are binary32; the weights e^{s_j - max} are rounded to
- * the inputs' type for the product with the values.  Deterministic.
+ * the inputs' type for the product with the values (bf16: to 8 bits; fp16: to 11
+ * bits, what is below 2^-31 of the largest to 0).  Deterministic.  Scores may be
+ * of any size that binary32 holds; 32 rows of which some have a largest |s_j|
+ * above 2.9 million take four to six times their time.  What is written
+ * overlaps nothing else that is passed (not checked).
  *
  *   q        : [tokens, q_heads, head_dim], strides in elements (token, head),
  *              multiples of 8; 16-byte aligned

@@ -531,7 +531,8 @@ __device__ __forceinline__ void load_rows(Rows<DP>& w, const AttnArgs& a, const 
 
 // The rows of a wave again, with references: 32 keys at a time, from first_key on every `step`-th such
 // group before end_key.  `lds`: 32 rows of DP elements of the wave's own, for the keys and then the values
-// of a group.  Rare: short rather than fast.
+// of a group.  Rare: short rather than fast (every wave of an 8192-token prompt: 590 -> 2250 us; of 8 decodes
+// over 8192 keys 48 -> 170 us, of 800 new tokens over them 173 -> 918 us).
 template <int DT, int DP, bool PAGED>
 __device__ __forceinline__ void again(Rows<DP>& w, const AttnArgs& a, const Source& s, const Item& it, int row0,
                                       int first_key, int end_key, int step, const Scaling& sc, uint32_t lds) {
@@ -903,10 +904,13 @@ __device__ __forceinline__ int wave_or(int v) {
 // (dispatched round robin) share a head.
 //
 // Bound by the matrix cores and the instructions beside them for long prompts
-// (8192 tokens, 550 GFLOP: 540 .. 555 us, 1.0 PFLOP/s, 0.68 of the rate of a
+// (8192 tokens, 550 GFLOP: 525 .. 555 us, 1.0 PFLOP/s, 0.68 of the rate of a
 // large matrix product; the matrix cores are busy 64 % of the cycles), for short
 // ones by a workgroup's start and end (ragged 8192 tokens, 365 keys a row on
-// average: 84 us with 31 us of products).
+// average: 94 us from memory, 83 where the caches hold part of the inputs, with
+// 33 us of products).  At 128 dimensions 11 to 12 registers are spilled, none of
+// them inside the blocks of 32 products; with rows shorter than 128 one is
+// reloaded in every second tile.
 template <int DT, int DP, bool FULL>
 __global__ void __launch_bounds__(64 * kPromptWaves, 2) prompt_attn_kernel(AttnArgs a) {
   constexpr int NW = kPromptWaves, kRows = 32 * NW, kThreads = 64 * NW, kHold = 4;
@@ -1028,8 +1032,9 @@ __global__ void __launch_bounds__(64 * kPromptWaves, 2) prompt_attn_kernel(AttnA
 // it, its queries, the first copies, its results) counts as kExtra units ahead
 // of its tiles; a share that ends among those has none of the item's work.  A share that starts or ends inside an item
 // leaves a part (O, m, l) in the workspace, and combine_kernel joins the parts.
-// Each workgroup sums the units of all requests itself (one load and one scan
-// for up to 256 requests), which is cheaper than another launch.
+// Each workgroup sums the units of all requests itself (up to 63 requests: one
+// load and one scan in every wave; more: consecutive requests per thread, of
+// which the kernels have 128, 512 and 256), which is cheaper than another launch.
 struct Split {
   int min_rows;   // requests with min_rows <= rows <= max_rows take part
   int max_rows;
@@ -1223,9 +1228,13 @@ __device__ __forceinline__ void for_segments(const AttnArgs& a, const Split& sp,
 }
 
 // ---------------------------------------------------------------- paged: many rows
-// Bound by the matrix cores and the instructions beside them, as prompts are:
-// 1700 new tokens over 16k keys, 515 GFLOP, take 530 .. 550 us, 0.6 of a large
-// matrix product's rate; the joining of the parts 22 us (67 MB written and read).
+// 1700 new tokens over 9k and 16k keys, 515 GFLOP, take 520 .. 550 us, 0.6 of a
+// large matrix product's rate; the joining of the parts 26 us (67 MB written and
+// read).  The matrix cores are busy 48 % of the cycles (a long prompt: 64 %): one
+// workgroup a CU, whose eight waves meet at a barrier every tile, finds a page
+// and forms a 64-bit address for each copy, and the XCDs' L2s fetch the keys and
+// values about three times over.  At 128 dimensions 50 to 55 registers are
+// spilled, none of them inside the blocks of 32 products.
 template <int DT, int DP, bool FULL>
 __global__ void __launch_bounds__(512, 2)
 paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
@@ -1263,9 +1272,9 @@ paged_rows_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // from LDS (scalar loads).
 //
 // Bound by memory where the keys are many: 64 requests of 100 .. 8192 keys (468
-// MB) take 100 us, 4.7 TB/s, with the joining of parts (7 us); 4 requests of 100k
-// keys (1.95 GB) 339 us, 5.8 TB/s, above the 5.1 TB/s of a copy that also writes.
-// One request of 1000 keys takes 10.4 us and 4.6 us to join: latency (lengths,
+// MB) take 102 us, 4.6 TB/s, with the joining of parts (7 us); 4 requests of 100k
+// keys (1.95 GB) 342 us, 5.7 TB/s, above the 5.1 TB/s of a copy that also writes.
+// One request of 1000 keys takes 10.1 us and 5.0 us to join: latency (lengths,
 // split, page ids, one or two tiles, exchange).
 constexpr int kWindow = 256;   // page ids a wave keeps
 constexpr int kFewRows = 32, kFewWaves = 2;
@@ -1454,8 +1463,9 @@ paged_few_kernel(AttnArgs a, Split sp, uint32_t magic, int shift) {
 // other XCDs' L2s, so a load takes most of a microsecond and what counts is
 // that few wait for one another: 8 teams of threads (DP = 128; a team holds a
 // row) either take 8 rows, each reading kBatch parts at a time (ROWS = 256: two
-// or three parts), or every 8th part of one row after another (ROWS = 32: a
-// long request alone has dozens of parts).
+// or three parts where the items are many; a single item has up to SHARES, which
+// are then read in sequence), or every 8th part of one row after another (ROWS =
+// 32: a long request alone has dozens of parts).
 constexpr int kBatch = 4;
 
 // Block (bx, by) of the items of one kind, whose parts are at ws.
