@@ -22,7 +22,7 @@
 // t_j - m is one fma(s_j, scale log2 e, -m): what m's own rounding leaves is the
 // same factor for all keys of a row and cancels in O / l, but it must not leave
 // the exponent's range, and from |m| = 2^28 on half a unit in m's last place
-// does.  A wave that met such a row (|m| >= kBig; no trained model has one)
+// does.  A wave that met such a row (|m| >= kBig, scores of millions)
 // computes its rows again, from a reference r, the largest raw score so far:
 // scores become s_j - r as they come, m stays at kShift and the maximum never lags
 // (see again).
@@ -58,7 +58,7 @@ constexpr float kKeep = 8.0f;   // the maximum may lag by this much (log2)
 // largest are not lost: the type rounds to 0 what is below 2^-25, here 2^-31 of the largest.
 template <int DT>
 constexpr float kShift = DT == kBf16 ? kKeep : -6.0f;
-constexpr float kBig = 4194304.0f;   // 2^22: a maximum's last place is still half a unit of log2
+constexpr float kBig = 4194304.0f;   // 2^22: the steps of a maximum are still half a unit of log2
 
 __device__ const uint4 kZeros[64] = {};   // rows that do not exist are copied from here
 
