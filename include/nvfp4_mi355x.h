@@ -357,6 +357,40 @@ int32_t nvfp4_mx_gemm(const uint8_t* a_tiled, const uint8_t* a_sf_tiled, const f
                       const float* w_gscale, void* y, int64_t B, int64_t N, int64_t K, void* stream);
 
 /*
+ * FP8 operands with a scale per 128 values: E4M3 codes (OCP E4M3FN, one byte)
+ * and binary32 scales, activations one per row and 128 k ([rows, ceil(K/128)]),
+ * weights one per 128 rows and 128 k ([ceil(N/128), ceil(K/128)]).  A value is
+ * code * scale; the last block of a row or column may be shorter.
+ *
+ * nvfp4_fp8_quantize -- per block, over y = the input after the activation of
+ * nvfp4_act_quant (binary32):
+ *   s = max(amax / 448, 2^-126),  code = E4M3_RNE(y * (1 / s))
+ * with correctly rounded division and reciprocal, so no code saturates.  NaN
+ * stays NaN and does not enter amax; a block that holds an infinity has s = inf
+ * (its finite values become 0, the infinity NaN).
+ *   x     : [rows, k] bf16 or fp16, [rows, 2*k] for SWIGLU (gate | up)
+ *   block_rows : 1 (activations) or 128 (weights)
+ *   codes : [rows, k] out; scale : [ceil(rows / block_rows), ceil(k / 128)] out
+ * Requires k % 16 == 0; x not 16-byte or codes not 8-byte aligned take a
+ * scalar path with identical results.
+ */
+int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int32_t act, int32_t block_rows,
+                           uint8_t* codes, float* scale, void* stream);
+/*
+ * nvfp4_fp8_gemm -- y[B, N] = sum_k a[b,k] a_scale[b,k/128] w[n,k] w_scale[n/128,k/128]
+ * (fp16 or bf16 out, rounded once; each K-block's sum and the sum over
+ * K-blocks are binary32).
+ *   a, w       : [B, K], [N, K] E4M3 codes, 16-byte aligned
+ *   a_scale    : [B, ceil(K/128)] float, w_scale : [ceil(N/128), ceil(K/128)] float
+ *   y          : [B, N] of out_dtype, 2-byte aligned (8-byte aligned and N % 4 == 0
+ *                for wide stores)
+ * Requires K % 16 == 0 (EINVAL), K < 2^24, ceil(B/128) * ceil(N/128) <= 2^22
+ * (EUNSUPPORTED).  B == 0 is a no-op.
+ */
+int32_t nvfp4_fp8_gemm(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, void* y,
+                       int32_t out_dtype, int64_t B, int64_t N, int64_t K, void* stream);
+
+/*
  * Serving attention: a paged cache of keys and values, its bookkeeping and
  * writer, and the attention of whole prompts and of new tokens over it.
  *
@@ -408,6 +442,42 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
                        int64_t k_stride, int64_t k_head_stride, int64_t v_stride, int64_t v_head_stride,
                        const int64_t* slot_map, void* k_cache, void* v_cache, int32_t page_size,
                        int64_t num_pages, void* stream);
+
+/*
+ * nvfp4_rope_kv_write -- rotates q and k [tokens, heads, head_dim] by their
+ * positions and appends k and v to the cache.  Pair i < rotary_dim / 2 of a
+ * head's row at position p turns by the angle p * inv_freq[i]:
+ *   (a, b) -> (a c - b s, a s + b c),  c = mscale cos, s = mscale sin
+ * (a, b) = elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved;
+ * elements past rotary_dim stay as they are.  Angles are formed in binary64,
+ * rotated in binary32, rounded once to the inputs' type.
+ *   q, k, v   : strides in elements (token, head), dense last dimension
+ *   positions : [tokens] int32; for a token of a negative position (a padded
+ *               batch) nothing at all is written
+ *   inv_freq  : [rotary_dim / 2] float
+ *   slot_map  : [tokens] int64; a slot outside [0, num_pages * page_size) is
+ *               skipped.  Where two tokens have the same slot, which of their
+ *               bytes stay there is not defined.
+ *   q_out     : rotated q by its strides; may be q itself (with q's strides).
+ *               q_heads may be 0 (q and q_out are not used).
+ *   k_out     : rotated k by its strides, may be k itself; or NULL: k goes to
+ *               the cache only
+ * What is written otherwise overlaps nothing that is passed (not checked).
+ * dtype: the type of q, k, v and of everything written (2-byte elements).
+ * mscale within -2^96 .. 2^96.  Pointers 2-byte, positions and inv_freq 4-byte,
+ * slot_map 8-byte aligned; rows whose parts are not all 16-byte aligned
+ * (rotary_dim % 16, head_dim % 8, strides % 8, pointers) take a 2-byte path.
+ * Requires rotary_dim even, <= head_dim (EINVAL) and <= 512, heads <= 2^16,
+ * (q_heads + 2 kv_heads) * head_dim <= 2^24, tokens < 2^24 (EUNSUPPORTED).
+ */
+int32_t nvfp4_rope_kv_write(const void* q, const void* k, const void* v, int32_t dtype, int64_t tokens,
+                            int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t q_stride,
+                            int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride, int64_t v_stride,
+                            int64_t v_head_stride, const int32_t* positions, const float* inv_freq,
+                            int32_t rotary_dim, int32_t interleaved, float mscale, const int64_t* slot_map,
+                            void* q_out, int64_t q_out_stride, int64_t q_out_head_stride, void* k_out,
+                            int64_t k_out_stride, int64_t k_out_head_stride, void* k_cache, void* v_cache,
+                            int32_t page_size, int64_t num_pages, void* stream);
 
 /*
  * Attention.  Row i of a request's m new tokens over L keys is at position

@@ -29,7 +29,7 @@ EXPORTS = [
     "nvfp4_pretile_weight", "nvfp4_gemm_pretiled", "nvfp4_mx_quantize", "nvfp4_mx_tile",
     "nvfp4_mx_gemm", "nvfp4_moe_w4a16_noalloc", "nvfp4_moe_w4a16_pretiled",
     "nvfp4_page_maps", "nvfp4_kv_write", "nvfp4_prompt_attn", "nvfp4_paged_attn",
-    "nvfp4_paged_attn_workspace_size",
+    "nvfp4_paged_attn_workspace_size", "nvfp4_rope_kv_write", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm",
 ]
 MX_ROWS, MX_TILED = 0, 1
 
@@ -97,6 +97,13 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_paged_attn.restype = i32
     L.nvfp4_paged_attn_workspace_size.argtypes = [i32, i64, i32, i32, i32]
     L.nvfp4_paged_attn_workspace_size.restype = sz
+    L.nvfp4_rope_kv_write.argtypes = [p, p, p, i32, i64, i32, i32, i32, i64, i64, i64, i64, i64, i64, p, p, i32, i32,
+                                      f32, p, p, i64, i64, p, i64, i64, p, p, i32, i64, p]
+    L.nvfp4_rope_kv_write.restype = i32
+    L.nvfp4_fp8_quantize.argtypes = [p, i32, i64, i64, i32, i32, p, p, p]
+    L.nvfp4_fp8_quantize.restype = i32
+    L.nvfp4_fp8_gemm.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p]
+    L.nvfp4_fp8_gemm.restype = i32
     return L
 
 
@@ -538,7 +545,7 @@ def mx_gemm(a: dict, a_g: torch.Tensor, w: dict, w_g: torch.Tensor, a_group_rows
     return y
 
 
-# ---------------------------------------------------------------- serving attention
+# ---------------------------------------------------------------- calls of a few microseconds
 #
 # A decode step's kernels take a few microseconds, about as long as checking their operands one by
 # one in Python.  Each call therefore first asks one plain question -- are the operands what they are
@@ -608,6 +615,104 @@ def _overlap(a, b) -> bool:
     x, y, n, m = a.data_ptr(), b.data_ptr(), a.numel() * a.element_size(), b.numel() * b.element_size()
     return n > 0 and m > 0 and x < y + m and y < x + n
 
+
+# ---------------------------------------------------------------- FP8, a scale per 128
+
+_FP8 = torch.float8_e4m3fn
+
+
+def _check_fp8_quantize(x, k, block_rows, out):
+    _need_2d(x, "x")
+    _dtype_code(x)
+    rows = x.shape[0]
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128, got %s" % (block_rows,))
+    if out is not None:
+        _dense(out.get("codes"), "out['codes']", _FP8, (rows, k))
+        _dense(out.get("scale"), "out['scale']", torch.float32, (-(-rows // block_rows), -(-k // 128)))
+    _need_gpu(x, *(() if out is None else (out["codes"], out["scale"])))
+
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1, act: str = "none", out: dict | None = None,
+                 stream=None) -> dict:
+    """E4M3 quantization of x [rows, k] (bfloat16 or float16; [rows, 2 k] for act="swiglu") with one float32
+    scale per 128 values of a row (block_rows=1: activations) or per 128 x 128 values (block_rows=128:
+    weights), with the optional activation in front.  Returns dict(codes [rows, k] float8_e4m3fn, scale
+    [ceil(rows / block_rows), ceil(k / 128)] float32)."""
+    a = ACT[act] if isinstance(act, str) else int(act)
+    dev = _gpu_of(x)
+    try:
+        rows, k_in = x.shape
+        k = k_in // 2 if a == 1 else k_in
+        plain = (dev >= 0 and x.dtype in _TYPE_CODE and x.is_contiguous() and (block_rows == 1 or block_rows == 128) and
+                 (out is None or (_is(out["codes"], _FP8, (rows, k), dev) and
+                                  _is(out["scale"], torch.float32, (-(-rows // block_rows), -(-k // 128)), dev))))
+    except (AttributeError, KeyError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        _need_2d(x, "x")
+        k_in = x.shape[1]
+        k = k_in // 2 if a == 1 else k_in
+        _check_fp8_quantize(x, k, block_rows, out)
+    if a == 1 and k_in % 2:
+        raise ValueError("x must hold a gate and an up half for swiglu, got %d columns" % k_in)
+    if out is None:
+        out = _fresh(stream, lambda: {
+            "codes": torch.empty((rows, k), dtype=_FP8, device=x.device),
+            "scale": torch.empty((-(-rows // block_rows), -(-k // 128)), dtype=torch.float32, device=x.device)})
+    st = _lib.nvfp4_fp8_quantize(x.data_ptr(), _TYPE_CODE[x.dtype], rows, k, a, block_rows, out["codes"].data_ptr(),
+                                 out["scale"].data_ptr(), _handle(stream, dev))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_fp8_quantize")
+    return out
+
+
+def _check_fp8_gemm(a, a_scale, w, w_scale, out):
+    _need_2d(a, "a")
+    _need_2d(w, "w")
+    (B, K), N = a.shape, w.shape[0]
+    _dense(a, "a", _FP8, (B, K))
+    _dense(w, "w", _FP8, (N, K))
+    _dense(a_scale, "a_scale", torch.float32, (B, -(-K // 128)))
+    _dense(w_scale, "w_scale", torch.float32, (-(-N // 128), -(-K // 128)))
+    if out is not None:
+        _need_2d(out, "out")
+        _dtype_code(out)
+        _dense(out, "out", out.dtype, (B, N))
+    _need_gpu(a, a_scale, w, w_scale, out)
+
+
+def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+             out_dtype: torch.dtype = torch.float16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[B, N] = sum_k a[b, k] a_scale[b, k / 128] w[n, k] w_scale[n / 128, k / 128] for float8_e4m3fn a [B, K]
+    and w [N, K] with float32 scales (fp8_quantize with block_rows 1 and 128, or a checkpoint's).
+    float16 or bfloat16 out (out_dtype, or the type of `out`)."""
+    dev = _gpu_of(a)
+    f32 = torch.float32
+    try:
+        (B, K), (N, K2) = a.shape, w.shape
+        nkb = -(-K // 128)
+        plain = (dev >= 0 and K == K2 and _is(a, _FP8, (B, K), dev) and _is(w, _FP8, (N, K), dev) and
+                 _is(a_scale, f32, (B, nkb), dev) and _is(w_scale, f32, (-(-N // 128), nkb), dev) and
+                 (out is None or (out.dtype in _TYPE_CODE and _is(out, out.dtype, (B, N), dev))))
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        _check_fp8_gemm(a, a_scale, w, w_scale, out)
+    if out is None:
+        if out_dtype not in _TYPE_CODE:
+            raise TypeError("out_dtype must be bfloat16 or float16")
+        out = _fresh(stream, lambda: torch.empty((B, N), dtype=out_dtype, device=a.device))
+    st = _lib.nvfp4_fp8_gemm(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
+                             _TYPE_CODE[out.dtype], B, N, K, _handle(stream, dev))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_fp8_gemm")
+    return out
+
+
+# ---------------------------------------------------------------- serving attention
 
 def _check_page_maps(ctx_lens, new_lens, block_table, free_pages, tokens, out):
     if not isinstance(ctx_lens, torch.Tensor) or ctx_lens.dim() != 1:
@@ -696,7 +801,7 @@ def _check_caches(k_cache, v_cache, dtype):
     _dense(v_cache, "v_cache", dtype, k_cache.shape)
 
 
-def _check_kv_write(k, v, slot_map, k_cache, v_cache):
+def _check_kv_operands(k, v, slot_map, k_cache, v_cache):
     _need_heads(k, "k")
     _need_heads(v, "v")
     _dtype_code(k)
@@ -706,6 +811,10 @@ def _check_kv_write(k, v, slot_map, k_cache, v_cache):
     if (k_cache.shape[1], k_cache.shape[3]) != (H, D):
         raise ValueError("the cache holds %d heads of %d, k has %d of %d" % (k_cache.shape[1], k_cache.shape[3], H, D))
     _dense(slot_map, "slot_map", torch.int64, (T,))
+
+
+def _check_kv_write(k, v, slot_map, k_cache, v_cache):
+    _check_kv_operands(k, v, slot_map, k_cache, v_cache)
     _need_gpu(k, v, slot_map, k_cache, v_cache)
 
 
@@ -738,6 +847,79 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: 
                              _handle(stream, dev))
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_kv_write")
+
+
+def _check_rope(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out, k_out):
+    _check_kv_operands(k, v, slot_map, k_cache, v_cache)
+    T, _, D = k.shape
+    if q is not None:
+        _need_heads(q, "q")
+        _need(q, "q", k.dtype, (T, q.shape[1], D))
+    _dense(positions, "positions", torch.int32, (T,))
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D tensor of half the rotary dimension")
+    _dense(inv_freq, "inv_freq", torch.float32, inv_freq.shape)
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is None:
+            continue
+        if like is None:
+            raise ValueError("%s needs its input" % name)
+        _need_heads(t, name)
+        _need(t, name, k.dtype, like.shape)
+        if t.data_ptr() == like.data_ptr() and _steps(t) != _steps(like) and t.numel() > 0:
+            raise ValueError("%s in the place of its input must have its strides" % name)
+    _need_gpu(k, v, slot_map, k_cache, v_cache, q, positions, inv_freq, q_out, k_out)
+
+
+def _plain_rope(q, k, positions, inv_freq, q_out, k_out, dev) -> bool:
+    try:
+        dt, (T, _, D) = k.dtype, k.shape
+        for x, y in ((q, q_out), (k, k_out)):
+            if x is not None and not (x.dtype is dt and x.shape == (T, x.shape[1], D) and x.stride(2) == 1 and
+                                      x.get_device() == dev):
+                return False
+            if y is not None and not (x is not None and y.dtype is dt and y.shape == x.shape and y.stride(2) == 1 and
+                                      y.get_device() == dev and (y.data_ptr() != x.data_ptr() or _steps(y) == _steps(x))):
+                return False
+        return (_is(positions, torch.int32, (T,), dev) and
+                _is(inv_freq, torch.float32, (inv_freq.shape[0],), dev))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
+
+
+def rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                  inv_freq: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  interleaved: bool = False, mscale: float = 1.0, q_out: torch.Tensor | None = None,
+                  k_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Rotates q [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] by positions [tokens]
+    int32 and inv_freq [rotary_dim / 2] float32, and writes k and v to their slots of the caches
+    [pages, kv_heads, page_size, head_dim], in one launch.  Pairs are (i, i + rotary_dim / 2), or
+    (2 i, 2 i + 1) with `interleaved`; cosine and sine are multiplied by mscale.  Returns q_out (new unless
+    given; may be q itself); k_out (may be k itself) receives the rotated keys too.  Nothing is written for
+    tokens of a negative position (in a new q_out their rows are undefined); slots outside the cache are
+    skipped.  q may be None."""
+    dev = _gpu_of(k)
+    if dev < 0 or not (_plain_kv_write(k, v, slot_map, k_cache, v_cache, dev) and
+                       _plain_rope(q, k, positions, inv_freq, q_out, k_out, dev)):
+        _check_rope(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out, k_out)
+    T, Hk, D = k.shape
+    pages, _, page_size, _ = k_cache.shape
+    half, Hq = inv_freq.shape[0], 0 if q is None else q.shape[1]
+    if (Hq | Hk | page_size | D | 2 * half) >> 31:
+        _need_32_bits(q_heads=Hq, kv_heads=Hk, page_size=page_size, head_dim=D, rotary_dim=2 * half)
+    if q is not None and q_out is None:
+        q_out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
+    (qt, qh), (kt, kh), (vt, vh) = (0, 0) if q is None else _steps(q), _steps(k), _steps(v)
+    (qot, qoh), (kot, koh) = ((0, 0) if t is None else _steps(t) for t in (q_out, k_out))
+    st = _lib.nvfp4_rope_kv_write(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
+                                  T, Hq, Hk, D, qt, qh, kt, kh, vt, vh, positions.data_ptr(), inv_freq.data_ptr(),
+                                  2 * half, 1 if interleaved else 0, mscale, slot_map.data_ptr(),
+                                  None if q_out is None else q_out.data_ptr(), qot, qoh,
+                                  None if k_out is None else k_out.data_ptr(), kot, koh,
+                                  k_cache.data_ptr(), v_cache.data_ptr(), page_size, pages, _handle(stream, dev))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_rope_kv_write")
+    return q_out
 
 
 def _check_attn_out(q, out, lse):

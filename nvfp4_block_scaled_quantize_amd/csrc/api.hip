@@ -8,6 +8,7 @@
 
 #include "../../include/nvfp4_mi355x.h"
 #include "attention.h"
+#include "fp8.h"
 #include "internal.h"
 
 namespace {
@@ -463,6 +464,81 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
   nvfp4::KvWriteArgs a{k, v, tokens, kv_heads, head_dim, k_stride, k_head_stride, v_stride, v_head_stride,
                        slot_map, k_cache, v_cache, page_size, num_pages};
   return hip_status(nvfp4::launch_kv_write(a, (hipStream_t)stream));
+}
+
+int32_t nvfp4_rope_kv_write(const void* q, const void* k, const void* v, int32_t dtype, int64_t tokens,
+                            int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t q_stride,
+                            int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride, int64_t v_stride,
+                            int64_t v_head_stride, const int32_t* positions, const float* inv_freq,
+                            int32_t rotary_dim, int32_t interleaved, float mscale, const int64_t* slot_map,
+                            void* q_out, int64_t q_out_stride, int64_t q_out_head_stride, void* k_out,
+                            int64_t k_out_stride, int64_t k_out_head_stride, void* k_cache, void* v_cache,
+                            int32_t page_size, int64_t num_pages, void* stream) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_FP16) return NVFP4_EINVAL;
+  if (tokens < 0 || q_heads < 0 || kv_heads < 1 || head_dim < 2 || page_size < 1 || num_pages < 0) return NVFP4_EINVAL;
+  if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2 != 0) return NVFP4_EINVAL;
+  if (!(mscale >= -0x1p96f && mscale <= 0x1p96f)) return NVFP4_EINVAL;
+  if (q_stride < 0 || q_head_stride < 0 || k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0 ||
+      q_out_stride < 0 || q_out_head_stride < 0 || k_out_stride < 0 || k_out_head_stride < 0)
+    return NVFP4_EINVAL;
+  if (rotary_dim > 512 || q_heads > 65536 || kv_heads > 65536 ||
+      ((int64_t)q_heads + 2 * (int64_t)kv_heads) * head_dim > (1 << 24) || tokens >= (1 << 24) ||
+      num_pages > (1LL << 50) / page_size)
+    return NVFP4_EUNSUPPORTED;
+  if (tokens == 0) return NVFP4_OK;
+  if (!k || !v || !positions || !inv_freq || !slot_map || (q_heads > 0 && (!q || !q_out)) ||
+      (num_pages > 0 && (!k_cache || !v_cache)))
+    return NVFP4_EINVAL;
+  if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)k_cache |
+        (uintptr_t)v_cache) % 2) != 0 || !aligned4(positions) || !aligned4(inv_freq) || ((uintptr_t)slot_map % 8) != 0)
+    return NVFP4_EINVAL;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::RopeKvArgs a{};
+  a.q = q; a.k = k; a.v = v; a.dtype = dtype; a.tokens = tokens; a.q_heads = q_heads; a.kv_heads = kv_heads;
+  a.head_dim = head_dim; a.q_stride = q_stride; a.q_head_stride = q_head_stride; a.k_stride = k_stride;
+  a.k_head_stride = k_head_stride; a.v_stride = v_stride; a.v_head_stride = v_head_stride; a.positions = positions;
+  a.inv_freq = inv_freq; a.rotary_dim = rotary_dim; a.interleaved = interleaved ? 1 : 0; a.mscale = mscale;
+  a.slot_map = slot_map; a.q_out = q_out; a.qo_stride = q_out_stride; a.qo_head_stride = q_out_head_stride;
+  a.k_out = k_out; a.ko_stride = k_out_stride; a.ko_head_stride = k_out_head_stride; a.k_cache = k_cache;
+  a.v_cache = v_cache; a.page_size = page_size; a.num_pages = num_pages;
+  return hip_status(nvfp4::launch_rope_kv(a, (hipStream_t)stream));
+}
+
+int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int32_t act, int32_t block_rows,
+                           uint8_t* codes, float* scale, void* stream) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_FP16) return NVFP4_EINVAL;
+  if (act != NVFP4_ACT_NONE && act != NVFP4_ACT_SWIGLU && act != NVFP4_ACT_RELU2) return NVFP4_EINVAL;
+  if (rows < 0 || k <= 0 || k % 16 != 0 || (block_rows != 1 && block_rows != 128)) return NVFP4_EINVAL;
+  if (rows == 0) return NVFP4_OK;
+  if (!x || !codes || !scale || ((uintptr_t)x % 2) != 0 || !aligned4(scale)) return NVFP4_EINVAL;
+  // one launch: fewer than 2^32 threads
+  const int64_t nkb = (k + 127) / 128;
+  if (k > (1LL << 30) || rows > (1LL << 37)) return NVFP4_EUNSUPPORTED;
+  if (block_rows == 1 ? rows > ((1LL << 30) - (1 << 16)) / nkb : (rows + 127) / 128 > ((1LL << 24) - 1) / nkb)
+    return NVFP4_EUNSUPPORTED;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::Fp8QuantArgs a{x, dtype, act, rows, (int)k, block_rows, codes, scale};
+  return hip_status(nvfp4::launch_fp8_quantize(a, (hipStream_t)stream));
+}
+
+int32_t nvfp4_fp8_gemm(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, void* y,
+                       int32_t out_dtype, int64_t B, int64_t N, int64_t K, void* stream) {
+  if (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_FP16) return NVFP4_EINVAL;
+  if (B < 0 || N <= 0 || K <= 0 || K % 16 != 0) return NVFP4_EINVAL;
+  if (B == 0) return NVFP4_OK;
+  if (!a || !a_scale || !w || !w_scale || !y) return NVFP4_EINVAL;
+  if ((((uintptr_t)a | (uintptr_t)w) % 16) != 0 || !aligned4(a_scale) || !aligned4(w_scale) || ((uintptr_t)y % 2) != 0)
+    return NVFP4_EINVAL;
+  // offsets inside a tile of 256 rows are 32 bits; tiles are counted in 24 bits
+  if (K >= (1 << 24) || B > (1 << 30) || N > (1 << 30) ||
+      ((B + 127) / 128) * ((N + 127) / 128) > (1 << 22))
+    return NVFP4_EUNSUPPORTED;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::Fp8GemmArgs g{a, a_scale, w, w_scale, y, out_dtype, (int)B, (int)N, (int)K};
+  return hip_status(nvfp4::launch_fp8_gemm(g, (hipStream_t)stream));
 }
 
 // Checks shared by both attention entry points.

@@ -62,6 +62,35 @@ struct KvWriteArgs {
 };
 hipError_t launch_kv_write(const KvWriteArgs& a, hipStream_t s);
 
+// Rotation of queries and keys by position, with the keys and values appended to the cache.
+struct RopeKvArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int dtype;
+  int64_t tokens;
+  int q_heads, kv_heads, head_dim;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;   // elements
+  const int32_t* positions;
+  const float* inv_freq;       // [rotary_dim / 2]
+  int rotary_dim, interleaved;
+  float mscale;
+  const int64_t* slot_map;
+  void* q_out;
+  int64_t qo_stride, qo_head_stride;
+  void* k_out;                 // may be null
+  int64_t ko_stride, ko_head_stride;
+  void* k_cache;
+  void* v_cache;
+  int page_size;
+  int64_t num_pages;
+  // set by the launcher
+  int tokens_each, items_row, items_token;
+  uint32_t half_magic, token_magic, row_magic;   // divisions (see divide)
+  int half_shift, token_shift, row_shift;
+};
+hipError_t launch_rope_kv(const RopeKvArgs& a, hipStream_t s);
+
 struct AttnArgs {
   const void* q;               // [tokens, q_heads, head_dim] by strides
   const void* k;               // prompt: [tokens, kv_heads, head_dim] by strides; paged: the cache
