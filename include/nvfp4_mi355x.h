@@ -292,6 +292,42 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
                                 int32_t norm_topk_prob, float routed_scaling, void* stream);
 
 /*
+ * nvfp4_moe_decode -- a whole routed MoE layer for up to 32 tokens (a decode
+ * step), on the expert weights of nvfp4_moe_w4a16: the router product, its
+ * selection, the experts and the weighted sum, in few launches.
+ *   x, router       : [tokens, hidden], [experts, hidden], fp16 or bf16 (dtype)
+ *   correction_bias : [experts] float (used for selection only)
+ *   w1, w1_sf, w1_g : fc1 [experts, R, hidden] in NVFP4 (codes, E4M3 bytes, [experts]
+ *                     globals), R = inter for RELU2, 2 * inter for SWIGLU (gate
+ *                     rows, then up rows)
+ *   w2, w2_sf, w2_g : fc2 [experts, hidden, inter]
+ *   tiled           : 0 = plain layout, 1 = pre-tiled (nvfp4_pretile_weight of the
+ *                     stacked matrices, as for nvfp4_moe_w4a16_pretiled)
+ *   out             : [tokens, hidden] of x's type
+ *   topk_ids_out, topk_w_out : [tokens, top_k] int32 / float, or NULL
+ *   act             : NVFP4_ACT_RELU2 or NVFP4_ACT_SWIGLU
+ * logits = x . router^T (binary32 sums); the selection is that of
+ * nvfp4_moe_w4a16 (a NaN ranks below every number).  out = sum_j w_j act(x W1_j^T)
+ * W2_j^T, everything between x and out in binary32 but for the operands of the matrix
+ * instructions: x (bf16) and the activations are carried in FP16 after an
+ * exact scaling to the token's largest, the activations in two parts (22 bits).
+ * Deterministic; a token's result does not depend on the others.
+ * Requires experts <= 256, top_k <= 16, hidden % 64 == 0, inter % 64 == 0
+ * (% 128 with tiled), groups as for nvfp4_moe_w4a16; x, router, w1, w2 16-byte, out 8-byte,
+ * scales 2-byte aligned (EINVAL otherwise); tokens <= 32, hidden and inter
+ * <= 65536 (EUNSUPPORTED).  workspace: nvfp4_moe_decode_workspace_size bytes,
+ * 256-byte aligned, contents before the call do not matter; calls that may
+ * overlap in time need workspaces of their own.
+ */
+int32_t nvfp4_moe_decode(const void* x, int32_t dtype, const void* router, const float* correction_bias,
+                         const uint8_t* w1, const uint8_t* w1_sf, const float* w1_g, const uint8_t* w2,
+                         const uint8_t* w2_sf, const float* w2_g, int32_t tiled, void* out, int32_t* topk_ids_out,
+                         float* topk_w_out, int32_t tokens, int32_t experts, int32_t top_k, int32_t hidden,
+                         int32_t inter, int32_t act, int32_t n_group, int32_t topk_group, int32_t norm_topk_prob,
+                         float routed_scaling, void* workspace, size_t workspace_bytes, void* stream);
+size_t nvfp4_moe_decode_workspace_size(int32_t tokens, int32_t experts, int32_t top_k, int32_t hidden, int32_t inter);
+
+/*
  * MXFP4 variant -- the UE8M0_SF switch of the block helper in "perf: optimize
  * per-token nvfp4 quantization kernel" (review): 32-element K-blocks whose
  * scale is one E8M0 byte b (value 2^(b-127)), the format gfx950's block-scaled

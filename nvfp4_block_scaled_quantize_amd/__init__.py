@@ -30,6 +30,7 @@ EXPORTS = [
     "nvfp4_mx_gemm", "nvfp4_moe_w4a16_noalloc", "nvfp4_moe_w4a16_pretiled",
     "nvfp4_page_maps", "nvfp4_kv_write", "nvfp4_prompt_attn", "nvfp4_paged_attn",
     "nvfp4_paged_attn_workspace_size", "nvfp4_rope_kv_write", "nvfp4_fp8_quantize", "nvfp4_fp8_gemm",
+    "nvfp4_moe_decode", "nvfp4_moe_decode_workspace_size",
 ]
 MX_ROWS, MX_TILED = 0, 1
 
@@ -104,6 +105,11 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_fp8_quantize.restype = i32
     L.nvfp4_fp8_gemm.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p]
     L.nvfp4_fp8_gemm.restype = i32
+    L.nvfp4_moe_decode.argtypes = [p, i32, p, p, p, p, p, p, p, p, i32, p, p, p, i32, i32, i32, i32, i32, i32, i32, i32,
+                                   i32, f32, p, sz, p]
+    L.nvfp4_moe_decode.restype = i32
+    L.nvfp4_moe_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    L.nvfp4_moe_decode_workspace_size.restype = sz
     return L
 
 
@@ -710,6 +716,87 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: t
     if st != NVFP4_OK:
         raise Nvfp4Error(st, "nvfp4_fp8_gemm")
     return out
+
+
+# ---------------------------------------------------------------- MoE layer of a decode step
+
+@functools.lru_cache(maxsize=1024)
+def moe_decode_workspace_size(tokens: int, experts: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(_lib.nvfp4_moe_decode_workspace_size(tokens, experts, top_k, hidden, inter))
+
+
+def _check_moe_decode(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, gated, out, workspace):
+    _need_2d(x, "x")
+    _dtype_code(x)
+    _need_2d(router, "router")
+    (T, hidden), E = x.shape, router.shape[0]
+    _dense(x, "x", x.dtype, (T, hidden))
+    _dense(router, "router", x.dtype, (E, hidden))
+    _dense(bias, "bias", torch.float32, (E,))
+    if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+        raise ValueError("w2 must be a 3-D tensor [experts, hidden, inter/2]")
+    inter = 2 * w2.shape[2]
+    rows = 2 * inter if gated else inter
+    _dense(w1, "w1", torch.uint8, (E, rows, hidden // 2))
+    _dense(w1_sf, "w1_sf", torch.uint8, (E, rows, hidden // 16))
+    _dense(w1_g, "w1_g", torch.float32, (E,))
+    _dense(w2, "w2", torch.uint8, (E, hidden, inter // 2))
+    _dense(w2_sf, "w2_sf", torch.uint8, (E, hidden, inter // 16))
+    _dense(w2_g, "w2_g", torch.float32, (E,))
+    if out is not None:
+        _dense(out, "out", x.dtype, (T, hidden))
+    _need_gpu(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, out, workspace)
+
+
+def _plain_moe_decode(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, gated, out, workspace, dev) -> bool:
+    try:
+        dt, u8, f32 = x.dtype, torch.uint8, torch.float32
+        (T, hidden), (E, _) = x.shape, router.shape
+        inter = 2 * w2.shape[2]
+        rows = 2 * inter if gated else inter
+        return (dt in _TYPE_CODE and _is(x, dt, (T, hidden), dev) and _is(router, dt, (E, hidden), dev) and
+                _is(bias, f32, (E,), dev) and _is(w1, u8, (E, rows, hidden // 2), dev) and
+                _is(w1_sf, u8, (E, rows, hidden // 16), dev) and _is(w1_g, f32, (E,), dev) and
+                _is(w2, u8, (E, hidden, inter // 2), dev) and _is(w2_sf, u8, (E, hidden, inter // 16), dev) and
+                _is(w2_g, f32, (E,), dev) and (out is None or _is(out, dt, (T, hidden), dev)) and
+                (workspace is None or workspace.get_device() == dev))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
+
+
+def moe_decode(x: torch.Tensor, router: torch.Tensor, bias: torch.Tensor, w1: torch.Tensor, w1_sf: torch.Tensor,
+               w1_g: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, w2_g: torch.Tensor, top_k: int,
+               n_group: int = 1, topk_group: int = 1, norm_topk_prob: bool = True, routed_scaling: float = 1.0,
+               act: str = "relu2", tiled: bool = False, out: torch.Tensor | None = None, want_routing: bool = False,
+               workspace: torch.Tensor | None = None, stream=None):
+    """A whole MoE layer for up to 32 tokens: x [tokens, hidden] and router [experts, hidden] (float16 or
+    bfloat16), the expert weights of moe_w4a16() (or, with `tiled`, of moe_pretile_weights()); for act="swiglu" w1
+    holds [experts, 2 inter, ...] gate and up rows.  Returns out [tokens, hidden] of x's type, or (out, ids,
+    weights) with want_routing."""
+    a = ACT[act] if isinstance(act, str) else int(act)
+    gated = a == ACT["swiglu"]
+    dev = _gpu_of(x)
+    if dev < 0 or not _plain_moe_decode(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, gated, out, workspace, dev):
+        _check_moe_decode(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, gated, out, workspace)
+    (T, hidden), E, inter = x.shape, router.shape[0], 2 * w2.shape[2]
+    if (T | hidden | E | inter | top_k | n_group | topk_group) >> 31:
+        _need_32_bits(tokens=T, hidden=hidden, experts=E, inter=inter, top_k=top_k, n_group=n_group, topk_group=topk_group)
+    if out is None:
+        out = _fresh(stream, lambda: torch.empty((T, hidden), dtype=x.dtype, device=x.device))
+    ids = wts = None
+    if want_routing:
+        ids, wts = _fresh(stream, lambda: (torch.empty((T, top_k), dtype=torch.int32, device=x.device),
+                                           torch.empty((T, top_k), dtype=torch.float32, device=x.device)))
+    ws, wsb = _fresh(stream, lambda: _workspace(moe_decode_workspace_size(T, E, top_k, hidden, inter), x.device, workspace))
+    st = _lib.nvfp4_moe_decode(x.data_ptr(), _TYPE_CODE[x.dtype], router.data_ptr(), bias.data_ptr(), w1.data_ptr(),
+                               w1_sf.data_ptr(), w1_g.data_ptr(), w2.data_ptr(), w2_sf.data_ptr(), w2_g.data_ptr(),
+                               1 if tiled else 0, out.data_ptr(), None if ids is None else ids.data_ptr(),
+                               None if wts is None else wts.data_ptr(), T, E, top_k, hidden, inter, a, n_group,
+                               topk_group, 1 if norm_topk_prob else 0, routed_scaling,
+                               None if ws is None else ws.data_ptr(), wsb, _handle(stream, dev))
+    if st != NVFP4_OK:
+        raise Nvfp4Error(st, "nvfp4_moe_decode")
+    return (out, ids, wts) if want_routing else out
 
 
 # ---------------------------------------------------------------- serving attention

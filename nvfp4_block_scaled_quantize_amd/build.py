@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4_mi355x.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "moe.hip", "mx_gemm.hip",
-           "kv_cache.hip", "attention.hip", "rope_kv.hip", "fp8_quantize.hip", "fp8_gemm.hip"]
+           "kv_cache.hip", "attention.hip", "rope_kv.hip", "fp8_quantize.hip", "fp8_gemm.hip", "moe_decode.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

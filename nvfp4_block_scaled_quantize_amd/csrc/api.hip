@@ -10,6 +10,7 @@
 #include "attention.h"
 #include "fp8.h"
 #include "internal.h"
+#include "moe_decode.h"
 
 namespace {
 
@@ -408,6 +409,48 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
                    topk_group, norm_topk_prob ? 1 : 0, routed_scaling, scratch, scratch_bytes,
                    current_device()->num_cus, 0};
   return hip_status(nvfp4::launch_moe(m, (hipStream_t)stream));
+}
+
+static bool moe_decode_sizes(int32_t tokens, int32_t experts, int32_t top_k, int32_t hidden, int32_t inter) {
+  return tokens >= 0 && experts >= 1 && experts <= 256 && top_k >= 1 && top_k <= 16 && top_k <= experts && hidden >= 64 &&
+         hidden % 64 == 0 && inter >= 64 && inter % 64 == 0;
+}
+
+size_t nvfp4_moe_decode_workspace_size(int32_t tokens, int32_t experts, int32_t top_k, int32_t hidden, int32_t inter) {
+  if (!moe_decode_sizes(tokens, experts, top_k, hidden, inter) || tokens < 1 || tokens > nvfp4::kMoeDecodeMaxTokens ||
+      hidden > 65536 || inter > 65536)
+    return 0;
+  return nvfp4::moe_decode_workspace_bytes(tokens, experts, top_k, hidden, inter);
+}
+
+int32_t nvfp4_moe_decode(const void* x, int32_t dtype, const void* router, const float* correction_bias,
+                         const uint8_t* w1, const uint8_t* w1_sf, const float* w1_g, const uint8_t* w2,
+                         const uint8_t* w2_sf, const float* w2_g, int32_t tiled, void* out, int32_t* topk_ids_out,
+                         float* topk_w_out, int32_t tokens, int32_t experts, int32_t top_k, int32_t hidden,
+                         int32_t inter, int32_t act, int32_t n_group, int32_t topk_group, int32_t norm_topk_prob,
+                         float routed_scaling, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_FP16) return NVFP4_EINVAL;
+  if (act != NVFP4_ACT_SWIGLU && act != NVFP4_ACT_RELU2) return NVFP4_EINVAL;
+  if (!moe_decode_sizes(tokens, experts, top_k, hidden, inter)) return NVFP4_EINVAL;
+  if (n_group < 1 || experts % n_group != 0 || topk_group < 1 || topk_group > n_group ||
+      top_k > topk_group * (experts / n_group))
+    return NVFP4_EINVAL;
+  if (tiled && (hidden % 128 != 0 || inter % 128 != 0)) return NVFP4_EINVAL;   // whole 128-k chunks
+  if (tokens > nvfp4::kMoeDecodeMaxTokens || hidden > 65536 || inter > 65536) return NVFP4_EUNSUPPORTED;
+  if (tokens == 0) return NVFP4_OK;
+  if (!x || !router || !correction_bias || !w1 || !w1_sf || !w1_g || !w2 || !w2_sf || !w2_g || !out) return NVFP4_EINVAL;
+  if ((((uintptr_t)x | (uintptr_t)router | (uintptr_t)w1 | (uintptr_t)w2) % 16) != 0 || ((uintptr_t)out % 8) != 0 ||
+      (((uintptr_t)w1_sf | (uintptr_t)w2_sf) % 2) != 0 || !aligned4(correction_bias) || !aligned4(w1_g) ||
+      !aligned4(w2_g) || !aligned4(topk_ids_out) || !aligned4(topk_w_out))
+    return NVFP4_EINVAL;
+  const size_t need = nvfp4::moe_decode_workspace_bytes(tokens, experts, top_k, hidden, inter);
+  if (!workspace || workspace_bytes < need || !aligned256(workspace)) return NVFP4_EWORKSPACE;
+  const int32_t ds = device_status();
+  if (ds != NVFP4_OK) return ds;
+  nvfp4::MoeDecodeArgs m{x, dtype, router, correction_bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, out, topk_ids_out,
+                         topk_w_out, tokens, experts, top_k, hidden, inter, act, n_group, topk_group,
+                         norm_topk_prob ? 1 : 0, routed_scaling, tiled ? 1 : 0, workspace};
+  return hip_status(nvfp4::launch_moe_decode(m, (hipStream_t)stream));
 }
 
 int32_t nvfp4_page_maps(const int32_t* ctx_lens, const int32_t* new_lens, int32_t seqs,

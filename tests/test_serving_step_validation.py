@@ -1,4 +1,4 @@
-"""What the FP8 operators and the rotation with the append refuse, before any launch: the C entry points by
+"""What the FP8 operators, the rotation with the append and the MoE layer of a decode step refuse, before any launch: the C entry points by
 status, the binding by exception.  No GPU: every call here fails a check (or has nothing to do) before a
 device is asked for."""
 import ctypes
@@ -30,6 +30,33 @@ ROPE = dict(q=P, k=P, v=P, dtype=0, tokens=4, hq=4, hk=2, dim=64, qs=256, qh=64,
             page=16, pages=4, stream=None)
 QUANT = dict(x=P, dtype=0, rows=4, k=256, act=0, block=1, codes=P, scale=P, stream=None)
 GEMM = dict(a=P, sa=P, w=P, sw=P, y=P, dtype=0, B=4, N=64, K=256, stream=None)
+
+MOE = dict(x=P, dtype=1, router=P, bias=P, w1=P, w1_sf=P, w1_g=P, w2=P, w2_sf=P, w2_g=P, tiled=0, out=P, ids=None, w=None,
+           tokens=4, experts=16, top_k=4, hidden=256, inter=128, act=2, groups=4, kept=2, norm=1, scaling=1.0, ws=P,
+           ws_bytes=1 << 40, stream=None)
+
+
+def test_moe_decode_status(nv):
+    fn = nv.lib().nvfp4_moe_decode
+    for c in [dict(dtype=2), dict(act=0), dict(act=3), dict(tokens=-1), dict(experts=0), dict(experts=257), dict(top_k=0),
+              dict(top_k=17), dict(top_k=9), dict(hidden=0), dict(hidden=96), dict(inter=0), dict(inter=96), dict(groups=0),
+              dict(groups=3), dict(kept=0), dict(kept=5), dict(hidden=192, tiled=1), dict(inter=192, tiled=1), dict(x=None),
+              dict(router=None), dict(bias=None), dict(w1=None), dict(w1_sf=None), dict(w1_g=None), dict(w2=None),
+              dict(w2_sf=None), dict(w2_g=None), dict(out=None), dict(x=EIGHT), dict(router=EIGHT), dict(w1=EIGHT),
+              dict(w2=EIGHT), dict(out=FOUR), dict(w1_sf=ODD), dict(w2_sf=ODD), dict(bias=TWO), dict(w1_g=TWO),
+              dict(w2_g=TWO), dict(ids=TWO), dict(w=TWO)]:
+        refuses(fn, MOE, nv.NVFP4_EINVAL, **c)
+    for c in [dict(tokens=33), dict(hidden=65536 + 64), dict(inter=65536 + 64)]:
+        refuses(fn, MOE, nv.NVFP4_EUNSUPPORTED, **c)
+    need = nv.moe_decode_workspace_size(4, 16, 4, 256, 128)
+    assert need > 0
+    for c in [dict(ws=None), dict(ws_bytes=need - 1), dict(ws=ctypes.c_void_p(4096 + 128))]:
+        refuses(fn, MOE, nv.NVFP4_EWORKSPACE, **c)
+    refuses(fn, MOE, nv.NVFP4_OK, tokens=0, x=None, out=None, ws=None)
+    size = nv.lib().nvfp4_moe_decode_workspace_size
+    for args in [(0, 16, 4, 256, 128), (33, 16, 4, 256, 128), (-1, 16, 4, 256, 128), (4, 0, 4, 256, 128),
+                 (4, 16, 17, 256, 128), (4, 16, 4, 100, 128), (4, 16, 4, 256, 0), (4, 16, 4, 1 << 20, 128)]:
+        assert size(*args) == 0, args
 
 
 def test_rope_kv_write_status(nv):
@@ -132,3 +159,24 @@ def test_fp8_gemm_operands(nv):
             nv.fp8_gemm(**dict(ok, **{key: bad}))
     with pytest.raises(ValueError, match="GPU"):
         nv.fp8_gemm(**ok)
+
+
+def test_moe_decode_operands(nv):
+    u8 = torch.uint8
+    ok = dict(x=z(4, 256), router=z(16, 256), bias=z(16, dtype=F32), w1=z(16, 128, 128, dtype=u8),
+              w1_sf=z(16, 128, 16, dtype=u8), w1_g=z(16, dtype=F32), w2=z(16, 256, 64, dtype=u8),
+              w2_sf=z(16, 256, 8, dtype=u8), w2_g=z(16, dtype=F32), top_k=4)
+    for key, bad, exc in [("x", z(4, 256, 1), ValueError), ("x", z(4, 256, dtype=F32), TypeError), ("x", z(256, 4).t(), ValueError),
+                          ("x", z(4, 128), ValueError), ("router", z(16, 256, dtype=BF16), TypeError),
+                          ("router", z(15, 256), ValueError), ("bias", z(16), TypeError), ("bias", z(15, dtype=F32), ValueError),
+                          ("w1", z(16, 256, 128, dtype=u8), ValueError), ("w1", z(16, 128, 128, dtype=torch.int8), TypeError),
+                          ("w1_sf", z(16, 128, 8, dtype=u8), ValueError), ("w1_g", z(1, dtype=F32), ValueError),
+                          ("w2", z(16, 256, dtype=u8), ValueError), ("w2", z(16, 64, 256, dtype=u8).transpose(1, 2), ValueError),
+                          ("w2_sf", z(16, 128, 8, dtype=u8), ValueError), ("w2_g", z(16), TypeError),
+                          ("out", z(4, 256, dtype=BF16), TypeError), ("out", z(4, 512)[:, ::2], ValueError),
+                          ("act", "swiglu", ValueError)]:
+        with pytest.raises(exc) as e:
+            nv.moe_decode(**dict(ok, **{key: bad}))
+        assert "GPU" not in str(e.value), key
+    with pytest.raises(ValueError, match="GPU"):
+        nv.moe_decode(**ok)
