@@ -310,7 +310,7 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
  * nvfp4_moe_w4a16 (a NaN ranks below every number).  out = sum_j w_j act(x W1_j^T)
  * W2_j^T, everything between x and out in binary32 but for the operands of the matrix
  * instructions: x (bf16) and the activations are carried in FP16 after an
- * exact scaling to the token's largest, the activations in two parts (22 bits).
+ * exact scaling to the token's largest, the activations in two parts (20 bits).
  * Deterministic; a token's result does not depend on the others.
  * Requires experts <= 256, top_k <= 16, hidden % 64 == 0, inter % 64 == 0
  * (% 128 with tiled), groups as for nvfp4_moe_w4a16; x, router, w1, w2 16-byte, out 8-byte,

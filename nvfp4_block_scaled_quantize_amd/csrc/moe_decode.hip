@@ -1,27 +1,28 @@
 // moe_decode.hip -- a whole routed MoE layer for up to 32 tokens on NVFP4 expert weights, for gfx950:
 // router product, sigmoid group top-k (the selection of moe.hip), fc1, activation (ReLU^2 or SwiGLU),
-// fc2 and the weighted sum, in three launches.
+// fc2 and the weighted sum, in three launches (four for more than 8 tokens).
 //
 //  1. router : logits[t, e] = x_t . Wr_e in binary32, one workgroup per expert; clears what the other
-//              launches count in.
-//  2. fc1    : one workgroup per (chosen expert, 16 RT weight rows).  Every workgroup selects the experts of
-//              all tokens again from the logits (a few hundred clocks per token; a launch of its own would
-//              cost more), takes its expert and the tokens that chose it, and computes
-//              h = act(W1_e x) for them, binary32.
-//  3. fc2    : one workgroup per (chosen expert, 16 RT rows of W2) computes o = W2_e h for the expert's tokens,
+//              launches count in; BF16 x also as scaled FP16 (below).
+//  (2. select: more than 8 tokens: one wave per token.)
+//  3. fc1    : one workgroup per (chosen expert, 16 RT weight rows).  For up to 8 tokens every workgroup
+//              selects all tokens' experts again from the logits, which takes less than a launch.  It
+//              finds its expert and the tokens that chose it, and computes h = act(W1_e x) for them,
+//              binary32.
+//  4. fc2    : one workgroup per (chosen expert, 16 RT rows of W2) computes o = W2_e h for the expert's tokens,
 //              binary32; the last workgroup of each row range to arrive (an atomic counter) adds the
 //              chosen experts' o with their weights in rank order, whatever the order of arrival.
 //
 // The weights' bytes bound it: each chosen expert's rows are read once, straight from memory into
-// registers (no LDS), eight waves of a workgroup splitting K in chunks of 128, all loads of a wave in
-// flight together; the waves' sums are joined through LDS.  A lane loads 16 bytes = 32 codes of its
-// row (lane r + 16 g: row r, k = 32 g ..), which feed four v_mfma_f32_16x16x32_f16: instruction m takes
-// codes 8 m .. 8 m + 7 of every lane, and the activation operand the same k.  E2M1 * E4M3 is exact in FP16.
+// registers (no LDS), the waves of a workgroup splitting K in chunks of 128, and the waves' sums are joined
+// through LDS.  A lane loads 16 bytes = 32 codes of its row (lane r + 16 g: row r, k = 32 g ..), which feed
+// four v_mfma_f32_16x16x32_f16: instruction m takes codes 8 m .. 8 m + 7 of every lane, and the activation
+// operand the same k.  E2M1 * E4M3 is exact in FP16.
 //
 // The activations must be FP16 for that.  FP16 x is used as it is.  BF16 x is multiplied by the power
 // of two that brings the token's largest value to [2^14, 2^15): exact down to 2^-31 of the largest, what is
-// below is off by at most 2^-39 of it.  h (binary32) is brought to the same range by the token's
-// largest h and split into two FP16 numbers, the value and what its rounding left: 22 bits.
+// below is off by at most 2^-39 of it.  h (binary32) is brought to the same range by the pair's
+// largest h and split into two FP16 numbers, the value and what its rounding left: off by less than 2^-20 of itself.
 #include "device_common.h"
 #include "internal.h"
 #include "moe_decode.h"
@@ -30,27 +31,31 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxT = kMoeDecodeMaxTokens;
 constexpr int kMaxK = 16;                    // top_k
 constexpr int kMaxPairs = kMaxT * kMaxK;
 constexpr int kPerLane = 4;                  // experts <= 256
+constexpr int kSelectAgain = 8;              // tokens up to which fc1 selects by itself
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// A pair (token, rank) has the number p = token * top_k + rank; its row q of h and o is its place when the
+// pairs are sorted by expert.
 struct Ws {
   float* logits;      // [T, E]
   uint32_t* xmax;     // [T] largest |x| (binary32 bits)
-  uint32_t* hmax;     // [P] largest |h| of the pair (binary32 bits)
-  int32_t* ids;       // [P]
-  float* wts;         // [P]
+  uint32_t* hmax;     // [P] largest |h| of row q (binary32 bits)
+  int32_t* ids;       // [P] expert of pair p
+  float* wts;         // [P] its weight
+  int32_t* row_of;    // [P] its row q
+  int4* chosen;       // [min(P, E)] {expert or -1, first row, rows, experts chosen}
   uint32_t* count;    // [row ranges of fc2] workgroups that are done
+  _Float16* xs;       // [T, hidden] scaled x (BF16 only)
   float* h;           // [P, inter]
   float* o;           // [P, hidden]
 };
 
-constexpr int kRanges(int hidden) { return (hidden + 31) / 32; }
+constexpr int ranges_of(int hidden) { return (hidden + 31) / 32; }
 
 size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
   unsigned char* p = reinterpret_cast<unsigned char*>(base);
@@ -66,11 +71,20 @@ size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
   s.hmax = reinterpret_cast<uint32_t*>(take((size_t)P * 4));
   s.ids = reinterpret_cast<int32_t*>(take((size_t)P * 4));
   s.wts = reinterpret_cast<float*>(take((size_t)P * 4));
-  s.count = reinterpret_cast<uint32_t*>(take((size_t)kRanges(hidden) * 4));
+  s.row_of = reinterpret_cast<int32_t*>(take((size_t)P * 4));
+  s.chosen = reinterpret_cast<int4*>(take((size_t)(P < E ? P : E) * 16));
+  s.count = reinterpret_cast<uint32_t*>(take((size_t)ranges_of(hidden) * 4));
+  s.xs = reinterpret_cast<_Float16*>(take((size_t)T * hidden * 2));
   s.h = reinterpret_cast<float*>(take((size_t)P * inter * 4));
   s.o = reinterpret_cast<float*>(take((size_t)P * hidden * 4));
   if (w) *w = s;
   return at;
+}
+
+// The power of two that brings a largest value to [2^14, 2^15).
+__device__ __forceinline__ float up_scale(uint32_t bits) {
+  const int e = (int)(bits >> 23) - 127;   // -127 for zeros and subnormal numbers
+  return __builtin_ldexpf(1.0f, 14 - e < 127 ? 14 - e : 127);
 }
 
 // ---------------------------------------------------------------- router
@@ -90,6 +104,7 @@ moe_router(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int 
   __shared__ float part[4][TB];
   __shared__ float top[4][TB];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int unit0 = (int)((int64_t)(hidden / 8) * e / E), unit1 = (int)((int64_t)(hidden / 8) * (e + 1) / E);
   if (e == 0) {
     for (int i = tid; i < P; i += 256) ws.hmax[i] = 0u;
     for (int i = tid; i < ranges; i += 256) ws.count[i] = 0u;
@@ -131,6 +146,25 @@ moe_router(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int 
         ws.xmax[t0 + tid] = __float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][tid], top[1][tid]),
                                                             __builtin_fmaxf(top[2][tid], top[3][tid])));
     }
+    if constexpr (DT == kBf16) {
+      // this workgroup's columns of the tokens in FP16
+      const int units = unit1 - unit0;
+      for (int i = tid; i < units * TB; i += 256) {
+        const int j = i / units, u = unit0 + i - j * units;
+        if (t0 + j >= T) continue;
+        const float scale = up_scale(__float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][j], top[1][j]),
+                                                                     __builtin_fmaxf(top[2][j], top[3][j]))));
+        const int64_t at = (int64_t)(t0 + j) * hidden + 8 * u;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(x + at);
+        v8h o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          o[2 * q] = (_Float16)(bf16_lo(v[q]) * scale);
+          o[2 * q + 1] = (_Float16)(bf16_hi(v[q]) * scale);
+        }
+        *reinterpret_cast<v8h*>(ws.xs + at) = o;
+      }
+    }
     __syncthreads();
   }
 }
@@ -143,13 +177,24 @@ __device__ __forceinline__ uint32_t rank_key(float v) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  const uint32_t u = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return u > v ? u : v;
+}
+// Largest over the wave (rows of 16 lanes by lane exchange, then the four rows).
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max_dpp<0xB1>(v);
+  v = max_dpp<0x4E>(v);
+  v = max_dpp<0x141>(v);
+  v = max_dpp<0x140>(v);
+  uint32_t m = 0u;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const uint32_t u = __shfl_xor(v, off, 64);
-    v = u > v ? u : v;
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t u = (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * r);
+    m = u > m ? u : m;
   }
-  return v;
+  return m;
 }
 
 struct RouteArgs {
@@ -225,7 +270,7 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const float* __
       if (e < 0 && hit != 0) {
         const int l = __builtin_ctzll(hit);
         e = l + 64 * i;
-        w = __shfl(s[i], l, 64);
+        w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s[i]), l));
         if (lane == l) key[i] = 0u;
       }
     }
@@ -239,6 +284,12 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const float* __
     ids[lane] = chosen;
     wts[lane] = (a.norm ? mine / sum : mine) * a.scaling;
   }
+}
+
+__global__ void __launch_bounds__(64) moe_select(RouteArgs a, Ws ws) {
+  __shared__ float sb[64 * kPerLane], sg[64 * kPerLane];
+  const int t = blockIdx.x;
+  select_token(a, ws.logits, t, sb, sg, ws.ids + t * a.top_k, ws.wts + t * a.top_k);
 }
 
 // ---------------------------------------------------------------- expert rows
@@ -284,185 +335,242 @@ __device__ __forceinline__ Piece load_piece(const uint8_t* __restrict__ w, const
   return p;
 }
 
-// The power of two that brings a largest value to [2^14, 2^15), and its inverse.
-__device__ __forceinline__ float up_scale(uint32_t bits) {
-  const int e = (int)(bits >> 23) - 127;   // -127 for zeros and subnormal numbers
-  return __builtin_ldexpf(1.0f, 14 - e < 127 ? 14 - e : 127);
-}
-
 struct FcArgs {
-  const void* x;         // FC 1: [T, hidden]
+  const void* src;       // FC 1: x or its scaled form [T, hidden]; FC 2: h
   const uint8_t* w;
   const uint8_t* sf;
   const float* g;
   int rows, K;           // rows of one expert, and their length
   int inter, hidden;
+  int scaled;            // FC 1: src is scaled by up_scale(xmax)
+  int select;            // FC 1: the experts are selected here
   RouteArgs route;
   int32_t* ids_out;
   float* w_out;
   void* out;             // FC 2: [T, hidden]
+  int out_type;
   Ws ws;
 };
 
-// The activation operand of one chunk for 16 token slots: lane (slot, g) holds k = 128 c + 32 g .. + 31.
-// FC 1, FP16: as stored.  FC 1, BF16: scaled.  FC 2: binary32 h scaled and split.
-template <int FC, int DT>
-__device__ __forceinline__ void load_act(const void* src, int64_t row, int K, int c, int g, float scale, v8h (&hi)[4],
-                                         v8h (&lo)[4]) {
-  const bool in = 128 * c + 32 * g < K;
-  const int64_t at = row * K + 128 * c + 32 * (in ? g : g - 2);
-  if constexpr (FC == 1) {
+// The activations of one chunk for 16 token slots as they are stored: lane (slot, g) holds
+// k = 128 c + 32 g .. + 31, as 32 FP16 or 32 binary32 numbers; zeros for slots without a token and past K.
+template <int FC>
+struct RawAct {
+  u32x4 v[FC == 1 ? 4 : 8];
+};
+template <int FC>
+__device__ __forceinline__ void load_act(const void* src, int64_t row, bool there, int K, int c, int g, RawAct<FC>& r) {
+  constexpr int kN = FC == 1 ? 4 : 8, kBytes = FC == 1 ? 2 : 4;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>((const uint16_t*)src + at + 8 * m);
-      if constexpr (DT == kFp16) {
-        hi[m] = __builtin_bit_cast(v8h, v);
-      } else {
+  for (int m = 0; m < kN; ++m) r.v[m] = u32x4{0u, 0u, 0u, 0u};
+  if (there && 128 * c + 32 * g < K) {
+    const u32x4* p = reinterpret_cast<const u32x4*>((const char*)src + (row * K + 128 * c + 32 * g) * kBytes);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hi[m][2 * i] = (_Float16)(bf16_lo(v[i]) * scale);
-          hi[m][2 * i + 1] = (_Float16)(bf16_hi(v[i]) * scale);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const v4f* p = reinterpret_cast<const v4f*>((const float*)src + at + 8 * m);
-      const v4f a = p[0], b = p[1];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = (i < 4 ? a[i & 3] : b[i & 3]) * scale;
-        hi[m][i] = (_Float16)v;
-        lo[m][i] = (_Float16)(v - (float)hi[m][i]);
-      }
-    }
-  }
-  if (!in) {
-    const v8h zero = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int m = 0; m < 4; ++m) hi[m] = lo[m] = zero;
+    for (int m = 0; m < kN; ++m) r.v[m] = p[m];
   }
 }
 
-template <int FC, int DT, int ACT, bool TW, int RT, int TT>
-__global__ void __launch_bounds__(kThreads) moe_expert_rows(FcArgs a) {
-  __shared__ v4f part[kWaves][RT * TT][64];
-  __shared__ float sb[FC == 1 ? kWaves : 1][64 * kPerLane], sg[FC == 1 ? kWaves : 1][64 * kPerLane];
-  __shared__ int32_t ids[kMaxPairs];
+// Operands of instruction m.  FC 1: as stored.  FC 2: scaled and split; both roundings are toward zero,
+// the first leaves less than 2^-10 of the value, the second less than 2^-10 of that.
+template <int FC>
+__device__ __forceinline__ void act_operand(const RawAct<FC>& r, int m, float scale, v8h& hi, v8h& lo) {
+  if constexpr (FC == 1) {
+    hi = __builtin_bit_cast(v8h, r.v[m]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = __uint_as_float(r.v[2 * m + i / 2][2 * (i & 1)]) * scale;
+      const float b = __uint_as_float(r.v[2 * m + i / 2][2 * (i & 1) + 1]) * scale;
+      const v2h p = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(a, b));
+      const v2h q = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(a - (float)p[0], b - (float)p[1]));
+      hi[2 * i] = p[0];
+      hi[2 * i + 1] = p[1];
+      lo[2 * i] = q[0];
+      lo[2 * i + 1] = q[1];
+    }
+  }
+}
+
+// Four numbers to and from memory that workgroups on other dies read: the accesses go past the caches
+// of this die one by one.  (A fence would write back a whole die's cache: with one in each workgroup fc2 of 16
+// tokens took 120 us instead of 27.)
+__device__ __forceinline__ void store_shared(float* p, const v4f& v) {
+  const uint64_t a = __float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32;
+  const uint64_t b = __float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32;
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ v4f load_shared(const float* p) {
+  const uint64_t a = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return v4f{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)b),
+             __uint_as_float((uint32_t)(b >> 32))};
+}
+
+template <int FC, bool GATED, bool TW, int RT, int TT, int NW>
+__global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcArgs a) {
+  constexpr int kThreads = 64 * NW;
+  constexpr int kAhead = FC == 1 ? 2 : 1;   // chunks of a wave in flight
+  __shared__ v4f part[NW][RT * TT][64];
+  __shared__ float scratch[FC == 1 ? NW : 1][2][64 * kPerLane];
+  __shared__ int32_t ids[FC == 1 ? kMaxPairs : 1];
   __shared__ float wts[kMaxPairs];
+  __shared__ int rows[kMaxPairs];         // FC 1: pair of each token slot; FC 2: row of each pair
   __shared__ uint32_t used[8];            // experts that some token chose
-  __shared__ int slot_pair[16 * TT];      // pair of each token slot
   __shared__ uint32_t slot_max[16 * TT];
-  __shared__ int nslots, last;
+  __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, grp = lane >> 4;
   const int T = a.route.T, top_k = a.route.top_k, P = T * top_k;
 
-  if (tid < 8) used[tid] = 0u;
-  if (tid < 16 * TT) slot_max[tid] = 0u;
+  int4 mine;   // this workgroup's expert, its first row, its rows, chosen experts
   if constexpr (FC == 1) {
-    for (int t = wave; t < T; t += kWaves)
-      select_token(a.route, a.ws.logits, t, sb[wave], sg[wave], ids + t * top_k, wts + t * top_k);
+    if (tid < 8) used[tid] = 0u;
+    if (tid < 16 * TT) slot_max[tid] = 0u;
+    if (a.select) {
+      for (int t = wave; t < T; t += NW)
+        select_token(a.route, a.ws.logits, t, scratch[wave][0], scratch[wave][1], ids + t * top_k, wts + t * top_k);
+    } else {
+      for (int p = tid; p < P; p += kThreads) {
+        ids[p] = a.ws.ids[p];
+        wts[p] = a.ws.wts[p];
+      }
+    }
+    __syncthreads();
+    for (int p = tid; p < P; p += kThreads) atomicOr(&used[ids[p] >> 5], 1u << (ids[p] & 31));
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      for (int p = tid; p < P; p += kThreads) {
+        if (a.select) a.ws.wts[p] = wts[p];
+        if (a.ids_out) a.ids_out[p] = ids[p];
+        if (a.w_out) a.w_out[p] = wts[p];
+      }
+    }
+    __syncthreads();
+    // the blockIdx.y-th chosen expert
+    int e = -1, n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = used[i];
+      const int c = __popc(m);
+      if (e < 0 && (int)blockIdx.y < n + c) {
+        for (int j = (int)blockIdx.y - n; j > 0; --j) m &= m - 1;
+        e = 32 * i + __builtin_ctz(m);
+      }
+      n += c;
+    }
+    mine = make_int4(__builtin_amdgcn_readfirstlane(e), 0, 0, n);
   } else {
-    for (int p = tid; p < P; p += kThreads) {
-      ids[p] = a.ws.ids[p];
-      wts[p] = a.ws.wts[p];
-    }
+    mine = a.ws.chosen[blockIdx.y];
+    mine.x = __builtin_amdgcn_readfirstlane(mine.x);
   }
-  __syncthreads();
-  for (int p = tid; p < P; p += kThreads) atomicOr(&used[ids[p] >> 5], 1u << (ids[p] & 31));
-  if (FC == 1 && blockIdx.x == 0 && blockIdx.y == 0) {
-    for (int p = tid; p < P; p += kThreads) {
-      a.ws.ids[p] = ids[p];
-      a.ws.wts[p] = wts[p];
-      if (a.ids_out) a.ids_out[p] = ids[p];
-      if (a.w_out) a.w_out[p] = wts[p];
-    }
+  const int e = mine.x;
+  if (e < 0) {   // fewer experts than workgroups: the whole workgroup
+    if (FC == 1 && blockIdx.x == 0 && tid == 0) a.ws.chosen[blockIdx.y] = mine;
+    return;
   }
-  __syncthreads();
-  // the blockIdx.y-th chosen expert
-  int e = -1, n = 0;
-  for (int i = 0; i < 8; ++i) {
-    uint32_t m = used[i];
-    const int c = __popc(m);
-    if (e < 0 && (int)blockIdx.y < n + c) {
-      for (int j = (int)blockIdx.y - n; j > 0; --j) m &= m - 1;
-      e = 32 * i + __builtin_ctz(m);
-    }
-    n += c;
-  }
-  if (e < 0) return;   // fewer experts than workgroups: the whole workgroup
-  // its pairs, in order (an expert appears at most once per token)
-  if (wave == 0) {
-    int at = 0;
-    for (int p0 = 0; p0 < P; p0 += 64) {
-      const int p = p0 + lane;
-      const uint64_t m = __ballot(p < P && ids[p < P ? p : 0] == e);
-      if ((m >> lane) & 1ull) slot_pair[at + __popcll(m & ((1ull << lane) - 1ull))] = p;
-      at += __popcll(m);
-    }
-    if (lane == 0) nslots = at;
-  }
-  __syncthreads();
-  const int ns = nslots;
 
   // weight rows of the tile's RT groups of 16: consecutive rows, or for SwiGLU in fc1 gate rows, then the up rows
-  constexpr bool kGated = FC == 1 && ACT == kActSwiglu;
-  constexpr int kCols = (kGated ? RT / 2 : RT) * 16;   // results per token
+  constexpr int kCols = (GATED ? RT / 2 : RT) * 16;   // results per token
   const int col0 = (int)blockIdx.x * kCols;
   int64_t row16[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const int r = !kGated ? col0 + 16 * i : i < RT / 2 ? col0 + 16 * i : a.inter + col0 + 16 * (i - RT / 2);
+    const int r = !GATED ? col0 + 16 * i : i < RT / 2 ? col0 + 16 * i : a.inter + col0 + 16 * (i - RT / 2);
     row16[i] = (int64_t)e * a.rows + r;
   }
+  // the first chunks' weights are on their way while the tokens are looked up
+  const int chunks = (a.K + 127) / 128;
+  Piece w[kAhead][RT];
+  auto load_weights = [&](int c0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int c = c0 + d * NW < chunks ? c0 + d * NW : c0;   // past the end: again the first, not used
+        w[d][i] = load_piece<TW>(a.w, a.sf, row16[i], c, a.K, lane);
+      }
+  };
+  if (wave < chunks) load_weights(wave);
+
+  if constexpr (FC == 1) {
+    // its pairs in order (an expert appears at most once per token), and how many pairs come before them
+    if (wave == 0) {
+      int at = 0, before = 0;
+      for (int p0 = 0; p0 < P; p0 += 64) {
+        const int p = p0 + lane, id = p < P ? ids[p] : 256;
+        const uint64_t m = __ballot(id == e);
+        before += __popcll(__ballot(id < e));
+        if ((m >> lane) & 1ull) rows[at + __popcll(m & ((1ull << lane) - 1ull))] = p;
+        at += __popcll(m);
+      }
+      if (lane == 0) {
+        found[0] = before;
+        found[1] = at;
+      }
+      if (blockIdx.x == 0) {
+        if (lane == 0) a.ws.chosen[blockIdx.y] = make_int4(e, before, at, mine.w);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (lane < at) a.ws.row_of[rows[lane]] = before + lane;
+      }
+    }
+    lds_barrier();   // does not wait for the weights
+    mine.y = found[0];
+    mine.z = found[1];
+  }
+  const int q0 = mine.y, ns = mine.z;
+
   // token slots of this lane
   int64_t arow[TT];
   float ascale[TT];
+  bool there[TT];
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int s = 16 * j + r16 < ns ? 16 * j + r16 : 0;   // empty slots: the first (computed, never stored)
-    const int p = slot_pair[s];
-    arow[j] = FC == 1 ? p / top_k : p;
-    ascale[j] = FC == 1 ? (DT == kBf16 ? up_scale(a.ws.xmax[arow[j]]) : 1.0f) : up_scale(a.ws.hmax[p]);
+    const int s = 16 * j + r16;
+    there[j] = s < ns;
+    arow[j] = FC == 1 ? (there[j] ? rows[s] / top_k : 0) : q0 + s;
+    ascale[j] = 1.0f;
+    if (FC == 2 && there[j]) ascale[j] = up_scale(a.ws.hmax[q0 + s]);
   }
-  const void* src = FC == 1 ? a.x : (const void*)a.ws.h;
-
   v4f acc[RT][TT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int chunks = (a.K + 127) / 128;
-  Piece next[RT];
-  if (wave < chunks) {
+
+  for (int c0 = wave; c0 < chunks; c0 += NW * kAhead) {
+    if (c0 != wave) load_weights(c0);
+    RawAct<FC> raw[kAhead][TT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) next[i] = load_piece<TW>(a.w, a.sf, row16[i], wave, a.K, lane);
-  }
-  for (int c = wave; c < chunks; c += kWaves) {
-    Piece now[RT];
+    for (int d = 0; d < kAhead; ++d)
 #pragma unroll
-    for (int i = 0; i < RT; ++i) now[i] = next[i];
-    if (c + kWaves < chunks) {
+      for (int j = 0; j < TT; ++j)
+        if (j == 0 || ns > 16 * j) load_act<FC>(a.src, arow[j], there[j], a.K, c0 + d * NW, grp, raw[d][j]);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) next[i] = load_piece<TW>(a.w, a.sf, row16[i], c + kWaves, a.K, lane);
-    }
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      if (j > 0 && ns <= 16 * j) break;   // the whole workgroup
-      v8h hi[4], lo[4];
-      load_act<FC, DT>(src, arow[j], a.K, c, grp, ascale[j], hi, lo);
+    for (int d = 0; d < kAhead; ++d) {
+      if (c0 + d * NW >= chunks) break;   // the whole wave
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const _Float16 s0 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)now[i].sf, 0);
-        const _Float16 s1 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)now[i].sf, 1);
+        const _Float16 s0 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)w[d][i].sf, 0);
+        const _Float16 s1 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)w[d][i].sf, 1);
+        w[d][i].sf = (uint32_t)__builtin_bit_cast(uint16_t, s0) | (uint32_t)__builtin_bit_cast(uint16_t, s1) << 16;
+      }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const v8h wv = dequant8(now[i].codes[m], m < 2 ? s0 : s1);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, hi[m], acc[i][j], 0, 0, 0);
-          if constexpr (FC == 2) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, lo[m], acc[i][j], 0, 0, 0);
+      for (int m = 0; m < 4; ++m) {
+        v8h wv[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          wv[i] = dequant8(w[d][i].codes[m], __builtin_bit_cast(_Float16, (uint16_t)(m < 2 ? w[d][i].sf : w[d][i].sf >> 16)));
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          if (j > 0 && ns <= 16 * j) break;   // the whole workgroup
+          v8h hi, lo;
+          act_operand<FC>(raw[d][j], m, ascale[j], hi, lo);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[i], hi, acc[i][j], 0, 0, 0);
+            if constexpr (FC == 2) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[i], lo, acc[i][j], 0, 0, 0);
+          }
         }
       }
     }
@@ -471,11 +579,18 @@ __global__ void __launch_bounds__(kThreads) moe_expert_rows(FcArgs a) {
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) part[wave][i * TT + j][lane] = acc[i][j];
+  if constexpr (FC == 2) {
+    // for the last workgroup of the row range
+    for (int p = tid; p < P; p += kThreads) {
+      rows[p] = a.ws.row_of[p];
+      wts[p] = a.ws.wts[p];
+    }
+  }
   __syncthreads();
   auto joined = [&](int tile) __attribute__((always_inline)) {
     v4f s = part[0][tile][lane];
 #pragma unroll
-    for (int v = 1; v < kWaves; ++v) {
+    for (int v = 1; v < NW; ++v) {
       const v4f q = part[v][tile][lane];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += q[i];
@@ -485,61 +600,60 @@ __global__ void __launch_bounds__(kThreads) moe_expert_rows(FcArgs a) {
   // results: lane (slot r16, columns 4 grp .. + 3) of a tile
   const float ge = a.g[e];
   constexpr int kOutTiles = kCols / 16 * TT;
-  for (int tile = wave; tile < kOutTiles; tile += kWaves) {
+  for (int tile = wave; tile < kOutTiles; tile += NW) {
     const int i = tile / TT, j = tile % TT, slot = 16 * j + r16;
     if (16 * j >= ns) continue;
     v4f y = joined(tile);
     v4f up;
-    if constexpr (kGated) up = joined(tile + RT / 2 * TT);
+    if constexpr (GATED) up = joined(tile + RT / 2 * TT);
     if (slot >= ns) continue;
-    const int p = slot_pair[slot];
     const int col = col0 + 16 * i + 4 * grp;
     if constexpr (FC == 1) {
-      const float f = DT == kBf16 ? ge / up_scale(a.ws.xmax[p / top_k]) : ge;
+      const float f = a.scaled ? ge / up_scale(a.ws.xmax[rows[slot] / top_k]) : ge;
       v4f hv;
       float m = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        hv[q] = kGated ? swiglu_f32(y[q] * f, up[q] * f) : relu2_f32(y[q] * f);
+        hv[q] = GATED ? swiglu_f32(y[q] * f, up[q] * f) : relu2_f32(y[q] * f);
         m = __builtin_fmaxf(m, __builtin_fabsf(hv[q]));
       }
-      *reinterpret_cast<v4f*>(a.ws.h + (int64_t)p * a.inter + col) = hv;
+      *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(q0 + slot) * a.inter + col) = hv;
       atomicMax(&slot_max[slot], __float_as_uint(m));
     } else {
-      const float f = ge / up_scale(a.ws.hmax[p]);
+      const float f = ge / up_scale(a.ws.hmax[q0 + slot]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) y[q] *= f;
-      *reinterpret_cast<v4f*>(a.ws.o + (int64_t)p * a.hidden + col) = y;
+      store_shared(a.ws.o + (int64_t)(q0 + slot) * a.hidden + col, y);
     }
   }
   if constexpr (FC == 1) {
     __syncthreads();
-    if (tid < ns) atomicMax(a.ws.hmax + slot_pair[tid], slot_max[tid]);
+    if (tid < ns) atomicMax(a.ws.hmax + q0 + tid, slot_max[tid]);
   } else {
     // this workgroup's results are in memory before it counts itself; the one that counts last sees all of them
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0) {
-      __threadfence();
-      last = atomicAdd(a.ws.count + blockIdx.x, 1u) == (uint32_t)(n - 1) ? 1 : 0;
-      __threadfence();
+      const uint32_t n = __hip_atomic_fetch_add(a.ws.count + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      found[0] = n == (uint32_t)(mine.w - 1) ? 1 : 0;
     }
     __syncthreads();
-    if (!last) return;
+    if (!found[0]) return;
     constexpr int kQuads = kCols / 4;
     for (int i = tid; i < T * kQuads; i += kThreads) {
       const int t = i / kQuads, col = col0 + 4 * (i - t * kQuads);
       v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
       for (int k = 0; k < top_k; ++k) {
-        const v4f v = *reinterpret_cast<const v4f*>(a.ws.o + (int64_t)(t * top_k + k) * a.hidden + col);
-        const float w = wts[t * top_k + k];
+        const v4f v = load_shared(a.ws.o + (int64_t)rows[t * top_k + k] * a.hidden + col);
+        const float wk = wts[t * top_k + k];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(w, v[q], s[q]);
+        for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(wk, v[q], s[q]);
       }
       uint16_t o[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        o[q] = DT == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s[q]) : __builtin_bit_cast(uint16_t, (_Float16)s[q]);
+        o[q] = a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s[q]) : __builtin_bit_cast(uint16_t, (_Float16)s[q]);
       u32x2 v = {o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16};
       *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)t * a.hidden + col) = v;
     }
@@ -551,22 +665,29 @@ void launch_router(const MoeDecodeArgs& m, const Ws& ws, int P, hipStream_t s) {
   const uint16_t* x = reinterpret_cast<const uint16_t*>(m.x);
   const uint16_t* wr = reinterpret_cast<const uint16_t*>(m.router);
   const dim3 grid(m.experts), block(256);
-  if (m.tokens == 1) moe_router<DT, 1><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, kRanges(m.hidden));
-  else if (m.tokens <= 4) moe_router<DT, 4><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, kRanges(m.hidden));
-  else moe_router<DT, 8><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, kRanges(m.hidden));
+  if (m.tokens == 1) moe_router<DT, 1><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
+  else if (m.tokens <= 4) moe_router<DT, 4><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
+  else moe_router<DT, 8><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
 }
 
-template <int FC, int DT, int ACT, bool TW, int RT>
+template <int FC, bool GATED, bool TW, int RT>
 void launch_rows(const FcArgs& a, int tiles, int experts, hipStream_t s) {
   const dim3 grid(tiles, experts);
-  if (a.route.T <= 16) moe_expert_rows<FC, DT, ACT, TW, RT, 1><<<grid, dim3(kThreads), 0, s>>>(a);
-  else moe_expert_rows<FC, DT, ACT, TW, RT, 2><<<grid, dim3(kThreads), 0, s>>>(a);
+  // eight waves where a workgroup has a compute unit for itself, four where several share one
+  if ((int64_t)tiles * experts <= 512) {
+    if (a.route.T <= 16) moe_expert_rows<FC, GATED, TW, RT, 1, 8><<<grid, dim3(512), 0, s>>>(a);
+    else moe_expert_rows<FC, GATED, TW, RT, 2, 8><<<grid, dim3(512), 0, s>>>(a);
+  } else {
+    if (a.route.T <= 16) moe_expert_rows<FC, GATED, TW, RT, 1, 4><<<grid, dim3(256), 0, s>>>(a);
+    else moe_expert_rows<FC, GATED, TW, RT, 2, 4><<<grid, dim3(256), 0, s>>>(a);
+  }
 }
 
-template <int DT, int ACT, bool TW>
+template <bool TW>
 void launch_layer(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   const int P = m.tokens * m.top_k;
   const int experts = P < m.experts ? P : m.experts;   // at most so many are chosen
+  const bool gated = m.act == kActSwiglu;
   FcArgs a{};
   a.route = RouteArgs{m.bias, m.tokens, m.experts, m.top_k, m.n_group, m.topk_group, m.norm, m.scaling};
   a.ids_out = m.ids_out;
@@ -574,32 +695,33 @@ void launch_layer(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   a.inter = m.inter;
   a.hidden = m.hidden;
   a.ws = ws;
-  a.x = m.x;
   a.out = m.out;
+  a.out_type = m.dtype;
+  a.select = m.tokens <= kSelectAgain;
+  if (!a.select) moe_select<<<dim3(m.tokens), dim3(64), 0, s>>>(a.route, ws);
+  a.scaled = m.dtype == kBf16;
+  a.src = a.scaled ? (const void*)ws.xs : m.x;
   a.w = m.w1;
   a.sf = m.w1_sf;
   a.g = m.w1_g;
-  a.rows = ACT == kActSwiglu ? 2 * m.inter : m.inter;
+  a.rows = gated ? 2 * m.inter : m.inter;
   a.K = m.hidden;
-  launch_rows<1, DT, ACT, TW, 2>(a, a.rows / 32, experts, s);
+  if (gated) launch_rows<1, true, TW, 2>(a, a.rows / 32, experts, s);
+  else launch_rows<1, false, TW, 2>(a, a.rows / 32, experts, s);
+  a.src = ws.h;
   a.w = m.w2;
   a.sf = m.w2_sf;
   a.g = m.w2_g;
   a.rows = m.hidden;
   a.K = m.inter;
-  launch_rows<2, DT, kActNone, TW, 4>(a, a.rows / 64, experts, s);
+  launch_rows<2, false, TW, 4>(a, a.rows / 64, experts, s);
 }
 
 template <int DT>
 void launch_type(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   launch_router<DT>(m, ws, m.tokens * m.top_k, s);
-  if (m.act == kActSwiglu) {
-    if (m.tiled) launch_layer<DT, kActSwiglu, true>(m, ws, s);
-    else launch_layer<DT, kActSwiglu, false>(m, ws, s);
-  } else {
-    if (m.tiled) launch_layer<DT, kActRelu2, true>(m, ws, s);
-    else launch_layer<DT, kActRelu2, false>(m, ws, s);
-  }
+  if (m.tiled) launch_layer<true>(m, ws, s);
+  else launch_layer<false>(m, ws, s);
 }
 
 }  // namespace
