@@ -311,10 +311,10 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
  * W2_j^T, everything between x and out in binary32 but for the operands of the matrix
  * instructions: x (bf16) and the activations are carried in FP16 after an
  * exact scaling to the token's largest, the activations in two parts (20 bits).
- * Deterministic; a token's result does not depend on the others.
+ * Deterministic; a token's result does not depend on the values of the others.
  * Requires experts <= 256, top_k <= 16, hidden % 64 == 0, inter % 64 == 0
  * (% 128 with tiled), groups as for nvfp4_moe_w4a16; x, router, w1, w2 16-byte, out 8-byte,
- * scales 2-byte aligned (EINVAL otherwise); tokens <= 32, hidden and inter
+ * scales 4-byte aligned (EINVAL otherwise); tokens <= 32, hidden and inter
  * <= 65536 (EUNSUPPORTED).  workspace: nvfp4_moe_decode_workspace_size bytes,
  * 256-byte aligned, contents before the call do not matter; calls that may
  * overlap in time need workspaces of their own.

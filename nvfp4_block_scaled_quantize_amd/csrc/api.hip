@@ -440,7 +440,7 @@ int32_t nvfp4_moe_decode(const void* x, int32_t dtype, const void* router, const
   if (tokens == 0) return NVFP4_OK;
   if (!x || !router || !correction_bias || !w1 || !w1_sf || !w1_g || !w2 || !w2_sf || !w2_g || !out) return NVFP4_EINVAL;
   if ((((uintptr_t)x | (uintptr_t)router | (uintptr_t)w1 | (uintptr_t)w2) % 16) != 0 || ((uintptr_t)out % 8) != 0 ||
-      (((uintptr_t)w1_sf | (uintptr_t)w2_sf) % 2) != 0 || !aligned4(correction_bias) || !aligned4(w1_g) ||
+      !aligned4(w1_sf) || !aligned4(w2_sf) || !aligned4(correction_bias) || !aligned4(w1_g) ||
       !aligned4(w2_g) || !aligned4(topk_ids_out) || !aligned4(topk_w_out))
     return NVFP4_EINVAL;
   const size_t need = nvfp4::moe_decode_workspace_bytes(tokens, experts, top_k, hidden, inter);

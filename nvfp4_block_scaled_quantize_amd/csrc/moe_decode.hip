@@ -1,14 +1,14 @@
 // moe_decode.hip -- a whole routed MoE layer for up to 32 tokens on NVFP4 expert weights, for gfx950:
 // router product, sigmoid group top-k (the selection of moe.hip), fc1, activation (ReLU^2 or SwiGLU),
-// fc2 and the weighted sum, in three launches (four for more than 8 tokens).
+// fc2 and the weighted sum, in four launches (three for one token).
 //
 //  1. router : logits[t, e] = x_t . Wr_e in binary32, one workgroup per expert; clears what the other
 //              launches count in; BF16 x also as scaled FP16 (below).
-//  (2. select: more than 8 tokens: one wave per token.)
-//  3. fc1    : one workgroup per (chosen expert, 16 RT weight rows).  For up to 8 tokens every workgroup
-//              selects all tokens' experts again from the logits, which takes less than a launch.  It
-//              finds its expert and the tokens that chose it, and computes h = act(W1_e x) for them,
-//              binary32.
+//  2. plan   : one workgroup: one wave per token selects its experts; then the chosen experts, the tokens of
+//              each, and a row for every pair of them.  For one token every wave of fc1 selects by itself:
+//              that takes 2 us of fc1's time, a launch 4 us.
+//  3. fc1    : one workgroup per (chosen expert, 16 RT weight rows): h = act(W1_e x) for the tokens that
+//              chose it, binary32.
 //  4. fc2    : one workgroup per (chosen expert, 16 RT rows of W2) computes o = W2_e h for the expert's tokens,
 //              binary32; the last workgroup of each row range to arrive (an atomic counter) adds the
 //              chosen experts' o with their weights in rank order, whatever the order of arrival.
@@ -35,7 +35,6 @@ constexpr int kMaxT = kMoeDecodeMaxTokens;
 constexpr int kMaxK = 16;                    // top_k
 constexpr int kMaxPairs = kMaxT * kMaxK;
 constexpr int kPerLane = 4;                  // experts <= 256
-constexpr int kSelectAgain = 8;              // tokens up to which fc1 selects by itself
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -45,10 +44,9 @@ struct Ws {
   float* logits;      // [T, E]
   uint32_t* xmax;     // [T] largest |x| (binary32 bits)
   uint32_t* hmax;     // [P] largest |h| of row q (binary32 bits)
-  int32_t* ids;       // [P] expert of pair p
-  float* wts;         // [P] its weight
+  float* wts;         // [P] weight of pair p
   int32_t* row_of;    // [P] its row q
-  int4* chosen;       // [min(P, E)] {expert or -1, first row, rows, experts chosen}
+  int4* chosen;       // [min(P, E)] {expert or -1, first row, mask of its tokens, experts chosen}
   uint32_t* count;    // [row ranges of fc2] workgroups that are done
   _Float16* xs;       // [T, hidden] scaled x (BF16 only)
   float* h;           // [P, inter]
@@ -69,7 +67,6 @@ size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
   s.logits = reinterpret_cast<float*>(take((size_t)T * E * 4));
   s.xmax = reinterpret_cast<uint32_t*>(take((size_t)T * 4));
   s.hmax = reinterpret_cast<uint32_t*>(take((size_t)P * 4));
-  s.ids = reinterpret_cast<int32_t*>(take((size_t)P * 4));
   s.wts = reinterpret_cast<float*>(take((size_t)P * 4));
   s.row_of = reinterpret_cast<int32_t*>(take((size_t)P * 4));
   s.chosen = reinterpret_cast<int4*>(take((size_t)(P < E ? P : E) * 16));
@@ -203,69 +200,101 @@ struct RouteArgs {
   float scaling;
 };
 
-// One wave selects one token's experts: lane l holds experts l + 64 i.  A group's score is the sum of its
-// two best biased scores, the best groups are kept, and the top_k experts of those are taken one
-// after the other, ties to the lower index.
+// The two largest of a group, joined with a neighbour's.
+__device__ __forceinline__ void join_two(float& v1, float& v2, float u1, float u2) {
+  v2 = __builtin_fmaxf(__builtin_fminf(v1, u1), __builtin_fmaxf(v2, u2));
+  v1 = __builtin_fmaxf(v1, u1);
+}
+
+// One wave selects one token's experts: lane l holds experts l + 64 i, i < N.  A group's score is the sum of
+// its two best biased scores, the best groups are kept, and the top_k experts of those are taken one
+// after the other, ties to the lower index: lane k receives the one of rank k and its weight.  Groups of 2, 4,
+// .. 64 experts are lanes next to one another; others go through LDS (sb, sg: E and n_group entries).
+template <int N>
 __device__ __forceinline__ void select_token(const RouteArgs& a, const float* __restrict__ logits, int t, float* sb,
-                                             float* sg, int32_t* ids, float* wts) {
+                                             float* sg, int& id, float& weight) {
   const int lane = threadIdx.x & 63;
   const int gsize = a.E / a.n_group;
-  float s[kPerLane];
-  uint32_t key[kPerLane];
+  const float ninf = -__builtin_inff();
+  float s[N], b[N];
+  uint32_t key[N];
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int e = lane + 64 * i;
     s[i] = 0.0f;
+    b[i] = ninf;
     key[i] = 0u;
     if (e < a.E) {
       s[i] = sigmoid_f32(logits[(int64_t)t * a.E + e]);
-      float b = s[i] + a.bias[e];
-      if (b != b) b = -__builtin_inff();
-      key[i] = rank_key(b);
-      if (a.n_group > 1) sb[e] = b;
+      b[i] = s[i] + a.bias[e];
+      if (b[i] != b[i]) b[i] = ninf;
+      key[i] = rank_key(b[i]);
     }
   }
   if (a.n_group > 1) {
-    const float ninf = -__builtin_inff();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // only this wave reads what it wrote
-    for (int g = lane; g < a.n_group; g += 64) {
-      float v1 = ninf, v2 = ninf;
-      for (int j = 0; j < gsize; ++j) {
-        const float v = sb[g * gsize + j];
-        v2 = __builtin_fmaxf(v2, __builtin_fminf(v1, v));
-        v1 = __builtin_fmaxf(v1, v);
-      }
-      float sum = gsize > 1 ? v1 + v2 : v1;
-      if (sum != sum) sum = ninf;
-      sg[g] = sum;
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    float mine[N];   // the score of each expert's group
+    int before[N];
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 64 * i;
-      if (e < a.E) {
-        const int g = e / gsize;
-        const float mine = sg[g];
-        int before = 0;
-        for (int j = 0; j < a.n_group; ++j) {
-          const float v = sg[j];
-          before += (v > mine || (v == mine && j < g)) ? 1 : 0;
+    for (int i = 0; i < N; ++i) before[i] = 0;
+    if ((gsize & (gsize - 1)) == 0 && gsize <= 64) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v1 = b[i], v2 = ninf;
+        if (gsize >= 2) join_two(v1, v2, dpp_f32<0xB1>(v1), dpp_f32<0xB1>(v2));
+        if (gsize >= 4) join_two(v1, v2, dpp_f32<0x4E>(v1), dpp_f32<0x4E>(v2));
+        if (gsize >= 8) join_two(v1, v2, dpp_f32<0x141>(v1), dpp_f32<0x141>(v2));
+        if (gsize >= 16) join_two(v1, v2, dpp_f32<0x140>(v1), dpp_f32<0x140>(v2));
+        if (gsize >= 32) join_two(v1, v2, __shfl_xor(v1, 16, 64), __shfl_xor(v2, 16, 64));
+        if (gsize >= 64) join_two(v1, v2, __shfl_xor(v1, 32, 64), __shfl_xor(v2, 32, 64));
+        mine[i] = gsize > 1 ? v1 + v2 : v1;
+        if (mine[i] != mine[i]) mine[i] = ninf;
+      }
+      int j = 0;   // group number, and its score
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        for (int l = 0; l < 64 && j < a.n_group; l += gsize, ++j) {
+          const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine[k]), l));
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const bool earlier = 64 * k + l + gsize <= lane + 64 * i;   // an earlier group than the lane's
+            before[i] += (v > mine[i] || (v == mine[i] && earlier)) ? 1 : 0;
+          }
         }
-        if (before >= a.topk_group) key[i] = 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (lane + 64 * i < a.E) sb[lane + 64 * i] = b[i];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // only this wave reads what it wrote
+      for (int g = lane; g < a.n_group; g += 64) {
+        float v1 = ninf, v2 = ninf;
+        for (int j = 0; j < gsize; ++j) join_two(v1, v2, sb[g * gsize + j], ninf);
+        float sum = gsize > 1 ? v1 + v2 : v1;
+        if (sum != sum) sum = ninf;
+        sg[g] = sum;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (lane + 64 * i >= a.E) continue;
+        const int g = (lane + 64 * i) / gsize;
+        for (int j = 0; j < a.n_group; ++j) before[i] += (sg[j] > sg[g] || (sg[j] == sg[g] && j < g)) ? 1 : 0;
       }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (before[i] >= a.topk_group) key[i] = 0u;
   }
   float sum = 0.0f, mine = 0.0f;
   int chosen = 0;
   for (int k = 0; k < a.top_k; ++k) {
     uint32_t m = key[0];
 #pragma unroll
-    for (int i = 1; i < kPerLane; ++i) m = key[i] > m ? key[i] : m;
+    for (int i = 1; i < N; ++i) m = key[i] > m ? key[i] : m;
     m = wave_max_u32(m);
     int e = -1;
     float w = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
+    for (int i = 0; i < N; ++i) {
       const uint64_t hit = __ballot(key[i] == m);
       if (e < 0 && hit != 0) {
         const int l = __builtin_ctzll(hit);
@@ -280,16 +309,83 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const float* __
       chosen = e;
     }
   }
-  if (lane < a.top_k) {
-    ids[lane] = chosen;
-    wts[lane] = (a.norm ? mine / sum : mine) * a.scaling;
-  }
+  id = chosen;
+  weight = (a.norm ? mine / sum : mine) * a.scaling;
 }
 
-__global__ void __launch_bounds__(64) moe_select(RouteArgs a, Ws ws) {
-  __shared__ float sb[64 * kPerLane], sg[64 * kPerLane];
-  const int t = blockIdx.x;
-  select_token(a, ws.logits, t, sb, sg, ws.ids + t * a.top_k, ws.wts + t * a.top_k);
+// ---------------------------------------------------------------- plan
+constexpr int kPlanWaves = 16;
+
+template <int N>
+__global__ void __launch_bounds__(64 * kPlanWaves) moe_plan(RouteArgs a, Ws ws, int32_t* ids_out, float* w_out) {
+  __shared__ float scratch[kPlanWaves][2][64 * N];
+  __shared__ int32_t ids[kMaxPairs];
+  __shared__ uint32_t takers[256];   // tokens that chose the expert
+  __shared__ int first[256];         // its first row
+  __shared__ int sums[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < 256) takers[tid] = 0u;
+  __syncthreads();
+  for (int t = wave; t < a.T; t += kPlanWaves) {
+    int id;
+    float w;
+    select_token<N>(a, ws.logits, t, scratch[wave][0], scratch[wave][1], id, w);
+    if (lane < a.top_k) {
+      const int p = t * a.top_k + lane;
+      ids[p] = id;
+      ws.wts[p] = w;
+      if (ids_out) ids_out[p] = id;
+      if (w_out) w_out[p] = w;
+      atomicOr(&takers[id], 1u << t);
+    }
+  }
+  __syncthreads();
+  // sums over the experts before each: rows, and experts that have any
+  uint32_t m = 0u;
+  int rows = 0, some = 0, r = 0, u = 0;
+  if (tid < 256) {
+    m = takers[tid];
+    r = rows = __popc(m);
+    u = some = m != 0u ? 1 : 0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int x = __shfl_up(r, off, 64), y = __shfl_up(u, off, 64);
+      if (lane >= off) {
+        r += x;
+        u += y;
+      }
+    }
+    if (lane == 63) {
+      sums[0][wave] = r;
+      sums[1][wave] = u;
+    }
+  }
+  __syncthreads();
+  int n = 0;
+  if (tid < 256) {
+    int br = 0, bu = 0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (v == wave) {
+        br = r - rows;
+        bu = u - some;
+      }
+      n += sums[1][v];
+    }
+    for (int v = 0; v < wave; ++v) {
+      br += sums[0][v];
+      bu += sums[1][v];
+    }
+    first[tid] = br;
+    if (m != 0u) ws.chosen[bu] = make_int4(tid, br, (int)m, n);
+    const int most = a.T * a.top_k < a.E ? a.T * a.top_k : a.E;
+    if (tid >= n && tid < most) ws.chosen[tid] = make_int4(-1, 0, 0, n);
+  }
+  __syncthreads();
+  for (int p = tid; p < a.T * a.top_k; p += 64 * kPlanWaves) {
+    const int e = ids[p], t = p / a.top_k;
+    ws.row_of[p] = first[e] + __popc(takers[e] & ((1u << t) - 1u));
+  }
 }
 
 // ---------------------------------------------------------------- expert rows
@@ -305,34 +401,50 @@ __device__ __forceinline__ v8h dequant8(uint32_t codes, _Float16 s16) {
   return r;
 }
 
-// A lane's part of one 128-k chunk of 16 rows: 32 codes and their two E4M3 bytes.
+// A lane's part of a 256-k block of 16 rows: 64 codes in two halves and their four E4M3 bytes, as loaded.
 struct Piece {
-  u32x4 codes;
-  uint32_t sf;
+  u32x4 codes[2];
+  uint32_t sf[2];   // plain: sf[0] holds all four; TW: two each
 };
 
-// Expert weights [E, rows, K]: plain (codes [rows, K / 2], E4M3 [rows, K / 16]) or TW, the layout of
-// nvfp4_pretile_weight of the stacked [E rows, K] matrix, in which a chunk of 16 rows is 1 KiB of codes
-// and 128 B of E4M3 pairs in lane order.  In the last chunk of a plain row with K % 128 = 64 lanes of
-// groups 2 and 3 have no k: they read the first half again, as zeros.
+// k of half d of lane group g in block c.  Plain rows: a lane's 64 k follow one another, so the four lanes
+// of a row read its whole 128-byte line and one dword of scales each.  TW (below): two chunks of 128.
 template <bool TW>
-__device__ __forceinline__ Piece load_piece(const uint8_t* __restrict__ w, const uint8_t* __restrict__ sf, int64_t row16,
-                                            int c, int K, int lane) {
-  Piece p;
+__device__ __forceinline__ int first_k(int c, int d, int g) {
+  return TW ? 256 * c + 128 * d + 32 * g : 256 * c + 64 * g + 32 * d;
+}
+
+// Expert weights [E, rows, K]: plain (codes [rows, K / 2], E4M3 [rows, K / 16]) or TW, the layout of
+// nvfp4_pretile_weight of the stacked [E rows, K] matrix, in which a 128-k chunk of 16 rows is 1 KiB of codes
+// and 128 B of E4M3 pairs in lane order.  K % 64 = 0 (TW: 128), so in the last block a lane's half is whole or
+// past the row; there it reads the block's start again, and scales() is 0.  (Nothing is done with what is
+// loaded before it is used: the loads after these must not wait.)
+template <bool TW>
+__device__ __forceinline__ void load_piece(const uint8_t* __restrict__ w, const uint8_t* __restrict__ sf, int64_t row16,
+                                           int c, int K, int lane, Piece& p) {
   if constexpr (TW) {
-    const int64_t tile = (row16 / 16) * (K / 128) + c;
-    p.codes = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + tile * 1024 + 16 * lane));
-    p.sf = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + tile * 128 + 2 * lane));
+    const int64_t tile = (row16 / 16) * (K / 128) + 2 * c;
+    const int64_t next = 256 * c + 128 < K ? tile + 1 : tile;
+    p.codes[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + tile * 1024 + 16 * lane));
+    p.codes[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + next * 1024 + 16 * lane));
+    p.sf[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + tile * 128 + 2 * lane));
+    p.sf[1] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + next * 128 + 2 * lane));
   } else {
+    const int g = lane >> 4;
+    const bool in = 256 * c + 64 * g < K;
     const int64_t row = row16 + (lane & 15);
-    int g = lane >> 4;
-    const bool in = 128 * c + 32 * g < K;
-    if (!in) g -= 2;
-    p.codes = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + row * (K / 2) + 64 * c + 16 * g));
-    p.sf = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + row * (K / 16) + 8 * c + 2 * g));
-    if (!in) p.sf = 0u;   // scale 0
+    const uint8_t* at = w + row * (K / 2) + 128 * c + (in ? 32 * g : 0);
+    p.codes[0] = *reinterpret_cast<const u32x4*>(at);
+    p.codes[1] = *reinterpret_cast<const u32x4*>(at + 16);
+    p.sf[0] = *reinterpret_cast<const uint32_t*>(sf + row * (K / 16) + 16 * c + (in ? 4 * g : 0));
   }
-  return p;
+}
+// The two scales of half d.
+template <bool TW>
+__device__ __forceinline__ void scales(const Piece& p, int d, int c, int K, int g, _Float16 (&s)[2]) {
+  const uint32_t b = first_k<TW>(c, d, g) < K ? (TW ? p.sf[d] : p.sf[0] >> (16 * d)) : 0u;
+  s[0] = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)b, 0);
+  s[1] = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)b, 1);
 }
 
 struct FcArgs {
@@ -343,28 +455,27 @@ struct FcArgs {
   int rows, K;           // rows of one expert, and their length
   int inter, hidden;
   int scaled;            // FC 1: src is scaled by up_scale(xmax)
-  int select;            // FC 1: the experts are selected here
   RouteArgs route;
-  int32_t* ids_out;
+  int32_t* ids_out;      // FC 1, one token
   float* w_out;
   void* out;             // FC 2: [T, hidden]
   int out_type;
   Ws ws;
 };
 
-// The activations of one chunk for 16 token slots as they are stored: lane (slot, g) holds
-// k = 128 c + 32 g .. + 31, as 32 FP16 or 32 binary32 numbers; zeros for slots without a token and past K.
+// The activations of one half of a block for 16 token slots as they are stored: lane (slot, g) holds 32 k,
+// as FP16 or binary32; zeros for slots without a token and past K.
 template <int FC>
 struct RawAct {
   u32x4 v[FC == 1 ? 4 : 8];
 };
 template <int FC>
-__device__ __forceinline__ void load_act(const void* src, int64_t row, bool there, int K, int c, int g, RawAct<FC>& r) {
+__device__ __forceinline__ void load_act(const void* src, int64_t row, bool there, int K, int k0, RawAct<FC>& r) {
   constexpr int kN = FC == 1 ? 4 : 8, kBytes = FC == 1 ? 2 : 4;
 #pragma unroll
   for (int m = 0; m < kN; ++m) r.v[m] = u32x4{0u, 0u, 0u, 0u};
-  if (there && 128 * c + 32 * g < K) {
-    const u32x4* p = reinterpret_cast<const u32x4*>((const char*)src + (row * K + 128 * c + 32 * g) * kBytes);
+  if (there && k0 < K) {
+    const u32x4* p = reinterpret_cast<const u32x4*>((const char*)src + (row * K + k0) * kBytes);
 #pragma unroll
     for (int m = 0; m < kN; ++m) r.v[m] = p[m];
   }
@@ -407,67 +518,76 @@ __device__ __forceinline__ v4f load_shared(const float* p) {
              __uint_as_float((uint32_t)(b >> 32))};
 }
 
-template <int FC, bool GATED, bool TW, int RT, int TT, int NW>
+// SEL > 0: fc1 of one token, whose experts (SEL 64 of them at most) every wave selects by itself.
+template <int FC, bool GATED, bool TW, int RT, int TT, int NW, int SEL>
 __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcArgs a) {
   constexpr int kThreads = 64 * NW;
-  constexpr int kAhead = FC == 1 ? 2 : 1;   // chunks of a wave in flight
+  constexpr int kPairsEach = (kMaxPairs + kThreads - 1) / kThreads;
   __shared__ v4f part[NW][RT * TT][64];
-  __shared__ float scratch[FC == 1 ? NW : 1][2][64 * kPerLane];
-  __shared__ int32_t ids[FC == 1 ? kMaxPairs : 1];
-  __shared__ float wts[kMaxPairs];
-  __shared__ int rows[kMaxPairs];         // FC 1: pair of each token slot; FC 2: row of each pair
-  __shared__ uint32_t used[8];            // experts that some token chose
+  __shared__ float scratch[SEL ? NW : 1][2][64 * (SEL ? SEL : 1)];
+  __shared__ float wts[FC == 2 ? kMaxPairs : 1];
+  __shared__ int rows[FC == 2 ? kMaxPairs : 1];   // row of each pair
   __shared__ uint32_t slot_max[16 * TT];
-  __shared__ int found[2];
+  __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, grp = lane >> 4;
   const int T = a.route.T, top_k = a.route.top_k, P = T * top_k;
 
-  int4 mine;   // this workgroup's expert, its first row, its rows, chosen experts
-  if constexpr (FC == 1) {
-    if (tid < 8) used[tid] = 0u;
-    if (tid < 16 * TT) slot_max[tid] = 0u;
-    if (a.select) {
-      for (int t = wave; t < T; t += NW)
-        select_token(a.route, a.ws.logits, t, scratch[wave][0], scratch[wave][1], ids + t * top_k, wts + t * top_k);
-    } else {
-      for (int p = tid; p < P; p += kThreads) {
-        ids[p] = a.ws.ids[p];
-        wts[p] = a.ws.wts[p];
-      }
-    }
-    __syncthreads();
-    for (int p = tid; p < P; p += kThreads) atomicOr(&used[ids[p] >> 5], 1u << (ids[p] & 31));
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      for (int p = tid; p < P; p += kThreads) {
-        if (a.select) a.ws.wts[p] = wts[p];
-        if (a.ids_out) a.ids_out[p] = ids[p];
-        if (a.w_out) a.w_out[p] = wts[p];
-      }
-    }
-    __syncthreads();
-    // the blockIdx.y-th chosen expert
-    int e = -1, n = 0;
+  // for the last workgroup of the row range: on its way before anything else
+  float pw[kPairsEach];
+  int pr[kPairsEach];
+  if constexpr (FC == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = used[i];
-      const int c = __popc(m);
-      if (e < 0 && (int)blockIdx.y < n + c) {
-        for (int j = (int)blockIdx.y - n; j > 0; --j) m &= m - 1;
-        e = 32 * i + __builtin_ctz(m);
-      }
-      n += c;
+    for (int i = 0; i < kPairsEach; ++i) {
+      const int p = tid + i * kThreads;
+      pw[i] = a.ws.wts[p < P ? p : 0];
+      pr[i] = a.ws.row_of[p < P ? p : 0];
     }
-    mine = make_int4(__builtin_amdgcn_readfirstlane(e), 0, 0, n);
+  } else {
+    if (tid < 16 * TT) slot_max[tid] = 0u;
+  }
+  // this workgroup's expert, its first row, its tokens, how many experts there are
+  int4 mine;
+  if constexpr (SEL > 0) {
+    int id;
+    float w;
+    select_token<SEL>(a.route, a.ws.logits, 0, scratch[wave][0], scratch[wave][1], id, w);
+    mine = make_int4(__builtin_amdgcn_readlane(id, (int)blockIdx.y), (int)blockIdx.y, 1, top_k);
+    if (blockIdx.x == 0 && wave == 0) {
+      if (lane == 0) a.ws.chosen[blockIdx.y] = mine;
+      if (blockIdx.y == 0 && lane < top_k) {
+        a.ws.wts[lane] = w;
+        a.ws.row_of[lane] = lane;
+        if (a.ids_out) a.ids_out[lane] = id;
+        if (a.w_out) a.w_out[lane] = w;
+      }
+    }
   } else {
     mine = a.ws.chosen[blockIdx.y];
-    mine.x = __builtin_amdgcn_readfirstlane(mine.x);
+    if (mine.x < 0) return;   // fewer experts than workgroups: the whole workgroup
   }
-  const int e = mine.x;
-  if (e < 0) {   // fewer experts than workgroups: the whole workgroup
-    if (FC == 1 && blockIdx.x == 0 && tid == 0) a.ws.chosen[blockIdx.y] = mine;
-    return;
+  const int e = mine.x, q0 = mine.y;
+  const uint32_t tokens = (uint32_t)mine.z;
+  const int ns = __popc(tokens);
+
+  // token slots of this lane: slot s is the s-th token of the mask
+  int64_t arow[TT];
+  uint32_t top[TT];   // bits of the largest value that the operand was, or will be, scaled by
+  bool there[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int s = 16 * j + r16;
+    there[j] = s < ns;
+    if constexpr (FC == 1) {
+      uint32_t m = tokens;
+      for (int i = 0; i < 16 * TT - 1; ++i) m = i < s ? m & (m - 1) : m;
+      arow[j] = there[j] ? __builtin_ctz(m) : 0;
+      top[j] = a.scaled ? a.ws.xmax[arow[j]] : 0u;
+    } else {
+      arow[j] = q0 + (there[j] ? s : 0);
+      top[j] = a.ws.hmax[arow[j]];
+    }
   }
 
   // weight rows of the tile's RT groups of 16: consecutive rows, or for SwiGLU in fc1 gate rows, then the up rows
@@ -479,93 +599,44 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
     const int r = !GATED ? col0 + 16 * i : i < RT / 2 ? col0 + 16 * i : a.inter + col0 + 16 * (i - RT / 2);
     row16[i] = (int64_t)e * a.rows + r;
   }
-  // the first chunks' weights are on their way while the tokens are looked up
-  const int chunks = (a.K + 127) / 128;
-  Piece w[kAhead][RT];
-  auto load_weights = [&](int c0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int c = c0 + d * NW < chunks ? c0 + d * NW : c0;   // past the end: again the first, not used
-        w[d][i] = load_piece<TW>(a.w, a.sf, row16[i], c, a.K, lane);
-      }
-  };
-  if (wave < chunks) load_weights(wave);
-
-  if constexpr (FC == 1) {
-    // its pairs in order (an expert appears at most once per token), and how many pairs come before them
-    if (wave == 0) {
-      int at = 0, before = 0;
-      for (int p0 = 0; p0 < P; p0 += 64) {
-        const int p = p0 + lane, id = p < P ? ids[p] : 256;
-        const uint64_t m = __ballot(id == e);
-        before += __popcll(__ballot(id < e));
-        if ((m >> lane) & 1ull) rows[at + __popcll(m & ((1ull << lane) - 1ull))] = p;
-        at += __popcll(m);
-      }
-      if (lane == 0) {
-        found[0] = before;
-        found[1] = at;
-      }
-      if (blockIdx.x == 0) {
-        if (lane == 0) a.ws.chosen[blockIdx.y] = make_int4(e, before, at, mine.w);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (lane < at) a.ws.row_of[rows[lane]] = before + lane;
-      }
-    }
-    lds_barrier();   // does not wait for the weights
-    mine.y = found[0];
-    mine.z = found[1];
-  }
-  const int q0 = mine.y, ns = mine.z;
-
-  // token slots of this lane
-  int64_t arow[TT];
-  float ascale[TT];
-  bool there[TT];
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int s = 16 * j + r16;
-    there[j] = s < ns;
-    arow[j] = FC == 1 ? (there[j] ? rows[s] / top_k : 0) : q0 + s;
-    ascale[j] = 1.0f;
-    if (FC == 2 && there[j]) ascale[j] = up_scale(a.ws.hmax[q0 + s]);
-  }
   v4f acc[RT][TT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const float ge = a.g[e];
 
-  for (int c0 = wave; c0 < chunks; c0 += NW * kAhead) {
-    if (c0 != wave) load_weights(c0);
-    RawAct<FC> raw[kAhead][TT];
+  const int blocks = (a.K + 255) / 256;
+  for (int c = wave; c < blocks; c += NW) {
+    Piece w[RT];
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d)
+    for (int i = 0; i < RT; ++i) load_piece<TW>(a.w, a.sf, row16[i], c, a.K, lane, w[i]);
+    RawAct<FC> raw[2][TT];
+    auto load_half = [&](int d) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < TT; ++j)
-        if (j == 0 || ns > 16 * j) load_act<FC>(a.src, arow[j], there[j], a.K, c0 + d * NW, grp, raw[d][j]);
+        if (j == 0 || ns > 16 * j) load_act<FC>(a.src, arow[j], there[j], a.K, first_k<TW>(c, d, grp), raw[d][j]);
+    };
+    load_half(0);
+    if constexpr (FC == 1) load_half(1);
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      if (c0 + d * NW >= chunks) break;   // the whole wave
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const _Float16 s0 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)w[d][i].sf, 0);
-        const _Float16 s1 = (_Float16)__builtin_amdgcn_cvt_f32_fp8((int)w[d][i].sf, 1);
-        w[d][i].sf = (uint32_t)__builtin_bit_cast(uint16_t, s0) | (uint32_t)__builtin_bit_cast(uint16_t, s1) << 16;
+    for (int d = 0; d < 2; ++d) {
+      if constexpr (FC == 2) {
+        if (d == 1) load_half(1);
       }
+      _Float16 sc[RT][2];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) scales<TW>(w[i], d, c, a.K, grp, sc[i]);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         v8h wv[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          wv[i] = dequant8(w[d][i].codes[m], __builtin_bit_cast(_Float16, (uint16_t)(m < 2 ? w[d][i].sf : w[d][i].sf >> 16)));
+        for (int i = 0; i < RT; ++i) wv[i] = dequant8(w[i].codes[d][m], sc[i][m / 2]);
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
           if (j > 0 && ns <= 16 * j) break;   // the whole workgroup
           v8h hi, lo;
-          act_operand<FC>(raw[d][j], m, ascale[j], hi, lo);
+          act_operand<FC>(raw[d][j], m, FC == 2 ? up_scale(top[j]) : 1.0f, hi, lo);
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[i], hi, acc[i][j], 0, 0, 0);
@@ -580,10 +651,13 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
 #pragma unroll
     for (int j = 0; j < TT; ++j) part[wave][i * TT + j][lane] = acc[i][j];
   if constexpr (FC == 2) {
-    // for the last workgroup of the row range
-    for (int p = tid; p < P; p += kThreads) {
-      rows[p] = a.ws.row_of[p];
-      wts[p] = a.ws.wts[p];
+#pragma unroll
+    for (int i = 0; i < kPairsEach; ++i) {
+      const int p = tid + i * kThreads;
+      if (p < P) {
+        rows[p] = pr[i];
+        wts[p] = pw[i];
+      }
     }
   }
   __syncthreads();
@@ -598,7 +672,6 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
     return s;
   };
   // results: lane (slot r16, columns 4 grp .. + 3) of a tile
-  const float ge = a.g[e];
   constexpr int kOutTiles = kCols / 16 * TT;
   for (int tile = wave; tile < kOutTiles; tile += NW) {
     const int i = tile / TT, j = tile % TT, slot = 16 * j + r16;
@@ -608,8 +681,9 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
     if constexpr (GATED) up = joined(tile + RT / 2 * TT);
     if (slot >= ns) continue;
     const int col = col0 + 16 * i + 4 * grp;
+    const uint32_t bits = TT == 1 || j == 0 ? top[0] : top[TT - 1];
+    const float f = FC == 2 || a.scaled ? ge / up_scale(bits) : ge;
     if constexpr (FC == 1) {
-      const float f = a.scaled ? ge / up_scale(a.ws.xmax[rows[slot] / top_k]) : ge;
       v4f hv;
       float m = 0.0f;
 #pragma unroll
@@ -620,7 +694,6 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
       *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(q0 + slot) * a.inter + col) = hv;
       atomicMax(&slot_max[slot], __float_as_uint(m));
     } else {
-      const float f = ge / up_scale(a.ws.hmax[q0 + slot]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) y[q] *= f;
       store_shared(a.ws.o + (int64_t)(q0 + slot) * a.hidden + col, y);
@@ -635,10 +708,10 @@ __global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcAr
     __syncthreads();
     if (tid == 0) {
       const uint32_t n = __hip_atomic_fetch_add(a.ws.count + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      found[0] = n == (uint32_t)(mine.w - 1) ? 1 : 0;
+      last = n == (uint32_t)(mine.w - 1) ? 1 : 0;
     }
     __syncthreads();
-    if (!found[0]) return;
+    if (!last) return;
     constexpr int kQuads = kCols / 4;
     for (int i = tid; i < T * kQuads; i += kThreads) {
       const int t = i / kQuads, col = col0 + 4 * (i - t * kQuads);
@@ -670,16 +743,33 @@ void launch_router(const MoeDecodeArgs& m, const Ws& ws, int P, hipStream_t s) {
   else moe_router<DT, 8><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
 }
 
-template <int FC, bool GATED, bool TW, int RT>
-void launch_rows(const FcArgs& a, int tiles, int experts, hipStream_t s) {
-  const dim3 grid(tiles, experts);
-  // eight waves where a workgroup has a compute unit for itself, four where several share one
-  if ((int64_t)tiles * experts <= 512) {
-    if (a.route.T <= 16) moe_expert_rows<FC, GATED, TW, RT, 1, 8><<<grid, dim3(512), 0, s>>>(a);
-    else moe_expert_rows<FC, GATED, TW, RT, 2, 8><<<grid, dim3(512), 0, s>>>(a);
+// 64 weight rows to a workgroup where there are enough of them to fill the chip, else 32; then eight waves where
+// a row is long enough for them.
+template <int FC, bool GATED, bool TW>
+void launch_rows(const FcArgs& a, int experts, hipStream_t s) {
+  const bool many = (int64_t)(a.rows / 64) * experts >= 512;
+  const dim3 grid(many ? a.rows / 64 : a.rows / 32, experts), block(256);
+  if constexpr (FC == 1) {
+    if (a.route.T == 1) {
+      const bool eight = a.K > 1024;
+      const dim3 one(a.rows / 32, experts), waves(eight ? 512 : 256);
+      if (a.route.E <= 64) {
+        if (eight) moe_expert_rows<FC, GATED, TW, 2, 1, 8, 1><<<one, waves, 0, s>>>(a);
+        else moe_expert_rows<FC, GATED, TW, 2, 1, 4, 1><<<one, waves, 0, s>>>(a);
+      } else {
+        if (eight) moe_expert_rows<FC, GATED, TW, 2, 1, 8, kPerLane><<<one, waves, 0, s>>>(a);
+        else moe_expert_rows<FC, GATED, TW, 2, 1, 4, kPerLane><<<one, waves, 0, s>>>(a);
+      }
+      return;
+    }
+  }
+  if (a.route.T <= 16) {
+    if (many) moe_expert_rows<FC, GATED, TW, 4, 1, 4, 0><<<grid, block, 0, s>>>(a);
+    else if (a.K > 1024) moe_expert_rows<FC, GATED, TW, 2, 1, 8, 0><<<grid, dim3(512), 0, s>>>(a);
+    else moe_expert_rows<FC, GATED, TW, 2, 1, 4, 0><<<grid, block, 0, s>>>(a);
   } else {
-    if (a.route.T <= 16) moe_expert_rows<FC, GATED, TW, RT, 1, 4><<<grid, dim3(256), 0, s>>>(a);
-    else moe_expert_rows<FC, GATED, TW, RT, 2, 4><<<grid, dim3(256), 0, s>>>(a);
+    if (many) moe_expert_rows<FC, GATED, TW, 4, 2, 4, 0><<<grid, block, 0, s>>>(a);
+    else moe_expert_rows<FC, GATED, TW, 2, 2, 4, 0><<<grid, block, 0, s>>>(a);
   }
 }
 
@@ -697,8 +787,12 @@ void launch_layer(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   a.ws = ws;
   a.out = m.out;
   a.out_type = m.dtype;
-  a.select = m.tokens <= kSelectAgain;
-  if (!a.select) moe_select<<<dim3(m.tokens), dim3(64), 0, s>>>(a.route, ws);
+  if (m.tokens > 1) {
+    const dim3 block(64 * kPlanWaves);
+    if (m.experts <= 64) moe_plan<1><<<dim3(1), block, 0, s>>>(a.route, ws, m.ids_out, m.w_out);
+    else if (m.experts <= 128) moe_plan<2><<<dim3(1), block, 0, s>>>(a.route, ws, m.ids_out, m.w_out);
+    else moe_plan<kPerLane><<<dim3(1), block, 0, s>>>(a.route, ws, m.ids_out, m.w_out);
+  }
   a.scaled = m.dtype == kBf16;
   a.src = a.scaled ? (const void*)ws.xs : m.x;
   a.w = m.w1;
@@ -706,15 +800,15 @@ void launch_layer(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   a.g = m.w1_g;
   a.rows = gated ? 2 * m.inter : m.inter;
   a.K = m.hidden;
-  if (gated) launch_rows<1, true, TW, 2>(a, a.rows / 32, experts, s);
-  else launch_rows<1, false, TW, 2>(a, a.rows / 32, experts, s);
+  if (gated) launch_rows<1, true, TW>(a, experts, s);
+  else launch_rows<1, false, TW>(a, experts, s);
   a.src = ws.h;
   a.w = m.w2;
   a.sf = m.w2_sf;
   a.g = m.w2_g;
   a.rows = m.hidden;
   a.K = m.inter;
-  launch_rows<2, false, TW, 4>(a, a.rows / 64, experts, s);
+  launch_rows<2, false, TW>(a, experts, s);
 }
 
 template <int DT>

@@ -123,19 +123,23 @@ def full(nv, layer, top_k, n_group, topk_group, norm=True, scaling=1.0, tiled=Fa
 @pytest.mark.parametrize("act", ["relu2", "swiglu"])
 @pytest.mark.parametrize("size", [(1, 64, 8, 8, 4, 512, 256), (2, 8, 2, 1, 1, 64, 64), (5, 16, 4, 4, 2, 320, 192),
                                   (16, 32, 6, 1, 1, 256, 128), (17, 16, 3, 8, 3, 192, 320), (32, 12, 4, 2, 1, 128, 64),
-                                  (31, 256, 16, 8, 4, 128, 64), (3, 100, 1, 10, 10, 1088, 64), (4, 1, 1, 1, 1, 2048, 128)])
+                                  (31, 256, 16, 8, 4, 128, 64), (3, 100, 1, 10, 10, 1088, 64), (4, 1, 1, 1, 1, 2048, 128),
+                                  (1, 128, 6, 8, 3, 1280, 192), (1, 256, 8, 16, 4, 64, 64), (1, 96, 5, 4, 2, 192, 64),
+                                  (2, 128, 8, 2, 1, 1088, 64), (32, 64, 8, 64, 20, 512, 512), (8, 250, 3, 5, 2, 64, 1088)])
 def test_against_binary64(nv, size, act, kind):
     tokens, experts, top_k, n_group, topk_group, hidden, inter = size
     full(nv, Layer(kind, tokens, experts, hidden, inter, act, seed=sum(size)), top_k, n_group, topk_group)
 
 
 @pytest.mark.parametrize("act", ["relu2", "swiglu"])
-@pytest.mark.parametrize("tokens", [1, 9, 20])
-def test_tiled_weights_are_the_same(nv, act, tokens):
-    layer = Layer("fp16", tokens, 16, 384, 256, act, seed=tokens)
-    a = run(nv, layer, 4, 4, 2, scaling=2.5)
-    b = run(nv, layer, 4, 4, 2, scaling=2.5, tiled=True)
-    assert all(torch.equal(u, v) for u, v in zip(a, b))
+@pytest.mark.parametrize("size", [(1, 384, 256), (9, 384, 256), (20, 256, 128), (3, 128, 640)])
+def test_tiled_weights(nv, act, size):
+    """The pre-tiled layout has the same values; the sums' order over k differs, so it is held against binary64 too."""
+    tokens, hidden, inter = size
+    layer = Layer("fp16", tokens, 16, hidden, inter, act, seed=tokens)
+    _, ids, wts = run(nv, layer, 4, 4, 2, scaling=2.5)
+    _, tids, twts = run(nv, layer, 4, 4, 2, scaling=2.5, tiled=True)
+    assert torch.equal(ids, tids) and torch.equal(wts, twts)
     full(nv, layer, 4, 4, 2, norm=False, scaling=2.5, tiled=True)
 
 
@@ -196,9 +200,10 @@ def test_tokens_do_not_depend_on_each_other(nv, tokens):
     out, ids, wts = run(nv, layer, 4, 4, 2)
     x = layer.x
     for t in (0, tokens - 1):
-        layer.x = x[t:t + 1].contiguous()
-        one, i1, w1 = run(nv, layer, 4, 4, 2)
-        assert torch.equal(i1, ids[t:t + 1]) and torch.equal(one[0], out[t])
+        layer.x = torch.randn(x.shape, generator=torch.Generator().manual_seed(t)).to(x.dtype)
+        layer.x[t] = x[t]
+        other, i1, w1 = run(nv, layer, 4, 4, 2)
+        assert torch.equal(i1[t], ids[t]) and torch.equal(w1[t], wts[t]) and torch.equal(other[t], out[t])
 
 
 def test_workspace_streams_and_replays(nv):

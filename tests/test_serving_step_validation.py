@@ -43,7 +43,7 @@ def test_moe_decode_status(nv):
               dict(groups=3), dict(kept=0), dict(kept=5), dict(hidden=192, tiled=1), dict(inter=192, tiled=1), dict(x=None),
               dict(router=None), dict(bias=None), dict(w1=None), dict(w1_sf=None), dict(w1_g=None), dict(w2=None),
               dict(w2_sf=None), dict(w2_g=None), dict(out=None), dict(x=EIGHT), dict(router=EIGHT), dict(w1=EIGHT),
-              dict(w2=EIGHT), dict(out=FOUR), dict(w1_sf=ODD), dict(w2_sf=ODD), dict(bias=TWO), dict(w1_g=TWO),
+              dict(w2=EIGHT), dict(out=FOUR), dict(w1_sf=TWO), dict(w2_sf=TWO), dict(bias=TWO), dict(w1_g=TWO),
               dict(w2_g=TWO), dict(ids=TWO), dict(w=TWO)]:
         refuses(fn, MOE, nv.NVFP4_EINVAL, **c)
     for c in [dict(tokens=33), dict(hidden=65536 + 64), dict(inter=65536 + 64)]:
