@@ -958,22 +958,6 @@ def _check_rope(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out,
     _need_gpu(k, v, slot_map, k_cache, v_cache, q, positions, inv_freq, q_out, k_out)
 
 
-def _plain_rope(q, k, positions, inv_freq, q_out, k_out, dev) -> bool:
-    try:
-        dt, (T, _, D) = k.dtype, k.shape
-        for x, y in ((q, q_out), (k, k_out)):
-            if x is not None and not (x.dtype is dt and x.shape == (T, x.shape[1], D) and x.stride(2) == 1 and
-                                      x.get_device() == dev):
-                return False
-            if y is not None and not (x is not None and y.dtype is dt and y.shape == x.shape and y.stride(2) == 1 and
-                                      y.get_device() == dev and (y.data_ptr() != x.data_ptr() or _steps(y) == _steps(x))):
-                return False
-        return (_is(positions, torch.int32, (T,), dev) and
-                _is(inv_freq, torch.float32, (inv_freq.shape[0],), dev))
-    except (AttributeError, IndexError, TypeError, ValueError):
-        return False
-
-
 def rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
                   inv_freq: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   interleaved: bool = False, mscale: float = 1.0, q_out: torch.Tensor | None = None,
@@ -985,19 +969,48 @@ def rope_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, posi
     given; may be q itself); k_out (may be k itself) receives the rotated keys too.  Nothing is written for
     tokens of a negative position (in a new q_out their rows are undefined); slots outside the cache are
     skipped.  q may be None."""
-    dev = _gpu_of(k)
-    if dev < 0 or not (_plain_kv_write(k, v, slot_map, k_cache, v_cache, dev) and
-                       _plain_rope(q, k, positions, inv_freq, q_out, k_out, dev)):
+    dev, i32, ints = _gpu_of(k), torch.int32, torch.int64
+    try:
+        shape, dt, cache = k.shape, k.dtype, k_cache.shape
+        T, Hk, D = shape
+        pages, heads, page_size, dim = cache
+        kt, kh, k1 = k.stride()
+        vt, vh, v1 = v.stride()
+        half = inv_freq.shape[0]
+        plain = (dev >= 0 and T > 0 and dt in _TYPE_CODE and heads == Hk and dim == D and k1 == v1 == 1 and
+                 v.dtype is dt and v.shape == shape and v.get_device() == dev and
+                 _is(k_cache, dt, cache, dev) and _is(v_cache, dt, cache, dev) and
+                 _is(slot_map, ints, (T,), dev) and _is(positions, i32, (T,), dev) and
+                 _is(inv_freq, torch.float32, (half,), dev))
+        Hq = qt = qh = qot = qoh = kot = koh = 0
+        if plain and q is not None:
+            _, Hq, _ = of_q = q.shape
+            qt, qh, q1 = q.stride()
+            plain = q.dtype is dt and of_q == (T, Hq, D) and q1 == 1 and q.get_device() == dev
+            if plain and q_out is not None:
+                qot, qoh, q1 = q_out.stride()
+                plain = (q_out.dtype is dt and q_out.shape == of_q and q1 == 1 and q_out.get_device() == dev and
+                         (q_out.data_ptr() != q.data_ptr() or (qot == qt and qoh == qh)))
+        elif q_out is not None:
+            plain = False
+        if plain and k_out is not None:
+            kot, koh, k1 = k_out.stride()
+            plain = (k_out.dtype is dt and k_out.shape == shape and k1 == 1 and k_out.get_device() == dev and
+                     (k_out.data_ptr() != k.data_ptr() or (kot == kt and koh == kh)))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        plain = False
+    if not plain:
         _check_rope(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out, k_out)
-    T, Hk, D = k.shape
-    pages, _, page_size, _ = k_cache.shape
-    half, Hq = inv_freq.shape[0], 0 if q is None else q.shape[1]
+        T, Hk, D = k.shape
+        pages, _, page_size, _ = k_cache.shape
+        half, Hq = inv_freq.shape[0], 0 if q is None else q.shape[1]
+        (qt, qh), (kt, kh), (vt, vh) = (0, 0) if q is None else _steps(q), _steps(k), _steps(v)
+        (qot, qoh), (kot, koh) = ((0, 0) if t is None else _steps(t) for t in (q_out, k_out))
     if (Hq | Hk | page_size | D | 2 * half) >> 31:
         _need_32_bits(q_heads=Hq, kv_heads=Hk, page_size=page_size, head_dim=D, rotary_dim=2 * half)
     if q is not None and q_out is None:
         q_out = _fresh(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
-    (qt, qh), (kt, kh), (vt, vh) = (0, 0) if q is None else _steps(q), _steps(k), _steps(v)
-    (qot, qoh), (kot, koh) = ((0, 0) if t is None else _steps(t) for t in (q_out, k_out))
+        qot, qoh = Hq * D, D
     st = _lib.nvfp4_rope_kv_write(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPE_CODE[k.dtype],
                                   T, Hq, Hk, D, qt, qh, kt, kh, vt, vh, positions.data_ptr(), inv_freq.data_ptr(),
                                   2 * half, 1 if interleaved else 0, mscale, slot_map.data_ptr(),

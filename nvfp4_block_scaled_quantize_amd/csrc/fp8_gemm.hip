@@ -1,14 +1,19 @@
 // fp8_gemm.hip -- y[B, N] = sum_k a[b, k] sa[b, k / 128] w[n, k] sw[n / 128, k / 128] for E4M3 operands
 // with binary32 scales per 128 (activations 1 x 128, weights 128 x 128), for gfx950.
 //
-// The matrix instruction that takes 128 k at once (v_mfma_f32_16x16x128_f8f6f4) forms the sum of one
-// K-block in binary32 from zero; the scale of the block, sa sw, is then applied by one fma per output
-// into the running binary32 sum.  The weight is the instruction's first operand: a lane's four results
-// are four consecutive columns of one row of y, so one product sa sw serves a whole 16 x 16 tile.  An
-// instruction takes 32 clocks, its four fmas 16 clocks of the vector pipe beside it.
+// The matrix instructions form the sum of one K-block in binary32 from zero (v_mfma_f32_32x32x64_f8f6f4 twice, or
+// v_mfma_f32_16x16x128_f8f6f4 once); the scale of the block, sa sw, is then applied by one fma per output
+// into the running binary32 sum.  The weight is the instruction's first operand: a lane's results lie in one
+// row of y, in runs of four consecutive columns, so one product sa sw serves a whole tile.  The instructions of
+// a tile and block take four times as long as its fmas, which run beside them.
 //
-// The k order inside a block is free as long as both operands share it: lane group g = lane / 16 takes the
-// 16-byte pieces g and g + 4 of its row's 128 bytes.
+// What the instruction adds is not quite binary32: it joins eight neighbouring products at a time, each cut to a
+// multiple of 2^(ea + eb - 13), 2^(ea + eb) the power of two in the largest of them (measured: beside 256 * 256 a
+// product of 8 stays, of 12 becomes 8, of 4 vanishes; the older v_mfma_f32_16x16x32_fp8_fp8 does the same).  For
+// normal operands a block's sums are off by 2^-16 of their size, an eighth of FP16's rounding.  Products in FP16
+// would avoid it at half the rate.
+//
+// The k order inside a block is free as long as both operands share it.
 #include <type_traits>
 
 #include "device_common.h"
@@ -22,10 +27,19 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
 // Sum of one K-block for a 16 x 16 tile: rows from w, columns from a.
 __device__ __forceinline__ v4f mfma_block(const v8i& w, const v8i& a) {
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// The same for a 32 x 32 tile in two instructions of 64 k: pieces (w0, a0) and (w1, a1) of the block.
+__device__ __forceinline__ v16f mfma_block32(const v8i (&w)[2], const v8i (&a)[2]) {
+  const v16f zero = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  const v16f p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[0], a[0], zero, 0, 0, 0, 0, 0, 0);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[1], a[1], p, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ v8i join(u32x4 p, u32x4 q) {
@@ -59,27 +73,38 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, bool wide, c
 // the next stage (global -> LDS, 16 bytes a lane) are in flight while a stage is computed.  LDS holds
 // the rows' 128 bytes with piece p of row r at p ^ ((r / 2) mod 8): the 16 lanes of an operand read
 // touch 16 different places of 16 bytes.
-template <int TT, int FT, int WT, int WF>
+//
+// The copies' lines bound it: every 64 x 16 bytes of a copy are eight lines of the L2, but one binary32 scale for
+// each of 64 rows is 64 lines.  So the scales of a row are copied four blocks at a time (SB = 4) where their rows
+// are aligned to that, and each line that the workgroups of a die share is asked for ahead by one of them.
+// CUT: K ends inside a block.
+template <int TT, int FT, int WT, int WF, int SB>
 struct Tile {
   static constexpr int kWaves = WT * WF;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kRowsA = 16 * TT * WT, kRowsW = 16 * FT * WF;
+  static constexpr int kRowsA = 32 * TT * WT, kRowsW = 32 * FT * WF;
   static constexpr int kCopies = (kRowsA + kRowsW) / 8 / kWaves;   // 16-byte copies of a wave and stage
   static constexpr int kWOff = 0, kAOff = kRowsW * 128;
-  static constexpr int kSAOff = (kRowsW + kRowsA) * 128;           // scales of the rows of a
-  static constexpr int kSWOff = kSAOff + kRowsA * 4;               // scales of the blocks of w, 64 entries
-  static constexpr int kStage = kSWOff + 256;
+  // scales of the rows of a, and of (up to 64) blocks of w: SB = 1: one block's with every stage; SB = 4: four
+  // blocks' in two buffers of their own
+  static constexpr int kScales = (kRowsA + 64) * 4 * SB;
+  static constexpr int kStage = (kRowsW + kRowsA) * 128 + (SB == 1 ? kScales : 0);
+  static constexpr int kSAOff = SB == 1 ? (kRowsW + kRowsA) * 128 : 2 * kStage;
+  static constexpr int kSWOff = kSAOff + kRowsA * 4 * SB;
+  static constexpr int kNowhere = 2 * kStage + (SB == 4 ? 2 * kScales : 0);   // 256 SB bytes per wave that nothing reads
+  static constexpr int kBytes = kNowhere + 256 * SB * kWaves;
   static constexpr int kScaleWaves = kRowsA / 64;                  // waves that copy scales of a
-  static_assert(kRowsW % (8 * kWaves) == 0 && kRowsA % (8 * kWaves) == 0, "a copy stays in one operand");
+  static_assert(kRowsW % (8 * kCopies) == 0 && kRowsA % (8 * kCopies) == 0 && kCopies % 2 == 0,
+                "a wave copies rows of one operand");
   static_assert(kScaleWaves < kWaves && kRowsA % 64 == 0, "one wave at least copies the scales of w");
-  static_assert(128 % (16 * FT) == 0, "a wave's columns share the scales of w");
+  static_assert(128 % (32 * FT) == 0, "a wave's columns share the scales of w");
 };
 
-template <int DT, int TT, int FT, int WT, int WF>
+template <int DT, int TT, int FT, int WT, int WF, int SB, bool CUT>
 __global__ void __launch_bounds__(64 * WT * WF)
 fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
-  using C = Tile<TT, FT, WT, WF>;
-  __shared__ __attribute__((aligned(256))) unsigned char lds[2 * C::kStage];
+  using C = Tile<TT, FT, WT, WF, SB>;
+  __shared__ __attribute__((aligned(256))) unsigned char lds[C::kBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave % WT, wf = wave / WT;
@@ -102,21 +127,27 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 
   // copies: wave w, copy i moves rows 8 (w kCopies + i) .. + 7 of the stage (rows of w first), lane l the
   // piece (l mod 8) of row l / 8.  Rows past an operand's end repeat its last row (never stored).
+  const bool copies_w = wave < C::kRowsW / 8 / C::kCopies;
+  const int row0 = copies_w ? 8 * wave * C::kCopies : 8 * wave * C::kCopies - C::kRowsW;   // first row of this wave's copies
+  const int last_row = copies_w ? g.N - 1 - n0 : g.B - 1 - m0;
+  // the piece: (l mod 8) ^ ((row / 2) mod 8), row = 8 i + l / 8 (row0 is a multiple of 16)
+  const int piece = (lane & 7) ^ (lane >> 4);   // even i; odd i: ^ 4
   uint32_t from[C::kCopies];
-  const int sub = lane >> 3;
 #pragma unroll
   for (int i = 0; i < C::kCopies; ++i) {
-    const int c = wave * C::kCopies + i;
-    const bool is_w = c < C::kRowsW / 8;
-    const int r = is_w ? 8 * c + sub : 8 * c - C::kRowsW + sub;
-    const int last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
-    from[i] = (uint32_t)(r < last ? r : last) * (uint32_t)K;
+    const int r = row0 + 8 * i + (lane >> 3);
+    from[i] = (uint32_t)(r < last_row ? r : last_row) * (uint32_t)K + 16u * (piece ^ (4 * (i & 1)));
+    asm volatile("" : "+v"(from[i]));   // one register each (the product's upper half is not kept)
   }
-  // the piece a lane copies: (l mod 8) ^ ((row / 2) mod 8), row = 8 c + l / 8
-  const int piece0 = (lane & 7) ^ (lane >> 4);   // even c; odd c: ^ 4
-  const int tail = (K & 127) / 16;               // pieces of the last block, 0: whole
-  const uint8_t* wbase = g.w + (int64_t)n0 * K;
-  const uint8_t* abase = g.a + (int64_t)m0 * K;
+  const uint8_t* base = copies_w ? g.w + (int64_t)n0 * K : g.a + (int64_t)m0 * K;
+  // in a last block that is cut short, pieces past the row's end are copied from zeros
+  const int tail = (K & 127) / 16;              // pieces of the last block, 0: whole
+  const bool gone[2] = {tail != 0 && piece >= tail, tail != 0 && (piece ^ 4) >= tail};
+  // lines of a later stage, brought into the L2 by a copy to a place nothing reads: the workgroups of a row (column)
+  // of tiles take every eighth (fourth) row each
+  const int r_ahead = copies_w ? row0 + 8 * (lane & 7) + (tm & 7) : row0 + 4 * (lane & 15) + (tn & 3);
+  uint32_t from_ahead = (uint32_t)(r_ahead < last_row ? r_ahead : last_row) * (uint32_t)K;
+  asm volatile("" : "+v"(from_ahead));
   // scales: a wave copies those of 64 rows of a, or the blocks of w
   const bool scales_a = wave < C::kScaleWaves;
   const float* sbase;
@@ -131,83 +162,147 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     sbase = g.ws + (int64_t)(n0 / 128) * nkb;
     sfrom = (uint32_t)(lane < b ? lane : b) * (uint32_t)nkb * 4u;
   }
-  const uint32_t sto = scales_a ? C::kSAOff + 256 * wave : C::kSWOff;
 
-  auto issue = [&](int kb) __attribute__((always_inline)) {
+  // copies [lo, hi) of stage kb, and with the first the scales.  There is no branch around them (the additions
+  // between the instructions would move behind it): a stage past the last copies the last block again.
+  auto issue = [&](int kb, int lo, int hi) __attribute__((always_inline)) {
     const uint32_t st = l0 + (kb & 1) * C::kStage;
-    const bool cut = tail != 0 && kb == nkb - 1;
-#pragma unroll
-    for (int i = 0; i < C::kCopies; ++i) {
-      const int c = wave * C::kCopies + i;   // kCopies is even: the parity of c is that of i
-      int p = piece0 ^ (4 * (i & 1));
-      if (cut && p >= tail) p = 0;           // past the row's end: any place of the row, cleared later
-      const bool is_w = c < C::kRowsW / 8;
-      dma16((is_w ? wbase : abase) + (int64_t)kb * 128, from[i] + 16u * p, st + c * 1024);
+    const bool end = kb >= nkb - 1;
+    kb = kb < nkb ? kb : nkb - 1;
+    const uint8_t* at = base + (int64_t)kb * 128;
+    if (lo == 0) {
+      const uint32_t to = scales_a ? C::kSAOff + 256 * SB * wave : C::kSWOff;
+      if constexpr (SB == 1) {
+        dma4(sbase + kb, sfrom, st + to);
+      } else {
+        // with the first of four blocks; with the others one line goes nowhere
+        const bool first = (kb & 3) == 0;
+        const uint32_t four = l0 + (kb >> 2 & 1) * C::kScales + to;
+        dma16(sbase + (kb & ~3), first ? sfrom : 0u, first ? four : l0 + C::kNowhere + 256 * SB * wave);
+      }
     }
-    dma4(sbase + kb, sfrom, st + sto);
+#pragma unroll
+    for (int i = lo; i < hi; ++i) {
+      const uint32_t to = st + (wave * C::kCopies + i) * 1024;
+      if constexpr (CUT)
+        dma16_at(gone[i & 1] && end ? reinterpret_cast<const uint8_t*>(kZeros) : at + from[i], to);
+      else
+        dma16(at, from[i], to);
+    }
+  };
+  auto issue_ahead = [&](int kb) __attribute__((always_inline)) {
+    dma4(base + (int64_t)(kb < nkb ? kb : nkb - 1) * 128, from_ahead, l0 + C::kNowhere + 256 * SB * wave);
   };
 
-  v4f acc[TT][FT];
+  v16f acc[TT][FT];
 #pragma unroll
   for (int j = 0; j < TT; ++j)
 #pragma unroll
-    for (int i = 0; i < FT; ++i) acc[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[j][i][q] = 0.0f;
 
-  const int r16 = lane & 15, grp = lane >> 4;
-  const uint32_t operand = r16 * 128 + 16 * (grp ^ (r16 >> 1 & 7));   // piece grp; piece grp + 4: ^ 64
-  typedef const __attribute__((address_space(3))) unsigned char* lptr;
+  // lane (row r32, half h): pieces h and h + 2 of its row for the first instruction, h + 4 and h + 6 for the second
+  const int r32 = lane & 31, h = lane >> 5;
+  const uint32_t operand = r32 * 128 + 16 * (h ^ (r32 >> 1 & 7));   // piece h; others: ^ 32, ^ 64, ^ 96
   auto read = [&](uint32_t at) __attribute__((always_inline)) {
     typedef const __attribute__((address_space(3))) u32x4* vptr;
     return *(vptr)(uintptr_t)at;
   };
-
-  issue(0);
-  for (int kb = 0; kb < nkb; ++kb) {
-    // this wave's copies have landed and its reads of the other buffer are done; then everyone's
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const uint32_t st = l0 + (kb & 1) * C::kStage;
-    if (kb + 1 < nkb) {
-      issue(kb + 1);
-    } else if (tail) {
-      // the pieces past the rows' end: zeros
-      for (int i = tid; i < (C::kRowsA + C::kRowsW) * 8; i += C::kThreads) {
-        const int r = i >> 3;
-        if (((i & 7) ^ (r >> 1 & 7)) >= tail) *reinterpret_cast<u32x4*>(lds + (kb & 1) * C::kStage + 16 * i) = u32x4{0, 0, 0, 0};
-      }
-      __syncthreads();
-    }
-    const uint32_t wl = st + C::kWOff + wf * (16 * FT) * 128 + operand;
-    const uint32_t al = st + C::kAOff + wt * (16 * TT) * 128 + operand;
-    v8i wv[FT];
-#pragma unroll
-    for (int i = 0; i < FT; ++i) wv[i] = join(read(wl + 2048 * i), read((wl ^ 64) + 2048 * i));
+  auto read1 = [&](uint32_t at) __attribute__((always_inline)) {
     typedef const __attribute__((address_space(3))) float* fptr;
-    const float sw = *(fptr)(uintptr_t)(st + C::kSWOff + 4 * ((n0 % 128 + wf * 16 * FT) / 128));
-    const uint32_t sa = st + C::kSAOff + 4 * (wt * 16 * TT + r16);
+    return *(fptr)(uintptr_t)at;
+  };
+
+  // Tile t = (j, i): its block sum is added to the running sum while the next tile's is formed.
+  v8i av[2][2], wv[FT][2];
+  v16f sum[2];
+  float scale[2], sw;
+  auto add = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      acc[t / FT][t % FT][q] = __builtin_fmaf(sum[t & 1][q], scale[t / FT & 1], acc[t / FT][t % FT][q]);
+  };
+  const uint32_t wl = l0 + wf * (32 * FT) * 128 + operand, al = l0 + C::kAOff + wt * (32 * TT) * 128 + operand;
+  const uint32_t sal = l0 + C::kSAOff + 4 * SB * (wt * 32 * TT + r32);
+  const uint32_t swl = l0 + C::kSWOff + 4 * SB * ((n0 % 128 + wf * 32 * FT) / 128);
+  auto scales_of = [&](int kb) __attribute__((always_inline)) {
+    return SB == 1 ? (kb & 1) * C::kStage : (kb >> 2 & 1) * C::kScales + 4 * (kb & 3);
+  };
+  auto read_a = [&](int kb, int j) __attribute__((always_inline)) {
+    const uint32_t at = al + (kb & 1) * C::kStage;
+    av[j & 1][0] = join(read(at + 4096 * j), read((at ^ 32) + 4096 * j));
+    av[j & 1][1] = join(read((at ^ 64) + 4096 * j), read((at ^ 96) + 4096 * j));
+    scale[j & 1] = read1(sal + scales_of(kb) + 128 * SB * j);
+  };
+  auto read_w = [&](int kb, int i) __attribute__((always_inline)) {
+    const uint32_t at = wl + (kb & 1) * C::kStage;
+    wv[i][0] = join(read(at + 4096 * i), read((at ^ 32) + 4096 * i));
+    wv[i][1] = join(read((at ^ 64) + 4096 * i), read((at ^ 96) + 4096 * i));
+  };
+
+  // Stage kb is computed while stage kb + 1 lands.  Before its last row of tiles everyone's copies of the next
+  // stage have landed and everyone's reads of this one are done: the next stage's first operands are read
+  // during that row, and the copies of stage kb + 2 follow into this stage's buffer, spread over it and the
+  // next stage's first rows.
+  constexpr int kParts = TT - 1;
+  constexpr int kEach = (C::kCopies + kParts - 1) / kParts;
+  constexpr int kRowsOf = (C::kCopies + kEach - 1) / kEach;   // rows of tiles that copies follow
+  static_assert(TT % 2 == 0 && kRowsOf < TT, "copies, then the line ahead, then the wait");
+  issue(0, 0, C::kCopies);
+  issue_ahead(2);
+  issue(1, 0, kEach);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kEach + 2) : "memory");
+  read_a(0, 0);
+#pragma unroll
+  for (int i = 0; i < FT; ++i) read_w(0, i);
+  sw = read1(swl + scales_of(0));
+  for (int kb = 0; kb < nkb; ++kb) {
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-      const v8i av = join(read(al + 2048 * j), read((al ^ 64) + 2048 * j));
-      const float s = *(fptr)(uintptr_t)(sa + 64 * j) * sw;
+      // all but the line ahead have landed
+      if (j + 1 == TT) asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      scale[j & 1] *= sw;
 #pragma unroll
       for (int i = 0; i < FT; ++i) {
-        const v4f p = mfma_block(wv[i], av);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j][i][q] = __builtin_fmaf(p[q], s, acc[j][i][q]);
+        const int t = j * FT + i;
+        sum[t & 1] = mfma_block32(wv[i], av[j & 1]);
+        if (t >= 1) add(t - 1);
+        if (i == 0) {
+          if (j + 1 < TT) read_a(kb, j + 1);
+          else read_a(kb + 1, 0);
+        }
+        if (j + 1 == TT) read_w(kb + 1, i);
       }
+      if (j + 1 == TT) {
+        add(TT * FT - 1);
+        sw = read1(swl + scales_of(kb + 1));
+      }
+      if (j + 1 == TT) {
+        issue(kb + 2, 0, kEach);
+      } else if (j + 1 < kRowsOf) {
+        issue(kb + 1, (j + 1) * kEach, (j + 2) * kEach < C::kCopies ? (j + 2) * kEach : C::kCopies);
+      }
+      if (j + 1 == kRowsOf || (kRowsOf == 1 && j == 0)) issue_ahead(kb + 3);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy into LDS outlives the workgroup
 
   const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int m = m0 + (wt * TT + j) * 16 + r16;
+    const int m = m0 + (wt * TT + j) * 32 + r32;
     if (m >= g.B) continue;
     uint16_t* row = (uint16_t*)g.y + (int64_t)m * g.N;
 #pragma unroll
-    for (int i = 0; i < FT; ++i) {
-      const int n = n0 + (wf * FT + i) * 16 + 4 * grp;
-      if (n < g.N) store4<DT>(row, n, g.N, vec, acc[j][i]);
-    }
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + (wf * FT + i) * 32 + 8 * q + 4 * h;
+        const v4f v = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+        if (n < g.N) store4<DT>(row, n, g.N, vec, v);
+      }
   }
 }
 
@@ -337,9 +432,17 @@ fp8_gemm_stream(Fp8GemmArgs g) {
 
 template <int DT, int TT, int FT, int WT, int WF>
 void tiles(const Fp8GemmArgs& g, hipStream_t s) {
-  using C = Tile<TT, FT, WT, WF>;
+  using C = Tile<TT, FT, WT, WF, 4>;
   const int tm = (g.B + C::kRowsA - 1) / C::kRowsA, tn = (g.N + C::kRowsW - 1) / C::kRowsW;
-  fp8_gemm_tiles<DT, TT, FT, WT, WF><<<dim3((unsigned)(tm * tn)), dim3(C::kThreads), 0, s>>>(g, tm, tn);
+  const dim3 grid((unsigned)(tm * tn)), block(C::kThreads);
+  const bool cut = g.K % 128 != 0, four = (g.K + 127) / 128 % 4 == 0 && (((uintptr_t)g.as | (uintptr_t)g.ws) % 16) == 0;
+  if (four) {
+    if (cut) fp8_gemm_tiles<DT, TT, FT, WT, WF, 4, true><<<grid, block, 0, s>>>(g, tm, tn);
+    else fp8_gemm_tiles<DT, TT, FT, WT, WF, 4, false><<<grid, block, 0, s>>>(g, tm, tn);
+  } else {
+    if (cut) fp8_gemm_tiles<DT, TT, FT, WT, WF, 1, true><<<grid, block, 0, s>>>(g, tm, tn);
+    else fp8_gemm_tiles<DT, TT, FT, WT, WF, 1, false><<<grid, block, 0, s>>>(g, tm, tn);
+  }
 }
 
 template <int DT, int TT, int FT, int U>
@@ -353,8 +456,8 @@ void launch(const Fp8GemmArgs& g, hipStream_t s) {
   if (g.B <= 32) return stream<DT, 2, 2, 2>(g, s);
   if (g.B <= 64) return stream<DT, 4, 2, 2>(g, s);
   const int64_t big = (int64_t)((g.B + 255) / 256) * ((g.N + 255) / 256);
-  if (big >= 192) return tiles<DT, 8, 4, 2, 4>(g, s);
-  return tiles<DT, 4, 4, 2, 2>(g, s);
+  if (big >= 192) return tiles<DT, 4, 2, 2, 4>(g, s);
+  return tiles<DT, 2, 2, 2, 2>(g, s);
 }
 
 }  // namespace
