@@ -306,6 +306,134 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   }
 }
 
+// ---------------------------------------------------------------- small tiles (a few hundred rows)
+// Where tiles of the sizes above would leave compute units idle: 64 rows of a by 128 rows of w, eight waves in two
+// groups that take the K-blocks in turn, three stage buffers each (two stages in flight while one is computed).
+// Bound by the lines between the L2 and the compute units.
+constexpr int kSmRowsA = 64, kSmRowsW = 128, kSmStages = 3, kSmGroups = 2, kSmWaves = 4;   // waves of a group
+constexpr int kSmCopies = (kSmRowsA + kSmRowsW) / 8 / kSmWaves;                            // of a wave and stage
+constexpr int kSmAOff = kSmRowsW * 128, kSmSAOff = (kSmRowsW + kSmRowsA) * 128, kSmSWOff = kSmSAOff + kSmRowsA * 4;
+constexpr int kSmStage = kSmSWOff + 256;
+static_assert(kSmRowsW % (8 * kSmWaves) == 0 && kSmRowsA == 64, "a copy stays in one operand; one wave copies the scales of a");
+
+template <int DT, bool CUT>
+__global__ void __launch_bounds__(64 * kSmWaves * kSmGroups)
+fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(256))) unsigned char lds[kSmGroups * kSmStages * kSmStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave / kSmWaves, gw = wave % kSmWaves;
+  // the tiles of one column of tiles (the same rows of w) follow one another on one XCD
+  int t = blockIdx.x;
+  const int total = tiles_m * tiles_n;
+  if (total % 8 == 0) t = (t & 7) * (total / 8) + (t >> 3);
+  const int tn = t / tiles_m, tm = t - tn * tiles_m;
+  const int K = g.K, nkb = (K + 127) / 128;
+  const int m0 = tm * kSmRowsA, n0 = tn * kSmRowsW;
+  const uint32_t l0 = lds_addr(lds) + group * (kSmStages * kSmStage);
+
+  // copies: wave w, copy i moves rows 8 (4 i + w) .. + 7 of the stage (rows of w first), lane l the piece (l mod 8)
+  // of row l / 8
+  uint32_t from[kSmCopies];
+  const int tail = (K & 127) / 16;
+  const int piece = (lane & 7) ^ (((gw & 1) * 4 + (lane >> 4)) & 7);   // ^ ((row / 2) mod 8), row = 32 i + 8 w + l / 8
+  const bool gone = tail != 0 && piece >= tail;
+#pragma unroll
+  for (int i = 0; i < kSmCopies; ++i) {
+    const bool is_w = 32 * i < kSmRowsW;
+    const int r = 32 * i + 8 * gw + (lane >> 3) - (is_w ? 0 : kSmRowsW), last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
+    from[i] = (uint32_t)(r < last ? r : last) * (uint32_t)K + 16u * piece;
+    asm volatile("" : "+v"(from[i]));   // one register each
+  }
+  const uint8_t* wbase = g.w + (int64_t)n0 * K;
+  const uint8_t* abase = g.a + (int64_t)m0 * K;
+  const float* sbase = gw == 0 ? g.as + (int64_t)m0 * nkb : g.ws + (int64_t)(n0 / 128) * nkb;
+  const uint32_t sfrom = gw == 0 ? (uint32_t)(lane < g.B - 1 - m0 ? lane : g.B - 1 - m0) * (uint32_t)nkb * 4u : 0u;
+  // stage s of this group: block s kSmGroups + group, or again the last block (not used)
+  auto issue = [&](int s, uint32_t buf) __attribute__((always_inline)) {
+    const int b = s * kSmGroups + group, kb = b < nkb ? b : nkb - 1;
+    const bool end = kb == nkb - 1;
+#pragma unroll
+    for (int i = 0; i < kSmCopies; ++i) {
+      const uint8_t* at = (32 * i < kSmRowsW ? wbase : abase) + (int64_t)kb * 128;
+      const uint32_t to = l0 + buf + (4 * i + gw) * 1024;
+      if constexpr (CUT) dma16_at(gone && end ? reinterpret_cast<const uint8_t*>(kZeros) : at + from[i], to);
+      else dma16(at, from[i], to);
+    }
+    dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? kSmSAOff : kSmSWOff));
+  };
+
+  const int wt = gw & 1, wf = gw >> 1;   // this wave's 32 rows of a and 64 of w
+  const int r32 = lane & 31, h = lane >> 5;
+  const uint32_t operand = r32 * 128 + 16 * (h ^ (r32 >> 1 & 7));
+  auto read = [&](uint32_t at) __attribute__((always_inline)) {
+    typedef const __attribute__((address_space(3))) u32x4* vptr;
+    return *(vptr)(uintptr_t)at;
+  };
+  auto read1 = [&](uint32_t at) __attribute__((always_inline)) {
+    typedef const __attribute__((address_space(3))) float* fptr;
+    return *(fptr)(uintptr_t)at;
+  };
+  v16f acc[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[i][q] = 0.0f;
+  auto compute = [&](uint32_t buf) __attribute__((always_inline)) {
+    const uint32_t al = l0 + buf + kSmAOff + wt * 4096 + operand, wl = l0 + buf + wf * 8192 + operand;
+    const v8i a[2] = {join(read(al), read(al ^ 32)), join(read(al ^ 64), read(al ^ 96))};
+    const float s = read1(l0 + buf + kSmSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + kSmSWOff);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const v8i w[2] = {join(read(wl + 4096 * i), read((wl ^ 32) + 4096 * i)),
+                        join(read((wl ^ 64) + 4096 * i), read((wl ^ 96) + 4096 * i))};
+      const v16f p = mfma_block32(w, a);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][q] = __builtin_fmaf(p[q], s, acc[i][q]);
+    }
+  };
+
+  const int steps = (nkb + kSmGroups - 1) / kSmGroups;
+  uint32_t buf = 0, fill = 0;
+#pragma unroll
+  for (int s = 0; s < kSmStages - 1; ++s) {
+    issue(s, fill);
+    fill += kSmStage;
+  }
+  for (int s = 0; s < steps; ++s) {
+    // this wave's copies of stage s have landed and its reads of the stage before are done; then everyone's
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kSmStages - 2) * (kSmCopies + 1)) : "memory");
+    issue(s + kSmStages - 1, fill);
+    fill = fill + kSmStage < kSmStages * kSmStage ? fill + kSmStage : 0;
+    if (s * kSmGroups + group < nkb) compute(buf);
+    buf = buf + kSmStage < kSmStages * kSmStage ? buf + kSmStage : 0;
+  }
+  // the second group's sums go to the first through LDS
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  v4f* part = reinterpret_cast<v4f*>(lds);
+  if (group == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        part[((gw * 2 + i) * 4 + q) * 64 + lane] = v4f{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+  }
+  __syncthreads();
+  const int m = m0 + wt * 32 + r32;
+  if (group == 1 || m >= g.B) return;
+  const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
+  uint16_t* row = (uint16_t*)g.y + (int64_t)m * g.N;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + wf * 64 + 32 * i + 8 * q + 4 * h;
+      v4f v = part[((gw * 2 + i) * 4 + q) * 64 + lane];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] += acc[i][4 * q + r];
+      if (n < g.N) store4<DT>(row, n, g.N, vec, v);
+    }
+}
+
 // ---------------------------------------------------------------- streams (few rows)
 // A workgroup holds all rows of a (up to 16 TT) against 16 FT rows of w; its eight waves take the
 // K-blocks in turn, straight from memory into registers (every byte of w is read once, by one wave),
@@ -445,6 +573,14 @@ void tiles(const Fp8GemmArgs& g, hipStream_t s) {
   }
 }
 
+template <int DT>
+void small_tiles(const Fp8GemmArgs& g, hipStream_t s) {
+  const int tm = (g.B + kSmRowsA - 1) / kSmRowsA, tn = (g.N + kSmRowsW - 1) / kSmRowsW;
+  const dim3 grid((unsigned)(tm * tn)), block(64 * kSmWaves * kSmGroups);
+  if (g.K % 128 != 0) fp8_gemm_small<DT, true><<<grid, block, 0, s>>>(g, tm, tn);
+  else fp8_gemm_small<DT, false><<<grid, block, 0, s>>>(g, tm, tn);
+}
+
 template <int DT, int TT, int FT, int U>
 void stream(const Fp8GemmArgs& g, hipStream_t s) {
   fp8_gemm_stream<DT, TT, FT, U><<<dim3((unsigned)((g.N + 16 * FT - 1) / (16 * FT))), dim3(64 * kSsWaves), 0, s>>>(g);
@@ -455,9 +591,19 @@ void launch(const Fp8GemmArgs& g, hipStream_t s) {
   if (g.B <= 16) return stream<DT, 1, 1, 4>(g, s);
   if (g.B <= 32) return stream<DT, 2, 2, 2>(g, s);
   if (g.B <= 64) return stream<DT, 4, 2, 2>(g, s);
-  const int64_t big = (int64_t)((g.B + 255) / 256) * ((g.N + 255) / 256);
-  if (big >= 192) return tiles<DT, 4, 2, 2, 4>(g, s);
-  return tiles<DT, 2, 2, 2, 2>(g, s);
+  // The sizes of tiles: microseconds per K-block for a round of tiles over the chip, as measured (K = 4096 to 8192),
+  // times the rounds.  64 x 128: 256 at a time (512 x 4096 x 4096: 16 us, with 128 x 128 tiles 27 us); 128 x 128: 512 at
+  // a time, faster while there is one per compute unit (2048 x 2048 x 4096: 28 us, with 64 x 128 33 us); 256 x 256: 256
+  // at a time (4096 x 8192 x 8192: 254 us; 1000 x 8192 x 8192: 127 us, with 128 x 128 tiles 89 us).
+  auto count = [&](int64_t rows, int64_t cols) { return (g.B + rows - 1) / rows * ((g.N + cols - 1) / cols); };
+  auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+  const int64_t mid = count(128, 128);
+  const double small_cost = 0.6 * rounds(count(64, 128), 256);
+  const double mid_cost = mid <= 256 ? 0.9 : 1.4 * rounds(mid, 512);
+  const double big_cost = 2.0 * rounds(count(256, 256), 256);
+  if (big_cost <= small_cost && big_cost <= mid_cost) return tiles<DT, 4, 2, 2, 4>(g, s);
+  if (mid_cost < small_cost) return tiles<DT, 2, 2, 2, 2>(g, s);
+  return small_tiles<DT>(g, s);
 }
 
 }  // namespace
