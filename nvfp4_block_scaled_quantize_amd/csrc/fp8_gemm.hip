@@ -82,7 +82,7 @@ template <int TT, int FT, int WT, int WF, int SB>
 struct Tile {
   static constexpr int kWaves = WT * WF;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kRowsA = 32 * TT * WT, kRowsW = 32 * FT * WF;
+  static constexpr int kRowsA = 16 * TT * WT, kRowsW = 16 * FT * WF;
   static constexpr int kCopies = (kRowsA + kRowsW) / 8 / kWaves;   // 16-byte copies of a wave and stage
   static constexpr int kWOff = 0, kAOff = kRowsW * 128;
   // scales of the rows of a, and of (up to 64) blocks of w: SB = 1: one block's with every stage; SB = 4: four
@@ -97,7 +97,7 @@ struct Tile {
   static_assert(kRowsW % (8 * kCopies) == 0 && kRowsA % (8 * kCopies) == 0 && kCopies % 2 == 0,
                 "a wave copies rows of one operand");
   static_assert(kScaleWaves < kWaves && kRowsA % 64 == 0, "one wave at least copies the scales of w");
-  static_assert(128 % (32 * FT) == 0, "a wave's columns share the scales of w");
+  static_assert(128 % (16 * FT) == 0, "a wave's columns share the scales of w");
 };
 
 template <int DT, int TT, int FT, int WT, int WF, int SB, bool CUT>
@@ -194,17 +194,14 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     dma4(base + (int64_t)(kb < nkb ? kb : nkb - 1) * 128, from_ahead, l0 + C::kNowhere + 256 * SB * wave);
   };
 
-  v16f acc[TT][FT];
+  v4f acc[TT][FT];
 #pragma unroll
   for (int j = 0; j < TT; ++j)
 #pragma unroll
-    for (int i = 0; i < FT; ++i)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[j][i][q] = 0.0f;
+    for (int i = 0; i < FT; ++i) acc[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // lane (row r32, half h): pieces h and h + 2 of its row for the first instruction, h + 4 and h + 6 for the second
-  const int r32 = lane & 31, h = lane >> 5;
-  const uint32_t operand = r32 * 128 + 16 * (h ^ (r32 >> 1 & 7));   // piece h; others: ^ 32, ^ 64, ^ 96
+  const int r16 = lane & 15, grp = lane >> 4;
+  const uint32_t operand = r16 * 128 + 16 * (grp ^ (r16 >> 1 & 7));   // piece grp; piece grp + 4: ^ 64
   auto read = [&](uint32_t at) __attribute__((always_inline)) {
     typedef const __attribute__((address_space(3))) u32x4* vptr;
     return *(vptr)(uintptr_t)at;
@@ -214,41 +211,37 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     return *(fptr)(uintptr_t)at;
   };
 
-  // Tile t = (j, i): its block sum is added to the running sum while the next tile's is formed.
-  v8i av[2][2], wv[FT][2];
-  v16f sum[2];
-  float scale[2], sw;
+  // Tile t = (j, i): its block sum is added to the running sum two instructions later, when it is there.
+  v8i av[4], wv[FT];
+  v4f sum[3];
+  float scale[4], sw;
   auto add = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-      acc[t / FT][t % FT][q] = __builtin_fmaf(sum[t & 1][q], scale[t / FT & 1], acc[t / FT][t % FT][q]);
+    for (int q = 0; q < 4; ++q)
+      acc[t / FT][t % FT][q] = __builtin_fmaf(sum[t % 3][q], scale[t / FT & 3], acc[t / FT][t % FT][q]);
   };
-  const uint32_t wl = l0 + wf * (32 * FT) * 128 + operand, al = l0 + C::kAOff + wt * (32 * TT) * 128 + operand;
-  const uint32_t sal = l0 + C::kSAOff + 4 * SB * (wt * 32 * TT + r32);
-  const uint32_t swl = l0 + C::kSWOff + 4 * SB * ((n0 % 128 + wf * 32 * FT) / 128);
+  const uint32_t wl = l0 + C::kWOff + wf * (16 * FT) * 128 + operand, al = l0 + C::kAOff + wt * (16 * TT) * 128 + operand;
+  const uint32_t sal = l0 + C::kSAOff + 4 * SB * (wt * 16 * TT + r16);
+  const uint32_t swl = l0 + C::kSWOff + 4 * SB * ((n0 % 128 + wf * 16 * FT) / 128);
   auto scales_of = [&](int kb) __attribute__((always_inline)) {
     return SB == 1 ? (kb & 1) * C::kStage : (kb >> 2 & 1) * C::kScales + 4 * (kb & 3);
   };
   auto read_a = [&](int kb, int j) __attribute__((always_inline)) {
-    const uint32_t at = al + (kb & 1) * C::kStage;
-    av[j & 1][0] = join(read(at + 4096 * j), read((at ^ 32) + 4096 * j));
-    av[j & 1][1] = join(read((at ^ 64) + 4096 * j), read((at ^ 96) + 4096 * j));
-    scale[j & 1] = read1(sal + scales_of(kb) + 128 * SB * j);
+    const uint32_t buf = (kb & 1) * C::kStage;
+    av[j & 3] = join(read(al + buf + 2048 * j), read((al ^ 64) + buf + 2048 * j));
+    scale[j & 3] = read1(sal + scales_of(kb) + 64 * SB * j);
   };
-  auto read_w = [&](int kb, int i) __attribute__((always_inline)) {
-    const uint32_t at = wl + (kb & 1) * C::kStage;
-    wv[i][0] = join(read(at + 4096 * i), read((at ^ 32) + 4096 * i));
-    wv[i][1] = join(read((at ^ 64) + 4096 * i), read((at ^ 96) + 4096 * i));
+  auto read_w = [&](uint32_t buf, int i) __attribute__((always_inline)) {
+    wv[i] = join(read(wl + buf + 2048 * i), read((wl ^ 64) + buf + 2048 * i));
   };
 
   // Stage kb is computed while stage kb + 1 lands.  Before its last row of tiles everyone's copies of the next
   // stage have landed and everyone's reads of this one are done: the next stage's first operands are read
   // during that row, and the copies of stage kb + 2 follow into this stage's buffer, spread over it and the
   // next stage's first rows.
-  constexpr int kParts = TT - 1;
-  constexpr int kEach = (C::kCopies + kParts - 1) / kParts;
-  constexpr int kRowsOf = (C::kCopies + kEach - 1) / kEach;   // rows of tiles that copies follow
-  static_assert(TT % 2 == 0 && kRowsOf < TT, "copies, then the line ahead, then the wait");
+  constexpr int kEach = TT >= 8 ? 2 : 4;
+  constexpr int kAheadRow = C::kCopies / kEach - 1;   // the row after the last copies
+  static_assert(TT % 4 == 0 && C::kCopies % kEach == 0 && kAheadRow < TT - 1, "copies, then the line ahead, then the wait");
   issue(0, 0, C::kCopies);
   issue_ahead(2);
   issue(1, 0, kEach);
@@ -256,34 +249,37 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   read_a(0, 0);
 #pragma unroll
   for (int i = 0; i < FT; ++i) read_w(0, i);
+  read_a(0, 1);
   sw = read1(swl + scales_of(0));
   for (int kb = 0; kb < nkb; ++kb) {
+    const uint32_t other = (~kb & 1) * C::kStage;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
       // all but the line ahead have landed
       if (j + 1 == TT) asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      scale[j & 1] *= sw;
+      if (j + 2 < TT) read_a(kb, j + 2);
+      if (j + 1 == TT) read_a(kb + 1, 0);
+      scale[j & 3] *= sw;
 #pragma unroll
       for (int i = 0; i < FT; ++i) {
         const int t = j * FT + i;
-        sum[t & 1] = mfma_block32(wv[i], av[j & 1]);
-        if (t >= 1) add(t - 1);
-        if (i == 0) {
-          if (j + 1 < TT) read_a(kb, j + 1);
-          else read_a(kb + 1, 0);
-        }
-        if (j + 1 == TT) read_w(kb + 1, i);
+        sum[t % 3] = mfma_block(wv[i], av[j & 3]);
+        if (t >= 2) add(t - 2);
+        if (j + 1 == TT) read_w(other, i);
       }
       if (j + 1 == TT) {
+        add(TT * FT - 2);
         add(TT * FT - 1);
         sw = read1(swl + scales_of(kb + 1));
+        read_a(kb + 1, 1);
       }
       if (j + 1 == TT) {
         issue(kb + 2, 0, kEach);
-      } else if (j + 1 < kRowsOf) {
-        issue(kb + 1, (j + 1) * kEach, (j + 2) * kEach < C::kCopies ? (j + 2) * kEach : C::kCopies);
+      } else if (j < kAheadRow) {
+        issue(kb + 1, (j + 1) * kEach, (j + 2) * kEach);
+      } else if (j == kAheadRow) {
+        issue_ahead(kb + 3);
       }
-      if (j + 1 == kRowsOf || (kRowsOf == 1 && j == 0)) issue_ahead(kb + 3);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -292,34 +288,36 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
-    const int m = m0 + (wt * TT + j) * 32 + r32;
+    const int m = m0 + (wt * TT + j) * 16 + r16;
     if (m >= g.B) continue;
     uint16_t* row = (uint16_t*)g.y + (int64_t)m * g.N;
 #pragma unroll
-    for (int i = 0; i < FT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + (wf * FT + i) * 32 + 8 * q + 4 * h;
-        const v4f v = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-        if (n < g.N) store4<DT>(row, n, g.N, vec, v);
-      }
+    for (int i = 0; i < FT; ++i) {
+      const int n = n0 + (wf * FT + i) * 16 + 4 * grp;
+      if (n < g.N) store4<DT>(row, n, g.N, vec, acc[j][i]);
+    }
   }
 }
 
 // ---------------------------------------------------------------- small tiles (a few hundred rows)
-// Where tiles of the sizes above would leave compute units idle: 64 rows of a by 128 rows of w, eight waves in two
-// groups that take the K-blocks in turn, three stage buffers each (two stages in flight while one is computed).
+// Where tiles of the sizes above would leave compute units idle: 64 rows of a by 64 FT rows of w, eight waves in two
+// groups that take the K-blocks in turn, S stage buffers each (S - 1 stages in flight while one is computed).
 // Bound by the lines between the L2 and the compute units.
-constexpr int kSmRowsA = 64, kSmRowsW = 128, kSmStages = 3, kSmGroups = 2, kSmWaves = 4;   // waves of a group
-constexpr int kSmCopies = (kSmRowsA + kSmRowsW) / 8 / kSmWaves;                            // of a wave and stage
-constexpr int kSmAOff = kSmRowsW * 128, kSmSAOff = (kSmRowsW + kSmRowsA) * 128, kSmSWOff = kSmSAOff + kSmRowsA * 4;
-constexpr int kSmStage = kSmSWOff + 256;
-static_assert(kSmRowsW % (8 * kSmWaves) == 0 && kSmRowsA == 64, "a copy stays in one operand; one wave copies the scales of a");
+constexpr int kSmRowsA = 64, kSmGroups = 2, kSmWaves = 4;   // waves of a group
+template <int FT, int S>
+struct Small {
+  static constexpr int kRowsW = 64 * FT;
+  static constexpr int kCopies = (kSmRowsA + kRowsW) / 8 / kSmWaves;   // of a wave and stage
+  static constexpr int kAOff = kRowsW * 128, kSAOff = (kRowsW + kSmRowsA) * 128, kSWOff = kSAOff + kSmRowsA * 4;
+  static constexpr int kStage = kSWOff + 256;
+  static_assert(kSmRowsA == 64, "a copy stays in one operand; one wave copies the scales of a");
+};
 
-template <int DT, bool CUT>
+template <int DT, int FT, int S, bool CUT>
 __global__ void __launch_bounds__(64 * kSmWaves * kSmGroups)
 fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(256))) unsigned char lds[kSmGroups * kSmStages * kSmStage];
+  using C = Small<FT, S>;
+  __shared__ __attribute__((aligned(256))) unsigned char lds[kSmGroups * S * C::kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave / kSmWaves, gw = wave % kSmWaves;
   // the tiles of one column of tiles (the same rows of w) follow one another on one XCD
@@ -328,19 +326,19 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   if (total % 8 == 0) t = (t & 7) * (total / 8) + (t >> 3);
   const int tn = t / tiles_m, tm = t - tn * tiles_m;
   const int K = g.K, nkb = (K + 127) / 128;
-  const int m0 = tm * kSmRowsA, n0 = tn * kSmRowsW;
-  const uint32_t l0 = lds_addr(lds) + group * (kSmStages * kSmStage);
+  const int m0 = tm * kSmRowsA, n0 = tn * C::kRowsW;
+  const uint32_t l0 = lds_addr(lds) + group * (S * C::kStage);
 
   // copies: wave w, copy i moves rows 8 (4 i + w) .. + 7 of the stage (rows of w first), lane l the piece (l mod 8)
   // of row l / 8
-  uint32_t from[kSmCopies];
+  uint32_t from[C::kCopies];
   const int tail = (K & 127) / 16;
   const int piece = (lane & 7) ^ (((gw & 1) * 4 + (lane >> 4)) & 7);   // ^ ((row / 2) mod 8), row = 32 i + 8 w + l / 8
   const bool gone = tail != 0 && piece >= tail;
 #pragma unroll
-  for (int i = 0; i < kSmCopies; ++i) {
-    const bool is_w = 32 * i < kSmRowsW;
-    const int r = 32 * i + 8 * gw + (lane >> 3) - (is_w ? 0 : kSmRowsW), last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
+  for (int i = 0; i < C::kCopies; ++i) {
+    const bool is_w = 32 * i < C::kRowsW;
+    const int r = 32 * i + 8 * gw + (lane >> 3) - (is_w ? 0 : C::kRowsW), last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
     from[i] = (uint32_t)(r < last ? r : last) * (uint32_t)K + 16u * piece;
     asm volatile("" : "+v"(from[i]));   // one register each
   }
@@ -353,16 +351,16 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     const int b = s * kSmGroups + group, kb = b < nkb ? b : nkb - 1;
     const bool end = kb == nkb - 1;
 #pragma unroll
-    for (int i = 0; i < kSmCopies; ++i) {
-      const uint8_t* at = (32 * i < kSmRowsW ? wbase : abase) + (int64_t)kb * 128;
+    for (int i = 0; i < C::kCopies; ++i) {
+      const uint8_t* at = (32 * i < C::kRowsW ? wbase : abase) + (int64_t)kb * 128;
       const uint32_t to = l0 + buf + (4 * i + gw) * 1024;
       if constexpr (CUT) dma16_at(gone && end ? reinterpret_cast<const uint8_t*>(kZeros) : at + from[i], to);
       else dma16(at, from[i], to);
     }
-    dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? kSmSAOff : kSmSWOff));
+    dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? C::kSAOff : C::kSWOff));
   };
 
-  const int wt = gw & 1, wf = gw >> 1;   // this wave's 32 rows of a and 64 of w
+  const int wt = gw & 1, wf = gw >> 1;   // this wave's 32 rows of a and 32 FT of w
   const int r32 = lane & 31, h = lane >> 5;
   const uint32_t operand = r32 * 128 + 16 * (h ^ (r32 >> 1 & 7));
   auto read = [&](uint32_t at) __attribute__((always_inline)) {
@@ -373,17 +371,17 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     typedef const __attribute__((address_space(3))) float* fptr;
     return *(fptr)(uintptr_t)at;
   };
-  v16f acc[2];
+  v16f acc[FT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[i][q] = 0.0f;
   auto compute = [&](uint32_t buf) __attribute__((always_inline)) {
-    const uint32_t al = l0 + buf + kSmAOff + wt * 4096 + operand, wl = l0 + buf + wf * 8192 + operand;
+    const uint32_t al = l0 + buf + C::kAOff + wt * 4096 + operand, wl = l0 + buf + wf * (4096 * FT) + operand;
     const v8i a[2] = {join(read(al), read(al ^ 32)), join(read(al ^ 64), read(al ^ 96))};
-    const float s = read1(l0 + buf + kSmSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + kSmSWOff);
+    const float s = read1(l0 + buf + C::kSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + C::kSWOff);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < FT; ++i) {
       const v8i w[2] = {join(read(wl + 4096 * i), read((wl ^ 32) + 4096 * i)),
                         join(read((wl ^ 64) + 4096 * i), read((wl ^ 96) + 4096 * i))};
       const v16f p = mfma_block32(w, a);
@@ -395,27 +393,27 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   const int steps = (nkb + kSmGroups - 1) / kSmGroups;
   uint32_t buf = 0, fill = 0;
 #pragma unroll
-  for (int s = 0; s < kSmStages - 1; ++s) {
+  for (int s = 0; s < S - 1; ++s) {
     issue(s, fill);
-    fill += kSmStage;
+    fill += C::kStage;
   }
   for (int s = 0; s < steps; ++s) {
     // this wave's copies of stage s have landed and its reads of the stage before are done; then everyone's
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kSmStages - 2) * (kSmCopies + 1)) : "memory");
-    issue(s + kSmStages - 1, fill);
-    fill = fill + kSmStage < kSmStages * kSmStage ? fill + kSmStage : 0;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (C::kCopies + 1)) : "memory");
+    issue(s + S - 1, fill);
+    fill = fill + C::kStage < S * C::kStage ? fill + C::kStage : 0;
     if (s * kSmGroups + group < nkb) compute(buf);
-    buf = buf + kSmStage < kSmStages * kSmStage ? buf + kSmStage : 0;
+    buf = buf + C::kStage < S * C::kStage ? buf + C::kStage : 0;
   }
   // the second group's sums go to the first through LDS
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   v4f* part = reinterpret_cast<v4f*>(lds);
   if (group == 1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < FT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        part[((gw * 2 + i) * 4 + q) * 64 + lane] = v4f{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+        part[((gw * FT + i) * 4 + q) * 64 + lane] = v4f{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
   }
   __syncthreads();
   const int m = m0 + wt * 32 + r32;
@@ -423,11 +421,11 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
   uint16_t* row = (uint16_t*)g.y + (int64_t)m * g.N;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int n = n0 + wf * 64 + 32 * i + 8 * q + 4 * h;
-      v4f v = part[((gw * 2 + i) * 4 + q) * 64 + lane];
+      const int n = n0 + wf * (32 * FT) + 32 * i + 8 * q + 4 * h;
+      v4f v = part[((gw * FT + i) * 4 + q) * 64 + lane];
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] += acc[i][4 * q + r];
       if (n < g.N) store4<DT>(row, n, g.N, vec, v);
@@ -435,127 +433,80 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 }
 
 // ---------------------------------------------------------------- streams (few rows)
-// A workgroup holds all rows of a (up to 16 TT) against 16 FT rows of w; its eight waves take the
-// K-blocks in turn, straight from memory into registers (every byte of w is read once, by one wave),
-// and their sums are joined through LDS.  Bound by the bytes of w.
-constexpr int kSsWaves = 8;
-
-template <int DT, int TT, int FT, int U>
-__global__ void __launch_bounds__(64 * kSsWaves)
+// A workgroup holds all rows of a (up to 16) against 16 rows of w; its NW waves take the K-blocks in turn, kAhead of
+// them in flight a wave, straight from memory into registers (every byte of w is read once, by one wave), and their
+// sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (NW kAhead) loads.
+constexpr int kAhead = 4;
+template <int DT, int NW>
+__global__ void __launch_bounds__(64 * NW)
 fp8_gemm_stream(Fp8GemmArgs g) {
-  __shared__ v4f part[kSsWaves][TT * FT][64];
+  __shared__ v4f part[NW][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, grp = lane >> 4;
   const int K = g.K, nkb = (K + 127) / 128;
-  const int n0 = blockIdx.x * 16 * FT;
-  const uint8_t* wrow[FT];
-  const uint8_t* arow[TT];
-  const float* srow[TT];
+  const int n0 = blockIdx.x * 16;
+  const int wr = n0 + r16 < g.N ? n0 + r16 : g.N - 1, ar = r16 < g.B ? r16 : g.B - 1;
+  const uint8_t* wrow = g.w + (int64_t)wr * K;
+  const uint8_t* arow = g.a + (int64_t)ar * K;
+  const float* srow = g.as + (int64_t)ar * nkb;
+  const float* swrow = g.ws + (int64_t)(n0 / 128) * nkb;
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const v8i& w, const v8i& a, float scale) __attribute__((always_inline)) {
+    const v4f p = mfma_block(w, a);
 #pragma unroll
-  for (int i = 0; i < FT; ++i) {
-    const int n = n0 + 16 * i + r16;
-    wrow[i] = g.w + (int64_t)(n < g.N ? n : g.N - 1) * K + 16 * grp;
-  }
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int m = 16 * j + r16 < g.B ? 16 * j + r16 : g.B - 1;
-    arow[j] = g.a + (int64_t)m * K + 16 * grp;
-    srow[j] = g.as + (int64_t)m * nkb;
-  }
-  const float* swrow = g.ws + (int64_t)(n0 / 128) * nkb;   // 16 FT divides 128
-  v4f acc[TT][FT];
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-#pragma unroll
-    for (int i = 0; i < FT; ++i) acc[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(p[q], scale, acc[q]);
+  };
 
   // K-blocks that are whole; a last one that is not goes through the masked turn below
   const int whole = K / 128;
-  int kb = wave;
-  for (; kb < whole; kb += kSsWaves * U) {
-    u32x4 wq[U][FT][2], aq[U][TT][2];
-    float sa[U][TT], sw[U];
+  for (int kb = wave; kb < whole; kb += NW * kAhead) {
+    u32x4 wq[kAhead][2], aq[kAhead][2];
+    float sa[kAhead], sw[kAhead];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = kb + kSsWaves * u < whole ? kb + kSsWaves * u : kb;   // past the end: again the first, with scale 0
-      const int64_t o = (int64_t)b * 128;
+    for (int u = 0; u < kAhead; ++u) {
+      const int b = kb + NW * u < whole ? kb + NW * u : kb;   // past the end: again the first, not used
 #pragma unroll
-      for (int i = 0; i < FT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          wq[u][i][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[i] + o + 64 * h));
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) aq[u][j][h] = *reinterpret_cast<const u32x4*>(arow[j] + o + 64 * h);
-        sa[u][j] = srow[j][b];
+      for (int h = 0; h < 2; ++h) {
+        wq[u][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow + 16 * grp + (int64_t)b * 128 + 64 * h));
+        aq[u][h] = *reinterpret_cast<const u32x4*>(arow + 16 * grp + (int64_t)b * 128 + 64 * h);
       }
+      sa[u] = srow[b];
       sw[u] = swrow[b];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u > 0 && kb + kSsWaves * u >= whole) break;   // the same for the whole wave
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const float s = sa[u][j] * sw[u];
-#pragma unroll
-        for (int i = 0; i < FT; ++i) {
-          const v4f p = mfma_block(join(wq[u][i][0], wq[u][i][1]), join(aq[u][j][0], aq[u][j][1]));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[j][i][q] = __builtin_fmaf(p[q], s, acc[j][i][q]);
-        }
-      }
+    for (int u = 0; u < kAhead; ++u) {
+      if (u > 0 && kb + NW * u >= whole) break;   // the same for the whole wave
+      add(join(wq[u][0], wq[u][1]), join(aq[u][0], aq[u][1]), sa[u] * sw[u]);
     }
   }
-  if (whole < nkb && wave == whole % kSsWaves) {
+  if (whole < nkb && wave == whole % NW) {
+    // pieces of 16 bytes past the row's end count as zeros; what is read in their place is the row's first piece
     const int valid = (K & 127) / 16;
-    const u32x4 zero = {0, 0, 0, 0};
-    const bool in0 = grp < valid, in1 = grp + 4 < valid;
-    const int64_t o0 = in0 ? (int64_t)whole * 128 : 0, o1 = in1 ? (int64_t)whole * 128 + 64 : 0;
-    v8i wv[FT];
+    const bool in[2] = {grp < valid, grp + 4 < valid};
+    u32x4 wv[2], av[2];
 #pragma unroll
-    for (int i = 0; i < FT; ++i) {
-      // K >= 128 is not given: the pieces read in place of missing ones are the row's first (16 grp < K
-      // does not hold for a short row, so those lanes read the row's start)
-      const uint8_t* base = wrow[i] - 16 * grp;
-      const u32x4 p = *reinterpret_cast<const u32x4*>(in0 ? wrow[i] + o0 : base);
-      const u32x4 q = *reinterpret_cast<const u32x4*>(in1 ? wrow[i] + o1 : base);
-      wv[i] = join(in0 ? p : zero, in1 ? q : zero);
+    for (int h = 0; h < 2; ++h) {
+      const int64_t o = in[h] ? (int64_t)whole * 128 + 64 * h + 16 * grp : 0;
+      const u32x4 zero = {0, 0, 0, 0};
+      wv[h] = *reinterpret_cast<const u32x4*>(wrow + o);
+      av[h] = *reinterpret_cast<const u32x4*>(arow + o);
+      if (!in[h]) wv[h] = av[h] = zero;
     }
-    const float sw = swrow[whole];
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const uint8_t* base = arow[j] - 16 * grp;
-      const u32x4 p = *reinterpret_cast<const u32x4*>(in0 ? arow[j] + o0 : base);
-      const u32x4 q = *reinterpret_cast<const u32x4*>(in1 ? arow[j] + o1 : base);
-      const v8i av = join(in0 ? p : zero, in1 ? q : zero);
-      const float s = srow[j][whole] * sw;
-#pragma unroll
-      for (int i = 0; i < FT; ++i) {
-        const v4f r = mfma_block(wv[i], av);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[j][i][t] = __builtin_fmaf(r[t], s, acc[j][i][t]);
-      }
-    }
+    add(join(wv[0], wv[1]), join(av[0], av[1]), srow[whole] * swrow[whole]);
   }
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-#pragma unroll
-    for (int i = 0; i < FT; ++i) part[wave][j * FT + i][lane] = acc[j][i];
+  part[wave][lane] = acc;
   __syncthreads();
-  const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
-  for (int t = wave; t < TT * FT; t += kSsWaves) {
-    v4f sum = part[0][t][lane];
+  if (wave != 0) return;
 #pragma unroll
-    for (int v = 1; v < kSsWaves; ++v) {
-      const v4f p = part[v][t][lane];
+  for (int v = 1; v < NW; ++v) {
+    const v4f p = part[v][lane];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sum[q] += p[q];
-    }
-    const int m = (t / FT) * 16 + r16, n = n0 + (t % FT) * 16 + 4 * grp;
-    if (m < g.B && n < g.N) store4<DT>((uint16_t*)g.y + (int64_t)m * g.N, n, g.N, vec, sum);
+    for (int q = 0; q < 4; ++q) acc[q] += p[q];
   }
+  const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
+  const int n = n0 + 4 * grp;
+  if (r16 < g.B && n < g.N) store4<DT>((uint16_t*)g.y + (int64_t)r16 * g.N, n, g.N, vec, acc);
 }
 
 template <int DT, int TT, int FT, int WT, int WF>
@@ -573,37 +524,43 @@ void tiles(const Fp8GemmArgs& g, hipStream_t s) {
   }
 }
 
-template <int DT>
+template <int DT, int FT, int S>
 void small_tiles(const Fp8GemmArgs& g, hipStream_t s) {
-  const int tm = (g.B + kSmRowsA - 1) / kSmRowsA, tn = (g.N + kSmRowsW - 1) / kSmRowsW;
+  const int tm = (g.B + kSmRowsA - 1) / kSmRowsA, tn = (g.N + 64 * FT - 1) / (64 * FT);
   const dim3 grid((unsigned)(tm * tn)), block(64 * kSmWaves * kSmGroups);
-  if (g.K % 128 != 0) fp8_gemm_small<DT, true><<<grid, block, 0, s>>>(g, tm, tn);
-  else fp8_gemm_small<DT, false><<<grid, block, 0, s>>>(g, tm, tn);
+  if (g.K % 128 != 0) fp8_gemm_small<DT, FT, S, true><<<grid, block, 0, s>>>(g, tm, tn);
+  else fp8_gemm_small<DT, FT, S, false><<<grid, block, 0, s>>>(g, tm, tn);
 }
 
-template <int DT, int TT, int FT, int U>
+template <int DT, int NW>
 void stream(const Fp8GemmArgs& g, hipStream_t s) {
-  fp8_gemm_stream<DT, TT, FT, U><<<dim3((unsigned)((g.N + 16 * FT - 1) / (16 * FT))), dim3(64 * kSsWaves), 0, s>>>(g);
+  fp8_gemm_stream<DT, NW><<<dim3((unsigned)((g.N + 15) / 16)), dim3(64 * NW), 0, s>>>(g);
 }
 
 template <int DT>
 void launch(const Fp8GemmArgs& g, hipStream_t s) {
-  if (g.B <= 16) return stream<DT, 1, 1, 4>(g, s);
-  if (g.B <= 32) return stream<DT, 2, 2, 2>(g, s);
-  if (g.B <= 64) return stream<DT, 4, 2, 2>(g, s);
+  // Few rows: streams while one workgroup per compute unit covers w (1 to 16 x 4096 x 4096: 6.4 to 7.1 us, with 64 x 64
+  // tiles 9.9 us), for up to 4 rows two of twice the waves (4 x 8192 x 8192: 16.2 us, tiles 17.1 us; 16 rows: 21.8 and
+  // 17.1 us).  Beyond, tiles: 8 x 28672 x 8192 51 us, streams 56 us.
+  if (g.B <= 16 && g.N <= 16 * 256) return stream<DT, 8>(g, s);
+  if (g.B <= 4 && g.N <= 16 * 512) return stream<DT, 16>(g, s);
   // The sizes of tiles: microseconds per K-block for a round of tiles over the chip, as measured (K = 4096 to 8192),
-  // times the rounds.  64 x 128: 256 at a time (512 x 4096 x 4096: 16 us, with 128 x 128 tiles 27 us); 128 x 128: 512 at
-  // a time, faster while there is one per compute unit (2048 x 2048 x 4096: 28 us, with 64 x 128 33 us); 256 x 256: 256
-  // at a time (4096 x 8192 x 8192: 254 us; 1000 x 8192 x 8192: 127 us, with 128 x 128 tiles 89 us).
+  // times the rounds.  64 x 64: 256 at a time (128 x 8192 x 8192: 19.5 us, with 64 x 128 tiles 27 us); 64 x 128: 256 at a
+  // time (512 x 4096 x 4096: 17 us, with 64 x 64 tiles 21 us, 128 x 128 31 us); 128 x 128: 512 at a time, faster while
+  // there is one per compute unit (2048 x 2048 x 4096: 29 us, with 64 x 128 34 us); 256 x 256: 256 at a time
+  // (4096 x 8192 x 8192: 248 us; 1000 x 8192 x 8192: 127 us, with 128 x 128 tiles 87 us).
   auto count = [&](int64_t rows, int64_t cols) { return (g.B + rows - 1) / rows * ((g.N + cols - 1) / cols); };
   auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
   const int64_t mid = count(128, 128);
+  const double least_cost = 0.36 * rounds(count(64, 64), 256);
   const double small_cost = 0.6 * rounds(count(64, 128), 256);
   const double mid_cost = mid <= 256 ? 0.9 : 1.4 * rounds(mid, 512);
   const double big_cost = 2.0 * rounds(count(256, 256), 256);
-  if (big_cost <= small_cost && big_cost <= mid_cost) return tiles<DT, 4, 2, 2, 4>(g, s);
-  if (mid_cost < small_cost) return tiles<DT, 2, 2, 2, 2>(g, s);
-  return small_tiles<DT>(g, s);
+  const double best = fmin(fmin(least_cost, small_cost), fmin(mid_cost, big_cost));
+  if (big_cost == best) return tiles<DT, 8, 4, 2, 4>(g, s);
+  if (mid_cost == best) return tiles<DT, 4, 4, 2, 2>(g, s);
+  if (small_cost == best) return small_tiles<DT, 2, 3>(g, s);
+  return small_tiles<DT, 1, 4>(g, s);
 }
 
 }  // namespace
