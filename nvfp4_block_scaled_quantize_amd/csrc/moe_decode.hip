@@ -46,14 +46,11 @@ struct Ws {
   uint32_t* hmax;     // [P] largest |h| of row q (binary32 bits)
   float* wts;         // [P] weight of pair p
   int32_t* row_of;    // [P] its row q
-  int4* chosen;       // [min(P, E)] {expert or -1, first row, mask of its tokens, experts chosen}
-  uint32_t* count;    // [row ranges of fc2] workgroups that are done
+  int4* chosen;       // [min(P, 2 E)] {expert, first row, mask of its tokens, entries}, one for up to 16 tokens
   _Float16* xs;       // [T, hidden] scaled x (BF16 only)
   float* h;           // [P, inter]
   float* o;           // [P, hidden]
 };
-
-constexpr int ranges_of(int hidden) { return (hidden + 31) / 32; }
 
 size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
   unsigned char* p = reinterpret_cast<unsigned char*>(base);
@@ -69,8 +66,7 @@ size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
   s.hmax = reinterpret_cast<uint32_t*>(take((size_t)P * 4));
   s.wts = reinterpret_cast<float*>(take((size_t)P * 4));
   s.row_of = reinterpret_cast<int32_t*>(take((size_t)P * 4));
-  s.chosen = reinterpret_cast<int4*>(take((size_t)(P < E ? P : E) * 16));
-  s.count = reinterpret_cast<uint32_t*>(take((size_t)ranges_of(hidden) * 4));
+  s.chosen = reinterpret_cast<int4*>(take((size_t)(P < 2 * E ? P : 2 * E) * 16));
   s.xs = reinterpret_cast<_Float16*>(take((size_t)T * hidden * 2));
   s.h = reinterpret_cast<float*>(take((size_t)P * inter * 4));
   s.o = reinterpret_cast<float*>(take((size_t)P * hidden * 4));
@@ -96,73 +92,68 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 template <int DT, int TB>
 __global__ void __launch_bounds__(256)
-moe_router(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int T, int E, int hidden, Ws ws, int P,
-           int ranges) {
+moe_router(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr, int T, int E, int hidden, Ws ws, int P) {
   __shared__ float part[4][TB];
   __shared__ float top[4][TB];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int unit0 = (int)((int64_t)(hidden / 8) * e / E), unit1 = (int)((int64_t)(hidden / 8) * (e + 1) / E);
-  if (e == 0) {
+  const int t0 = (int)blockIdx.y * TB;
+  if (e == 0 && t0 == 0)
     for (int i = tid; i < P; i += 256) ws.hmax[i] = 0u;
-    for (int i = tid; i < ranges; i += 256) ws.count[i] = 0u;
+  float sum[TB], big[TB];
+#pragma unroll
+  for (int j = 0; j < TB; ++j) sum[j] = big[j] = 0.0f;
+  for (int u = tid; u < hidden / 8; u += 256) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(wr + (int64_t)e * hidden + 8 * u);
+    u32x4 v[TB];
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      v[j] = *reinterpret_cast<const u32x4*>(x + (int64_t)(t0 + j < T ? t0 + j : T - 1) * hidden + 8 * u);
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b, c, d;
+        unpack2<DT>(w[i], a, b);
+        unpack2<DT>(v[j][i], c, d);
+        sum[j] = __builtin_fmaf(a, c, sum[j]);
+        sum[j] = __builtin_fmaf(b, d, sum[j]);
+        big[j] = __builtin_fmaxf(big[j], __builtin_fmaxf(__builtin_fabsf(c), __builtin_fabsf(d)));
+      }
   }
-  for (int t0 = 0; t0 < T; t0 += TB) {
-    float sum[TB], big[TB];
 #pragma unroll
-    for (int j = 0; j < TB; ++j) sum[j] = big[j] = 0.0f;
-    for (int u = tid; u < hidden / 8; u += 256) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(wr + (int64_t)e * hidden + 8 * u);
-      u32x4 v[TB];
-#pragma unroll
-      for (int j = 0; j < TB; ++j)
-        v[j] = *reinterpret_cast<const u32x4*>(x + (int64_t)(t0 + j < T ? t0 + j : T - 1) * hidden + 8 * u);
-#pragma unroll
-      for (int j = 0; j < TB; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a, b, c, d;
-          unpack2<DT>(w[i], a, b);
-          unpack2<DT>(v[j][i], c, d);
-          sum[j] = __builtin_fmaf(a, c, sum[j]);
-          sum[j] = __builtin_fmaf(b, d, sum[j]);
-          big[j] = __builtin_fmaxf(big[j], __builtin_fmaxf(__builtin_fabsf(c), __builtin_fabsf(d)));
-        }
+  for (int j = 0; j < TB; ++j) {
+    const float s = wave_sum(sum[j]), m = wave_max_dpp(big[j]);
+    if (lane == 0) {
+      part[wave][j] = s;
+      top[wave][j] = m;
     }
+  }
+  __syncthreads();
+  if (tid < TB && t0 + tid < T) {
+    ws.logits[(int64_t)(t0 + tid) * E + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+    if (e == 0)
+      ws.xmax[t0 + tid] = __float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][tid], top[1][tid]),
+                                                          __builtin_fmaxf(top[2][tid], top[3][tid])));
+  }
+  if constexpr (DT == kBf16) {
+    // this workgroup's columns of the tokens in FP16
+    const int units = unit1 - unit0;
+    for (int i = tid; i < units * TB; i += 256) {
+      const int j = i / units, u = unit0 + i - j * units;
+      if (t0 + j >= T) continue;
+      const float scale = up_scale(__float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][j], top[1][j]),
+                                                                   __builtin_fmaxf(top[2][j], top[3][j]))));
+      const int64_t at = (int64_t)(t0 + j) * hidden + 8 * u;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + at);
+      v8h o;
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const float s = wave_sum(sum[j]), m = wave_max_dpp(big[j]);
-      if (lane == 0) {
-        part[wave][j] = s;
-        top[wave][j] = m;
+      for (int q = 0; q < 4; ++q) {
+        o[2 * q] = (_Float16)(bf16_lo(v[q]) * scale);
+        o[2 * q + 1] = (_Float16)(bf16_hi(v[q]) * scale);
       }
+      *reinterpret_cast<v8h*>(ws.xs + at) = o;
     }
-    __syncthreads();
-    if (tid < TB && t0 + tid < T) {
-      ws.logits[(int64_t)(t0 + tid) * E + e] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
-      if (e == 0)
-        ws.xmax[t0 + tid] = __float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][tid], top[1][tid]),
-                                                            __builtin_fmaxf(top[2][tid], top[3][tid])));
-    }
-    if constexpr (DT == kBf16) {
-      // this workgroup's columns of the tokens in FP16
-      const int units = unit1 - unit0;
-      for (int i = tid; i < units * TB; i += 256) {
-        const int j = i / units, u = unit0 + i - j * units;
-        if (t0 + j >= T) continue;
-        const float scale = up_scale(__float_as_uint(__builtin_fmaxf(__builtin_fmaxf(top[0][j], top[1][j]),
-                                                                     __builtin_fmaxf(top[2][j], top[3][j]))));
-        const int64_t at = (int64_t)(t0 + j) * hidden + 8 * u;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(x + at);
-        v8h o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          o[2 * q] = (_Float16)(bf16_lo(v[q]) * scale);
-          o[2 * q + 1] = (_Float16)(bf16_hi(v[q]) * scale);
-        }
-        *reinterpret_cast<v8h*>(ws.xs + at) = o;
-      }
-    }
-    __syncthreads();
   }
 }
 
@@ -206,18 +197,17 @@ __device__ __forceinline__ void join_two(float& v1, float& v2, float u1, float u
   v1 = __builtin_fmaxf(v1, u1);
 }
 
-// One wave selects one token's experts: lane l holds experts l + 64 i, i < N.  A group's score is the sum of
-// its two best biased scores, the best groups are kept, and the top_k experts of those are taken one
-// after the other, ties to the lower index: lane k receives the one of rank k and its weight.  Groups of 2, 4,
-// .. 64 experts are lanes next to one another; others go through LDS (sb, sg: E and n_group entries).
+// One wave scores one token's experts: lane l holds experts l + 64 i, i < N, their scores s and the keys of their biased
+// scores.  A group's score is the sum of its two best biased scores, and the experts outside the best groups have
+// the key 0.  Groups of 2, 4, .. 64 experts are lanes next to one another; others go through LDS (sb, sg: E and
+// n_group entries).
 template <int N>
-__device__ __forceinline__ void select_token(const RouteArgs& a, const float* __restrict__ logits, int t, float* sb,
-                                             float* sg, int& id, float& weight) {
+__device__ __forceinline__ void score_token(const RouteArgs& a, const float* __restrict__ logits, int t, float* sb,
+                                            float* sg, float (&s)[N], uint32_t (&key)[N]) {
   const int lane = threadIdx.x & 63;
   const int gsize = a.E / a.n_group;
   const float ninf = -__builtin_inff();
-  float s[N], b[N];
-  uint32_t key[N];
+  float b[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = lane + 64 * i;
@@ -284,6 +274,17 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const float* __
     for (int i = 0; i < N; ++i)
       if (before[i] >= a.topk_group) key[i] = 0u;
   }
+}
+
+// One wave takes a token's top_k experts one after the other, ties to the lower index: lane k receives the one of
+// rank k and its weight.
+template <int N>
+__device__ __forceinline__ void select_token(const RouteArgs& a, const float* __restrict__ logits, int t, float* sb,
+                                             float* sg, int& id, float& weight) {
+  const int lane = threadIdx.x & 63;
+  float s[N];
+  uint32_t key[N];
+  score_token<N>(a, logits, t, sb, sg, s, key);
   float sum = 0.0f, mine = 0.0f;
   int chosen = 0;
   for (int k = 0; k < a.top_k; ++k) {
@@ -340,13 +341,13 @@ __global__ void __launch_bounds__(64 * kPlanWaves) moe_plan(RouteArgs a, Ws ws, 
     }
   }
   __syncthreads();
-  // sums over the experts before each: rows, and experts that have any
+  // sums over the experts before each: rows and entries
   uint32_t m = 0u;
-  int rows = 0, some = 0, r = 0, u = 0;
+  int rows = 0, some = 0, r = 0, u = 0;   // some: entries of the expert, up to 16 tokens each
   if (tid < 256) {
     m = takers[tid];
     r = rows = __popc(m);
-    u = some = m != 0u ? 1 : 0;
+    u = some = (rows + 15) / 16;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int x = __shfl_up(r, off, 64), y = __shfl_up(u, off, 64);
@@ -377,9 +378,10 @@ __global__ void __launch_bounds__(64 * kPlanWaves) moe_plan(RouteArgs a, Ws ws, 
       bu += sums[1][v];
     }
     first[tid] = br;
-    if (m != 0u) ws.chosen[bu] = make_int4(tid, br, (int)m, n);
-    const int most = a.T * a.top_k < a.E ? a.T * a.top_k : a.E;
-    if (tid >= n && tid < most) ws.chosen[tid] = make_int4(-1, 0, 0, n);
+    uint32_t rest = m;   // the tokens after the 16th
+    for (int i = 0; i < 16; ++i) rest &= rest - 1u;
+    if (some > 0) ws.chosen[bu] = make_int4(tid, br, (int)(m ^ rest), n);
+    if (some > 1) ws.chosen[bu + 1] = make_int4(tid, br + 16, (int)rest, n);
   }
   __syncthreads();
   for (int p = tid; p < a.T * a.top_k; p += 64 * kPlanWaves) {
@@ -417,28 +419,46 @@ __device__ __forceinline__ int first_k(int c, int d, int g) {
 // Expert weights [E, rows, K]: plain (codes [rows, K / 2], E4M3 [rows, K / 16]) or TW, the layout of
 // nvfp4_pretile_weight of the stacked [E rows, K] matrix, in which a 128-k chunk of 16 rows is 1 KiB of codes
 // and 128 B of E4M3 pairs in lane order.  K % 64 = 0 (TW: 128), so in the last block a lane's half is whole or
-// past the row; there it reads the block's start again, and scales() is 0.  (Nothing is done with what is
+// past the row; there it reads the block's start again, and scales() is 0.  Not live: one address for all lanes.  (Nothing is done with what is
 // loaded before it is used: the loads after these must not wait.)
 template <bool TW>
 __device__ __forceinline__ void load_piece(const uint8_t* __restrict__ w, const uint8_t* __restrict__ sf, int64_t row16,
-                                           int c, int K, int lane, Piece& p) {
+                                           int c, int K, int lane, bool live, Piece& p) {
   if constexpr (TW) {
     const int64_t tile = (row16 / 16) * (K / 128) + 2 * c;
     const int64_t next = 256 * c + 128 < K ? tile + 1 : tile;
-    p.codes[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + tile * 1024 + 16 * lane));
-    p.codes[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + next * 1024 + 16 * lane));
-    p.sf[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + tile * 128 + 2 * lane));
-    p.sf[1] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + next * 128 + 2 * lane));
+    const int l = live ? lane : 0;
+    p.codes[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + tile * 1024 + 16 * l));
+    p.codes[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + next * 1024 + 16 * l));
+    p.sf[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + tile * 128 + 2 * l));
+    p.sf[1] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(sf + next * 128 + 2 * l));
   } else {
     const int g = lane >> 4;
-    const bool in = 256 * c + 64 * g < K;
-    const int64_t row = row16 + (lane & 15);
+    const bool in = live && 256 * c + 64 * g < K;
+    const int64_t row = row16 + (live ? lane & 15 : 0);
     const uint8_t* at = w + row * (K / 2) + 128 * c + (in ? 32 * g : 0);
     p.codes[0] = *reinterpret_cast<const u32x4*>(at);
     p.codes[1] = *reinterpret_cast<const u32x4*>(at + 16);
     p.sf[0] = *reinterpret_cast<const uint32_t*>(sf + row * (K / 16) + 16 * c + (in ? 4 * g : 0));
   }
 }
+// The pieces loaded ahead, once they are there.  (A plain copy ends up after the next loads, at the loop's end, and
+// waits for them.)
+__device__ __forceinline__ uint32_t take(uint32_t from) {
+  uint32_t to;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(to) : "v"(from) : "memory");
+  return to;
+}
+template <bool TW>
+__device__ __forceinline__ void take(Piece& to, const Piece& from) {
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) to.codes[d][q] = take(from.codes[d][q]);
+    if (TW || d == 0) to.sf[d] = take(from.sf[d]);
+  }
+}
+
 // The two scales of half d.
 template <bool TW>
 __device__ __forceinline__ void scales(const Piece& p, int d, int c, int K, int g, _Float16 (&s)[2]) {
@@ -502,275 +522,444 @@ __device__ __forceinline__ void act_operand(const RawAct<FC>& r, int m, float sc
   }
 }
 
-// Four numbers to and from memory that workgroups on other dies read: the accesses go past the caches
-// of this die one by one.  (A fence would write back a whole die's cache: with one in each workgroup fc2 of 16
-// tokens took 120 us instead of 27.)
-__device__ __forceinline__ void store_shared(float* p, const v4f& v) {
-  const uint64_t a = __float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32;
-  const uint64_t b = __float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32;
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + 1, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ v4f load_shared(const float* p) {
-  const uint64_t a = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const uint64_t b = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return v4f{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)b),
-             __uint_as_float((uint32_t)(b >> 32))};
-}
-
-// SEL > 0: fc1 of one token, whose experts (SEL 64 of them at most) every wave selects by itself.
-template <int FC, bool GATED, bool TW, int RT, int TT, int NW, int SEL>
-__global__ void __launch_bounds__(64 * NW, TT == 1 ? 4 : 2) moe_expert_rows(FcArgs a) {
-  constexpr int kThreads = 64 * NW;
-  constexpr int kPairsEach = (kMaxPairs + kThreads - 1) / kThreads;
-  __shared__ v4f part[NW][RT * TT][64];
-  __shared__ float scratch[SEL ? NW : 1][2][64 * (SEL ? SEL : 1)];
-  __shared__ float wts[FC == 2 ? kMaxPairs : 1];
-  __shared__ int rows[FC == 2 ? kMaxPairs : 1];   // row of each pair
-  __shared__ uint32_t slot_max[16 * TT];
-  __shared__ int last;
+// 16 RT weight rows of an entry (an expert and up to 16 of its tokens) are a unit; the units of all entries, in
+// order, are divided evenly among the workgroups, so one has a few units of one entry or two.  Its waves take the
+// 256-k blocks of a unit in turn, each loads the weights of its next block (of this unit or the next) before it
+// works on the one at hand, and their sums are joined through LDS, in two buffers: one barrier for a unit.
+// KEEP: a wave has one block of every unit, and holds its activations for all units of the entry.
+template <int FC, bool GATED, bool TW, int RT, int NW, bool KEEP>
+__global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int units) {
+  __shared__ v4f part[2][NW][RT][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, grp = lane >> 4;
-  const int T = a.route.T, top_k = a.route.top_k, P = T * top_k;
 
-  // for the last workgroup of the row range: on its way before anything else
-  float pw[kPairsEach];
-  int pr[kPairsEach];
-  if constexpr (FC == 2) {
-#pragma unroll
-    for (int i = 0; i < kPairsEach; ++i) {
-      const int p = tid + i * kThreads;
-      pw[i] = a.ws.wts[p < P ? p : 0];
-      pr[i] = a.ws.row_of[p < P ? p : 0];
-    }
-  } else {
-    if (tid < 16 * TT) slot_max[tid] = 0u;
-  }
-  // this workgroup's expert, its first row, its tokens, how many experts there are
-  int4 mine;
-  if constexpr (SEL > 0) {
-    int id;
-    float w;
-    select_token<SEL>(a.route, a.ws.logits, 0, scratch[wave][0], scratch[wave][1], id, w);
-    mine = make_int4(__builtin_amdgcn_readlane(id, (int)blockIdx.y), (int)blockIdx.y, 1, top_k);
-    if (blockIdx.x == 0 && wave == 0) {
-      if (lane == 0) a.ws.chosen[blockIdx.y] = mine;
-      if (blockIdx.y == 0 && lane < top_k) {
-        a.ws.wts[lane] = w;
-        a.ws.row_of[lane] = lane;
-        if (a.ids_out) a.ids_out[lane] = id;
-        if (a.w_out) a.w_out[lane] = w;
-      }
-    }
-  } else {
-    mine = a.ws.chosen[blockIdx.y];
-    if (mine.x < 0) return;   // fewer experts than workgroups: the whole workgroup
-  }
-  const int e = mine.x, q0 = mine.y;
-  const uint32_t tokens = (uint32_t)mine.z;
-  const int ns = __popc(tokens);
+  const int n = __builtin_amdgcn_readfirstlane(a.ws.chosen[0].w);
+  auto entry = [&](int y) __attribute__((always_inline)) {
+    int4 v = a.ws.chosen[y];
+    v.x = __builtin_amdgcn_readfirstlane(v.x);
+    v.y = __builtin_amdgcn_readfirstlane(v.y);
+    v.z = __builtin_amdgcn_readfirstlane(v.z);
+    return v;
+  };
+  const uint32_t total = (uint32_t)n * (uint32_t)units, each = total / gridDim.x, more_by_one = total - each * gridDim.x;
+  const int lo = (int)(blockIdx.x * each + (blockIdx.x < more_by_one ? blockIdx.x : more_by_one));
+  const int hi = lo + (int)each + (blockIdx.x < more_by_one ? 1 : 0);
+  if (lo >= hi) return;   // the whole workgroup
+  int y = (int)((uint32_t)lo / (uint32_t)units), x = lo - y * units;
+  int4 mine = entry(y), after = entry(y + 1 < n ? y + 1 : y);
 
-  // token slots of this lane: slot s is the s-th token of the mask
-  int64_t arow[TT];
-  uint32_t top[TT];   // bits of the largest value that the operand was, or will be, scaled by
-  bool there[TT];
+  // weight rows of a unit's RT groups of 16: consecutive rows, or for SwiGLU in fc1 gate rows, then the up rows
+  constexpr int kCols = (GATED ? RT / 2 : RT) * 16;   // results per token
+  auto row16 = [&](int e, int x, int i) __attribute__((always_inline)) {
+    const int r = !GATED || i < RT / 2 ? x * kCols + 16 * i : a.inter + x * kCols + 16 * (i - RT / 2);
+    return (int64_t)e * a.rows + r;
+  };
+  const int blocks = (a.K + 255) / 256;
+
+  // what belongs to an entry: lane (slot r16, grp) has the slot's token (slot s: the s-th of the mask) or row of h, the
+  // bits of the largest value that it was, or will be, scaled by, and with KEEP its operands
+  int ns = 0;
+  bool there = false;
+  int64_t arow = 0;
+  uint32_t top = 0u;
+  float ge = 0.0f, big = 0.0f;
+  RawAct<FC> raw[2];
+  v8h kept[2][4], kept_lo[2][4];
+  auto load_acts = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int s = 16 * j + r16;
-    there[j] = s < ns;
+    for (int d = 0; d < 2; ++d) load_act<FC>(a.src, arow, there, a.K, first_k<TW>(c, d, grp), raw[d]);
+  };
+  auto enter = [&]() __attribute__((always_inline)) {
+    const uint32_t tokens = (uint32_t)mine.z;
+    ns = __popc(tokens);
+    there = r16 < ns;
     if constexpr (FC == 1) {
       uint32_t m = tokens;
-      for (int i = 0; i < 16 * TT - 1; ++i) m = i < s ? m & (m - 1) : m;
-      arow[j] = there[j] ? __builtin_ctz(m) : 0;
-      top[j] = a.scaled ? a.ws.xmax[arow[j]] : 0u;
-    } else {
-      arow[j] = q0 + (there[j] ? s : 0);
-      top[j] = a.ws.hmax[arow[j]];
-    }
-  }
-
-  // weight rows of the tile's RT groups of 16: consecutive rows, or for SwiGLU in fc1 gate rows, then the up rows
-  constexpr int kCols = (GATED ? RT / 2 : RT) * 16;   // results per token
-  const int col0 = (int)blockIdx.x * kCols;
-  int64_t row16[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = !GATED ? col0 + 16 * i : i < RT / 2 ? col0 + 16 * i : a.inter + col0 + 16 * (i - RT / 2);
-    row16[i] = (int64_t)e * a.rows + r;
-  }
-  v4f acc[RT][TT];
+      for (int i = 0; i < 15; ++i) m = i < r16 ? m & (m - 1) : m;
+      arow = there ? __builtin_ctz(m) : 0;
+      top = a.scaled ? a.ws.xmax[arow] : 0u;
+    } else {
+      arow = mine.y + (there ? r16 : 0);
+      top = a.ws.hmax[arow];
+    }
+    ge = a.g[mine.x];
+    asm volatile("" : "+v"(top), "+v"(ge));   // waited for here, and not in a unit with loads on their way
+    big = 0.0f;
+    if constexpr (KEEP) {
+      if (wave < blocks) {
+        load_acts(wave);
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            act_operand<FC>(raw[d], m, FC == 2 ? up_scale(top) : 1.0f, kept[d][m], kept_lo[d][m]);
+      }
+    }
+  };
+  // fc1: the entry's largest |h| of each token
+  auto leave = [&]() __attribute__((always_inline)) {
+    if constexpr (FC == 1) {
+      big = __builtin_fmaxf(big, __shfl_xor(big, 16, 64));
+      big = __builtin_fmaxf(big, __shfl_xor(big, 32, 64));
+      if (wave < kCols / 16 && grp == 0 && there) atomicMax(a.ws.hmax + mine.y + r16, __float_as_uint(big));
+    }
+  };
+
+  Piece ahead[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
+    load_piece<TW>(a.w, a.sf, row16(mine.x, x, i), wave < blocks ? wave : 0, a.K, lane, true, ahead[i]);
+  enter();
+  for (int u = lo; u < hi; ++u) {
+    v4f acc[RT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const float ge = a.g[e];
-
-  const int blocks = (a.K + 255) / 256;
-  for (int c = wave; c < blocks; c += NW) {
-    Piece w[RT];
+    for (int i = 0; i < RT; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const bool crosses = x + 1 == units;
+    for (int c = wave; c < blocks; c += NW) {
+      Piece w[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) load_piece<TW>(a.w, a.sf, row16[i], c, a.K, lane, w[i]);
-    RawAct<FC> raw[2][TT];
-    auto load_half = [&](int d) __attribute__((always_inline)) {
+      for (int i = 0; i < RT; ++i) take<TW>(w[i], ahead[i]);
+      if constexpr (!KEEP) load_acts(c);
+      // the next block; after the last one the lanes read one piece, and nothing uses it (a branch here would make
+      // the waits for the activations wait for these loads as well)
+      const bool more = !KEEP && c + NW < blocks, live = more || u + 1 < hi;
+      const int ne = more || !crosses ? mine.x : after.x, nx = more ? x : crosses ? 0 : x + 1;
 #pragma unroll
-      for (int j = 0; j < TT; ++j)
-        if (j == 0 || ns > 16 * j) load_act<FC>(a.src, arow[j], there[j], a.K, first_k<TW>(c, d, grp), raw[d][j]);
-    };
-    load_half(0);
-    if constexpr (FC == 1) load_half(1);
+      for (int i = 0; i < RT; ++i)
+        load_piece<TW>(a.w, a.sf, row16(ne, nx, i), more ? c + NW : wave, a.K, lane, live, ahead[i]);
+      __builtin_amdgcn_sched_barrier(0);   // issued before the work, not after it
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      if constexpr (FC == 2) {
-        if (d == 1) load_half(1);
-      }
-      _Float16 sc[RT][2];
+      for (int d = 0; d < 2; ++d) {
+        _Float16 sc[RT][2];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) scales<TW>(w[i], d, c, a.K, grp, sc[i]);
+        for (int i = 0; i < RT; ++i) scales<TW>(w[i], d, c, a.K, grp, sc[i]);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        v8h wv[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) wv[i] = dequant8(w[i].codes[d][m], sc[i][m / 2]);
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          if (j > 0 && ns <= 16 * j) break;   // the whole workgroup
-          v8h hi, lo;
-          act_operand<FC>(raw[d][j], m, FC == 2 ? up_scale(top[j]) : 1.0f, hi, lo);
+        for (int m = 0; m < 4; ++m) {
+          v8h hi8, lo8;
+          if constexpr (KEEP) {
+            hi8 = kept[d][m];
+            lo8 = kept_lo[d][m];
+          } else {
+            act_operand<FC>(raw[d], m, FC == 2 ? up_scale(top) : 1.0f, hi8, lo8);
+          }
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[i], hi, acc[i][j], 0, 0, 0);
-            if constexpr (FC == 2) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[i], lo, acc[i][j], 0, 0, 0);
+            const v8h wv = dequant8(w[i].codes[d][m], sc[i][m / 2]);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, hi8, acc[i], 0, 0, 0);
+            if constexpr (FC == 2) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, lo8, acc[i], 0, 0, 0);
           }
         }
       }
     }
-  }
+    v4f(*sums)[RT][64] = part[(u - lo) & 1];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i) sums[wave][i][lane] = acc[i];
+    // LDS only: the loads ahead stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto joined = [&](int tile) __attribute__((always_inline)) {
+      v4f s = sums[0][tile][lane];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) part[wave][i * TT + j][lane] = acc[i][j];
-  if constexpr (FC == 2) {
+      for (int v = 1; v < NW; ++v) {
+        const v4f q = sums[v][tile][lane];
 #pragma unroll
-    for (int i = 0; i < kPairsEach; ++i) {
-      const int p = tid + i * kThreads;
-      if (p < P) {
-        rows[p] = pr[i];
-        wts[p] = pw[i];
+        for (int i = 0; i < 4; ++i) s[i] += q[i];
+      }
+      return s;
+    };
+    // results: lane (slot r16, columns 4 grp .. + 3) of a tile, one tile a wave
+    static_assert(kCols / 16 <= NW, "one tile a wave");
+    if (wave < kCols / 16) {
+      v4f v = joined(wave);
+      v4f up;
+      if constexpr (GATED) up = joined(wave + RT / 2);
+      const int col = x * kCols + 16 * wave + 4 * grp;
+      const float f = FC == 2 || a.scaled ? ge / up_scale(top) : ge;
+      if constexpr (FC == 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = GATED ? swiglu_f32(v[q] * f, up[q] * f) : relu2_f32(v[q] * f);
+          big = __builtin_fmaxf(big, __builtin_fabsf(v[q]));
+        }
+        if (there) *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(mine.y + r16) * a.inter + col) = v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] *= f;
+        if (there) *reinterpret_cast<v4f*>(a.ws.o + (int64_t)(mine.y + r16) * a.hidden + col) = v;
       }
     }
+    ++x;
+    if (crosses && u + 1 < hi) {
+      leave();
+      x = 0;
+      ++y;
+      mine = after;
+      after = entry(y + 1 < n ? y + 1 : y);
+      enter();
+    }
+  }
+  leave();
+}
+
+// out[t] = sum over the token's experts, in rank order, of weight times o, binary32: a thread has four columns.
+__global__ void __launch_bounds__(128) moe_combine(FcArgs a) {
+  const int t = blockIdx.y, top_k = a.route.top_k;
+  const int col = ((int)blockIdx.x * 128 + (int)threadIdx.x) * 4;
+  if (col >= a.hidden) return;
+  v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int k = 0; k < top_k; ++k) {
+    const v4f v = *reinterpret_cast<const v4f*>(a.ws.o + (int64_t)a.ws.row_of[t * top_k + k] * a.hidden + col);
+    const float wk = a.ws.wts[t * top_k + k];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(wk, v[q], s[q]);
+  }
+  uint16_t o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    o[q] = a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s[q]) : __builtin_bit_cast(uint16_t, (_Float16)s[q]);
+  const u32x2 v = {o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16};
+  *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)t * a.hidden + col) = v;
+}
+
+// fc1 for one token: 32 weight rows of one of its experts a workgroup.  Every workgroup selects by itself: all waves
+// score the experts, each ranks them against its share of the keys, and the sums of the ranks are the places;
+// experts of the same key have the same rank, and take the places from there on in order.  The last wave of the first
+// workgroup lists the selection for fc2.  All 16 columns of the matrix instruction are the token.
+constexpr int kOneRowsWaves = 8;
+template <bool GATED, bool TW, int N>
+__global__ void __launch_bounds__(64 * kOneRowsWaves) moe_one_rows(FcArgs a) {
+  constexpr int NW = kOneRowsWaves;
+  __shared__ float scratch[NW][2][64 * N];
+  __shared__ int ranks[NW][64 * N];
+  __shared__ float part[NW][32];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = lane >> 4, y = blockIdx.y, top_k = a.route.top_k;
+  const int blocks = (a.K + 255) / 256;
+  float s[N];
+  uint32_t key[N];
+  score_token<N>(a.route, a.ws.logits, 0, scratch[wave][0], scratch[wave][1], s, key);
+  {
+    int rank[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) rank[i] = 0;
+    // wave w: the experts 64 k + 8 w .. + 7 of every k
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int j = 0; j < 64 / NW; ++j) {
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[k], wave * (64 / NW) + j);
+#pragma unroll
+        for (int i = 0; i < N; ++i) rank[i] += other > key[i] ? 1 : 0;
+      }
+#pragma unroll
+    for (int i = 0; i < N; ++i) ranks[wave][64 * i + lane] = rank[i];
   }
   __syncthreads();
-  auto joined = [&](int tile) __attribute__((always_inline)) {
-    v4f s = part[0][tile][lane];
+  int rank[N];
 #pragma unroll
-    for (int v = 1; v < NW; ++v) {
-      const v4f q = part[v][tile][lane];
+  for (int i = 0; i < N; ++i) {
+    int r = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += q[i];
+    for (int v = 0; v < NW; ++v) r += ranks[v][64 * i + lane];
+    rank[i] = key[i] != 0u ? r : 64 * N;
+  }
+  // place k: the first of those of the largest rank that is not above k, after as many as it has places before k
+  auto at_place = [&](int k) __attribute__((always_inline)) {
+    for (int r = k; r >= 0; --r) {
+      int skip = k - r, e = -1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint64_t hit = __ballot(rank[i] == r);
+        if (e >= 0 || hit == 0) continue;
+        for (; skip > 0 && hit != 0; --skip) hit &= hit - 1;
+        if (hit != 0) e = 64 * i + __builtin_ctzll(hit);
+      }
+      if (e >= 0) return e;
     }
-    return s;
+    return 0;
   };
-  // results: lane (slot r16, columns 4 grp .. + 3) of a tile
-  constexpr int kOutTiles = kCols / 16 * TT;
-  for (int tile = wave; tile < kOutTiles; tile += NW) {
-    const int i = tile / TT, j = tile % TT, slot = 16 * j + r16;
-    if (16 * j >= ns) continue;
-    v4f y = joined(tile);
-    v4f up;
-    if constexpr (GATED) up = joined(tile + RT / 2 * TT);
-    if (slot >= ns) continue;
-    const int col = col0 + 16 * i + 4 * grp;
-    const uint32_t bits = TT == 1 || j == 0 ? top[0] : top[TT - 1];
-    const float f = FC == 2 || a.scaled ? ge / up_scale(bits) : ge;
-    if constexpr (FC == 1) {
-      v4f hv;
-      float m = 0.0f;
+  const int e = at_place(y);
+
+  v4f acc[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        hv[q] = GATED ? swiglu_f32(y[q] * f, up[q] * f) : relu2_f32(y[q] * f);
-        m = __builtin_fmaxf(m, __builtin_fabsf(hv[q]));
-      }
-      *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(q0 + slot) * a.inter + col) = hv;
-      atomicMax(&slot_max[slot], __float_as_uint(m));
-    } else {
+  for (int i = 0; i < 2; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t row = (int64_t)e * a.rows + (int64_t)blockIdx.x * (GATED ? 16 : 32);
+  for (int c = wave; c < blocks; c += NW) {
+    Piece w[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) y[q] *= f;
-      store_shared(a.ws.o + (int64_t)(q0 + slot) * a.hidden + col, y);
+    for (int i = 0; i < 2; ++i)
+      load_piece<TW>(a.w, a.sf, row + (GATED ? a.inter : 16) * i, c, a.K, lane, true, w[i]);
+    RawAct<1> x[2];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) load_act<1>(a.src, 0, true, a.K, first_k<TW>(c, d, grp), x[d]);
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      _Float16 sc[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) scales<TW>(w[i], d, c, a.K, grp, sc[i]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(w[i].codes[d][m], sc[i][m / 2]),
+                                                          __builtin_bit_cast(v8h, x[d].v[m]), acc[i], 0, 0, 0);
     }
   }
-  if constexpr (FC == 1) {
-    __syncthreads();
-    if (tid < ns) atomicMax(a.ws.hmax + q0 + tid, slot_max[tid]);
-  } else {
-    // this workgroup's results are in memory before it counts itself; the one that counts last sees all of them
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t n = __hip_atomic_fetch_add(a.ws.count + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = n == (uint32_t)(mine.w - 1) ? 1 : 0;
-    }
-    __syncthreads();
-    if (!last) return;
-    constexpr int kQuads = kCols / 4;
-    for (int i = tid; i < T * kQuads; i += kThreads) {
-      const int t = i / kQuads, col = col0 + 4 * (i - t * kQuads);
-      v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-      for (int k = 0; k < top_k; ++k) {
-        const v4f v = load_shared(a.ws.o + (int64_t)rows[t * top_k + k] * a.hidden + col);
-        const float wk = wts[t * top_k + k];
+  if ((lane & 15) == 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = __builtin_fmaf(wk, v[q], s[q]);
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<v4f*>(&part[wave][16 * i + 4 * grp]) = acc[i];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    constexpr int kCols = GATED ? 16 : 32;
+    float v = part[0][lane & 31];
+#pragma unroll
+    for (int q = 1; q < NW; ++q) v += part[q][lane & 31];
+    const float f = a.scaled ? a.g[e] / up_scale(a.ws.xmax[0]) : a.g[e];
+    float h;
+    if constexpr (GATED) h = swiglu_f32(v * f, __shfl_xor(v, 16, 64) * f);
+    else h = relu2_f32(v * f);
+    if (lane < kCols) a.ws.h[(int64_t)y * a.inter + (int64_t)blockIdx.x * kCols + lane] = h;
+    const uint32_t big = wave_max_u32(lane < kCols ? __float_as_uint(__builtin_fmaxf(__builtin_fabsf(h), 0.0f)) : 0u);
+    if (lane == 0) atomicMax(a.ws.hmax + y, big);
+  }
+  if (blockIdx.x == 0 && y == 0 && wave == NW - 1) {
+    float sum = 0.0f, mine = 0.0f;
+    int id = 0;
+    for (int k = 0; k < top_k; ++k) {
+      const int ek = at_place(k);
+      float w = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (ek / 64 == i) w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s[i]), ek % 64));
+      sum = sum + w;
+      if (lane == k) {
+        mine = w;
+        id = ek;
       }
-      uint16_t o[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        o[q] = a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s[q]) : __builtin_bit_cast(uint16_t, (_Float16)s[q]);
-      u32x2 v = {o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16};
-      *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)t * a.hidden + col) = v;
+    }
+    if (lane < top_k) {
+      const float w = (a.route.norm ? mine / sum : mine) * a.route.scaling;
+      a.ws.chosen[lane] = make_int4(id, lane, 1, top_k);
+      a.ws.wts[lane] = w;
+      if (a.ids_out) a.ids_out[lane] = id;
+      if (a.w_out) a.w_out[lane] = w;
     }
   }
+}
+
+// fc2 and the sum for one token: a workgroup has 16 output columns of all its experts, as one product over the
+// experts' h one after the other, each h already times weight and scale of its expert.  The 16 waves take the (expert,
+// 256-k block) steps in turn, two at a time.  A wave converts the 256 h of a step once (4 a lane) and hands them to its
+// lanes through LDS; all 16 columns of the matrix instruction are the same token.
+constexpr int kOneWaves = 16;
+template <bool TW>
+__global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
+  __shared__ __attribute__((aligned(16))) _Float16 acts[kOneWaves][2][2][256];   // wave, step of two, high and low part
+  __shared__ float part[kOneWaves][16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = lane >> 4, top_k = a.route.top_k;
+  const int blocks = (a.K + 255) / 256, steps = top_k * blocks;
+  const int k = lane < top_k ? lane : 0;
+  const int e = a.ws.chosen[k].x;
+  const float hm = __uint_as_float(a.ws.hmax[k]);
+  const float f = a.ws.wts[k] * a.g[e];
+  // the largest h times its factor goes to [2^14, 2^15)
+  const float scale = up_scale(wave_max_u32(__float_as_uint(__builtin_fmaxf(hm * __builtin_fabsf(f), 0.0f))));
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = wave; s0 < steps; s0 += 2 * kOneWaves) {
+    Piece w[2];
+    v4f h[2];
+    float fk[2];
+    int c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = s0 + i * kOneWaves < steps ? s0 + i * kOneWaves : s0, rank = s / blocks;
+      c[i] = s - rank * blocks;
+      const int ek = __builtin_amdgcn_readlane(e, rank);
+      fk[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), rank));
+      load_piece<TW>(a.w, a.sf, (int64_t)ek * a.rows + 16 * (int)blockIdx.x, c[i], a.K, lane, true, w[i]);
+      const int at = 256 * c[i] + 4 * lane;
+      h[i] = *reinterpret_cast<const v4f*>(a.ws.h + (int64_t)rank * a.inter + (at < a.K ? at : 0));
+      if (at >= a.K) h[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const float v0 = h[i][q] * fk[i] * scale, v1 = h[i][q + 1] * fk[i] * scale;
+        const v2h p = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(v0, v1));
+        const v2h r = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(v0 - (float)p[0], v1 - (float)p[1]));
+        *reinterpret_cast<v2h*>(&acts[wave][i][0][4 * lane + q]) = p;
+        *reinterpret_cast<v2h*>(&acts[wave][i][1][4 * lane + q]) = r;
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // only this wave reads what it wrote
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i > 0 && s0 + kOneWaves >= steps) break;   // the whole wave
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        _Float16 sc[2];
+        scales<TW>(w[i], d, c[i], a.K, grp, sc);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const v8h wv = dequant8(w[i].codes[d][m], sc[m / 2]);
+          const int at = first_k<TW>(0, d, grp) + 8 * m;
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, *reinterpret_cast<const v8h*>(&acts[wave][i][0][at]), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, *reinterpret_cast<const v8h*>(&acts[wave][i][1][at]), acc, 0, 0, 0);
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+  if ((lane & 15) == 0) *reinterpret_cast<v4f*>(&part[wave][4 * grp]) = acc;
+  __syncthreads();
+  if (tid >= 16) return;
+  float s = part[0][tid];
+#pragma unroll
+  for (int v = 1; v < kOneWaves; ++v) s += part[v][tid];
+  s /= scale;
+  ((uint16_t*)a.out)[16 * (int)blockIdx.x + tid] =
+      a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s) : __builtin_bit_cast(uint16_t, (_Float16)s);
 }
 
 template <int DT>
 void launch_router(const MoeDecodeArgs& m, const Ws& ws, int P, hipStream_t s) {
   const uint16_t* x = reinterpret_cast<const uint16_t*>(m.x);
   const uint16_t* wr = reinterpret_cast<const uint16_t*>(m.router);
-  const dim3 grid(m.experts), block(256);
-  if (m.tokens == 1) moe_router<DT, 1><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
-  else if (m.tokens <= 4) moe_router<DT, 4><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
-  else moe_router<DT, 8><<<grid, block, 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P, ranges_of(m.hidden));
+  if (m.tokens == 1) moe_router<DT, 1><<<dim3(m.experts), dim3(256), 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P);
+  else moe_router<DT, 4><<<dim3(m.experts, (m.tokens + 3) / 4), dim3(256), 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P);
 }
 
-// 64 weight rows to a workgroup where there are enough of them to fill the chip, else 32; then eight waves where
-// a row is long enough for them.
+// 64 weight rows to a unit where there are enough of them to fill the chip, else 32; eight waves where a row is long
+// enough for them (two workgroups of four to a compute unit, or one of eight).
+template <int FC, bool GATED, bool TW, int RT>
+void launch_units(const FcArgs& a, int experts, hipStream_t s) {
+  const int units = a.rows / (16 * RT), blocks = (a.K + 255) / 256;
+  const int64_t most = (int64_t)units * experts;
+  const int nw = blocks > 4 ? 8 : 4, slots = nw == 8 ? 256 : 512;
+  const dim3 grid((unsigned)(most < slots ? most : slots)), block(64 * nw);
+  if (blocks <= 4) moe_expert_rows<FC, GATED, TW, RT, 4, true><<<grid, block, 0, s>>>(a, units);
+  else if (blocks <= 8) moe_expert_rows<FC, GATED, TW, RT, 8, true><<<grid, block, 0, s>>>(a, units);
+  else moe_expert_rows<FC, GATED, TW, RT, 8, false><<<grid, block, 0, s>>>(a, units);
+}
+
 template <int FC, bool GATED, bool TW>
 void launch_rows(const FcArgs& a, int experts, hipStream_t s) {
-  const bool many = (int64_t)(a.rows / 64) * experts >= 512;
-  const dim3 grid(many ? a.rows / 64 : a.rows / 32, experts), block(256);
-  if constexpr (FC == 1) {
-    if (a.route.T == 1) {
-      const bool eight = a.K > 1024;
-      const dim3 one(a.rows / 32, experts), waves(eight ? 512 : 256);
-      if (a.route.E <= 64) {
-        if (eight) moe_expert_rows<FC, GATED, TW, 2, 1, 8, 1><<<one, waves, 0, s>>>(a);
-        else moe_expert_rows<FC, GATED, TW, 2, 1, 4, 1><<<one, waves, 0, s>>>(a);
-      } else {
-        if (eight) moe_expert_rows<FC, GATED, TW, 2, 1, 8, kPerLane><<<one, waves, 0, s>>>(a);
-        else moe_expert_rows<FC, GATED, TW, 2, 1, 4, kPerLane><<<one, waves, 0, s>>>(a);
-      }
-      return;
-    }
-  }
-  if (a.route.T <= 16) {
-    if (many) moe_expert_rows<FC, GATED, TW, 4, 1, 4, 0><<<grid, block, 0, s>>>(a);
-    else if (a.K > 1024) moe_expert_rows<FC, GATED, TW, 2, 1, 8, 0><<<grid, dim3(512), 0, s>>>(a);
-    else moe_expert_rows<FC, GATED, TW, 2, 1, 4, 0><<<grid, block, 0, s>>>(a);
-  } else {
-    if (many) moe_expert_rows<FC, GATED, TW, 4, 2, 4, 0><<<grid, block, 0, s>>>(a);
-    else moe_expert_rows<FC, GATED, TW, 2, 2, 4, 0><<<grid, block, 0, s>>>(a);
-  }
+  if ((int64_t)(a.rows / 64) * experts >= 512) launch_units<FC, GATED, TW, 4>(a, experts, s);
+  else launch_units<FC, GATED, TW, 2>(a, experts, s);
+}
+
+template <bool GATED, bool TW>
+void launch_one_rows(const FcArgs& a, hipStream_t s) {
+  const dim3 grid(a.rows / 32, a.route.top_k), block(64 * kOneRowsWaves);
+  if (a.route.E <= 64) moe_one_rows<GATED, TW, 1><<<grid, block, 0, s>>>(a);
+  else moe_one_rows<GATED, TW, kPerLane><<<grid, block, 0, s>>>(a);
 }
 
 template <bool TW>
@@ -800,15 +989,25 @@ void launch_layer(const MoeDecodeArgs& m, const Ws& ws, hipStream_t s) {
   a.g = m.w1_g;
   a.rows = gated ? 2 * m.inter : m.inter;
   a.K = m.hidden;
-  if (gated) launch_rows<1, true, TW>(a, experts, s);
-  else launch_rows<1, false, TW>(a, experts, s);
+  if (m.tokens == 1) {
+    if (gated) launch_one_rows<true, TW>(a, s);
+    else launch_one_rows<false, TW>(a, s);
+  } else {
+    if (gated) launch_rows<1, true, TW>(a, experts, s);
+    else launch_rows<1, false, TW>(a, experts, s);
+  }
   a.src = ws.h;
   a.w = m.w2;
   a.sf = m.w2_sf;
   a.g = m.w2_g;
   a.rows = m.hidden;
   a.K = m.inter;
-  launch_rows<2, false, TW>(a, experts, s);
+  if (m.tokens == 1) {
+    moe_one_out<TW><<<dim3(m.hidden / 16), dim3(64 * kOneWaves), 0, s>>>(a);
+  } else {
+    launch_rows<2, false, TW>(a, experts, s);
+    moe_combine<<<dim3((m.hidden + 511) / 512, m.tokens), dim3(128), 0, s>>>(a);
+  }
 }
 
 template <int DT>
