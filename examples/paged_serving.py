@@ -1,7 +1,7 @@
 """An attention block served from a paged cache: NVFP4 projections around the serving attention
-operators.
+operators; with --layer a whole layer, FP8 projections and routed NVFP4 experts.
 
-    python examples/paged_serving.py [--hidden 4096 --q-heads 32 --kv-heads 8 --head-dim 128]
+    python examples/paged_serving.py [--hidden 4096 --q-heads 32 --kv-heads 8 --head-dim 128] [--layer]
 
 A step takes the new tokens of all requests, packed: whole prompts, a chunk of a long prompt, single
 tokens, in any mixture.
@@ -11,6 +11,9 @@ tokens, in any mixture.
     kv_write    k, v -> their slots in the cache
     prompt_attn where no request has cached tokens, else paged_attn
     act_quant + gemm_pretiled      output projection
+
+The layer (`Layer`) has fp8_quantize + fp8_gemm for the projections, rope_kv_write for the rotation and the
+cache in one pass, and moe_decode for its experts.
 
 The host knows how many tokens it sends, so it follows the free pages without asking the GPU.  Decode
 steps read their lengths from device memory only: `DecodeGraph` records one and replays it.
@@ -39,6 +42,37 @@ class Linear:
         return nv.gemm_pretiled(a["codes"], a["scale"], self.tiles, self.g)
 
 
+class Fp8Linear:
+    """E4M3 weights [n, k] with a scale for every 128 x 128."""
+
+    def __init__(self, n, k, gen):
+        w = (torch.randn((n, k), generator=gen) * k ** -0.5).to(torch.bfloat16).cuda()
+        self.w = nv.fp8_quantize(w, block_rows=128)
+
+    def __call__(self, x):
+        a = nv.fp8_quantize(x)
+        return nv.fp8_gemm(a["codes"], a["scale"], self.w["codes"], self.w["scale"])
+
+
+class Experts:
+    """Routed SwiGLU experts with NVFP4 weights, for up to 32 tokens a call."""
+
+    def __init__(self, experts, top_k, hidden, inter, gen):
+        self.router = (torch.randn((experts, hidden), generator=gen) * hidden ** -0.5).half().cuda()
+        self.bias, self.top_k = torch.zeros(experts, device="cuda"), top_k
+        self.weights = []
+        for rows, k in ((2 * inter, hidden), (hidden, inter)):
+            w = (torch.randn((experts * rows, k), generator=gen) * k ** -0.5).to(torch.bfloat16).cuda()
+            q = nv.quantize(w, group_rows=rows, want_scale=False)
+            self.weights += [q["codes"].view(experts, rows, -1), q["sf"].view(experts, rows, -1), q["g_dec"]]
+
+    def __call__(self, x):
+        out = torch.empty_like(x)
+        for a, b in zip(x.split(32), out.split(32)):
+            nv.moe_decode(a, self.router, self.bias, *self.weights, self.top_k, act="swiglu", out=b)
+        return out
+
+
 def rotate(x, positions, base=10000.0):
     """Rotary embedding of x [tokens, heads, dim], in place, in binary32."""
     half = x.shape[2] // 2
@@ -57,8 +91,7 @@ class Server:
         gen = torch.Generator().manual_seed(seed)
         self.hidden, self.q_heads, self.kv_heads, self.head_dim = hidden, q_heads, kv_heads, head_dim
         self.window, self.page_size, self.seqs = window, page_size, seqs
-        self.qkv = Linear((q_heads + 2 * kv_heads) * head_dim, hidden, gen)
-        self.proj = Linear(hidden, q_heads * head_dim, gen)
+        self.make_weights(gen)
         shape = (pages, kv_heads, page_size, head_dim)
         self.k_cache = torch.empty(shape, dtype=torch.float16, device="cuda")
         self.v_cache = torch.empty(shape, dtype=torch.float16, device="cuda")
@@ -66,6 +99,19 @@ class Server:
         self.free = torch.randperm(pages, generator=gen).to(torch.int32).cuda()
         self.lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")   # cached tokens
         self.held = [0] * seqs                                            # the same on the host
+
+    def make_weights(self, gen):
+        self.qkv = Linear((self.q_heads + 2 * self.kv_heads) * self.head_dim, self.hidden, gen)
+        self.proj = Linear(self.hidden, self.q_heads * self.head_dim, gen)
+
+    def cache(self, q, k, v, m):
+        """Rotates q and k in place and writes k and v to their slots."""
+        rotate(q, m["positions"])
+        rotate(k, m["positions"])
+        nv.kv_write(k, v, m["slot_map"], self.k_cache, self.v_cache)
+
+    def finish(self, x, attended):
+        return self.proj(attended)
 
     def pages_for(self, new):
         """Pages a step with new[i] tokens takes."""
@@ -79,16 +125,14 @@ class Server:
         m = nv.page_maps(self.lens, new_lens, self.table, free, self.page_size, x.shape[0])
         hq, hk, d = self.q_heads, self.kv_heads, self.head_dim
         q, k, v = self.qkv(x).view(x.shape[0], hq + 2 * hk, d).split([hq, hk, hk], dim=1)
-        rotate(q, m["positions"])
-        rotate(k, m["positions"])
-        nv.kv_write(k, v, m["slot_map"], self.k_cache, self.v_cache)
+        self.cache(q, k, v, m)
         if fresh:
             out = nv.prompt_attn(q, k, v, m["cu_new"], window=self.window)
         else:
             out = nv.paged_attn(q, self.k_cache, self.v_cache, self.table, m["cu_new"], m["kv_lens"],
                                 window=self.window)
         self.lens.copy_(m["kv_lens"])
-        return self.proj(out.view(x.shape[0], hq * d))
+        return self.finish(x, out.view(x.shape[0], hq * d))
 
     def step(self, x, new):
         """x [sum(new), hidden] FP16 or BF16, new[i] tokens of request i (0 for a request that waits)."""
@@ -102,6 +146,29 @@ class Server:
         self.free = self.free[take:]
         self.held = [h + m for h, m in zip(self.held, new)]
         return y
+
+
+class Layer(Server):
+    """The block with FP8 projections, and routed experts behind it."""
+
+    def __init__(self, *args, experts=64, top_k=8, inter=1024, **kw):
+        self.moe = (experts, top_k, inter)
+        super().__init__(*args, **kw)
+
+    def make_weights(self, gen):
+        experts, top_k, inter = self.moe
+        self.qkv = Fp8Linear((self.q_heads + 2 * self.kv_heads) * self.head_dim, self.hidden, gen)
+        self.proj = Fp8Linear(self.hidden, self.q_heads * self.head_dim, gen)
+        self.experts = Experts(experts, top_k, self.hidden, inter, gen)
+        half = self.head_dim // 2
+        self.freq = 10000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float32) / half)
+
+    def cache(self, q, k, v, m):
+        nv.rope_kv_write(q, k, v, m["positions"], self.freq, m["slot_map"], self.k_cache, self.v_cache, q_out=q, k_out=k)
+
+    def finish(self, x, attended):
+        y = x + self.proj(attended)
+        return y + self.experts(y)
 
 
 class DecodeGraph:
@@ -142,8 +209,10 @@ def main():
     for name, value in (("hidden", 4096), ("q-heads", 32), ("kv-heads", 8), ("head-dim", 128), ("page-size", 16),
                         ("steps", 200)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--layer", action="store_true")
     a = ap.parse_args()
-    s = Server(a.hidden, a.q_heads, a.kv_heads, a.head_dim, seqs=4, page_size=a.page_size, pages=40960 // a.page_size,
+    kind = Layer if a.layer else Server
+    s = kind(a.hidden, a.q_heads, a.kv_heads, a.head_dim, seqs=4, page_size=a.page_size, pages=40960 // a.page_size,
                max_pages=16384 // a.page_size)
     gen = torch.Generator(device="cuda").manual_seed(1)
 
@@ -159,7 +228,7 @@ def main():
         print("%-44s %8d tokens  %9.3f ms  %10.0f tokens/s" % (what, n, t * 1e3, n / t), flush=True)
 
     prompts = [1900, 37, 800, 1]
-    warm = Server(a.hidden, a.q_heads, a.kv_heads, a.head_dim, seqs=4, pages=512, max_pages=256)
+    warm = kind(a.hidden, a.q_heads, a.kv_heads, a.head_dim, seqs=4, pages=512, max_pages=256)
     warm.step(tokens(sum(prompts)), prompts)   # loads the kernels
     warm.step(tokens(4), [1, 1, 1, 1])
     del warm

@@ -234,3 +234,60 @@ def test_no_tokens(nv):
     args = Layer("fp16", 1, 8, 64, 64, "relu2").args()
     args[0] = args[0][:0]
     assert nv.moe_decode(*args, 2).shape == (0, 64)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("size", [(2, 8, 3, 4, 2, 2112, 192, "relu2"), (5, 6, 2, 1, 1, 192, 2112, "swiglu"),
+                                  (1, 16, 5, 4, 2, 2112, 4160, "relu2"), (1, 70, 16, 7, 3, 64, 2112, "swiglu"),
+                                  (16, 64, 8, 8, 4, 1024, 1024, "relu2"), (3, 40, 8, 4, 4, 1088, 1536, "swiglu")])
+def test_long_rows_and_many_units(nv, size, kind):
+    """Rows of more blocks than waves, and more units than workgroups, so that a workgroup crosses into the next expert."""
+    tokens, experts, top_k, n_group, topk_group, hidden, inter, act = size
+    full(nv, Layer(kind, tokens, experts, hidden, inter, act, seed=sum(size[:7])), top_k, n_group, topk_group)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(17, 4, 4), (32, 2, 1), (32, 3, 2), (31, 16, 16), (32, 40, 16)])
+def test_experts_of_more_than_sixteen_tokens(nv, tokens, experts, top_k):
+    """Such an expert is worked on in two parts; with an expert of exactly 16 beside it, and of one."""
+    layer = Layer("fp16", tokens, experts, 320, 192, "swiglu", seed=tokens + experts)
+    layer.bias[0] += 0.3
+    full(nv, layer, top_k, 1, 1)
+    # by hand: token t to expert 0 below 16, to expert 1 from there on, and so on
+    layer = Layer("bf16", 32, 8, 64, 64, "relu2", seed=1)
+    layer.x[:] = layer.x.abs() * 0.01
+    layer.router[:] = 0
+    for e, members in enumerate((range(0, 16), range(16, 31), range(31, 32))):
+        for t in members:
+            layer.x[t, e] = 8
+        layer.router[e, e] = 1
+    _, ids, _ = run(nv, layer, 1, 1, 1)
+    assert ids[:, 0].tolist() == [0] * 16 + [1] * 15 + [2]
+    full(nv, layer, 1, 1, 1)
+
+
+@pytest.mark.parametrize("tokens", [1, 2])
+@pytest.mark.parametrize("experts,n_group,topk_group", [(16, 4, 2), (64, 1, 1), (64, 8, 3), (200, 10, 4), (256, 256, 100)])
+def test_ties(nv, tokens, experts, n_group, topk_group):
+    """Equal scores: the lower index first, within an order of a few different biases."""
+    layer = Layer("fp16", tokens, experts, 64, 64, "relu2", seed=experts)
+    layer.router[:] = 0
+    g = torch.Generator().manual_seed(experts + tokens)
+    for few in (1, 2, 3, 8):
+        layer.bias = torch.tensor([0.0, 0.5, -0.25, 1.0, 2.0, -3.0, 0.125, 4.0])[torch.randint(0, few, (experts,), generator=g)]
+        for top_k in (1, 3, 8):
+            full(nv, layer, top_k, n_group, topk_group)
+
+
+def test_one_token_that_is_not_finite(nv):
+    layer = Layer("fp16", 1, 64, 128, 64, "relu2", seed=2)
+    layer.x[0, 3] = float("nan")
+    out, ids, wts = run(nv, layer, 4, 8, 2)
+    assert out.isnan().all() and ids.tolist() == [[0, 1, 2, 3]] and wts.isnan().all()
+    layer = Layer("bf16", 1, 64, 128, 64, "relu2", seed=2)
+    layer.bias[:32], layer.bias[40] = float("nan"), float("-inf")
+    _, ids, _ = run(nv, layer, 16, 1, 1)
+    assert (ids >= 32).all() and not (ids == 40).any()
+    # weights times globals far outside binary16: the sum's own scale takes them
+    layer = Layer("bf16", 1, 16, 128, 64, "relu2", seed=3)
+    layer.w2 = (layer.w2[0], layer.w2[1], layer.w2[2] * 2.0 ** 60)
+    full(nv, layer, 4, 1, 1, scaling=2.0 ** 30)
