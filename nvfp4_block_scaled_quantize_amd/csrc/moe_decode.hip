@@ -1,28 +1,33 @@
 // moe_decode.hip -- a whole routed MoE layer for up to 32 tokens on NVFP4 expert weights, for gfx950:
 // router product, sigmoid group top-k (the selection of moe.hip), fc1, activation (ReLU^2 or SwiGLU),
-// fc2 and the weighted sum, in four launches (three for one token).
+// fc2 and the weighted sum, in five launches (three for one token).
 //
-//  1. router : logits[t, e] = x_t . Wr_e in binary32, one workgroup per expert; clears what the other
-//              launches count in; BF16 x also as scaled FP16 (below).
-//  2. plan   : one workgroup: one wave per token selects its experts; then the chosen experts, the tokens of
-//              each, and a row for every pair of them.  For one token every wave of fc1 selects by itself:
-//              that takes 2 us of fc1's time, a launch 4 us.
-//  3. fc1    : one workgroup per (chosen expert, 16 RT weight rows): h = act(W1_e x) for the tokens that
-//              chose it, binary32.
-//  4. fc2    : one workgroup per (chosen expert, 16 RT rows of W2) computes o = W2_e h for the expert's tokens,
-//              binary32; the last workgroup of each row range to arrive (an atomic counter) adds the
-//              chosen experts' o with their weights in rank order, whatever the order of arrival.
+//  1. router  : logits[t, e] = x_t . Wr_e in binary32, one workgroup per expert and four tokens; clears the
+//               maxima that fc1 takes; BF16 x also as scaled FP16 (below).
+//  2. plan    : one workgroup: one wave per token selects its experts; then the entries (an expert and up to 16 of
+//               its tokens) and a row of h and o for every pair of token and expert.
+//  3. fc1     : h = act(W1_e x) for the rows of every entry, binary32, and each row's largest |h|.
+//  4. fc2     : o = W2_e h for the rows of every entry, binary32.
+//  5. combine : the weighted sum over each token's o, in rank order.
+// One token: fc1 selects by itself (2 us less than a launch for it), and fc2 has all its experts in one
+// workgroup, so their sum needs no launch either.
 //
-// The weights' bytes bound it: each chosen expert's rows are read once, straight from memory into
-// registers (no LDS), the waves of a workgroup splitting K in chunks of 128, and the waves' sums are joined
-// through LDS.  A lane loads 16 bytes = 32 codes of its row (lane r + 16 g: row r, k = 32 g ..), which feed
-// four v_mfma_f32_16x16x32_f16: instruction m takes codes 8 m .. 8 m + 7 of every lane, and the activation
-// operand the same k.  E2M1 * E4M3 is exact in FP16.
+// The weights' bytes bound it: each chosen expert's rows are read once (twice with more than 16 tokens), straight
+// from memory into registers, the waves of a workgroup splitting K in blocks of 256, and the waves' sums are
+// joined through LDS.  A lane's 16 bytes = 32 codes of its row feed four v_mfma_f32_16x16x32_f16: instruction m takes
+// codes 8 m .. 8 m + 7 of every lane, and the activation operand the same k.  E2M1 * E4M3 is exact in FP16.
 //
 // The activations must be FP16 for that.  FP16 x is used as it is.  BF16 x is multiplied by the power
 // of two that brings the token's largest value to [2^14, 2^15): exact down to 2^-31 of the largest, what is
 // below is off by at most 2^-39 of it.  h (binary32) is brought to the same range by the pair's
 // largest h and split into two FP16 numbers, the value and what its rounding left: off by less than 2^-20 of itself.
+//
+// Measured (launches included), of which the weights at the rate of a large copy (5.1 TB/s) take the second figure:
+// 1 token, 8 of 64 experts, 2048 / 1024, ReLU^2    router 2.7, fc1 9.9, fc2 6.6 us: 17.7 us of             3.7 us
+// 16 tokens of the same layer                      3.5, plan 5.5, 17.6, 18.7, combine 4.0: 46.0 us of      26 us
+// 4 tokens, 8 of 128, 4096 / 1536, SwiGLU          4.8, 5.3, 50.5, 28.5, 4.7: 83.3 us of                   61 us
+// What is above it is the launches' own time, the dependent loads at their starts (4 to 5 us of a large one) and the
+// last round of units, which not all workgroups have.
 #include "device_common.h"
 #include "internal.h"
 #include "moe_decode.h"
@@ -523,7 +528,8 @@ __device__ __forceinline__ void act_operand(const RawAct<FC>& r, int m, float sc
 }
 
 // 16 RT weight rows of an entry (an expert and up to 16 of its tokens) are a unit; the units of all entries, in
-// order, are divided evenly among the workgroups, so one has a few units of one entry or two.  Its waves take the
+// order, are divided evenly among the workgroups (one unit to a workgroup instead: fc1 of 16 tokens 31 us, not
+// 18), so one has a few units of one entry or two.  Its waves take the
 // 256-k blocks of a unit in turn, each loads the weights of its next block (of this unit or the next) before it
 // works on the one at hand, and their sums are joined through LDS, in two buffers: one barrier for a unit.
 // KEEP: a wave has one block of every unit, and holds its activations for all units of the entry.
@@ -936,23 +942,26 @@ void launch_router(const MoeDecodeArgs& m, const Ws& ws, int P, hipStream_t s) {
   else moe_router<DT, 4><<<dim3(m.experts, (m.tokens + 3) / 4), dim3(256), 0, s>>>(x, wr, m.tokens, m.experts, m.hidden, ws, P);
 }
 
-// 64 weight rows to a unit where there are enough of them to fill the chip, else 32; eight waves where a row is long
-// enough for them (two workgroups of four to a compute unit, or one of eight).
+// Eight waves where a row is long enough for them (K = 2048: fc1 of 16 tokens 18 us, with four 24 us), else four: one or
+// two workgroups to a compute unit; more of them at a time divide the units worse (4 tokens of 64 experts: 33 us,
+// twice as many 39 us).  64 weight rows to a unit where that leaves six units to each of them (4 tokens of 128
+// experts of 4096 / 1536, SwiGLU: 92 us, with 32 rows 98 us), else 32 (8 tokens of 64 experts of 2048 / 1024: 41 us, with 64
+// rows 45 us).
 template <int FC, bool GATED, bool TW, int RT>
-void launch_units(const FcArgs& a, int experts, hipStream_t s) {
+void launch_units(const FcArgs& a, int experts, int slots, hipStream_t s) {
   const int units = a.rows / (16 * RT), blocks = (a.K + 255) / 256;
   const int64_t most = (int64_t)units * experts;
-  const int nw = blocks > 4 ? 8 : 4, slots = nw == 8 ? 256 : 512;
-  const dim3 grid((unsigned)(most < slots ? most : slots)), block(64 * nw);
-  if (blocks <= 4) moe_expert_rows<FC, GATED, TW, RT, 4, true><<<grid, block, 0, s>>>(a, units);
-  else if (blocks <= 8) moe_expert_rows<FC, GATED, TW, RT, 8, true><<<grid, block, 0, s>>>(a, units);
-  else moe_expert_rows<FC, GATED, TW, RT, 8, false><<<grid, block, 0, s>>>(a, units);
+  const dim3 grid((unsigned)(most < slots ? most : slots));
+  if (blocks <= 4) moe_expert_rows<FC, GATED, TW, RT, 4, true><<<grid, dim3(256), 0, s>>>(a, units);
+  else if (blocks <= 8) moe_expert_rows<FC, GATED, TW, RT, 8, true><<<grid, dim3(512), 0, s>>>(a, units);
+  else moe_expert_rows<FC, GATED, TW, RT, 8, false><<<grid, dim3(512), 0, s>>>(a, units);
 }
 
 template <int FC, bool GATED, bool TW>
 void launch_rows(const FcArgs& a, int experts, hipStream_t s) {
-  if ((int64_t)(a.rows / 64) * experts >= 512) launch_units<FC, GATED, TW, 4>(a, experts, s);
-  else launch_units<FC, GATED, TW, 2>(a, experts, s);
+  const int slots = a.K > 1024 ? 256 : 512;
+  if ((int64_t)(a.rows / 64) * experts >= 6 * slots) launch_units<FC, GATED, TW, 4>(a, experts, slots, s);
+  else launch_units<FC, GATED, TW, 2>(a, experts, slots, s);
 }
 
 template <bool GATED, bool TW>
