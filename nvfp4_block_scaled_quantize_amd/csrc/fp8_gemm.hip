@@ -77,6 +77,7 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, bool wide, c
 // The copies' lines bound it: every 64 x 16 bytes of a copy are eight lines of the L2, but one binary32 scale for
 // each of 64 rows is 64 lines.  So the scales of a row are copied four blocks at a time (SB = 4) where their rows
 // are aligned to that, and each line that the workgroups of a die share is asked for ahead by one of them.
+// 4096 x 8192 x 8192: 248 us, 2.2 PFLOP/s, matrix cores 57 % busy; a library product with one scale takes 202 us.
 // CUT: K ends inside a block.
 template <int TT, int FT, int WT, int WF, int SB>
 struct Tile {
@@ -302,7 +303,7 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 // ---------------------------------------------------------------- small tiles (a few hundred rows)
 // Where tiles of the sizes above would leave compute units idle: 64 rows of a by 64 FT rows of w, eight waves in two
 // groups that take the K-blocks in turn, S stage buffers each (S - 1 stages in flight while one is computed).
-// Bound by the lines between the L2 and the compute units.
+// Bound by the lines between the L2 and the compute units: 777 x 2120 x 7184 35 us, 64 x 8192 x 8192 18.8 us (3.6 TB/s).
 constexpr int kSmRowsA = 64, kSmGroups = 2, kSmWaves = 4;   // waves of a group
 template <int FT, int S>
 struct Small {
@@ -435,7 +436,8 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 // ---------------------------------------------------------------- streams (few rows)
 // A workgroup holds all rows of a (up to 16) against 16 rows of w; its NW waves take the K-blocks in turn, kAhead of
 // them in flight a wave, straight from memory into registers (every byte of w is read once, by one wave), and their
-// sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (NW kAhead) loads.
+// sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (NW kAhead) loads: 1 x 4096 x 4096 6.6 us,
+// 1 x 8192 x 4096 8.8 us.
 constexpr int kAhead = 4;
 template <int DT, int NW>
 __global__ void __launch_bounds__(64 * NW)

@@ -8,7 +8,8 @@
 // of 10^5 would already be off by 2^-8 radians.
 //
 // Bound by memory (each row is read once and written once or twice); a pair's sine and cosine cost some
-// hundred operations, so they are formed once per token for all heads and kept in LDS.
+// hundred operations, so they are formed once per token for all heads and kept in LDS.  Measured, 32/8 heads of
+// 128: 16384 tokens 90 us (436 MB, 4.8 TB/s; a large copy 5.1 TB/s), 64 tokens 4.4 us, a launch and a chain of two loads.
 #include "attention.h"
 #include "device_common.h"
 #include "internal.h"
