@@ -303,7 +303,7 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
  *   w2, w2_sf, w2_g : fc2 [experts, hidden, inter]
  *   tiled           : 0 = plain layout, 1 = pre-tiled (nvfp4_pretile_weight of the
  *                     stacked matrices, as for nvfp4_moe_w4a16_pretiled)
- *   out             : [tokens, hidden] of x's type
+ *   out             : [tokens, hidden] of x's type, may be x itself
  *   topk_ids_out, topk_w_out : [tokens, top_k] int32 / float, or NULL
  *   act             : NVFP4_ACT_RELU2 or NVFP4_ACT_SWIGLU
  * logits = x . router^T (binary32 sums); the selection is that of
@@ -498,7 +498,9 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
  *               q_heads may be 0 (q and q_out are not used).
  *   k_out     : rotated k by its strides, may be k itself; or NULL: k goes to
  *               the cache only
- * What is written otherwise overlaps nothing that is passed (not checked).
+ * Rows of q_out, and of k_out, lie apart (EINVAL): heads within a token's
+ * stride, or tokens within a head's.  What is written otherwise overlaps nothing
+ * that is passed (not checked).
  * dtype: the type of q, k, v and of everything written (2-byte elements).
  * mscale within -2^96 .. 2^96.  Pointers 2-byte, positions and inv_freq 4-byte,
  * slot_map 8-byte aligned; rows whose parts are not all 16-byte aligned

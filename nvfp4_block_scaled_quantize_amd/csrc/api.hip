@@ -509,6 +509,17 @@ int32_t nvfp4_kv_write(const void* k, const void* v, int64_t tokens, int32_t kv_
   return hip_status(nvfp4::launch_kv_write(a, (hipStream_t)stream));
 }
 
+// Whether the rows [tokens, heads] of dim elements lie apart: heads within tokens, or tokens within heads.
+static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t stride, int64_t head_stride) {
+  if (tokens <= 1 && heads <= 1) return true;
+  if (tokens <= 1) return head_stride >= dim;
+  if (heads <= 1) return stride >= dim;
+  auto inside = [dim](int64_t n, int64_t small, int64_t large) {   // n rows `small` apart, again after `large`
+    return small >= dim && large >= dim && small <= (large - dim) / (n - 1);
+  };
+  return inside(heads, head_stride, stride) || inside(tokens, stride, head_stride);
+}
+
 int32_t nvfp4_rope_kv_write(const void* q, const void* k, const void* v, int32_t dtype, int64_t tokens,
                             int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t q_stride,
                             int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride, int64_t v_stride,
@@ -534,6 +545,9 @@ int32_t nvfp4_rope_kv_write(const void* q, const void* k, const void* v, int32_t
     return NVFP4_EINVAL;
   if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)k_cache |
         (uintptr_t)v_cache) % 2) != 0 || !aligned4(positions) || !aligned4(inv_freq) || ((uintptr_t)slot_map % 8) != 0)
+    return NVFP4_EINVAL;
+  if ((q_heads > 0 && !rows_apart(tokens, q_heads, head_dim, q_out_stride, q_out_head_stride)) ||
+      (k_out && !rows_apart(tokens, kv_heads, head_dim, k_out_stride, k_out_head_stride)))
     return NVFP4_EINVAL;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;

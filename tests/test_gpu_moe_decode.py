@@ -291,3 +291,13 @@ def test_one_token_that_is_not_finite(nv):
     layer = Layer("bf16", 1, 16, 128, 64, "relu2", seed=3)
     layer.w2 = (layer.w2[0], layer.w2[1], layer.w2[2] * 2.0 ** 60)
     full(nv, layer, 4, 1, 1, scaling=2.0 ** 30)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 9])
+def test_in_place(nv, tokens, kind):
+    layer = Layer(kind, tokens, 16, 256, 128, "relu2", seed=tokens)
+    want, _, _ = run(nv, layer, 4, 1, 1)
+    args = layer.args()
+    got = nv.moe_decode(*args, 4, act="relu2", out=args[0])
+    assert got is args[0] and torch.equal(got, want)

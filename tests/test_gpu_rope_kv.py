@@ -203,3 +203,23 @@ def test_streams_and_replays(nv):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((qo, kc, vc), want)), turn
+
+
+def test_broadcast_inputs_and_transposed_outputs(nv):
+    """Heads that share one row (stride 0) as inputs; outputs [heads, tokens, dim]; in place of a shared row it is refused."""
+    g = torch.Generator().manual_seed(8)
+    row = torch.randn((9, 1, 64), generator=g).half()
+    q, k = row.cuda().expand(9, 6, 64), row.cuda().expand(9, 2, 64)
+    positions, freq = torch.arange(9, dtype=torch.int32), 1000.0 ** -(torch.arange(32) / 32)
+    caches = [torch.zeros((2, 2, 8, 64), dtype=torch.float16, device="cuda") for _ in range(2)]
+    args = (positions.cuda(), freq.cuda(), torch.arange(9, device="cuda"), *caches)
+    out = torch.zeros((6, 9, 64), dtype=torch.float16, device="cuda").transpose(0, 1)
+    nv.rope_kv_write(q, k, k, *args, q_out=out)
+    want, room = turned(row, positions, freq, False, 1.0)
+    for h in range(6):
+        near(out[:, h:h + 1].cpu(), want, room, torch.float16)
+    near(caches[0].transpose(1, 2).reshape(16, 2, 64)[:9].cpu(), np.repeat(want, 2, 1), np.repeat(room, 2, 1), torch.float16)
+    assert torch.equal(caches[1].transpose(1, 2).reshape(16, 2, 64)[:9], k)
+    for kw in (dict(q_out=q), dict(q_out=out, k_out=k)):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.rope_kv_write(q, k, k, *args, **kw)

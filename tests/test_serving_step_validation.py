@@ -180,3 +180,17 @@ def test_moe_decode_operands(nv):
         assert "GPU" not in str(e.value), key
     with pytest.raises(ValueError, match="GPU"):
         nv.moe_decode(**ok)
+
+
+def test_rope_kv_write_rows_of_an_output_lie_apart(nv):
+    fn = nv.lib().nvfp4_rope_kv_write
+    for c in [dict(qoh=0), dict(qoh=63), dict(qos=0), dict(qos=255), dict(qoh=64, qos=64), dict(koh=0), dict(kos=127),
+              dict(koh=65, kos=128), dict(qoh=1 << 62, qos=63), dict(qoh=255, qos=64), dict(tokens=1, qoh=63),
+              dict(hq=1, qos=63)]:
+        refuses(fn, ROPE, nv.NVFP4_EINVAL, **c)
+    # apart: these get as far as the device (none here), or run
+    q = torch.zeros((3, 1, 64), dtype=F16).expand(3, 4, 64)
+    z = torch.zeros
+    with pytest.raises((nv.Nvfp4Error, ValueError)):
+        nv.rope_kv_write(q, z((3, 2, 64), dtype=F16), z((3, 2, 64), dtype=F16), z(3, dtype=I32), z(32), z(3, dtype=torch.int64),
+                         z((2, 2, 16, 64), dtype=F16), z((2, 2, 16, 64), dtype=F16), q_out=q)
