@@ -68,6 +68,12 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, bool wide, c
   }
 }
 
+// Workgroup b of `total` runs on XCD b mod 8: its place when each XCD has one run of consecutive places.
+__device__ __forceinline__ int run_of_die(int b, int total) {
+  const int die = b & 7, more = total & 7;
+  return die * (total >> 3) + (die < more ? die : more) + (b >> 3);
+}
+
 // ---------------------------------------------------------------- tiles (many rows)
 // BT rows of a by BF rows of w per workgroup, one 128-k block per stage, two stage buffers: the copies of
 // the next stage (global -> LDS, 16 bytes a lane) are in flight while a stage is computed.  LDS holds
@@ -114,8 +120,7 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
     // consecutive ids go to different XCDs: each XCD walks its own run of tiles, eight rows of tiles deep,
     // so its resident workgroups share row stripes of both operands in its L2
     const int total = tiles_m * tiles_n;
-    int t = blockIdx.x;
-    if (total % 8 == 0) t = (t & 7) * (total / 8) + (t >> 3);
+    const int t = run_of_die(blockIdx.x, total);
     constexpr int kDeep = 8;
     const int band = t / (kDeep * tiles_n), rest = t - band * kDeep * tiles_n;
     const int deep = tiles_m - band * kDeep < kDeep ? tiles_m - band * kDeep : kDeep;
@@ -301,45 +306,46 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 }
 
 // ---------------------------------------------------------------- small tiles (a few hundred rows)
-// Where tiles of the sizes above would leave compute units idle: 64 rows of a by 64 FT rows of w, eight waves in two
-// groups that take the K-blocks in turn, S stage buffers each (S - 1 stages in flight while one is computed).
-// Bound by the lines between the L2 and the compute units: 777 x 2120 x 7184 35 us, 64 x 8192 x 8192 18.8 us (3.6 TB/s).
-constexpr int kSmRowsA = 64, kSmGroups = 2, kSmWaves = 4;   // waves of a group
-template <int FT, int S>
+// Where tiles of the sizes above would leave compute units idle: 64 rows of a by 32, 64 or 128 rows of w, eight waves in
+// groups of W that take the K-blocks in turn, S stage buffers each: S - 1 stages are in flight while the block of one
+// more is in registers and worked on.  A compute unit takes in about 33 bytes a clock of what is not in its L2 yet (of
+// lines that are, 64), however early it asks: issuing the copies is what the waves wait for, so as many compute units
+// as possible are kept busy.  777 x 2120 x 7184 31 us, 64 x 8192 x 8192 15.3 us (4.5 TB/s).
+constexpr int kSmRowsA = 64, kSmAll = 8;   // waves
+template <int FT, int W, int S>
 struct Small {
-  static constexpr int kRowsW = 64 * FT;
-  static constexpr int kCopies = (kSmRowsA + kRowsW) / 8 / kSmWaves;   // of a wave and stage
+  static constexpr int kGroups = kSmAll / W;
+  static constexpr int kRowsW = 16 * FT * W;
+  static constexpr int kCopies = (kSmRowsA + kRowsW) / 8 / W;   // of a wave and stage
   static constexpr int kAOff = kRowsW * 128, kSAOff = (kRowsW + kSmRowsA) * 128, kSWOff = kSAOff + kSmRowsA * 4;
   static constexpr int kStage = kSWOff + 256;
   static_assert(kSmRowsA == 64, "a copy stays in one operand; one wave copies the scales of a");
 };
 
-template <int DT, int FT, int S, bool CUT>
-__global__ void __launch_bounds__(64 * kSmWaves * kSmGroups)
+template <int DT, int FT, int W, int S, bool CUT>
+__global__ void __launch_bounds__(64 * kSmAll)
 fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
-  using C = Small<FT, S>;
-  __shared__ __attribute__((aligned(256))) unsigned char lds[kSmGroups * S * C::kStage];
+  using C = Small<FT, W, S>;
+  __shared__ __attribute__((aligned(256))) unsigned char lds[C::kGroups * S * C::kStage];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave / kSmWaves, gw = wave % kSmWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave / W, gw = wave % W;
   // the tiles of one column of tiles (the same rows of w) follow one another on one XCD
-  int t = blockIdx.x;
-  const int total = tiles_m * tiles_n;
-  if (total % 8 == 0) t = (t & 7) * (total / 8) + (t >> 3);
+  const int t = run_of_die(blockIdx.x, tiles_m * tiles_n);
   const int tn = t / tiles_m, tm = t - tn * tiles_m;
   const int K = g.K, nkb = (K + 127) / 128;
   const int m0 = tm * kSmRowsA, n0 = tn * C::kRowsW;
   const uint32_t l0 = lds_addr(lds) + group * (S * C::kStage);
 
-  // copies: wave w, copy i moves rows 8 (4 i + w) .. + 7 of the stage (rows of w first), lane l the piece (l mod 8)
+  // copies: wave w, copy i moves rows 8 (W i + w) .. + 7 of the stage (rows of w first), lane l the piece (l mod 8)
   // of row l / 8
   uint32_t from[C::kCopies];
   const int tail = (K & 127) / 16;
-  const int piece = (lane & 7) ^ (((gw & 1) * 4 + (lane >> 4)) & 7);   // ^ ((row / 2) mod 8), row = 32 i + 8 w + l / 8
+  const int piece = (lane & 7) ^ (((gw & 1) * 4 + (lane >> 4)) & 7);   // ^ ((row / 2) mod 8), row = 8 W i + 8 w + l / 8
   const bool gone = tail != 0 && piece >= tail;
 #pragma unroll
   for (int i = 0; i < C::kCopies; ++i) {
-    const bool is_w = 32 * i < C::kRowsW;
-    const int r = 32 * i + 8 * gw + (lane >> 3) - (is_w ? 0 : C::kRowsW), last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
+    const bool is_w = 8 * W * i < C::kRowsW;
+    const int r = 8 * W * i + 8 * gw + (lane >> 3) - (is_w ? 0 : C::kRowsW), last = is_w ? g.N - 1 - n0 : g.B - 1 - m0;
     from[i] = (uint32_t)(r < last ? r : last) * (uint32_t)K + 16u * piece;
     asm volatile("" : "+v"(from[i]));   // one register each
   }
@@ -347,18 +353,19 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   const uint8_t* abase = g.a + (int64_t)m0 * K;
   const float* sbase = gw == 0 ? g.as + (int64_t)m0 * nkb : g.ws + (int64_t)(n0 / 128) * nkb;
   const uint32_t sfrom = gw == 0 ? (uint32_t)(lane < g.B - 1 - m0 ? lane : g.B - 1 - m0) * (uint32_t)nkb * 4u : 0u;
-  // stage s of this group: block s kSmGroups + group, or again the last block (not used)
-  auto issue = [&](int s, uint32_t buf) __attribute__((always_inline)) {
-    const int b = s * kSmGroups + group, kb = b < nkb ? b : nkb - 1;
+  // stage s of this group: block s kGroups + group, or again the last block (not used)
+  auto issue = [&](int s, uint32_t buf, int first, int past) __attribute__((always_inline)) {
+    const int b = s * C::kGroups + group, kb = b < nkb ? b : nkb - 1;
     const bool end = kb == nkb - 1;
 #pragma unroll
     for (int i = 0; i < C::kCopies; ++i) {
-      const uint8_t* at = (32 * i < C::kRowsW ? wbase : abase) + (int64_t)kb * 128;
-      const uint32_t to = l0 + buf + (4 * i + gw) * 1024;
+      if (i < first || i >= past) continue;
+      const uint8_t* at = (8 * W * i < C::kRowsW ? wbase : abase) + (int64_t)kb * 128;
+      const uint32_t to = l0 + buf + (W * i + gw) * 1024;
       if constexpr (CUT) dma16_at(gone && end ? reinterpret_cast<const uint8_t*>(kZeros) : at + from[i], to);
       else dma16(at, from[i], to);
     }
-    dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? C::kSAOff : C::kSWOff));
+    if (past == C::kCopies) dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? C::kSAOff : C::kSWOff));
   };
 
   const int wt = gw & 1, wf = gw >> 1;   // this wave's 32 rows of a and 32 FT of w
@@ -377,48 +384,67 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   for (int i = 0; i < FT; ++i)
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[i][q] = 0.0f;
-  auto compute = [&](uint32_t buf) __attribute__((always_inline)) {
+  // operands and scale of a block in registers: read while the block before is worked on
+  v8i a[2][2], w[2][FT][2];
+  float scale[2];
+  auto fetch = [&](uint32_t buf, int set) __attribute__((always_inline)) {
     const uint32_t al = l0 + buf + C::kAOff + wt * 4096 + operand, wl = l0 + buf + wf * (4096 * FT) + operand;
-    const v8i a[2] = {join(read(al), read(al ^ 32)), join(read(al ^ 64), read(al ^ 96))};
-    const float s = read1(l0 + buf + C::kSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + C::kSWOff);
+    a[set][0] = join(read(al), read(al ^ 32));
+    a[set][1] = join(read(al ^ 64), read(al ^ 96));
 #pragma unroll
     for (int i = 0; i < FT; ++i) {
-      const v8i w[2] = {join(read(wl + 4096 * i), read((wl ^ 32) + 4096 * i)),
-                        join(read((wl ^ 64) + 4096 * i), read((wl ^ 96) + 4096 * i))};
-      const v16f p = mfma_block32(w, a);
+      w[set][i][0] = join(read(wl + 4096 * i), read((wl ^ 32) + 4096 * i));
+      w[set][i][1] = join(read((wl ^ 64) + 4096 * i), read((wl ^ 96) + 4096 * i));
+    }
+    scale[set] = read1(l0 + buf + C::kSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + C::kSWOff);
+  };
+  const int steps = (nkb + C::kGroups - 1) / C::kGroups;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][q] = __builtin_fmaf(p[q], s, acc[i][q]);
+  for (int s = 0; s < S; ++s) issue(s, s * C::kStage, 0, C::kCopies);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * (C::kCopies + 1)) : "memory");
+  fetch(0, 0);
+  uint32_t buf = 0;   // of the stage at hand
+  auto step = [&](int s, int set) __attribute__((always_inline)) {
+    const uint32_t next = buf + C::kStage < S * C::kStage ? buf + C::kStage : 0;
+    // this wave's copies of the next stage have landed and its reads of this one are done; then everyone's
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (C::kCopies + 1)) : "memory");
+    // the copies (a compute unit takes 16 clocks for each) go between the products: before them all, a wave would
+    // stand and wait to issue them for as long as the products take
+    v16f p[FT];
+#pragma unroll
+    for (int i = 0; i < FT; ++i) {
+      p[i] = mfma_block32(w[set][i], a[set]);
+      __builtin_amdgcn_sched_barrier(0);
+      issue(s + S, buf, C::kCopies * i / FT, C::kCopies * (i + 1) / FT);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    fetch(next, set ^ 1);
+    buf = next;
+    if (s * C::kGroups + group < nkb) {
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][q] = __builtin_fmaf(p[i][q], scale[set], acc[i][q]);
     }
   };
-
-  const int steps = (nkb + kSmGroups - 1) / kSmGroups;
-  uint32_t buf = 0, fill = 0;
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
-    issue(s, fill);
-    fill += C::kStage;
+  for (int s = 0; s < steps; s += 2) {
+    step(s, 0);
+    if (s + 1 < steps) step(s + 1, 1);
   }
-  for (int s = 0; s < steps; ++s) {
-    // this wave's copies of stage s have landed and its reads of the stage before are done; then everyone's
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (C::kCopies + 1)) : "memory");
-    issue(s + S - 1, fill);
-    fill = fill + C::kStage < S * C::kStage ? fill + C::kStage : 0;
-    if (s * kSmGroups + group < nkb) compute(buf);
-    buf = buf + C::kStage < S * C::kStage ? buf + C::kStage : 0;
-  }
-  // the second group's sums go to the first through LDS
+  // the other groups' sums go to the first through LDS
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   v4f* part = reinterpret_cast<v4f*>(lds);
-  if (group == 1) {
+  if (group > 0) {
 #pragma unroll
     for (int i = 0; i < FT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        part[((gw * FT + i) * 4 + q) * 64 + lane] = v4f{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+        part[(((wave - W) * FT + i) * 4 + q) * 64 + lane] =
+            v4f{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
   }
   __syncthreads();
   const int m = m0 + wt * 32 + r32;
-  if (group == 1 || m >= g.B) return;
+  if (group > 0 || m >= g.B) return;
   const bool vec = g.N % 4 == 0 && ((uintptr_t)g.y % 8) == 0;
   uint16_t* row = (uint16_t*)g.y + (int64_t)m * g.N;
 #pragma unroll
@@ -426,22 +452,26 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int n = n0 + wf * (32 * FT) + 32 * i + 8 * q + 4 * h;
-      v4f v = part[((gw * FT + i) * 4 + q) * 64 + lane];
+      v4f v = {acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += acc[i][4 * q + r];
+      for (int h = 1; h < C::kGroups; ++h) {
+        const v4f o = part[((((h - 1) * W + gw) * FT + i) * 4 + q) * 64 + lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += o[r];
+      }
       if (n < g.N) store4<DT>(row, n, g.N, vec, v);
     }
 }
 
 // ---------------------------------------------------------------- streams (few rows)
-// A workgroup holds all rows of a (up to 16) against 16 rows of w; its NW waves take the K-blocks in turn, kAhead of
+// A workgroup holds all rows of a (up to 16) against 16 rows of w; its waves take the K-blocks in turn, kAhead of
 // them in flight a wave, straight from memory into registers (every byte of w is read once, by one wave), and their
-// sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (NW kAhead) loads: 1 x 4096 x 4096 6.6 us,
-// 1 x 8192 x 4096 8.8 us.
-constexpr int kAhead = 4;
-template <int DT, int NW>
-__global__ void __launch_bounds__(64 * NW)
+// sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (8 kAhead) loads: 1 x 4096 x 4096 6.6 us.
+constexpr int kAhead = 4, kStreamWaves = 8;
+template <int DT>
+__global__ void __launch_bounds__(64 * kStreamWaves)
 fp8_gemm_stream(Fp8GemmArgs g) {
+  constexpr int NW = kStreamWaves;
   __shared__ v4f part[NW][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -526,33 +556,34 @@ void tiles(const Fp8GemmArgs& g, hipStream_t s) {
   }
 }
 
-template <int DT, int FT, int S>
+template <int DT, int FT, int W, int S>
 void small_tiles(const Fp8GemmArgs& g, hipStream_t s) {
-  const int tm = (g.B + kSmRowsA - 1) / kSmRowsA, tn = (g.N + 64 * FT - 1) / (64 * FT);
-  const dim3 grid((unsigned)(tm * tn)), block(64 * kSmWaves * kSmGroups);
-  if (g.K % 128 != 0) fp8_gemm_small<DT, FT, S, true><<<grid, block, 0, s>>>(g, tm, tn);
-  else fp8_gemm_small<DT, FT, S, false><<<grid, block, 0, s>>>(g, tm, tn);
+  constexpr int kRowsW = Small<FT, W, S>::kRowsW;
+  const int tm = (g.B + kSmRowsA - 1) / kSmRowsA, tn = (g.N + kRowsW - 1) / kRowsW;
+  const dim3 grid((unsigned)(tm * tn)), block(64 * kSmAll);
+  if (g.K % 128 != 0) fp8_gemm_small<DT, FT, W, S, true><<<grid, block, 0, s>>>(g, tm, tn);
+  else fp8_gemm_small<DT, FT, W, S, false><<<grid, block, 0, s>>>(g, tm, tn);
 }
 
-template <int DT, int NW>
+template <int DT>
 void stream(const Fp8GemmArgs& g, hipStream_t s) {
-  fp8_gemm_stream<DT, NW><<<dim3((unsigned)((g.N + 15) / 16)), dim3(64 * NW), 0, s>>>(g);
+  fp8_gemm_stream<DT><<<dim3((unsigned)((g.N + 15) / 16)), dim3(64 * kStreamWaves), 0, s>>>(g);
 }
 
 template <int DT>
 void launch(const Fp8GemmArgs& g, hipStream_t s) {
-  // Few rows: streams while one workgroup per compute unit covers w (1 to 16 x 4096 x 4096: 6.4 to 7.1 us, with 64 x 64
-  // tiles 9.9 us), for up to 4 rows two of twice the waves (4 x 8192 x 8192: 16.2 us, tiles 17.1 us; 16 rows: 21.8 and
-  // 17.1 us).  Beyond, tiles: 8 x 28672 x 8192 51 us, streams 56 us.
-  if (g.B <= 16 && g.N <= 16 * 256) return stream<DT, 8>(g, s);
-  if (g.B <= 4 && g.N <= 16 * 512) return stream<DT, 16>(g, s);
+  // Few rows: streams while one workgroup per compute unit covers w (4 x 4096 x 8192: 9.1 us, with 64 x 32 tiles 10.6 us;
+  // 16 rows: 11.7 and 10.7 us).  Beyond, tiles: 4 x 8192 x 4096 8.2 us, streams 10.3 us.
+  if (g.B <= 8 && g.N <= 16 * 256) return stream<DT>(g, s);
   // The sizes of tiles: microseconds per K-block for a round of tiles over the chip, as measured (K = 4096 to 8192),
-  // times the rounds.  64 x 64: 256 at a time (128 x 8192 x 8192: 19.5 us, with 64 x 128 tiles 27 us); 64 x 128: 256 at a
-  // time (512 x 4096 x 4096: 17 us, with 64 x 64 tiles 21 us, 128 x 128 31 us); 128 x 128: 512 at a time, faster while
+  // times the rounds.  64 x 32: one round (64 x 8192 x 8192: 15.3 us, with 64 x 64 tiles 18.4 us); 64 x 64: 256 at a time
+  // (128 x 8192 x 8192: 19.4 us, with 64 x 32 tiles 28 us, 64 x 128 25 us); 64 x 128: 256 at a time (512 x 4096 x 4096: 17
+  // us, with 64 x 64 tiles 21 us, 128 x 128 31 us); 128 x 128: 512 at a time, faster while
   // there is one per compute unit (2048 x 2048 x 4096: 29 us, with 64 x 128 34 us); 256 x 256: 256 at a time
   // (4096 x 8192 x 8192: 248 us; 1000 x 8192 x 8192: 127 us, with 128 x 128 tiles 87 us).
   auto count = [&](int64_t rows, int64_t cols) { return (g.B + rows - 1) / rows * ((g.N + cols - 1) / cols); };
   auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+  if (count(64, 32) <= 256) return small_tiles<DT, 1, 2, 3>(g, s);
   const int64_t mid = count(128, 128);
   const double least_cost = 0.36 * rounds(count(64, 64), 256);
   const double small_cost = 0.6 * rounds(count(64, 128), 256);
@@ -561,8 +592,8 @@ void launch(const Fp8GemmArgs& g, hipStream_t s) {
   const double best = fmin(fmin(least_cost, small_cost), fmin(mid_cost, big_cost));
   if (big_cost == best) return tiles<DT, 8, 4, 2, 4>(g, s);
   if (mid_cost == best) return tiles<DT, 4, 4, 2, 2>(g, s);
-  if (small_cost == best) return small_tiles<DT, 2, 3>(g, s);
-  return small_tiles<DT, 1, 4>(g, s);
+  if (small_cost == best) return small_tiles<DT, 2, 4, 3>(g, s);
+  return small_tiles<DT, 1, 4, 4>(g, s);
 }
 
 }  // namespace

@@ -259,3 +259,15 @@ def test_quantized_product_is_near_the_product(nv):
     y = nv.fp8_gemm(a["codes"], a["scale"], q["codes"], q["scale"]).double()
     want = x.double() @ w.double().t()
     assert float((y - want).norm() / want.norm()) < 2.0 ** -4 * (2 / 3) ** 0.5 * (1 + 2.0 ** -4)
+
+
+@pytest.mark.parametrize("size", [(20, 4100, 528), (64, 8192, 400), (70, 6000, 272), (130, 5000, 1040), (128, 8192, 128),
+                                  (200, 7000, 272), (400, 5000, 656), (64, 9000, 48)])
+def test_every_tile_size(nv, size):
+    """Sizes around the limits between the kernels for a few rows, K not a multiple of 128 and fewer blocks than groups of waves."""
+    a, sa, w, sw = exact_operands(*size, seed=sum(size))
+    want, _ = binary64(a, sa, w, sw)
+    y = nv.fp8_gemm(a, sa, w, sw)
+    assert torch.equal(y, want.to(torch.float16))
+    b = operands(*size, seed=1)
+    check(nv.fp8_gemm(*b, out_dtype=torch.bfloat16), *binary64(*b), size[2])
