@@ -310,23 +310,27 @@ fp8_gemm_tiles(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 // groups of W that take the K-blocks in turn, S stage buffers each: S - 1 stages are in flight while the block of one
 // more is in registers and worked on.  A compute unit takes in about 33 bytes a clock of what is not in its L2 yet (of
 // lines that are, 64), however early it asks: issuing the copies is what the waves wait for, so as many compute units
-// as possible are kept busy.  777 x 2120 x 7184 31 us, 64 x 8192 x 8192 15.3 us (4.5 TB/s).
+// as possible are kept busy, and the scales, a line for each row, are copied four blocks at a time.  777 x 2120 x 7184
+// 29.5 us, 64 x 8192 x 8192 14.0 us (4.9 TB/s).
 constexpr int kSmRowsA = 64, kSmAll = 8;   // waves
 template <int FT, int W, int S>
 struct Small {
   static constexpr int kGroups = kSmAll / W;
   static constexpr int kRowsW = 16 * FT * W;
   static constexpr int kCopies = (kSmRowsA + kRowsW) / 8 / W;   // of a wave and stage
-  static constexpr int kAOff = kRowsW * 128, kSAOff = (kRowsW + kSmRowsA) * 128, kSWOff = kSAOff + kSmRowsA * 4;
-  static constexpr int kStage = kSWOff + 256;
-  static_assert(kSmRowsA == 64, "a copy stays in one operand; one wave copies the scales of a");
+  static constexpr int kAOff = kRowsW * 128, kStage = (kRowsW + kSmRowsA) * 128;
+  // scales of four blocks at a time, in four buffers: 64 rows of a, then w
+  static constexpr int kScales = kGroups * S * kStage, kScalesW = 64 * 16, kFour = kScalesW + 256;
+  static constexpr int kNowhere = kScales + 4 * kFour, kBytes = kNowhere + 256;
+  static_assert(kSmRowsA == 64 && kRowsW % (8 * W) == 0, "a copy stays in one operand");
+  static_assert(kGroups == 2 || kGroups == 4, "a stage has two or four blocks");
 };
 
 template <int DT, int FT, int W, int S, bool CUT>
 __global__ void __launch_bounds__(64 * kSmAll)
 fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   using C = Small<FT, W, S>;
-  __shared__ __attribute__((aligned(256))) unsigned char lds[C::kGroups * S * C::kStage];
+  __shared__ __attribute__((aligned(256))) unsigned char lds[C::kBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), group = wave / W, gw = wave % W;
   // the tiles of one column of tiles (the same rows of w) follow one another on one XCD
@@ -334,7 +338,7 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   const int tn = t / tiles_m, tm = t - tn * tiles_m;
   const int K = g.K, nkb = (K + 127) / 128;
   const int m0 = tm * kSmRowsA, n0 = tn * C::kRowsW;
-  const uint32_t l0 = lds_addr(lds) + group * (S * C::kStage);
+  const uint32_t lds0 = lds_addr(lds), l0 = lds0 + group * (S * C::kStage);
 
   // copies: wave w, copy i moves rows 8 (W i + w) .. + 7 of the stage (rows of w first), lane l the piece (l mod 8)
   // of row l / 8
@@ -351,8 +355,12 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   }
   const uint8_t* wbase = g.w + (int64_t)n0 * K;
   const uint8_t* abase = g.a + (int64_t)m0 * K;
-  const float* sbase = gw == 0 ? g.as + (int64_t)m0 * nkb : g.ws + (int64_t)(n0 / 128) * nkb;
-  const uint32_t sfrom = gw == 0 ? (uint32_t)(lane < g.B - 1 - m0 ? lane : g.B - 1 - m0) * (uint32_t)nkb * 4u : 0u;
+  // the scales: waves 0 to 3 copy four blocks of 16 rows of a each, the others those of w (all lanes' rows the same)
+  const bool of_a = wave < 4;
+  const int srow = 16 * wave + (lane >> 2);
+  const uint32_t sfrom = of_a ? (uint32_t)(srow < g.B - 1 - m0 ? srow : g.B - 1 - m0) * (uint32_t)nkb * 4u : 0u;
+  const float* wscale = g.ws + (int64_t)(n0 / 128) * nkb;
+  const float* sbase = of_a ? g.as + (int64_t)m0 * nkb : wscale;
   // stage s of this group: block s kGroups + group, or again the last block (not used)
   auto issue = [&](int s, uint32_t buf, int first, int past) __attribute__((always_inline)) {
     const int b = s * C::kGroups + group, kb = b < nkb ? b : nkb - 1;
@@ -365,7 +373,12 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
       if constexpr (CUT) dma16_at(gone && end ? reinterpret_cast<const uint8_t*>(kZeros) : at + from[i], to);
       else dma16(at, from[i], to);
     }
-    if (past == C::kCopies) dma4(sbase + kb, sfrom, l0 + buf + (gw == 0 ? C::kSAOff : C::kSWOff));
+    if (past < C::kCopies) return;
+    const int first4 = s * C::kGroups & ~3, sb = first4 + (lane & 3);
+    const uint32_t at = 4u * (uint32_t)(sb < nkb ? sb : nkb - 1);
+    const uint32_t four = lds0 + C::kScales + (first4 / 4 & 3) * C::kFour;
+    if (C::kGroups == 4 || s % 2 == 0) dma4(sbase, sfrom + at, four + (of_a ? 256 * wave : C::kScalesW));
+    else dma4(wscale, 0u, lds0 + C::kNowhere);   // every stage is the same number of copies
   };
 
   const int wt = gw & 1, wf = gw >> 1;   // this wave's 32 rows of a and 32 FT of w
@@ -387,7 +400,7 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
   // operands and scale of a block in registers: read while the block before is worked on
   v8i a[2][2], w[2][FT][2];
   float scale[2];
-  auto fetch = [&](uint32_t buf, int set) __attribute__((always_inline)) {
+  auto fetch = [&](int s, uint32_t buf, int set) __attribute__((always_inline)) {
     const uint32_t al = l0 + buf + C::kAOff + wt * 4096 + operand, wl = l0 + buf + wf * (4096 * FT) + operand;
     a[set][0] = join(read(al), read(al ^ 32));
     a[set][1] = join(read(al ^ 64), read(al ^ 96));
@@ -396,13 +409,15 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
       w[set][i][0] = join(read(wl + 4096 * i), read((wl ^ 32) + 4096 * i));
       w[set][i][1] = join(read((wl ^ 64) + 4096 * i), read((wl ^ 96) + 4096 * i));
     }
-    scale[set] = read1(l0 + buf + C::kSAOff + 4 * (wt * 32 + r32)) * read1(l0 + buf + C::kSWOff);
+    const int kb = s * C::kGroups + group;
+    const uint32_t four = lds0 + C::kScales + (kb / 4 & 3) * C::kFour + 4 * (kb & 3);
+    scale[set] = read1(four + 16 * (wt * 32 + r32)) * read1(four + C::kScalesW);
   };
   const int steps = (nkb + C::kGroups - 1) / C::kGroups;
 #pragma unroll
   for (int s = 0; s < S; ++s) issue(s, s * C::kStage, 0, C::kCopies);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * (C::kCopies + 1)) : "memory");
-  fetch(0, 0);
+  fetch(0, 0, 0);
   uint32_t buf = 0;   // of the stage at hand
   auto step = [&](int s, int set) __attribute__((always_inline)) {
     const uint32_t next = buf + C::kStage < S * C::kStage ? buf + C::kStage : 0;
@@ -418,7 +433,7 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
       issue(s + S, buf, C::kCopies * i / FT, C::kCopies * (i + 1) / FT);
       __builtin_amdgcn_sched_barrier(0);
     }
-    fetch(next, set ^ 1);
+    fetch(s + 1, next, set ^ 1);
     buf = next;
     if (s * C::kGroups + group < nkb) {
 #pragma unroll
@@ -575,19 +590,19 @@ void launch(const Fp8GemmArgs& g, hipStream_t s) {
   // Few rows: streams while one workgroup per compute unit covers w (4 x 4096 x 8192: 9.1 us, with 64 x 32 tiles 10.6 us;
   // 16 rows: 11.7 and 10.7 us).  Beyond, tiles: 4 x 8192 x 4096 8.2 us, streams 10.3 us.
   if (g.B <= 8 && g.N <= 16 * 256) return stream<DT>(g, s);
-  // The sizes of tiles: microseconds per K-block for a round of tiles over the chip, as measured (K = 4096 to 8192),
-  // times the rounds.  64 x 32: one round (64 x 8192 x 8192: 15.3 us, with 64 x 64 tiles 18.4 us); 64 x 64: 256 at a time
-  // (128 x 8192 x 8192: 19.4 us, with 64 x 32 tiles 28 us, 64 x 128 25 us); 64 x 128: 256 at a time (512 x 4096 x 4096: 17
-  // us, with 64 x 64 tiles 21 us, 128 x 128 31 us); 128 x 128: 512 at a time, faster while
-  // there is one per compute unit (2048 x 2048 x 4096: 29 us, with 64 x 128 34 us); 256 x 256: 256 at a time
-  // (4096 x 8192 x 8192: 248 us; 1000 x 8192 x 8192: 127 us, with 128 x 128 tiles 87 us).
+  // The sizes of tiles: microseconds per K-block as measured (K = 4096 to 8192).  64 x 32: one round (64 x 8192 x 8192:
+  // 14.0 us, with 64 x 64 tiles 18 us).  64 x 64: 256 at a time (128 x 8192 x 8192: 17.5 us, 64 x 128 25 us; 200 x 5000 x
+  // 8192: 30 us, 64 x 128 22 us).  64 x 128: the same, but further ones in proportion (400 x 8192 x 4096: 27 us, 64 x 64 36
+  // us, 128 x 128 31 us).  128 x 128: 512 at a time, faster while there is one per compute unit (2048 x 2048 x 4096: 29
+  // us, 64 x 128 32 us).  256 x 256: 256 at a time (4096 x 8192 x 8192: 248 us, 128 x 128 335 us; 1000 x 8192 x 8192: 127
+  // us, 128 x 128 86 us).
   auto count = [&](int64_t rows, int64_t cols) { return (g.B + rows - 1) / rows * ((g.N + cols - 1) / cols); };
   auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
   if (count(64, 32) <= 256) return small_tiles<DT, 1, 2, 3>(g, s);
   const int64_t mid = count(128, 128);
-  const double least_cost = 0.36 * rounds(count(64, 64), 256);
-  const double small_cost = 0.6 * rounds(count(64, 128), 256);
-  const double mid_cost = mid <= 256 ? 0.9 : 1.4 * rounds(mid, 512);
+  const double least_cost = 0.29 * rounds(count(64, 64), 256);
+  const double small_cost = 0.52 + 0.55 * fmax(0.0, (double)(count(64, 128) - 256) / 256.0);
+  const double mid_cost = mid <= 256 ? 0.95 : mid <= 512 ? 1.25 : 1.4 * rounds(mid, 512);
   const double big_cost = 2.0 * rounds(count(256, 256), 256);
   const double best = fmin(fmin(least_cost, small_cost), fmin(mid_cost, big_cost));
   if (big_cost == best) return tiles<DT, 8, 4, 2, 4>(g, s);
