@@ -418,8 +418,7 @@ int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k
  * K-blocks are binary32).
  *   a, w       : [B, K], [N, K] E4M3 codes, 16-byte aligned
  *   a_scale    : [B, ceil(K/128)] float, w_scale : [ceil(N/128), ceil(K/128)] float
- *   y          : [B, N] of out_dtype, 2-byte aligned (8-byte aligned and N % 4 == 0
- *                for wide stores)
+ *   y          : [B, N] of out_dtype, 2-byte aligned
  * Requires K % 16 == 0 (EINVAL), K < 2^24, ceil(B/128) * ceil(N/128) <= 2^22
  * (EUNSUPPORTED).  B == 0 is a no-op.
  */

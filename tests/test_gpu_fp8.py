@@ -271,3 +271,17 @@ def test_every_tile_size(nv, size):
     assert torch.equal(y, want.to(torch.float16))
     b = operands(*size, seed=1)
     check(nv.fp8_gemm(*b, out_dtype=torch.bfloat16), *binary64(*b), size[2])
+
+
+@pytest.mark.parametrize("B", [3, 70, 300, 1500])
+@pytest.mark.parametrize("N", [257, 514, 1027])
+def test_rows_at_any_alignment(nv, N, B):
+    """Rows that start at any two bytes, the output itself too: exact results, and nothing beside them is touched."""
+    a, sa, w, sw = exact_operands(B, N, 400, seed=N + B)
+    want = binary64(a, sa, w, sw)[0].to(torch.float16)
+    for shift in (0, 1, 2, 3):
+        room = torch.full((B * N + 8,), 7.0, dtype=torch.float16, device="cuda")
+        y = room[shift:shift + B * N].view(B, N)
+        nv.fp8_gemm(a, sa, w, sw, out=y)
+        assert torch.equal(y, want)
+        assert (room[:shift] == 7).all() and (room[shift + B * N:] == 7).all()
