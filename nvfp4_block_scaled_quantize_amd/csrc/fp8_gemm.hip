@@ -18,6 +18,7 @@
 
 #include "device_common.h"
 #include "fp8.h"
+#include "fp8_tiles.h"
 #include "internal.h"
 #include "lds_dma.h"
 
@@ -584,30 +585,26 @@ void stream(const Fp8GemmArgs& g, hipStream_t s) {
   fp8_gemm_stream<DT><<<dim3((unsigned)((g.N + 15) / 16)), dim3(64 * kStreamWaves), 0, s>>>(g);
 }
 
+constexpr bool is(Fp8Tiles t, int rows, int cols, int threads) {
+  return kFp8TileSizes[t].rows == rows && kFp8TileSizes[t].cols == cols && kFp8TileSizes[t].threads == threads;
+}
+static_assert(is(kFp8Tiles64x32, kSmRowsA, Small<1, 2, 3>::kRowsW, 64 * kSmAll) &&
+              is(kFp8Tiles64x64, kSmRowsA, Small<1, 4, 4>::kRowsW, 64 * kSmAll) &&
+              is(kFp8Tiles64x128, kSmRowsA, Small<2, 4, 3>::kRowsW, 64 * kSmAll) &&
+              is(kFp8Tiles128x128, Tile<4, 4, 2, 2, 4>::kRowsA, Tile<4, 4, 2, 2, 4>::kRowsW, Tile<4, 4, 2, 2, 4>::kThreads) &&
+              is(kFp8Tiles256x256, Tile<8, 4, 2, 4, 4>::kRowsA, Tile<8, 4, 2, 4, 4>::kRowsW, Tile<8, 4, 2, 4, 4>::kThreads),
+              "the kernels have the sizes that they are chosen by");
+
 template <int DT>
 void launch(const Fp8GemmArgs& g, hipStream_t s) {
-  // Few rows: streams while one workgroup per compute unit covers w (4 x 4096 x 8192: 9.1 us, with 64 x 32 tiles 10.6 us;
-  // 16 rows: 11.7 and 10.7 us).  Beyond, tiles: 4 x 8192 x 4096 8.2 us, streams 10.3 us.
-  if (g.B <= 8 && g.N <= 16 * 256) return stream<DT>(g, s);
-  // The sizes of tiles: microseconds per K-block as measured (K = 4096 to 8192).  64 x 32: one round (64 x 8192 x 8192:
-  // 14.0 us, with 64 x 64 tiles 18 us).  64 x 64: 256 at a time (128 x 8192 x 8192: 17.5 us, 64 x 128 25 us; 200 x 5000 x
-  // 8192: 30 us, 64 x 128 22 us).  64 x 128: the same, but further ones in proportion (400 x 8192 x 4096: 27 us, 64 x 64 36
-  // us, 128 x 128 31 us).  128 x 128: 512 at a time, faster while there is one per compute unit (2048 x 2048 x 4096: 29
-  // us, 64 x 128 32 us).  256 x 256: 256 at a time (4096 x 8192 x 8192: 248 us, 128 x 128 335 us; 1000 x 8192 x 8192: 127
-  // us, 128 x 128 86 us).
-  auto count = [&](int64_t rows, int64_t cols) { return (g.B + rows - 1) / rows * ((g.N + cols - 1) / cols); };
-  auto rounds = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
-  if (count(64, 32) <= 256) return small_tiles<DT, 1, 2, 3>(g, s);
-  const int64_t mid = count(128, 128);
-  const double least_cost = 0.29 * rounds(count(64, 64), 256);
-  const double small_cost = 0.52 + 0.55 * fmax(0.0, (double)(count(64, 128) - 256) / 256.0);
-  const double mid_cost = mid <= 256 ? 0.95 : mid <= 512 ? 1.25 : 1.4 * rounds(mid, 512);
-  const double big_cost = 2.0 * rounds(count(256, 256), 256);
-  const double best = fmin(fmin(least_cost, small_cost), fmin(mid_cost, big_cost));
-  if (big_cost == best) return tiles<DT, 8, 4, 2, 4>(g, s);
-  if (mid_cost == best) return tiles<DT, 4, 4, 2, 2>(g, s);
-  if (small_cost == best) return small_tiles<DT, 2, 4, 3>(g, s);
-  return small_tiles<DT, 1, 4, 4>(g, s);
+  switch (fp8_tiles(g.B, g.N)) {
+    case kFp8Stream: return stream<DT>(g, s);
+    case kFp8Tiles64x32: return small_tiles<DT, 1, 2, 3>(g, s);
+    case kFp8Tiles64x64: return small_tiles<DT, 1, 4, 4>(g, s);
+    case kFp8Tiles64x128: return small_tiles<DT, 2, 4, 3>(g, s);
+    case kFp8Tiles128x128: return tiles<DT, 4, 4, 2, 2>(g, s);
+    case kFp8Tiles256x256: return tiles<DT, 8, 4, 2, 4>(g, s);
+  }
 }
 
 }  // namespace
