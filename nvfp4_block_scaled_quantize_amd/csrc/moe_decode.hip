@@ -506,6 +506,14 @@ __device__ __forceinline__ void load_act(const void* src, int64_t row, bool ther
   }
 }
 
+// What the FP16 numbers p leave of a and b.  Nothing of an infinity: inf - inf is NaN, of which and a number the maximum is
+// the number, and beside the infinity that changes no sum.  (A remainder is below 2^-10 of 2^15.)
+__device__ __forceinline__ v2h rest2(float a, float b, const v2h& p) {
+  const v2h q = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(a - (float)p[0], b - (float)p[1]));
+  const v2h least = {(_Float16)-64.0f, (_Float16)-64.0f};
+  return __builtin_elementwise_max(q, least);
+}
+
 // Operands of instruction m.  FC 1: as stored.  FC 2: scaled and split; both roundings are toward zero,
 // the first leaves less than 2^-10 of the value, the second less than 2^-10 of that.
 template <int FC>
@@ -518,7 +526,7 @@ __device__ __forceinline__ void act_operand(const RawAct<FC>& r, int m, float sc
       const float a = __uint_as_float(r.v[2 * m + i / 2][2 * (i & 1)]) * scale;
       const float b = __uint_as_float(r.v[2 * m + i / 2][2 * (i & 1) + 1]) * scale;
       const v2h p = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(a, b));
-      const v2h q = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(a - (float)p[0], b - (float)p[1]));
+      const v2h q = rest2(a, b, p);
       hi[2 * i] = p[0];
       hi[2 * i + 1] = p[1];
       lo[2 * i] = q[0];
@@ -899,7 +907,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
       for (int q = 0; q < 4; q += 2) {
         const float v0 = h[i][q] * fk[i] * scale, v1 = h[i][q + 1] * fk[i] * scale;
         const v2h p = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(v0, v1));
-        const v2h r = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(v0 - (float)p[0], v1 - (float)p[1]));
+        const v2h r = rest2(v0, v1, p);
         *reinterpret_cast<v2h*>(&acts[wave][i][0][4 * lane + q]) = p;
         *reinterpret_cast<v2h*>(&acts[wave][i][1][4 * lane + q]) = r;
       }

@@ -1,0 +1,68 @@
+"""The MoE layer at the ends of binary32: activations of an expert that overflow."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_moe_decode as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_block_scaled_quantize_amd as nv
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return nv
+
+
+def one_large_row(tokens, hidden, inter, act, seed):
+    """BF16 tokens of 2^57 times a normal number; of every expert's h a few rows are beyond binary32, the others not."""
+    layer = moe.Layer("bf16", tokens, 4, hidden, inter, act, seed=seed, x_scale=2.0 ** 57)
+    layer.router = torch.zeros_like(layer.router)
+    layer.bias = torch.zeros(4)
+    codes, sf, glob = layer.w1
+    sf = torch.full(sf.shape, 2.0 ** -6).to(moe.FP8).view(torch.uint8)
+    at = torch.randperm(inter, generator=torch.Generator().manual_seed(seed))[:3]
+    for rows in ((at, at + inter) if act == "swiglu" else (at,)):
+        sf[:, rows] = torch.tensor(448.0).to(moe.FP8).view(torch.uint8)
+    layer.w1 = (codes, sf, glob * 2.0 ** 7)
+    return layer
+
+
+def by_definition(layer, ids, wts):
+    """h in binary32 (overflow is an infinity), then products and sums of the definition: 0 * inf and inf - inf are NaN."""
+    x = layer.x.double()
+    out = torch.zeros(x.shape, dtype=torch.float64)
+    few = 0
+    for t in range(len(ids)):
+        for e, w in zip(ids[t], wts[t]):
+            w1, w2 = (moe.values(m[0][e], m[1][e], m[2][e]) for m in (layer.w1, layer.w2))
+            y = w1 @ x[t]
+            if layer.act == "swiglu":
+                gate, up = y[:layer.inter], y[layer.inter:]
+                h = gate * torch.sigmoid(gate) * up
+            else:
+                h = torch.clamp(y, min=0) ** 2
+            # none so near the border that the sum's roundings decide
+            border = 2.0 ** 128
+            assert ((h.abs() < border / 4) | (h.abs() > border * 4)).all()
+            h = h.to(torch.float32).double()
+            few += int(torch.isinf(h).sum())
+            out[t] += w * (w2 * h).sum(1)
+    assert few > 0
+    return out
+
+
+@pytest.mark.parametrize("act", ["relu2", "swiglu"])
+@pytest.mark.parametrize("size", [(1, 256, 128), (6, 256, 128), (3, 192, 2112), (1, 192, 2112), (20, 64, 1088)])
+def test_infinite_activations(nv, size, act):
+    """An output is an infinity where the definition has one, and NaN only where it has NaN."""
+    tokens, hidden, inter = size
+    for seed in range(2):
+        layer = one_large_row(tokens, hidden, inter, act, seed)
+        out, ids, wts = moe.run(nv, layer, 2, 1, 1)
+        want = by_definition(layer, ids.tolist(), wts.double().tolist()).numpy()
+        got = out.double().cpu().numpy()
+        assert np.isinf(want).any()
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
