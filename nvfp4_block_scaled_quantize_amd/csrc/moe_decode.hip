@@ -80,10 +80,23 @@ size_t carve(void* base, int T, int E, int P, int hidden, int inter, Ws* w) {
 }
 
 // The power of two that brings a largest value to [2^14, 2^15).
-__device__ __forceinline__ float up_scale(uint32_t bits) {
+__device__ __forceinline__ int up_exponent(uint32_t bits) {
   const int e = (int)(bits >> 23) - 127;   // -127 for zeros and subnormal numbers
-  return __builtin_ldexpf(1.0f, 14 - e < 127 ? 14 - e : 127);
+  return 14 - e < 127 ? 14 - e : 127;
 }
+__device__ __forceinline__ float up_scale(uint32_t bits) { return __builtin_ldexpf(1.0f, up_exponent(bits)); }
+
+// A factor as its fraction (0.5 <= |f| < 1, or 0, inf, NaN) and the power of two beside it: of a global scale and the power
+// of two that a sum was scaled by, or of a weight and a global, the quotient or product may leave binary32 where the result
+// does not.
+struct Factor {
+  float f;
+  int e;
+};
+__device__ __forceinline__ Factor split(float x) {
+  return Factor{__builtin_amdgcn_frexp_mantf(x), __builtin_amdgcn_frexp_expf(x)};
+}
+__device__ __forceinline__ float times(float v, const Factor& x) { return __builtin_ldexpf(v * x.f, x.e); }
 
 // ---------------------------------------------------------------- router
 __device__ __forceinline__ float wave_sum(float v) {
@@ -689,17 +702,18 @@ __global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int unit
       v4f up;
       if constexpr (GATED) up = joined(wave + RT / 2);
       const int col = x * kCols + 16 * wave + 4 * grp;
-      const float f = FC == 2 || a.scaled ? ge / up_scale(top) : ge;
+      Factor f = split(ge);
+      if (FC == 2 || a.scaled) f.e -= up_exponent(top);
       if constexpr (FC == 1) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          v[q] = GATED ? swiglu_f32(v[q] * f, up[q] * f) : relu2_f32(v[q] * f);
+          v[q] = GATED ? swiglu_f32(times(v[q], f), times(up[q], f)) : relu2_f32(times(v[q], f));
           big = __builtin_fmaxf(big, __builtin_fabsf(v[q]));
         }
         if (there) *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(mine.y + r16) * a.inter + col) = v;
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] *= f;
+        for (int q = 0; q < 4; ++q) v[q] = times(v[q], f);
         if (there) *reinterpret_cast<v4f*>(a.ws.o + (int64_t)(mine.y + r16) * a.hidden + col) = v;
       }
     }
@@ -832,10 +846,11 @@ __global__ void __launch_bounds__(64 * kOneRowsWaves) moe_one_rows(FcArgs a) {
     float v = part[0][lane & 31];
 #pragma unroll
     for (int q = 1; q < NW; ++q) v += part[q][lane & 31];
-    const float f = a.scaled ? a.g[e] / up_scale(a.ws.xmax[0]) : a.g[e];
+    Factor f = split(a.g[e]);
+    if (a.scaled) f.e -= up_exponent(a.ws.xmax[0]);
     float h;
-    if constexpr (GATED) h = swiglu_f32(v * f, __shfl_xor(v, 16, 64) * f);
-    else h = relu2_f32(v * f);
+    if constexpr (GATED) h = swiglu_f32(times(v, f), times(__shfl_xor(v, 16, 64), f));
+    else h = relu2_f32(times(v, f));
     if (lane < kCols) a.ws.h[(int64_t)y * a.inter + (int64_t)blockIdx.x * kCols + lane] = h;
     const uint32_t big = wave_max_u32(lane < kCols ? __float_as_uint(__builtin_fmaxf(__builtin_fabsf(h), 0.0f)) : 0u);
     if (lane == 0) atomicMax(a.ws.hmax + y, big);
@@ -880,22 +895,24 @@ __global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
   const int blocks = (a.K + 255) / 256, steps = top_k * blocks;
   const int k = lane < top_k ? lane : 0;
   const int e = a.ws.chosen[k].x;
-  const float hm = __uint_as_float(a.ws.hmax[k]);
-  const float f = a.ws.wts[k] * a.g[e];
-  // the largest h times its factor goes to [2^14, 2^15)
-  const float scale = up_scale(wave_max_u32(__float_as_uint(__builtin_fmaxf(hm * __builtin_fabsf(f), 0.0f))));
+  const Factor fw = split(a.ws.wts[k]), fg = split(a.g[e]);
+  const Factor f{fw.f * fg.f, fw.e + fg.e};
+  // the largest h times its factor goes to [2^14, 2^15): the exponents of the products, and the largest of them (|e| < 512)
+  const uint32_t big = __float_as_uint(__uint_as_float(a.ws.hmax[k]) * f.f) & 0x7FFFFFFFu;
+  const int up = 14 + 512 - (int)wave_max_u32(big != 0u ? (uint32_t)((int)(big >> 23) - 127 + f.e + 512) : 0u);
   v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s0 = wave; s0 < steps; s0 += 2 * kOneWaves) {
     Piece w[2];
     v4f h[2];
-    float fk[2];
+    Factor fk[2];
     int c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = s0 + i * kOneWaves < steps ? s0 + i * kOneWaves : s0, rank = s / blocks;
       c[i] = s - rank * blocks;
       const int ek = __builtin_amdgcn_readlane(e, rank);
-      fk[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), rank));
+      fk[i].f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f.f), rank));
+      fk[i].e = __builtin_amdgcn_readlane(f.e, rank) + up;
       load_piece<TW>(a.w, a.sf, (int64_t)ek * a.rows + 16 * (int)blockIdx.x, c[i], a.K, lane, true, w[i]);
       const int at = 256 * c[i] + 4 * lane;
       h[i] = *reinterpret_cast<const v4f*>(a.ws.h + (int64_t)rank * a.inter + (at < a.K ? at : 0));
@@ -905,7 +922,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int q = 0; q < 4; q += 2) {
-        const float v0 = h[i][q] * fk[i] * scale, v1 = h[i][q + 1] * fk[i] * scale;
+        const float v0 = times(h[i][q], fk[i]), v1 = times(h[i][q + 1], fk[i]);
         const v2h p = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(v0, v1));
         const v2h r = rest2(v0, v1, p);
         *reinterpret_cast<v2h*>(&acts[wave][i][0][4 * lane + q]) = p;
@@ -937,7 +954,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
   float s = part[0][tid];
 #pragma unroll
   for (int v = 1; v < kOneWaves; ++v) s += part[v][tid];
-  s /= scale;
+  s = __builtin_ldexpf(s, -up);
   ((uint16_t*)a.out)[16 * (int)blockIdx.x + tid] =
       a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s) : __builtin_bit_cast(uint16_t, (_Float16)s);
 }

@@ -1,9 +1,11 @@
-"""The MoE layer at the ends of binary32: activations of an expert that overflow."""
+"""The MoE layer at the ends of binary32: activations of an expert that overflow, and small ones whose scales' product
+leaves the normal range though the result does not."""
 import numpy as np
 import pytest
 import torch
 
 import test_gpu_moe_decode as moe
+import test_gpu_moe_decode_kernels as kernels
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,21 @@ def test_infinite_activations(nv, size, act):
         assert np.isinf(want).any()
         assert np.array_equal(np.isnan(got), np.isnan(want))
         assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+
+
+def tiny(tokens):
+    """h of about 2^-84, fc2 of one large value everywhere, and globals that bring the sum to about 2^-125."""
+    layer = moe.Layer("bf16", tokens, 8, 256, 2048, "relu2", seed=21, x_scale=2.0 ** -50)
+    layer.w1 = (layer.w1[0], (layer.w1[1].view(moe.FP8).float() * 256).to(moe.FP8).view(torch.uint8), layer.w1[2])
+    codes, sf, glob = layer.w2
+    largest = torch.tensor(448.0).to(moe.FP8).view(torch.uint8)
+    layer.w2 = (torch.full_like(codes, 0x77), torch.full_like(sf, int(largest)), glob * 2.0 ** -58)
+    return layer
+
+
+@pytest.mark.parametrize("tokens", [1, 6])
+def test_scales_whose_product_is_subnormal(nv, tokens):
+    """Outputs that are normal numbers of BF16, though h times the global, and the global over the power of two that h is
+    scaled by, are not."""
+    out = kernels.full(nv, tiny(tokens), 8)
+    assert out.abs().median() > 2.0 ** -126
