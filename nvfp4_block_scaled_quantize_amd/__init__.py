@@ -164,6 +164,20 @@ def _dtype_code(x: torch.Tensor) -> int:
     raise TypeError("input must be bfloat16 or float16")
 
 
+def _need_32_bits(**numbers):
+    """The C entry points take these as 32-bit integers, and ctypes would cut them without a word."""
+    for name, v in numbers.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError("%s must fit 32 bits, got %d" % (name, v))
+
+
+def _act_code(act) -> int:
+    a = ACT[act] if isinstance(act, str) else int(act)
+    if a >> 31:
+        _need_32_bits(act=a)
+    return a
+
+
 def _workspace(nbytes: int, device, workspace: torch.Tensor | None):
     if nbytes == 0:
         return None, 0
@@ -221,7 +235,7 @@ def act_quant(x: torch.Tensor, act: str = "none", want_scale: bool = True, out: 
     _need_2d(x, "x")
     _dtype_code(x)
     rows, k_in = x.shape
-    a = ACT[act] if isinstance(act, str) else int(act)
+    a = _act_code(act)
     k_out = k_in // 2 if a == ACT["swiglu"] else k_in
     if out is not None:
         _quant_out(out, rows, k_out, rows)
@@ -475,7 +489,7 @@ def mx_quantize(x: torch.Tensor, act: str = "none", group_rows: int = 1, tiled: 
     _need_2d(x, "x")
     _dtype_code(x)
     rows, k_in = x.shape
-    a = ACT[act] if isinstance(act, str) else int(act)
+    a = _act_code(act)
     k = k_in // 2 if a == ACT["swiglu"] else k_in
     if out is not None:
         if tiled:
@@ -609,13 +623,6 @@ def _handle(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _need_32_bits(**numbers):
-    """The C entry points take these as 32-bit integers, and ctypes would cut them without a word."""
-    for name, v in numbers.items():
-        if not -(1 << 31) <= v < 1 << 31:
-            raise ValueError("%s must fit 32 bits, got %d" % (name, v))
-
-
 def _overlap(a, b) -> bool:
     """Whether two dense tensors share memory."""
     x, y, n, m = a.data_ptr(), b.data_ptr(), a.numel() * a.element_size(), b.numel() * b.element_size()
@@ -647,7 +654,7 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, act: str = "none", out: d
     scale per 128 values of a row (block_rows=1: activations) or per 128 x 128 values (block_rows=128:
     weights), with the optional activation in front.  Returns dict(codes [rows, k] float8_e4m3fn, scale
     [ceil(rows / block_rows), ceil(k / 128)] float32)."""
-    a = ACT[act] if isinstance(act, str) else int(act)
+    a = _act_code(act)
     dev = _gpu_of(x)
     try:
         rows, k_in = x.shape
@@ -722,6 +729,7 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: t
 
 @functools.lru_cache(maxsize=1024)
 def moe_decode_workspace_size(tokens: int, experts: int, top_k: int, hidden: int, inter: int) -> int:
+    _need_32_bits(tokens=tokens, experts=experts, top_k=top_k, hidden=hidden, inter=inter)
     return int(_lib.nvfp4_moe_decode_workspace_size(tokens, experts, top_k, hidden, inter))
 
 
@@ -773,7 +781,7 @@ def moe_decode(x: torch.Tensor, router: torch.Tensor, bias: torch.Tensor, w1: to
     bfloat16), the expert weights of moe_w4a16() (or, with `tiled`, of moe_pretile_weights()); for act="swiglu" w1
     holds [experts, 2 inter, ...] gate and up rows.  Returns out [tokens, hidden] of x's type, or (out, ids,
     weights) with want_routing."""
-    a = ACT[act] if isinstance(act, str) else int(act)
+    a = _act_code(act)
     gated = a == ACT["swiglu"]
     dev = _gpu_of(x)
     if dev < 0 or not _plain_moe_decode(x, router, bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, gated, out, workspace, dev):
