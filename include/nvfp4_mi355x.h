@@ -317,7 +317,8 @@ int32_t nvfp4_moe_w4a16_noalloc(const float* router_logits, const float* correct
  * scales 4-byte aligned (EINVAL otherwise); tokens <= 32, hidden and inter
  * <= 65536 (EUNSUPPORTED).  workspace: nvfp4_moe_decode_workspace_size bytes,
  * 256-byte aligned, contents before the call do not matter; calls that may
- * overlap in time need workspaces of their own.
+ * overlap in time need workspaces of their own.  What is written overlaps
+ * nothing else that is passed, but for an out that is x (EINVAL).
  */
 int32_t nvfp4_moe_decode(const void* x, int32_t dtype, const void* router, const float* correction_bias,
                          const uint8_t* w1, const uint8_t* w1_sf, const float* w1_g, const uint8_t* w2,
@@ -408,7 +409,8 @@ int32_t nvfp4_mx_gemm(const uint8_t* a_tiled, const uint8_t* a_sf_tiled, const f
  *   block_rows : 1 (activations) or 128 (weights)
  *   codes : [rows, k] out; scale : [ceil(rows / block_rows), ceil(k / 128)] out
  * Requires k % 16 == 0; x not 16-byte or codes not 8-byte aligned take a
- * scalar path with identical results.
+ * scalar path with identical results.  codes, scale and x overlap nowhere
+ * (EINVAL).
  */
 int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int32_t act, int32_t block_rows,
                            uint8_t* codes, float* scale, void* stream);
@@ -420,7 +422,7 @@ int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k
  *   a_scale    : [B, ceil(K/128)] float, w_scale : [ceil(N/128), ceil(K/128)] float
  *   y          : [B, N] of out_dtype, 2-byte aligned
  * Requires K % 16 == 0 (EINVAL), K < 2^24, ceil(B/128) * ceil(N/128) <= 2^22
- * (EUNSUPPORTED).  B == 0 is a no-op.
+ * (EUNSUPPORTED).  y overlaps no operand (EINVAL).  B == 0 is a no-op.
  */
 int32_t nvfp4_fp8_gemm(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, void* y,
                        int32_t out_dtype, int64_t B, int64_t N, int64_t K, void* stream);

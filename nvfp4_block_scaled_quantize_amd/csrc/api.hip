@@ -55,6 +55,13 @@ bool overlap(const Bytes& a, const Bytes& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
 }
+// Whether one of the first `written` buffers overlaps another of the n.
+bool any_overlap(const Bytes* b, int written, int n) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(b[i], b[j])) return true;
+  return false;
+}
 bool aligned256(const void* p) { return ((uintptr_t)p % 256) == 0; }
 
 // External weights of "Fused Nvfp4 GEMM All Reduce Plugin" (external-weight
@@ -445,6 +452,13 @@ int32_t nvfp4_moe_decode(const void* x, int32_t dtype, const void* router, const
     return NVFP4_EINVAL;
   const size_t need = nvfp4::moe_decode_workspace_bytes(tokens, experts, top_k, hidden, inter);
   if (!workspace || workspace_bytes < need || !aligned256(workspace)) return NVFP4_EWORKSPACE;
+  // what is written overlaps nothing else, but out may be x
+  const size_t t = (size_t)tokens, e = (size_t)experts, values = (size_t)hidden * inter;
+  const size_t n1 = e * values * (act == NVFP4_ACT_SWIGLU ? 2 : 1), n2 = e * values, pairs = t * top_k * 4, io = t * hidden * 2;
+  const Bytes all[] = {{out, io}, {topk_ids_out, topk_ids_out ? pairs : 0}, {topk_w_out, topk_w_out ? pairs : 0},
+                       {workspace, need}, {router, e * hidden * 2}, {correction_bias, e * 4}, {w1, n1 / 2}, {w1_sf, n1 / 16},
+                       {w1_g, e * 4}, {w2, n2 / 2}, {w2_sf, n2 / 16}, {w2_g, e * 4}, {x, out == x ? 0 : io}};
+  if (any_overlap(all, 4, 13)) return NVFP4_EINVAL;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
   nvfp4::MoeDecodeArgs m{x, dtype, router, correction_bias, w1, w1_sf, w1_g, w2, w2_sf, w2_g, out, topk_ids_out,
@@ -574,6 +588,10 @@ int32_t nvfp4_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k
   if (k > (1LL << 30) || rows > (1LL << 37)) return NVFP4_EUNSUPPORTED;
   if (block_rows == 1 ? rows > ((1LL << 30) - (1 << 16)) / nkb : (rows + 127) / 128 > ((1LL << 24) - 1) / nkb)
     return NVFP4_EUNSUPPORTED;
+  // workgroups write while others still read
+  const size_t r = (size_t)rows, row = (size_t)k * (act == NVFP4_ACT_SWIGLU ? 4 : 2);
+  const Bytes all[] = {{codes, r * k}, {scale, (r + block_rows - 1) / block_rows * nkb * 4}, {x, r * row}};
+  if (any_overlap(all, 2, 3)) return NVFP4_EINVAL;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
   nvfp4::Fp8QuantArgs a{x, dtype, act, rows, (int)k, block_rows, codes, scale};
@@ -592,6 +610,10 @@ int32_t nvfp4_fp8_gemm(const uint8_t* a, const float* a_scale, const uint8_t* w,
   if (K >= (1 << 24) || B > (1 << 30) || N > (1 << 30) ||
       ((B + 127) / 128) * ((N + 127) / 128) > (1 << 22))
     return NVFP4_EUNSUPPORTED;
+  const size_t nkb = ((size_t)K + 127) / 128;
+  const Bytes all[] = {{y, (size_t)B * N * 2}, {a, (size_t)B * K}, {a_scale, B * nkb * 4}, {w, (size_t)N * K},
+                       {w_scale, ((size_t)N + 127) / 128 * nkb * 4}};
+  if (any_overlap(all, 1, 5)) return NVFP4_EINVAL;
   const int32_t ds = device_status();
   if (ds != NVFP4_OK) return ds;
   nvfp4::Fp8GemmArgs g{a, a_scale, w, w_scale, y, out_dtype, (int)B, (int)N, (int)K};
