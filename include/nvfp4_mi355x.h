@@ -68,7 +68,7 @@ extern "C" {
 /* Activations fused in front of the quantizer. */
 #define NVFP4_ACT_NONE 0
 #define NVFP4_ACT_SWIGLU 1    /* y = silu(gate) * up; gate = first half of the row */
-#define NVFP4_ACT_RELU2 2     /* y = max(x, 0)^2 */
+#define NVFP4_ACT_RELU2 2     /* y = max(x, 0)^2; of NaN 0 (NaN for nvfp4_fp8_quantize and nvfp4_moe_decode) */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* nvfp4_status_string(int32_t status);

@@ -90,8 +90,13 @@ __device__ __forceinline__ float silu_f32(float g) {
 // SwiGLU output silu(g) * u.
 __device__ __forceinline__ float swiglu_f32(float g, float u) { return silu_f32(g) * u; }
 
+// max(x, 0)^2; of NaN 0, since E2M1 has none (relu2_f32), or NaN.
 __device__ __forceinline__ float relu2_f32(float x) {
   float r = (x > 0.0f) ? x : 0.0f;
+  return r * r;
+}
+__device__ __forceinline__ float relu2_or_nan_f32(float x) {
+  const float r = (x <= 0.0f) ? 0.0f : x;
   return r * r;
 }
 

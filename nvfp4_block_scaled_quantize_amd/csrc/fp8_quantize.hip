@@ -33,8 +33,8 @@ __device__ __forceinline__ void values8(const u32x4& g, const u32x4& u, float* y
       a = swiglu_f32(a, c);
       b = swiglu_f32(b, d);
     } else if constexpr (ACT == kActRelu2) {
-      a = relu2_f32(a);
-      b = relu2_f32(b);
+      a = relu2_or_nan_f32(a);
+      b = relu2_or_nan_f32(b);
     }
     y[2 * i] = a;
     y[2 * i + 1] = b;

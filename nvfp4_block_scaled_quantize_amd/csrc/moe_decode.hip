@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int unit
       if constexpr (FC == 1) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          v[q] = GATED ? swiglu_f32(times(v[q], f), times(up[q], f)) : relu2_f32(times(v[q], f));
+          v[q] = GATED ? swiglu_f32(times(v[q], f), times(up[q], f)) : relu2_or_nan_f32(times(v[q], f));
           big = __builtin_fmaxf(big, __builtin_fabsf(v[q]));
         }
         if (there) *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(mine.y + r16) * a.inter + col) = v;
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(64 * kOneRowsWaves) moe_one_rows(FcArgs a) {
     if (a.scaled) f.e -= up_exponent(a.ws.xmax[0]);
     float h;
     if constexpr (GATED) h = swiglu_f32(times(v, f), times(__shfl_xor(v, 16, 64), f));
-    else h = relu2_f32(times(v, f));
+    else h = relu2_or_nan_f32(times(v, f));
     if (lane < kCols) a.ws.h[(int64_t)y * a.inter + (int64_t)blockIdx.x * kCols + lane] = h;
     const uint32_t big = wave_max_u32(lane < kCols ? __float_as_uint(__builtin_fmaxf(__builtin_fabsf(h), 0.0f)) : 0u);
     if (lane == 0) atomicMax(a.ws.hmax + y, big);
