@@ -585,12 +585,12 @@ __global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int unit
   const int blocks = (a.K + 255) / 256;
 
   // what belongs to an entry: lane (slot r16, grp) has the slot's token (slot s: the s-th of the mask) or row of h, the
-  // bits of the largest value that it was, or will be, scaled by, and with KEEP its operands
+  // bits of the largest value that it was, or will be, scaled by, what turns its sums into results, and with KEEP its operands
   int ns = 0;
   bool there = false;
   int64_t arow = 0;
   uint32_t top = 0u;
-  float ge = 0.0f, big = 0.0f;
+  float big = 0.0f, ge = 0.0f, rest = 1.0f;   // fc2: times ge, times rest
   RawAct<FC> raw[2];
   v8h kept[2][4], kept_lo[2][4];
   auto load_acts = [&](int c) __attribute__((always_inline)) {
@@ -612,7 +612,13 @@ __global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int unit
       top = a.ws.hmax[arow];
     }
     ge = a.g[mine.x];
-    asm volatile("" : "+v"(top), "+v"(ge));   // waited for here, and not in a unit with loads on their way
+    if constexpr (FC == 2) {
+      const Factor f = split(ge);
+      const int e = f.e - up_exponent(top);   // half of it each: neither leaves binary32 before the result does
+      ge = __builtin_ldexpf(f.f, e / 2);
+      rest = __builtin_ldexpf(1.0f, e - e / 2);
+    }
+    asm volatile("" : "+v"(top), "+v"(ge), "+v"(rest));   // waited for here, and not in a unit with loads on their way
     big = 0.0f;
     if constexpr (KEEP) {
       if (wave < blocks) {
@@ -702,18 +708,18 @@ __global__ void __launch_bounds__(64 * NW, 2) moe_expert_rows(FcArgs a, int unit
       v4f up;
       if constexpr (GATED) up = joined(wave + RT / 2);
       const int col = x * kCols + 16 * wave + 4 * grp;
-      Factor f = split(ge);
-      if (FC == 2 || a.scaled) f.e -= up_exponent(top);
       if constexpr (FC == 1) {
+        // sums are below 2^43, and h above 2^-126 comes of a result above 2^-63: f stays above 2^-106 where it matters
+        const float f = a.scaled ? ge / up_scale(top) : ge;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          v[q] = GATED ? swiglu_f32(times(v[q], f), times(up[q], f)) : relu2_or_nan_f32(times(v[q], f));
+          v[q] = GATED ? swiglu_f32(v[q] * f, up[q] * f) : relu2_or_nan_f32(v[q] * f);
           big = __builtin_fmaxf(big, __builtin_fabsf(v[q]));
         }
         if (there) *reinterpret_cast<v4f*>(a.ws.h + (int64_t)(mine.y + r16) * a.inter + col) = v;
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = times(v[q], f);
+        for (int q = 0; q < 4; ++q) v[q] = v[q] * ge * rest;
         if (there) *reinterpret_cast<v4f*>(a.ws.o + (int64_t)(mine.y + r16) * a.hidden + col) = v;
       }
     }
