@@ -974,25 +974,27 @@ void launch_router(const MoeDecodeArgs& m, const Ws& ws, int P, hipStream_t s) {
 }
 
 // Eight waves where a row is long enough for them (K = 2048: fc1 of 16 tokens 18 us, with four 24 us), else four: one or
-// two workgroups to a compute unit; more of them at a time divide the units worse (4 tokens of 64 experts: 33 us,
-// twice as many 39 us).  64 weight rows to a unit where that leaves six units to each of them (4 tokens of 128
-// experts of 4096 / 1536, SwiGLU: 92 us, with 32 rows 98 us), else 32 (8 tokens of 64 experts of 2048 / 1024: 41 us, with 64
-// rows 45 us).
-template <int FC, bool GATED, bool TW, int RT>
-void launch_units(const FcArgs& a, int experts, int slots, hipStream_t s) {
-  const int units = a.rows / (16 * RT), blocks = (a.K + 255) / 256;
-  const int64_t most = (int64_t)units * experts;
-  const dim3 grid((unsigned)(most < slots ? most : slots));
-  if (blocks <= 4) moe_expert_rows<FC, GATED, TW, RT, 4, true><<<grid, dim3(256), 0, s>>>(a, units);
-  else if (blocks <= 8) moe_expert_rows<FC, GATED, TW, RT, 8, true><<<grid, dim3(512), 0, s>>>(a, units);
-  else moe_expert_rows<FC, GATED, TW, RT, 8, false><<<grid, dim3(512), 0, s>>>(a, units);
-}
-
+// two workgroups to a compute unit (`slots`); more of them at a time divide the units worse (4 tokens of 64 experts: 33 us,
+// twice as many 39 us).
+//
+// 32 weight rows to a unit, 64 for long rows (more than a block for every wave, so that activations are read again with
+// every unit) where that leaves three units to a workgroup.  Whole layers, hidden = inter, one token for each expert, us,
+// with 32 / 64 rows:
+//   K = 2304: 16 experts (2.2 units each) 52 / 56, 24 (3.4) 68 / 65, 32 (4.5) 84 / 80, 64 (9) 150 / 126;
+//   K = 2112: 16 (2.1) 51 / 55, 24 (3.1) 62 / 61, 64 (8.2) 139 / 122;  K = 4096: 16 (4) 107 / 100, 48 (12) 274 / 226.
+// Shorter rows, where a wave holds its activations: 64 rows are never better.  K = 2048: 16 experts (2) 36 / 44, 48 (6)
+// 62 / 68, 128 (16) 125 / 139;  K = 1280: 48 (3.8) 40 / 42, 152 (12) 91 / 91;  K = 1024: 64 (2) 35 / 42, 256 (8) 89 / 91.
 template <int FC, bool GATED, bool TW>
 void launch_rows(const FcArgs& a, int experts, hipStream_t s) {
-  const int slots = a.K > 1024 ? 256 : 512;
-  if ((int64_t)(a.rows / 64) * experts >= 6 * slots) launch_units<FC, GATED, TW, 4>(a, experts, slots, s);
-  else launch_units<FC, GATED, TW, 2>(a, experts, slots, s);
+  const int blocks = (a.K + 255) / 256, slots = blocks <= 4 ? 512 : 256;
+  const bool wide = blocks > 8 && (int64_t)(a.rows / 64) * experts >= 3 * slots;
+  const int units = a.rows / (wide ? 64 : 32);
+  const int64_t most = (int64_t)units * experts;
+  const dim3 grid((unsigned)(most < slots ? most : slots));
+  if (blocks <= 4) moe_expert_rows<FC, GATED, TW, 2, 4, true><<<grid, dim3(256), 0, s>>>(a, units);
+  else if (blocks <= 8) moe_expert_rows<FC, GATED, TW, 2, 8, true><<<grid, dim3(512), 0, s>>>(a, units);
+  else if (!wide) moe_expert_rows<FC, GATED, TW, 2, 8, false><<<grid, dim3(512), 0, s>>>(a, units);
+  else moe_expert_rows<FC, GATED, TW, 4, 8, false><<<grid, dim3(512), 0, s>>>(a, units);
 }
 
 template <bool GATED, bool TW>

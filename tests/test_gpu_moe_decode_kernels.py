@@ -86,12 +86,12 @@ def full(nv, layer, top_k, n_group=1, topk_group=1, norm=True, scaling=1.0, tile
     return out
 
 
-# (tokens, experts, hidden, inter): the chosen experts are all of them or nearly.  With `slots` workgroups (256 for rows
-# of more than 1024, else 512) units have 64 weight rows from rows / 64 * experts >= 6 * slots on, else 32; a row has up
-# to four, up to eight, or more blocks of 256.
-UNITS = {"64 rows, four blocks": (32, 256, 896, 896), "64 rows, eight blocks": (10, 80, 1408, 1664),
-         "64 rows, more blocks": (8, 64, 2176, 2304), "32 rows, four blocks": (4, 32, 896, 896),
-         "32 rows, eight blocks": (2, 16, 1408, 1664), "32 rows, more blocks": (2, 16, 2176, 2304)}
+# (tokens, experts, hidden, inter): the chosen experts are all of them or nearly.  A row has up to four, up to eight, or
+# more blocks of 256; units have 32 weight rows, of rows of more than eight blocks 64 where that leaves three units to each of
+# 256 workgroups.  There are more units than workgroups (256, of rows of up to four blocks 512), so that they cross experts.
+UNITS = {"64 rows, more blocks": (8, 64, 2176, 2304), "32 rows, more blocks": (2, 10, 2176, 2304),
+         "many, eight blocks": (10, 80, 1408, 1664), "eight blocks": (2, 16, 1408, 1664),
+         "many, four blocks": (32, 256, 896, 896), "four blocks": (4, 32, 896, 896)}
 
 
 @pytest.mark.parametrize("tiled", [False, True])
@@ -99,10 +99,11 @@ UNITS = {"64 rows, four blocks": (32, 256, 896, 896), "64 rows, eight blocks": (
 @pytest.mark.parametrize("case", UNITS)
 def test_every_instance(nv, case, act, tiled):
     tokens, experts, hidden, inter = UNITS[case]
-    wide, at_once = case.startswith("64"), min(8 * tokens, experts)
-    for rows, k in ((2 * inter if act == "swiglu" else inter, hidden), (hidden, inter)):
-        slots = 256 if k > 1024 else 512
-        assert (rows // 64 * at_once >= 6 * slots) == wide and rows // 32 * at_once > slots
+    at_once = min(8 * tokens, experts)
+    for rows, k in ((inter, hidden), (2 * inter, hidden), (hidden, inter)):
+        blocks = -(-k // 256)
+        assert blocks <= 8 or (rows // 64 * at_once >= 3 * 256) == case.startswith("64")
+        assert rows // 32 * at_once > (512 if blocks <= 4 else 256)
     full(nv, moe.Layer("bf16" if tiled else "fp16", tokens, experts, hidden, inter, act, seed=hidden + tokens), 8, tiled=tiled)
 
 
