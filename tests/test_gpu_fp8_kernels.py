@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 # K of each form: whole K-blocks or a last one that is cut, and their number a multiple of four (the scales' copies) or not
 FORMS = {"four": 512, "four, cut": 400, "one": 384, "one, cut": 272, "many": 2816, "many, cut": 2000}
 SIZES = {STREAM: [(1, 4096), (7, 1001)], T64X32: [(9, 4096), (33, 2001), (64, 8192)], T64X64: [(128, 8192), (100, 5003)],
-         T64X128: [(400, 5000), (333, 4999)], T128X128: [(2048, 2048), (1901, 2117)], T256X256: [(4096, 3200), (4000, 3333)]}
+         T64X128: [(400, 5000), (333, 4999)], T128X128: [(2048, 4096), (1901, 3333)], T256X256: [(4096, 3200), (4000, 3333)]}
 CASES = [(kernel, b, n) for kernel, sizes in SIZES.items() for b, n in sizes]
 
 

@@ -36,6 +36,6 @@ def test_every_product_fits_a_launch(choose):
 
 def test_sizes_and_kernels(choose):
     want = {(1, 4096): STREAM, (8, 4096): STREAM, (9, 4096): T64X32, (1, 8192): T64X32, (64, 8192): T64X32,
-            (128, 8192): T64X64, (777, 2120): T64X128, (400, 8192): T64X128, (1000, 8192): T128X128, (2048, 2048): T128X128,
-            (4096, 8192): T256X256, (4096, 4096): T256X256}
+            (128, 8192): T64X64, (777, 2120): T64X128, (400, 8192): T64X128, (512, 8192): T64X128, (1000, 8192): T128X128, (2048, 4096): T128X128, (2048, 2048): T64X128,
+            (1500, 2700): T128X128, (4096, 8192): T256X256, (4096, 4096): T256X256}
     assert dict(zip(want, (c[0] for c in choose(list(want))))) == want
