@@ -86,3 +86,13 @@ def test_scales_whose_product_is_subnormal(nv, tokens):
     scaled by, are not."""
     out = kernels.full(nv, tiny(tokens), 8)
     assert out.abs().median() > 2.0 ** -126
+
+
+@pytest.mark.parametrize("tokens", [1, 6])
+def test_small_activations_beside_a_large_one(nv, tokens):
+    """One h is some 2^29 times the others, and fc2 has zeros for it: the others are held to 2^-38 of the large one."""
+    layer = moe.Layer("bf16", tokens, 8, 256, 512, "relu2", seed=5)
+    layer.w1[1][:] = torch.tensor(2.0 ** -6).to(moe.FP8).view(torch.uint8)
+    layer.w1[1][:, 77] = torch.tensor(448.0).to(moe.FP8).view(torch.uint8)
+    layer.w2[0][:, :, 77 // 2] &= 0x0F      # the odd one of the pair
+    kernels.full(nv, layer, 3)
