@@ -49,6 +49,14 @@ __device__ __forceinline__ float unpack1(uint16_t h) {
   else return (float)__builtin_bit_cast(_Float16, h);
 }
 
+// To the nearest number of 16 bits, ties to even.
+template <int DT>
+__device__ __forceinline__ uint16_t round16(float x) {
+  if constexpr (DT == 0) return __builtin_bit_cast(uint16_t, (__bf16)x);
+  else return __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+__device__ __forceinline__ uint16_t round16(float x, int dtype) { return dtype == 0 ? round16<0>(x) : round16<1>(x); }
+
 // ---------------------------------------------------------------- exp
 // exp(x) as a fixed binary32 evaluation (Cody-Waite reduction with ln 2 split
 // into two binary32 parts, degree-7 Taylor polynomial by Horner with fma,

@@ -48,12 +48,6 @@ __device__ __forceinline__ v8i join(u32x4 p, u32x4 q) {
   return r;
 }
 
-template <int DT>
-__device__ __forceinline__ uint16_t round16(float x) {
-  if constexpr (DT == kBf16) return __builtin_bit_cast(uint16_t, (__bf16)x);
-  else return __builtin_bit_cast(uint16_t, (_Float16)x);
-}
-
 // Four consecutive columns n .. n + 3 of a row, of which those below N exist.  One store of eight bytes at any
 // alignment of two (global memory takes those): 3000 x 4098 x 1024 23 us, with four stores 42 us
 // (4097 columns, rows at odd places: 32 and 41 us).

@@ -751,8 +751,7 @@ __global__ void __launch_bounds__(128) moe_combine(FcArgs a) {
   }
   uint16_t o[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    o[q] = a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s[q]) : __builtin_bit_cast(uint16_t, (_Float16)s[q]);
+  for (int q = 0; q < 4; ++q) o[q] = round16(s[q], a.out_type);
   const u32x2 v = {o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16};
   *reinterpret_cast<u32x2*>((uint16_t*)a.out + (int64_t)t * a.hidden + col) = v;
 }
@@ -961,8 +960,7 @@ __global__ void __launch_bounds__(64 * kOneWaves) moe_one_out(FcArgs a) {
 #pragma unroll
   for (int v = 1; v < kOneWaves; ++v) s += part[v][tid];
   s = __builtin_ldexpf(s, -up);
-  ((uint16_t*)a.out)[16 * (int)blockIdx.x + tid] =
-      a.out_type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)s) : __builtin_bit_cast(uint16_t, (_Float16)s);
+  ((uint16_t*)a.out)[16 * (int)blockIdx.x + tid] = round16(s, a.out_type);
 }
 
 template <int DT>

@@ -23,12 +23,6 @@ constexpr int kPairs = 256;        // pairs of a workgroup's tokens (a rotary di
 constexpr int kMaxTokens = 8;      // tokens of a workgroup
 constexpr int kDeep = 4;           // items of a thread in flight
 
-template <int DT>
-__device__ __forceinline__ uint16_t pack1(float x) {
-  if constexpr (DT == kBf16) return __builtin_bit_cast(uint16_t, (__bf16)x);
-  else return __builtin_bit_cast(uint16_t, (_Float16)x);
-}
-
 // A thread's unit of E pairs: E = 8 (16-byte accesses) or 1.  `first` and `second` are the raw
 // elements of the unit in memory order: split pairs (2 E elements in two runs), neighbours (one run).
 template <int E>
@@ -164,8 +158,8 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(RopeKvArgs a) {
           const int ia = PAIRED ? 2 * e : e, ib = PAIRED ? 2 * e + 1 : e + E;
           const float2 cs = turn[m[d].pair + e];
           const float p = unpack1<DT>(x[d].v[ia]), q = unpack1<DT>(x[d].v[ib]);
-          x[d].v[ia] = pack1<DT>(__builtin_fmaf(p, cs.x, -(q * cs.y)));
-          x[d].v[ib] = pack1<DT>(__builtin_fmaf(p, cs.y, q * cs.x));
+          x[d].v[ia] = round16<DT>(__builtin_fmaf(p, cs.x, -(q * cs.y)));
+          x[d].v[ib] = round16<DT>(__builtin_fmaf(p, cs.y, q * cs.x));
         }
       }
       if (m[d].to) {
