@@ -701,7 +701,8 @@ def fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: t
              out_dtype: torch.dtype = torch.float16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[B, N] = sum_k a[b, k] a_scale[b, k / 128] w[n, k] w_scale[n / 128, k / 128] for float8_e4m3fn a [B, K]
     and w [N, K] with float32 scales (fp8_quantize with block_rows 1 and 128, or a checkpoint's).
-    float16 or bfloat16 out (out_dtype, or the type of `out`)."""
+    float16 or bfloat16 out (out_dtype, or the type of `out`).  The sums inside a block of 128 are those of the E4M3 matrix
+    instructions (about 2^-16 of the block's size, at most 7 * 2^-13), the others binary32."""
     dev = _gpu_of(a)
     f32 = torch.float32
     try:
@@ -779,7 +780,7 @@ def moe_decode(x: torch.Tensor, router: torch.Tensor, bias: torch.Tensor, w1: to
                workspace: torch.Tensor | None = None, stream=None):
     """A whole MoE layer for up to 32 tokens: x [tokens, hidden] and router [experts, hidden] (float16 or
     bfloat16), the expert weights of moe_w4a16() (or, with `tiled`, of moe_pretile_weights()); for act="swiglu" w1
-    holds [experts, 2 inter, ...] gate and up rows.  Returns out [tokens, hidden] of x's type, or (out, ids,
+    holds [experts, 2 inter, ...] gate and up rows.  `out` may be x.  Returns out [tokens, hidden] of x's type, or (out, ids,
     weights) with want_routing."""
     a = _act_code(act)
     gated = a == ACT["swiglu"]

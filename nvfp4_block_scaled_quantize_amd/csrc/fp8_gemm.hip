@@ -77,10 +77,13 @@ __device__ __forceinline__ int run_of_die(int b, int total) {
 // the rows' 128 bytes with piece p of row r at p ^ ((r / 2) mod 8): the 16 lanes of an operand read
 // touch 16 different places of 16 bytes.
 //
-// The copies' lines bound it: every 64 x 16 bytes of a copy are eight lines of the L2, but one binary32 scale for
-// each of 64 rows is 64 lines.  So the scales of a row are copied four blocks at a time (SB = 4) where their rows
-// are aligned to that, and each line that the workgroups of a die share is asked for ahead by one of them.
-// 4096 x 8192 x 8192: 248 us, 2.2 PFLOP/s, matrix cores 57 % busy; a library product with one scale takes 202 us.
+// The matrix cores are busy for 57 % of the time: operand reads from LDS, the issue of the copies and the scales' fma do
+// not hide behind them fully.  What the copies cost is lines: every 64 x 16 bytes of one are eight lines of the L2, but one
+// binary32 scale for each of 64 rows is 64 lines.  So the scales of a row are copied four blocks at a time (SB = 4) where
+// their rows are aligned to that (us, against one block at a time: 4096 x 8192 x 8192 239 / 243, x 8176 260 / 267, 1000 x
+// 8192 x 8192 82.4 / 83.6, but 2048 x 2048 x 4096 30.2 / 28.8), and each line that the workgroups of a die share is asked
+// for ahead by one of them.  4096 x 8192 x 8192: 239 to 255 us by the clocks of the moment, 2.2 PFLOP/s; a library product
+// with one scale takes 202 us.
 // CUT: K ends inside a block.
 template <int TT, int FT, int WT, int WF, int SB>
 struct Tile {
@@ -474,7 +477,7 @@ fp8_gemm_small(Fp8GemmArgs g, int tiles_m, int tiles_n) {
 }
 
 // ---------------------------------------------------------------- streams (few rows)
-// A workgroup holds all rows of a (up to 16) against 16 rows of w; its waves take the K-blocks in turn, kAhead of
+// A workgroup holds all rows of a (up to 8; the instruction has room for 16) against 16 rows of w; its waves take the K-blocks in turn, kAhead of
 // them in flight a wave, straight from memory into registers (every byte of w is read once, by one wave), and their
 // sums are joined through LDS.  Bound by the latency of a chain of K / 128 / (8 kAhead) loads: 1 x 4096 x 4096 6.6 us.
 constexpr int kAhead = 4, kStreamWaves = 8;

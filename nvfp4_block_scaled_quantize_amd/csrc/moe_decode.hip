@@ -20,12 +20,15 @@
 // The activations must be FP16 for that.  FP16 x is used as it is.  BF16 x is multiplied by the power
 // of two that brings the token's largest value to [2^14, 2^15): exact down to 2^-31 of the largest, what is
 // below is off by at most 2^-39 of it.  h (binary32) is brought to the same range by the pair's
-// largest h and split into two FP16 numbers, the value and what its rounding left: off by less than 2^-20 of itself.
+// largest h and split into two FP16 numbers, the value and what its rounding left: off by less than 2^-20 of itself or,
+// where FP16's smallest step of 2^-24 is more, 2^-38 of the largest (for one token: of the largest h times its factor).
 //
-// Measured (launches included), of which the weights at the rate of a large copy (5.1 TB/s) take the second figure:
-// 1 token, 8 of 64 experts, 2048 / 1024, ReLU^2    router 2.7, fc1 9.9, fc2 6.6 us: 17.7 us of             3.7 us
-// 16 tokens of the same layer                      3.5, plan 5.5, 17.6, 18.7, combine 4.0: 46.0 us of      26 us
-// 4 tokens, 8 of 128, 4096 / 1536, SwiGLU          4.8, 5.3, 50.5, 28.5, 4.7: 83.3 us of                   61 us
+// Measured: the kernels' medians in a trace (which adds some 0.4 us to each), the whole layer without one (among other
+// calls; with weights that the last cache may hold, and with ones that it cannot), and the weights at the rate of a large
+// copy (5.1 TB/s):
+// 1 token, 8 of 64 experts, 2048 / 1024, ReLU^2    router 2.6, fc1 9.5, fc2 6.7; 17.9 us;                     3.7 us
+// 16 tokens of the same layer                      3.9, plan 5.2, 17.1, 18.4, combine 4.6; 44 to 46 us;       26 us
+// 4 tokens, 8 of 128, 4096 / 1536, SwiGLU          4.8, 5.1, 50.0, 27.2, 4.8; 82 to 88 us;                    61 us
 // What is above it is the launches' own time, the dependent loads at their starts (4 to 5 us of a large one) and the
 // last round of units, which not all workgroups have.
 #include "device_common.h"
@@ -527,8 +530,8 @@ __device__ __forceinline__ v2h rest2(float a, float b, const v2h& p) {
   return __builtin_elementwise_max(q, least);
 }
 
-// Operands of instruction m.  FC 1: as stored.  FC 2: scaled and split; both roundings are toward zero,
-// the first leaves less than 2^-10 of the value, the second less than 2^-10 of that.
+// Operands of instruction m.  FC 1: as stored.  FC 2: scaled and split; both roundings are toward zero, the first
+// leaves less than 2^-10 of the value (of normal numbers), the second less than 2^-10 of that or 2^-24.
 template <int FC>
 __device__ __forceinline__ void act_operand(const RawAct<FC>& r, int m, float scale, v8h& hi, v8h& lo) {
   if constexpr (FC == 1) {

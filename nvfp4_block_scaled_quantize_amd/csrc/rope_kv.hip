@@ -10,6 +10,8 @@
 // Bound by memory (each row is read once and written once or twice); a pair's sine and cosine cost some
 // hundred operations, so they are formed once per token for all heads and kept in LDS.  Measured, 32/8 heads of
 // 128: 16384 tokens 90 us (436 MB, 4.8 TB/s; a large copy 5.1 TB/s), 64 tokens 4.4 us, a launch and a chain of two loads.
+// Where the rows or the turning runs are not aligned to 16 bytes, everything goes element by element: 16384 tokens
+// of odd strides 179 us, of dimension 80 with 40 turned 140 us (all 80 turned, aligned: 64 us).
 #include "attention.h"
 #include "device_common.h"
 #include "internal.h"
